@@ -1,6 +1,7 @@
 """In-tree build of the C-ABI library ``libgs.so`` for sm_103a.
 
-Every source under ``csrc/`` is compiled in parallel into ``_build/`` and linked
+Every source under ``csrc/`` (the guided step) and ``csrc_decode/`` (the decode
+operators) is compiled in parallel into ``_build/`` and linked
 into ``bucketized_guidance_step_gb300/libgs.so`` (the CUDA runtime is linked
 statically, so the library needs only the driver at run time).  The build is
 skipped when the library is newer than every source and header.
@@ -24,6 +25,7 @@ from concurrent.futures import ThreadPoolExecutor
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
+CSRC_DECODE = os.path.join(PKG, "csrc_decode")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgs.so")
@@ -38,13 +40,14 @@ def _nvcc() -> str:
 
 
 def _sources():
-    return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC)
+    return sorted(os.path.join(d, f) for d in (CSRC, CSRC_DECODE) for f in os.listdir(d)
                   if f.endswith((".cu", ".cpp")))
 
 
 def _inputs():
     files = _sources() + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
-    files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh", ".inc"))]
+    files += [os.path.join(d, f) for d in (CSRC, CSRC_DECODE) for f in os.listdir(d)
+              if f.endswith((".h", ".cuh", ".inc"))]
     files.append(os.path.abspath(__file__))
     return files
 

@@ -1,0 +1,584 @@
+// Pages of a key-value cache: extend, fork, free, compact, and the copies they cause (sm_103a).
+//
+// The bookkeeping of one call (which pages are free, who gets which) is small: a few words
+// a sequence and one word a page.  It runs in one cluster of 8 blocks, so that the count of
+// every page is read once, by eighths, without a grid-wide pass: each block counts the free
+// pages of its eighth, the counts are exchanged through distributed shared memory, and each
+// block then hands out its own free pages by rank.  The rank of a free page decides which
+// entry of the list takes it, so the outcome does not depend on timing.
+//
+// The copies (fork: the filled rows of a partly filled page; compact: whole pages) are a
+// second kernel over a list that the first one leaves in the workspace, launched without the
+// host knowing the list's length.  It is bound by HBM: each byte is read once and written once.
+#include "decode_common.cuh"
+
+namespace gs_decode {
+namespace {
+
+constexpr int kCluster = 8;
+constexpr int kMeta = 512;               // threads of a bookkeeping block
+constexpr int kCopy = 256;               // threads of a copy block
+constexpr int kNone = 0x7fffffff;
+
+// Workspace: [0] the number of copies, [4 ..] the copies as (from, to, tokens, -),
+// then (compact) a word a page: the rank of a moved page.
+struct Copy {
+    int from, to, tokens, pad;
+};
+__device__ __forceinline__ Copy* copies_of(int* work) { return reinterpret_cast<Copy*>(work + 4); }
+inline long long copy_slots(const gs_kv_cache* c) {
+    return c->pages > c->seqs ? c->pages : c->seqs;
+}
+
+__device__ __forceinline__ int pages_of(int len, int page) { return (len + page - 1) / page; }
+
+// The free pages of this block's eighth, and what the whole cluster has: avail = all free
+// pages, before = those of the lower blocks.  Contains two cluster barriers; `mine` is read by
+// the other blocks until the second.
+__device__ __forceinline__ void count_free(const CacheView& c, int lo, int hi, int* mine, int* tmp,
+                                           int* avail, int* before) {
+    int n = 0;
+    for (int p = lo + static_cast<int>(threadIdx.x); p < hi; p += kMeta)
+        n += __ldcg(c.refs + p) == 0 ? 1 : 0;
+    int total;
+    block_scan<kMeta>(n, tmp, &total);
+    if (threadIdx.x == 0) *mine = total;
+    cluster_sync();
+    const unsigned rank = cluster_rank();
+    int a = 0, b = 0;
+#pragma unroll
+    for (unsigned r = 0; r < kCluster; ++r) {
+        const int v = cluster_read(mine, r);
+        a += v;
+        if (r < rank) b += v;
+    }
+    *avail = a;
+    *before = b;
+    cluster_sync();
+}
+
+// The eighth [lo, hi) of block `rank`.
+__device__ __forceinline__ void eighth(int n, int* lo, int* hi) {
+    const long long rank = cluster_rank();
+    *lo = static_cast<int>(n * rank / kCluster);
+    *hi = static_cast<int>(n * (rank + 1) / kCluster);
+}
+
+// The last i in [0, n) with at[i] <= r (at rises, at[0] = 0).
+__device__ __forceinline__ int owner_of(const int* at, int n, int r) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (at[mid] <= r) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+// at[i] = the sum of need[0 .. i), held at `cap` at most; returns the sum of all, held likewise.
+__device__ __forceinline__ int prefix_of(const int* need, int* at, int n, int cap,
+                                         long long* tmp) {
+    long long carry = 0;
+    for (int i0 = 0; i0 < n; i0 += kMeta) {
+        const int i = i0 + static_cast<int>(threadIdx.x);
+        long long total;
+        const long long ex =
+            carry + block_scan<kMeta>(i < n ? static_cast<long long>(need[i]) : 0ll, tmp, &total);
+        if (i < n) at[i] = static_cast<int>(ex < cap ? ex : cap);
+        carry += total;
+    }
+    __syncthreads();
+    return static_cast<int>(carry < cap ? carry : cap);
+}
+
+// First entry of the list that names each sequence (kNone: none).  Ends with a barrier.
+__device__ __forceinline__ void mark_first(int* mark, int seqs, const int* list, int n) {
+    for (int s = threadIdx.x; s < seqs; s += kMeta) mark[s] = kNone;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kMeta) {
+        const int s = list[i];
+        if (s >= 0 && s < seqs) atomicMin(mark + s, i);
+    }
+    __syncthreads();
+}
+
+__global__ void __launch_bounds__(kMeta)
+extend_kernel(CacheView c, const int* __restrict__ seq, const int* __restrict__ add, int n) {
+    extern __shared__ int smem[];
+    int* mark = smem;                    // [seqs]
+    int* need = mark + c.seqs;           // [n] pages wanted
+    int* held = need + n;                // [n] pages held, -1: not to be served
+    int* at = held + n;                  // [n] pages wanted by the entries before
+    __shared__ long long tmp64[kMeta / 32 + 1];
+    __shared__ int tmp[kMeta / 32 + 1];
+    __shared__ int mine;
+    grid_wait();
+    mark_first(mark, c.seqs, seq, n);
+    const bool first_block = cluster_rank() == 0;
+    for (int i = threadIdx.x; i < n; i += kMeta) {
+        const int s = seq[i];
+        const int more = add != nullptr ? add[i] : 1;
+        int want = 0, have = -1;
+        if (s >= 0 && s < c.seqs && mark[s] == i && more >= 0) {
+            const int len = __ldcg(c.lens + s);
+            const long long total = static_cast<long long>(len) + more;
+            if (len < 0 || len > c.cols * c.page) {
+                if (first_block) flag(c.status, GS_DEV_BAD_SEQ);
+            } else if (total > static_cast<long long>(c.cols) * c.page) {
+                if (first_block) flag(c.status, GS_DEV_NO_PAGE);
+            } else {
+                have = pages_of(len, c.page);
+                want = pages_of(static_cast<int>(total), c.page) - have;
+            }
+        } else if (first_block) {
+            flag(c.status, GS_DEV_BAD_SEQ);
+        }
+        need[i] = want;
+        held[i] = have;
+    }
+    __syncthreads();
+    const int total = prefix_of(need, at, n, c.pages + 1, tmp64);
+    int avail = 0;
+    if (total > 0) {
+        int lo, hi, rank;
+        eighth(c.pages, &lo, &hi);
+        count_free(c, lo, hi, &mine, tmp, &avail, &rank);
+        const int end = total < avail ? total : avail;
+        for (int p0 = lo; p0 < hi && rank < end; p0 += kMeta) {
+            const int p = p0 + static_cast<int>(threadIdx.x);
+            const int is_free = p < hi && __ldcg(c.refs + p) == 0 ? 1 : 0;
+            int found;
+            const int r = rank + block_scan<kMeta>(is_free, tmp, &found);
+            rank += found;
+            if (is_free && r < end) {
+                const int i = owner_of(at, n, r);
+                if (at[i] + need[i] <= avail) {
+                    c.table[static_cast<long long>(seq[i]) * c.cols + held[i] + (r - at[i])] = p;
+                    c.refs[p] = 1;
+                }
+            }
+        }
+    } else {
+        cluster_sync();                  // every block has read the lengths
+    }
+    for (int i = cluster_rank() * kMeta + threadIdx.x; i < n; i += kCluster * kMeta) {
+        if (held[i] < 0) continue;
+        if (need[i] == 0 || at[i] + need[i] <= avail)
+            c.lens[seq[i]] += add != nullptr ? add[i] : 1;
+        else
+            flag(c.status, GS_DEV_NO_PAGE);
+    }
+}
+
+__global__ void __launch_bounds__(kMeta)
+fork_kernel(CacheView c, const int* __restrict__ src, const int* __restrict__ dst, int n) {
+    extern __shared__ int smem[];
+    int* mark = smem;                    // [seqs]
+    int* from = mark + c.seqs;           // [n] length of src, -1: pair refused
+    int* need = from + n;                // [n] 1: src's last page is partly filled
+    int* at = need + n;                  // [n]
+    __shared__ long long tmp64[kMeta / 32 + 1];
+    __shared__ int tmp[kMeta / 32 + 1];
+    __shared__ int mine;
+    grid_wait();
+    mark_first(mark, c.seqs, dst, n);
+    const bool first_block = cluster_rank() == 0;
+    const int most = c.cols * c.page;
+    for (int i = threadIdx.x; i < n; i += kMeta) {
+        const int s = src[i], d = dst[i];
+        int len = -1;
+        if (s >= 0 && s < c.seqs && d >= 0 && d < c.seqs && mark[d] == i && mark[s] == kNone) {
+            len = __ldcg(c.lens + s);
+            const int old = __ldcg(c.lens + d);
+            if (len < 0 || len > most || old < 0 || old > most) len = -1;
+        }
+        if (len < 0 && first_block) flag(c.status, GS_DEV_BAD_SEQ);
+        from[i] = len;
+        need[i] = len > 0 && len % c.page != 0 ? 1 : 0;
+    }
+    __syncthreads();
+    const int total = prefix_of(need, at, n, c.pages + 1, tmp64);
+    // Release what the destinations hold, share the sources' full pages.
+    const int self = cluster_rank() * kMeta + threadIdx.x;
+    const long long cells = static_cast<long long>(n) * c.cols;
+    for (long long q = self; q < cells; q += kCluster * kMeta) {
+        const int i = static_cast<int>(q / c.cols), j = static_cast<int>(q % c.cols);
+        if (from[i] < 0) continue;
+        if (j < pages_of(__ldcg(c.lens + dst[i]), c.page)) {
+            const int p = __ldcg(c.table + static_cast<long long>(dst[i]) * c.cols + j);
+            if (p >= 0 && p < c.pages) atomicSub(c.refs + p, 1);
+            else flag(c.status, GS_DEV_BAD_SEQ);
+        }
+        if (j < from[i] / c.page) {
+            const int p = __ldcg(c.table + static_cast<long long>(src[i]) * c.cols + j);
+            if (p >= 0 && p < c.pages) atomicAdd(c.refs + p, 1);
+            else flag(c.status, GS_DEV_BAD_SEQ);
+        }
+    }
+    cluster_sync();
+    int avail = 0;
+    if (total > 0) {
+        int lo, hi, rank;
+        eighth(c.pages, &lo, &hi);
+        count_free(c, lo, hi, &mine, tmp, &avail, &rank);
+        const int end = total < avail ? total : avail;
+        for (int p0 = lo; p0 < hi && rank < end; p0 += kMeta) {
+            const int p = p0 + static_cast<int>(threadIdx.x);
+            const int is_free = p < hi && __ldcg(c.refs + p) == 0 ? 1 : 0;
+            int found;
+            const int r = rank + block_scan<kMeta>(is_free, tmp, &found);
+            rank += found;
+            if (is_free && r < end) {
+                const int i = owner_of(at, n, r);
+                const int col = from[i] / c.page;
+                const int last = __ldcg(c.table + static_cast<long long>(src[i]) * c.cols + col);
+                Copy w;
+                w.from = last;
+                w.to = p;
+                w.tokens = last >= 0 && last < c.pages ? from[i] % c.page : 0;
+                w.pad = 0;
+                copies_of(c.work)[r] = w;
+                c.table[static_cast<long long>(dst[i]) * c.cols + col] = p;
+                c.refs[p] = 1;
+            }
+        }
+    }
+    if (self == 0) c.work[0] = total < avail ? total : avail;
+    for (long long q = self; q < cells; q += kCluster * kMeta) {
+        const int i = static_cast<int>(q / c.cols), j = static_cast<int>(q % c.cols);
+        if (from[i] < 0) continue;
+        const int full = from[i] / c.page;
+        const bool served = need[i] == 0 || at[i] < avail;
+        if (j == 0) {
+            c.lens[dst[i]] = served ? from[i] : 0;
+            if (!served) flag(c.status, GS_DEV_NO_PAGE);
+        }
+        int* to = c.table + static_cast<long long>(dst[i]) * c.cols + j;
+        int p = -1;
+        if (j < full) {
+            p = __ldcg(c.table + static_cast<long long>(src[i]) * c.cols + j);
+            if (!served) {
+                if (p >= 0 && p < c.pages) atomicSub(c.refs + p, 1);
+                p = -1;
+            }
+        } else if (j == full && need[i] != 0 && served) {
+            continue;                    // the page taken above
+        }
+        *to = p;
+    }
+    cluster_sync();                      // no block ends while another reads its count
+}
+
+// One warp a listed sequence.  Its length is taken once (atomicExch), so that a second listing
+// finds nothing to release.
+__global__ void __launch_bounds__(128) free_kernel(CacheView c, const int* __restrict__ seq, int n) {
+    grid_wait();
+    const int i = (blockIdx.x * 128 + threadIdx.x) >> 5, lane = threadIdx.x & 31;
+    if (i >= n) return;
+    const int s = seq[i];
+    if (s < 0 || s >= c.seqs) {
+        if (lane == 0) flag(c.status, GS_DEV_BAD_SEQ);
+        return;
+    }
+    int len = 0;
+    if (lane == 0) len = atomicExch(c.lens + s, 0);
+    len = __shfl_sync(0xffffffffu, len, 0);
+    if (len < 0 || len > c.cols * c.page) {
+        if (lane == 0) flag(c.status, GS_DEV_BAD_SEQ);
+        return;
+    }
+    const int held = pages_of(len, c.page);
+    int* row = c.table + static_cast<long long>(s) * c.cols;
+    for (int j = lane; j < held; j += 32) {
+        const int p = row[j];
+        if (p >= 0 && p < c.pages) atomicSub(c.refs + p, 1);
+        else flag(c.status, GS_DEV_BAD_SEQ);
+        row[j] = -1;
+    }
+}
+
+// n = held pages.  The k-th lowest free page below n (rank among the free pages: k) takes the
+// k-th highest held page (n - 1 - held pages before it = k).  The counts of the moved pages go
+// through the list, so that refs_out may be refs.
+__global__ void __launch_bounds__(kMeta)
+compact_kernel(CacheView c, int* __restrict__ refs_out, int* __restrict__ live_out) {
+    __shared__ int tmp[kMeta / 32 + 1];
+    __shared__ int mine;
+    grid_wait();
+    int lo, hi, avail, before;
+    eighth(c.pages, &lo, &hi);
+    count_free(c, lo, hi, &mine, tmp, &avail, &before);
+    const int live = c.pages - avail;
+    Copy* copies = copies_of(c.work);
+    int* rank_of = c.work + 4 + 4 * static_cast<long long>(c.pages > c.seqs ? c.pages : c.seqs);
+    int moved = 0;
+    for (int p0 = lo; p0 < hi; p0 += kMeta) {
+        const int p = p0 + static_cast<int>(threadIdx.x);
+        const int count = p < hi ? __ldcg(c.refs + p) : 1;
+        int found;
+        const int f = before + block_scan<kMeta>(count == 0 ? 1 : 0, tmp, &found);   // free before p
+        before += found;
+        if (p < hi) {
+            if (count == 0 && p < live) {
+                copies[f].to = p;                               // filled below
+            } else if (count != 0 && p >= live) {
+                const int k = live - 1 - (p - f);
+                copies[k].from = p;
+                copies[k].tokens = c.page;
+                copies[k].pad = count;
+                rank_of[p] = k;
+                ++moved;
+            }
+        }
+    }
+    int total;
+    block_scan<kMeta>(moved, tmp, &total);
+    if (threadIdx.x == 0) mine = total;
+    cluster_sync();
+    int all = 0;
+#pragma unroll
+    for (unsigned r = 0; r < kCluster; ++r) all += cluster_read(&mine, r);
+    if (cluster_rank() == 0 && threadIdx.x == 0) {
+        c.work[0] = all;
+        c.work[1] = live;
+        if (live_out != nullptr) *live_out = live;
+    }
+    // Counts: what stays is copied, what is above n is 0; then the moved pages' counts.
+    for (int p = lo + static_cast<int>(threadIdx.x); p < hi; p += kMeta) {
+        const int count = __ldcg(c.refs + p);
+        if (p >= live) refs_out[p] = 0;
+        else if (count != 0) refs_out[p] = count;
+    }
+    for (int k = cluster_rank() * kMeta + threadIdx.x; k < all; k += kCluster * kMeta) {
+        const int4 w = __ldcg(reinterpret_cast<const int4*>(copies + k));
+        refs_out[w.y] = w.w;
+    }
+    cluster_sync();
+}
+
+// The listed copies: a unit of work is one page of one layer of K or V.  16-byte vectors,
+// several in flight a thread.  With `table` set, the table's entries are renumbered too
+// (compact).
+template <bool REMAP>
+__global__ void __launch_bounds__(kCopy)
+copy_kernel(CacheView c, int es, int* __restrict__ table_out) {
+    grid_wait();
+    const int count = __ldcg(c.work);
+    const Copy* copies = copies_of(c.work);
+    if constexpr (REMAP) {
+        const int live = __ldcg(c.work + 1);
+        const int* rank_of = c.work + 4 + 4 * static_cast<long long>(c.pages > c.seqs ? c.pages : c.seqs);
+        const long long cells = static_cast<long long>(c.seqs) * c.cols;
+        for (long long q = static_cast<long long>(blockIdx.x) * kCopy + threadIdx.x; q < cells;
+             q += static_cast<long long>(gridDim.x) * kCopy) {
+            int p = c.table[q];
+            // Entries past a sequence's pages may hold anything: only held pages are renumbered.
+            const int s = static_cast<int>(q / c.cols), j = static_cast<int>(q % c.cols);
+            if (p >= live && p < c.pages && j < pages_of(__ldcg(c.lens + s), c.page))
+                p = __ldcg(&copies[rank_of[p]].to);
+            table_out[q] = p;
+        }
+    }
+    const int per = c.dim * es / 16;                     // vectors of a row
+    const long long units = 2ll * count * c.layers;
+    for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+        const int4 w = __ldcg(reinterpret_cast<const int4*>(copies + u / (2 * c.layers)));
+        const int which = static_cast<int>(u % (2 * c.layers));
+        char* base = ((which & 1) != 0 ? c.v : c.k) + (which >> 1) * c.layer_stride * es;
+        const char* src = base + w.x * c.page_stride * es;
+        char* dst = base + w.y * c.page_stride * es;
+        const int vecs = c.heads * w.z * per;
+        constexpr int U = 4;
+        for (int v0 = threadIdx.x; v0 < vecs; v0 += kCopy * U) {
+            uint4 r[U];
+            long long off[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int v = v0 + i * kCopy;
+                if (v < vecs) {
+                    const int row = v / per;
+                    const int head = row / w.z;
+                    off[i] = (head * c.head_stride + (row - head * w.z) * c.token_stride) * es +
+                             16ll * (v - row * per);
+                    r[i] = __ldcs(reinterpret_cast<const uint4*>(src + off[i]));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (v0 + i * kCopy < vecs) __stcs(reinterpret_cast<uint4*>(dst + off[i]), r[i]);
+        }
+    }
+}
+
+// New tokens' K and V into one layer: a warp a token and K or V, 16 bytes a lane.
+template <class T>
+__global__ void __launch_bounds__(kCopy)
+write_kernel(CacheView c, int layer, const T* __restrict__ k, const T* __restrict__ v,
+             long long token_stride, long long head_stride, int src_aligned, int tokens,
+             const int* __restrict__ seq, const int* __restrict__ start, int n) {
+    grid_wait();
+    const int lane = threadIdx.x & 31;
+    const long long w = (static_cast<long long>(blockIdx.x) * kCopy + threadIdx.x) >> 5;
+    const int t = static_cast<int>(w >> 1);
+    if (t >= tokens || t < start[0] || t >= start[n]) return;
+    int lo = 0, hi = n;                                  // the last i with start[i] <= t
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (start[mid] <= t) lo = mid; else hi = mid;
+    }
+    const int s = seq[lo];
+    bool ok = s >= 0 && s < c.seqs;
+    long long pos = -1;
+    if (ok) {
+        const int len = c.lens[s];
+        pos = static_cast<long long>(len) - (start[lo + 1] - t);
+        ok = pos >= 0 && len <= c.cols * c.page;
+    }
+    int p = -1;
+    if (ok) {
+        p = c.table[static_cast<long long>(s) * c.cols + pos / c.page];
+        ok = p >= 0 && p < c.pages;
+    }
+    if (!ok) {
+        if (lane == 0) flag(c.status, GS_DEV_BAD_SEQ);
+        return;
+    }
+    constexpr int E = 16 / sizeof(T);
+    const T* src = ((w & 1) != 0 ? v : k) + t * token_stride;
+    T* dst = reinterpret_cast<T*>((w & 1) != 0 ? c.v : c.k) + layer * c.layer_stride +
+             p * c.page_stride + (pos % c.page) * c.token_stride;
+    const int per = c.dim / E;
+    for (int q = lane; q < c.heads * per; q += 32) {
+        const int head = q / per, x = (q - head * per) * E;
+        *reinterpret_cast<uint4*>(dst + head * c.head_stride + x) =
+            load16_any(src + head * head_stride + x, src_aligned != 0);
+    }
+}
+
+long long workspace_need(const gs_kv_cache* c) {
+    return 4 * (4 + 4 * copy_slots(c) + static_cast<long long>(c->pages));
+}
+
+gs_status check_call(const gs_kv_cache* cache, int32_t n, CacheView* view) {
+    const gs_status st = check_cache(cache, view);
+    if (st != GS_OK) return st;
+    if (n < 0) return GS_ERR_INVALID_ARG;
+    if (n > GS_MAX_SEQS) return GS_ERR_UNSUPPORTED;
+    return GS_OK;
+}
+
+gs_status check_workspace(const gs_kv_cache* c) {
+    if (c->workspace == nullptr || !aligned(c->workspace, 16) ||
+        c->workspace_bytes < workspace_need(c))
+        return GS_ERR_INVALID_ARG;
+    return GS_OK;
+}
+
+template <bool REMAP>
+gs_status launch_copies(const CacheView& c, int dtype, long long most, int* table_out,
+                        gs_stream stream) {
+    long long blocks = most * 2 * c.layers;
+    const long long full = static_cast<long long>(sm_count()) * 8;
+    if (blocks > full) blocks = full;
+    if (blocks < 1) blocks = 1;
+    return launch(copy_kernel<REMAP>, dim3(static_cast<unsigned>(blocks)), kCopy, 0, 1, stream, c,
+                  static_cast<int>(elem_size(dtype)), table_out);
+}
+
+}  // namespace
+}  // namespace gs_decode
+
+using namespace gs_decode;
+
+extern "C" gs_status gs_pages_workspace(const gs_kv_cache* cache, int64_t* bytes) {
+    if (bytes == nullptr) return GS_ERR_INVALID_ARG;
+    const gs_status st = check_cache_sizes(cache);
+    if (st != GS_OK) return st;
+    *bytes = workspace_need(cache);
+    return GS_OK;
+}
+
+extern "C" gs_status gs_pages_extend(const gs_kv_cache* cache, const int32_t* seq,
+                                     const int32_t* add, int32_t n, gs_stream stream) {
+    CacheView c;
+    const gs_status st = check_call(cache, n, &c);
+    if (st != GS_OK) return st;
+    if (n == 0) return GS_OK;
+    if (seq == nullptr) return GS_ERR_INVALID_ARG;
+    const int smem = 4 * (c.seqs + 3 * n);
+    if (!allow_smem<extend_kernel>(smem)) return GS_ERR_CUDA;
+    return launch(extend_kernel, dim3(kCluster), kMeta, smem, kCluster, stream, c, seq, add, n);
+}
+
+extern "C" gs_status gs_pages_fork(const gs_kv_cache* cache, const int32_t* src,
+                                   const int32_t* dst, int32_t n, gs_stream stream) {
+    CacheView c;
+    gs_status st = check_call(cache, n, &c);
+    if (st != GS_OK) return st;
+    if (n == 0) return GS_OK;
+    if (src == nullptr || dst == nullptr) return GS_ERR_INVALID_ARG;
+    st = check_workspace(cache);
+    if (st != GS_OK) return st;
+    const int smem = 4 * (c.seqs + 3 * n);
+    if (!allow_smem<fork_kernel>(smem)) return GS_ERR_CUDA;
+    st = launch(fork_kernel, dim3(kCluster), kMeta, smem, kCluster, stream, c, src, dst, n);
+    if (st != GS_OK) return st;
+    return launch_copies<false>(c, cache->dtype, n, nullptr, stream);
+}
+
+extern "C" gs_status gs_pages_free(const gs_kv_cache* cache, const int32_t* seq, int32_t n,
+                                   gs_stream stream) {
+    CacheView c;
+    const gs_status st = check_call(cache, n, &c);
+    if (st != GS_OK) return st;
+    if (n == 0) return GS_OK;
+    if (seq == nullptr) return GS_ERR_INVALID_ARG;
+    return launch(free_kernel, dim3(static_cast<unsigned>((n + 3) / 4)), 128, 0, 1, stream, c, seq,
+                  n);
+}
+
+extern "C" gs_status gs_pages_compact(const gs_kv_cache* cache, int32_t* table_out,
+                                      int32_t* refs_out, int32_t* live_out, gs_stream stream) {
+    CacheView c;
+    gs_status st = check_call(cache, 0, &c);
+    if (st != GS_OK) return st;
+    if (table_out == nullptr || refs_out == nullptr) return GS_ERR_INVALID_ARG;
+    st = check_workspace(cache);
+    if (st != GS_OK) return st;
+    st = launch(compact_kernel, dim3(kCluster), kMeta, 0, kCluster, stream, c, refs_out, live_out);
+    if (st != GS_OK) return st;
+    return launch_copies<true>(c, cache->dtype, c.pages, table_out, stream);
+}
+
+extern "C" gs_status gs_kv_write(const gs_kv_cache* cache, int32_t layer, const void* k,
+                                 const void* v, int64_t token_stride, int64_t head_stride,
+                                 int32_t tokens, const int32_t* seq, const int32_t* start,
+                                 int32_t n, gs_stream stream) {
+    CacheView c;
+    const gs_status st = check_call(cache, n, &c);
+    if (st != GS_OK) return st;
+    if (layer < 0 || layer >= c.layers || tokens < 0) return GS_ERR_INVALID_ARG;
+    if (n == 0 || tokens == 0) return GS_OK;
+    const long long es = elem_size(cache->dtype);
+    if (k == nullptr || v == nullptr || seq == nullptr || start == nullptr ||
+        !aligned(k, es) || !aligned(v, es) || token_stride < 0 || head_stride < 0)
+        return GS_ERR_INVALID_ARG;
+    const int vec = aligned(k, 16) && aligned(v, 16) && (token_stride * es) % 16 == 0 &&
+                    (head_stride * es) % 16 == 0;
+    const long long blocks = (2ll * tokens * 32 + kCopy - 1) / kCopy;
+    const dim3 grid(static_cast<unsigned>(blocks));
+    switch (cache->dtype) {
+        case GS_DTYPE_F32:
+            return launch(write_kernel<float>, grid, kCopy, 0, 1, stream, c, layer,
+                          static_cast<const float*>(k), static_cast<const float*>(v), token_stride,
+                          head_stride, vec, tokens, seq, start, n);
+        case GS_DTYPE_BF16:
+            return launch(write_kernel<__nv_bfloat16>, grid, kCopy, 0, 1, stream, c, layer,
+                          static_cast<const __nv_bfloat16*>(k),
+                          static_cast<const __nv_bfloat16*>(v), token_stride, head_stride, vec,
+                          tokens, seq, start, n);
+        default:
+            return launch(write_kernel<__half>, grid, kCopy, 0, 1, stream, c, layer,
+                          static_cast<const __half*>(k), static_cast<const __half*>(v),
+                          token_stride, head_stride, vec, tokens, seq, start, n);
+    }
+}
