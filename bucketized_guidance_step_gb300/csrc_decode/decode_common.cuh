@@ -114,9 +114,13 @@ inline bool allow_smem(int bytes) {
     if (cudaGetDevice(&dev) != cudaSuccess) return false;
     const unsigned long long bit = 1ull << (dev & 63);
     if ((done.load(std::memory_order_relaxed) & bit) != 0) return true;
-    if (cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) !=
-        cudaSuccess)
+    cudaFuncAttributes a;
+    if (cudaFuncGetAttributes(&a, K) != cudaSuccess ||
+        cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             227 * 1024 - static_cast<int>(a.sharedSizeBytes)) != cudaSuccess) {
+        (void)cudaGetLastError();
         return false;
+    }
     done.fetch_or(bit, std::memory_order_relaxed);
     return true;
 }

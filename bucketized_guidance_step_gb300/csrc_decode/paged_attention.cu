@@ -1,11 +1,10 @@
-// Attention of one new token over a paged cache: the argument checks, and the kernel that
-// computes with fp32 multiply-adds (sm_103a).
+// Attention of one new token over a paged cache (sm_103a): the argument checks, and the policy
+// that computes with fp32 multiply-adds, for fp32 caches.
 //
-// For each query head and visible position: s = q . k (fp32), the running maximum and sum of a
-// softmax in powers of two, and o += 2^(s - m) v.  K and V are read once for `part` query heads
-// that share them.  Eight lanes hold a row of K (16 bytes a lane and vector, so a warp reads
-// four rows at a time, coalesced); each group of eight lanes keeps a maximum, sum and output of
-// its own, and they meet once a segment, by shuffles and then through shared memory.
+// For each query head and position: s = q . k, the running maximum and sum of a softmax in
+// powers of two, and o += 2^(s - m) v, all in fp32.  Eight lanes hold a row (a 16-byte piece
+// every eighth), so a warp works on four positions at a time; each group of eight lanes keeps
+// a maximum, sum and output of its own, and they meet at the segment's end.
 #include <cmath>
 
 #include "paged_attention.cuh"
@@ -13,235 +12,142 @@
 namespace gs_decode {
 namespace {
 
-// Values of a row that a lane holds, for rows of up to 8 * E values; query heads of a part: the
-// output takes PART * E = 64 registers.
-template <class T, int NV>
-struct Shape {
-    static constexpr int V = 16 / sizeof(T);
-    static constexpr int E = NV * V;
-    static constexpr int PART = 64 / E;
-    static constexpr int DIM = 8 * E;
-};
+// NV: 16-byte pieces of a row that a lane holds.  The query heads and the output of a part take
+// 64 registers each.
+template <int NV>
+struct Fp32 {
+    using T = float;
+    static constexpr int DP = 32 * NV, RUN = 8, STAGES = NV <= 2 ? 6 : 3, HEADS = 16 / NV;
+    static constexpr int E = 4 * NV, U = RUN / 4;
+    static_assert(HEADS <= kRound, "one dump");
+    float q[HEADS][E], o[HEADS][E], top[HEADS], sum[HEADS];
 
-template <class T, int NV>
-__global__ void __launch_bounds__(kThreads)
-attention_kernel(const __grid_constant__ AttnParams p) {
-    using S = Shape<T, NV>;
-    constexpr int V = S::V, E = S::E, PART = S::PART, DIM = S::DIM, U = 2;
-    extern __shared__ int at[];                          // [batch + 1]
-    __shared__ int tmp[kWarps + 1];
-    __shared__ int turn;
-    __shared__ __align__(16) float sq[PART * DIM];       // the query heads, scaled
-    __shared__ float sm[kWarps][PART], ss[kWarps][PART];
-    __shared__ float so[kWarps][PART * DIM];
-    __shared__ float rm[PART], rs[PART];
-    grid_wait();
-    grid_trigger();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int sub = lane & 7, group = lane >> 3;
-    const int dim = p.c.dim;
-    number_tiles(p, at, tmp);
-    put_empty_rows<T>(p, at);
-    Walk walk;
-    walk.begin(p, at);
-    while (walk.t < walk.t1) {
-        const Segment seg = walk.next(p, at);
-        const int first_head = seg.head * p.group + seg.part * PART;
-        const int heads = min(PART, p.group - seg.part * PART);
-        for (int x = threadIdx.x; x < PART * DIM; x += kThreads) {
-            const int g = x / DIM, d = x - g * DIM;
-            float f = 0.0f;
-            if (g < heads && d < dim)
-                f = to_float(static_cast<const T*>(p.q)[seg.b * p.q_batch +
-                                                        (first_head + g) * p.q_head + d]);
-            sq[x] = f * p.scale_log2;
-        }
-        __syncthreads();
-        const int* table = p.c.table + static_cast<long long>(seg.row.seq) * p.c.cols;
-        const long long head_at = p.layer * p.c.layer_stride + seg.head * p.c.head_stride;
-        T* const kc = reinterpret_cast<T*>(p.c.k) + head_at;
-        T* const vc = reinterpret_cast<T*>(p.c.v) + head_at;
-        const T* const kn = static_cast<const T*>(p.k_new) + (p.k_new != nullptr ? seg.b * p.new_batch + seg.head * p.new_head : 0);
-        const T* const vn = static_cast<const T*>(p.v_new) + (p.k_new != nullptr ? seg.b * p.new_batch + seg.head * p.new_head : 0);
-        float m[PART], sum[PART], o[PART][E];
+    __device__ __forceinline__ void begin(const float* query, long long head_stride, int heads,
+                                          int dim) {
+        const int sub = threadIdx.x & 7;
 #pragma unroll
-        for (int g = 0; g < PART; ++g) {
-            m[g] = kNegInf;
-            sum[g] = 0.0f;
-#pragma unroll
-            for (int e = 0; e < E; ++e) o[g][e] = 0.0f;
-        }
-        for (int j0 = seg.first + warp * 4 * U; j0 < seg.last; j0 += kWarps * 4 * U) {
-            uint4 k[U][NV], v[U][NV];
-            bool seen[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int j = j0 + u * 4 + group;
-                seen[u] = j < seg.last;
-                const int pos = position(seg.row, seen[u] ? j : seg.first);
-                const int col = pos / p.c.page;
-                const int pg = table[col];
-                const bool ok = pg >= 0 && pg < p.c.pages;
-                const long long off = (ok ? pg : 0) * p.c.page_stride +
-                                      (pos - col * p.c.page) * p.c.token_stride;
-                const bool fresh = seen[u] && p.k_new != nullptr && pos == seg.row.len - 1;
-                if (!ok && sub == 0) flag(p.c.status, GS_DEV_BAD_SEQ);
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int d = (sub + 8 * i) * V;
-                    k[u][i] = v[u][i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (d >= dim || !seen[u]) continue;
-                    if (fresh) {
-                        k[u][i] = load16_any(kn + d, p.new_aligned != 0);
-                        v[u][i] = load16_any(vn + d, p.new_aligned != 0);
-                        if (ok && seg.part == 0) {
-                            *reinterpret_cast<uint4*>(kc + off + d) = k[u][i];
-                            *reinterpret_cast<uint4*>(vc + off + d) = v[u][i];
-                        }
-                    } else if (ok) {
-                        k[u][i] = *reinterpret_cast<const uint4*>(kc + off + d);
-                        v[u][i] = *reinterpret_cast<const uint4*>(vc + off + d);
-                    }
-                }
-            }
-            float s[U][PART];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int g = 0; g < PART; ++g) s[u][g] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                float kf[U][V];
-#pragma unroll
-                for (int u = 0; u < U; ++u) unpack16<T>(k[u][i], kf[u]);
-#pragma unroll
-                for (int g = 0; g < PART; ++g) {
-                    const float* qp = sq + g * DIM + (sub + 8 * i) * V;
-#pragma unroll
-                    for (int e = 0; e < V; e += 4) {
-                        const float4 f = *reinterpret_cast<const float4*>(qp + e);
-#pragma unroll
-                        for (int u = 0; u < U; ++u) {
-                            s[u][g] = fmaf(f.x, kf[u][e], s[u][g]);
-                            s[u][g] = fmaf(f.y, kf[u][e + 1], s[u][g]);
-                            s[u][g] = fmaf(f.z, kf[u][e + 2], s[u][g]);
-                            s[u][g] = fmaf(f.w, kf[u][e + 3], s[u][g]);
-                        }
-                    }
-                }
-            }
-#pragma unroll
-            for (int g = 0; g < PART; ++g) {
-                float top = m[g];
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-#pragma unroll
-                    for (int d = 1; d < 8; d <<= 1) s[u][g] += __shfl_xor_sync(0xffffffffu, s[u][g], d);
-                    if (!seen[u]) s[u][g] = kNegInf;
-                    top = fmaxf(top, s[u][g]);
-                }
-                if (top > m[g]) {
-                    const float w = exp2f(m[g] - top);           // 0 at the first position
-                    sum[g] *= w;
-#pragma unroll
-                    for (int e = 0; e < E; ++e) o[g][e] *= w;
-                    m[g] = top;
-                }
-                const float base = top == kNegInf ? 0.0f : top;
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    s[u][g] = exp2f(s[u][g] - base);
-                    sum[g] += s[u][g];
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    float vf[V];
-                    unpack16<T>(v[u][i], vf);
-#pragma unroll
-                    for (int g = 0; g < PART; ++g)
-#pragma unroll
-                        for (int e = 0; e < V; ++e)
-                            o[g][i * V + e] = fmaf(s[u][g], vf[e], o[g][i * V + e]);
-                }
-        }
-        // The four groups of the warp, then the warps.
-#pragma unroll
-        for (int g = 0; g < PART; ++g) {
-            float top = m[g];
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            const float w = exp2f(m[g] - (top == kNegInf ? 0.0f : top));
-            sum[g] *= w;
-            sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 8);
-            sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 16);
+        for (int h = 0; h < HEADS; ++h) {
+            top[h] = kNegInf;
+            sum[h] = 0.0f;
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                float x = o[g][e] * w;
-                x += __shfl_xor_sync(0xffffffffu, x, 8);
-                x += __shfl_xor_sync(0xffffffffu, x, 16);
-                if (group == 0) so[warp][g * DIM + (sub + 8 * (e / V)) * V + e % V] = x;
-            }
-            if (lane == 0) {
-                sm[warp][g] = top;
-                ss[warp][g] = sum[g];
+                const int d = (sub + 8 * (e / 4)) * 4 + e % 4;
+                q[h][e] = h < heads && d < dim ? query[h * head_stride + d] : 0.0f;
+                o[h][e] = 0.0f;
             }
         }
-        __syncthreads();
-        for (int x = threadIdx.x; x < PART * dim; x += kThreads) {
-            const int g = x / dim, d = x - g * dim;
-            float top = kNegInf;
+    }
+
+    __device__ __forceinline__ void step(const char* stage, int j, int end, float scale) {
+        const int sub = threadIdx.x & 7, group = (threadIdx.x >> 3) & 3;
+        float s[U][HEADS];
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w][g]);
-            const float base = top == kNegInf ? 0.0f : top;
-            float acc = 0.0f, all = 0.0f;
+        for (int u = 0; u < U; ++u) {
+            const int r = u * 4 + group;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = exp2f(sm[w][g] - base);
-                acc = fmaf(so[w][g * DIM + d], f, acc);
-                all = fmaf(ss[w][g], f, all);
-            }
-            sq[x] = acc;                                  // the queries are not needed any more
-            if (d == 0) {
-                rm[g] = top;
-                rs[g] = all;
+            for (int h = 0; h < HEADS; ++h) s[u][h] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const float4 k = *reinterpret_cast<const float4*>(
+                    stage + r * DP * 4 + (((sub + 8 * i) ^ (r & 7)) << 4));
+#pragma unroll
+                for (int h = 0; h < HEADS; ++h) {
+                    s[u][h] = fmaf(q[h][4 * i], k.x, s[u][h]);
+                    s[u][h] = fmaf(q[h][4 * i + 1], k.y, s[u][h]);
+                    s[u][h] = fmaf(q[h][4 * i + 2], k.z, s[u][h]);
+                    s[u][h] = fmaf(q[h][4 * i + 3], k.w, s[u][h]);
+                }
             }
         }
-        __syncthreads();
-        finish<T>(p, seg, rm, rs, sq, &turn);
+#pragma unroll
+        for (int h = 0; h < HEADS; ++h) {
+            float up = top[h];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+#pragma unroll
+                for (int d = 1; d < 8; d <<= 1) s[u][h] += __shfl_xor_sync(0xffffffffu, s[u][h], d);
+                s[u][h] = j + u * 4 + group < end ? s[u][h] * scale : kNegInf;
+                up = fmaxf(up, s[u][h]);
+            }
+            if (up > top[h]) {
+                const float w = exp2f(top[h] - up);      // 0 at the first position
+                sum[h] *= w;
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[h][e] *= w;
+                top[h] = up;
+            }
+            const float base = up == kNegInf ? 0.0f : up;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                s[u][h] = exp2f(s[u][h] - base);
+                sum[h] += s[u][h];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = u * 4 + group;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const float4 v = *reinterpret_cast<const float4*>(
+                    stage + (RUN + r) * DP * 4 + (((sub + 8 * i) ^ (r & 7)) << 4));
+#pragma unroll
+                for (int h = 0; h < HEADS; ++h) {
+                    o[h][4 * i] = fmaf(s[u][h], v.x, o[h][4 * i]);
+                    o[h][4 * i + 1] = fmaf(s[u][h], v.y, o[h][4 * i + 1]);
+                    o[h][4 * i + 2] = fmaf(s[u][h], v.z, o[h][4 * i + 2]);
+                    o[h][4 * i + 3] = fmaf(s[u][h], v.w, o[h][4 * i + 3]);
+                }
+            }
+        }
     }
-}
 
-template <class T, int NV>
-gs_status launch_one(const AttnParams& p, int blocks, gs_stream stream) {
-    const int smem = 4 * (p.batch + 1);
-    if (!allow_smem<attention_kernel<T, NV>>(smem + 24 * 1024)) return GS_ERR_CUDA;
-    return launch(attention_kernel<T, NV>, dim3(static_cast<unsigned>(blocks)), kThreads, smem, 1,
-                  stream, p);
-}
-
-// 16-byte vectors a lane holds of a row: 1, 2, 4 or 8.
-int vectors_of(int dtype, int dim) {
-    const int v = static_cast<int>((dim * elem_size(dtype) / 16 + 7) / 8);
-    return v <= 1 ? 1 : v <= 2 ? 2 : v <= 4 ? 4 : 8;
-}
-int part_of(int dtype, int dim) {
-    return 64 / static_cast<int>(vectors_of(dtype, dim) * 16 / elem_size(dtype));
-}
-
-template <class T>
-gs_status launch_simple(int dtype, const AttnParams& p, int blocks, gs_stream stream) {
-    switch (vectors_of(dtype, p.c.dim)) {
-        case 1: return launch_one<T, 1>(p, blocks, stream);
-        case 2: return launch_one<T, 2>(p, blocks, stream);
-        case 4: return launch_one<T, 4>(p, blocks, stream);
-        default:
-            if constexpr (sizeof(T) == 4) return launch_one<T, 8>(p, blocks, stream);
-            return GS_ERR_UNSUPPORTED;
+    __device__ __forceinline__ void dump(float* m, float* s, float* out, int, int heads, int dim) {
+        const int lane = threadIdx.x & 31, sub = lane & 7, group = lane >> 3;
+#pragma unroll
+        for (int h = 0; h < HEADS; ++h) {
+            float up = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 8));
+            up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 16));
+            const float w = exp2f(top[h] - (up == kNegInf ? 0.0f : up));
+            float all = sum[h] * w;
+            all += __shfl_xor_sync(0xffffffffu, all, 8);
+            all += __shfl_xor_sync(0xffffffffu, all, 16);
+            if (lane == 0 && h < heads) {
+                m[h] = up;
+                s[h] = all;
+            }
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[e] = o[h][4 * i + e] * w;
+                    x[e] += __shfl_xor_sync(0xffffffffu, x[e], 8);
+                    x[e] += __shfl_xor_sync(0xffffffffu, x[e], 16);
+                }
+                const int d = (sub + 8 * i) * 4;
+                if (group == 0 && h < heads && d < dim)
+                    *reinterpret_cast<float4*>(out + h * dim + d) = make_float4(x[0], x[1], x[2], x[3]);
+            }
+        }
     }
+};
+
+}  // namespace
+
+// Rings of 96 KB a block (192 KB for rows over 512 bytes).
+Serves fp32_serves(int dim) {
+    if (dim <= 64) return {Layout<Fp32<2>>::kTile, Fp32<2>::HEADS, 2};
+    if (dim <= 128) return {Layout<Fp32<4>>::kTile, Fp32<4>::HEADS, 2};
+    return {Layout<Fp32<8>>::kTile, Fp32<8>::HEADS, 1};
 }
+
+gs_status launch_fp32(const AttnParams& p, int blocks, gs_stream stream) {
+    if (p.c.dim <= 64) return launch_policy<Fp32<2>>(p, blocks, stream);
+    if (p.c.dim <= 128) return launch_policy<Fp32<4>>(p, blocks, stream);
+    return launch_policy<Fp32<8>>(p, blocks, stream);
+}
+
+namespace {
 
 struct Plan {
     int part, parts, blocks;
@@ -259,21 +165,20 @@ gs_status plan_of(const gs_paged_attention_args* a, Plan* plan) {
         return GS_ERR_INVALID_ARG;
     if (a->batch > GS_MAX_SEQS || a->q_heads > (1 << 16)) return GS_ERR_UNSUPPORTED;
     const int group = a->q_heads / c->kv_heads;
-    plan->part = part_of(c->dtype, c->dim);
-    if (plan->part > group) plan->part = group;
-    plan->parts = (group + plan->part - 1) / plan->part;
+    const Serves by = c->dtype == GS_DTYPE_F32 ? fp32_serves(c->dim) : mma_serves(c->dim);
+    plan->parts = (group + by.heads - 1) / by.heads;
+    plan->part = (group + plan->parts - 1) / plan->parts;
     long long most = static_cast<long long>(c->cols) * c->page;
     const long long visible = static_cast<long long>(a->window) + a->sinks;
     if (a->window > 0 && visible < most) most = visible;
-    const long long tiles = a->batch * ((most + kTile - 1) / kTile);
     const long long items = static_cast<long long>(a->batch) * c->kv_heads * plan->parts;
+    const long long tiles = items * ((most + by.tile - 1) / by.tile);
     if (tiles > 0x7fffffffll || items > 0x3fffffffll) return GS_ERR_UNSUPPORTED;
-    // Two blocks an SM (registers), no more blocks than tiles.
-    const long long full = 2ll * sm_count();
-    const long long all = tiles * c->kv_heads * plan->parts;
-    plan->blocks = static_cast<int>(all < full ? (all > 0 ? all : 1) : full);
+    // What is resident at once, no more blocks than tiles.
+    const long long full = static_cast<long long>(by.per_sm) * sm_count();
+    plan->blocks = static_cast<int>(tiles < full ? (tiles > 0 ? tiles : 1) : full);
     plan->counters = (items + 3) / 4 * 4;
-    plan->slots = 2ll * plan->blocks * plan->part * (c->dim + 2);
+    plan->slots = 2ll * plan->blocks * slot_size(plan->part, c->dim);
     return GS_OK;
 }
 
@@ -334,6 +239,8 @@ extern "C" gs_status gs_paged_attention(const gs_paged_attention_args* args, gs_
     p.new_head = args->new_head_stride;
     p.new_aligned = aligned(args->k_new, 16) && aligned(args->v_new, 16) &&
                     (args->new_batch_stride * es) % 16 == 0 && (args->new_head_stride * es) % 16 == 0;
+    p.out_aligned = aligned(args->out, 4 * es) && args->out_batch_stride % 4 == 0 &&
+                    args->out_head_stride % 4 == 0;
     p.scale_log2 = args->scale * kLog2e;
     p.window = args->window;
     p.sinks = args->sinks;
@@ -343,10 +250,6 @@ extern "C" gs_status gs_paged_attention(const gs_paged_attention_args* args, gs_
     p.lse = args->lse;
     p.arrived = static_cast<int*>(args->workspace);
     p.slots = static_cast<float*>(args->workspace) + plan.counters;
-    switch (args->cache->dtype) {
-        case GS_DTYPE_F32: return launch_simple<float>(args->cache->dtype, p, plan.blocks, stream);
-        case GS_DTYPE_BF16:
-            return launch_simple<__nv_bfloat16>(args->cache->dtype, p, plan.blocks, stream);
-        default: return launch_simple<__half>(args->cache->dtype, p, plan.blocks, stream);
-    }
+    if (args->cache->dtype == GS_DTYPE_F32) return launch_fp32(p, plan.blocks, stream);
+    return launch_mma(args->cache->dtype, p, plan.blocks, stream);
 }

@@ -1,0 +1,234 @@
+// Attention of one new token over a paged cache: the tensor-core policy, for 16-bit caches
+// (sm_103a).
+//
+// The query heads that share a kv head are the columns of two matrix products with that
+// head's K and V: S^T = K Q^T (positions x heads) and O^T = V^T P^T (dim x heads).  Positions
+// and dim take the rows of the instruction (m16n8k16) and heads its 8 columns, so groups of
+// 1 to 8 heads cost one instruction and 9 to 16 two; K and V pass once for all of them.
+// The warp-wide mma.sync is used rather than tcgen05: a tile has 8 or 16 columns, each byte of
+// K and V is used for a few operations only, and the time goes to reading them from HBM.
+//
+// The weights 2^(s - m) enter the second product as two 16-bit numbers, hi + lo: with hi alone
+// the rounding of the weights would add as much error as the rounding of the output.  The sum
+// of the weights is taken before they are rounded.  For fp16 the weights are scaled by 2^12
+// (the reference of the softmax is m - 12), so that small ones stay clear of fp16's subnormals.
+#include "paged_attention.cuh"
+
+namespace gs_decode {
+namespace {
+
+__device__ __forceinline__ void load_matrix(unsigned a, unsigned (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void load_matrix_t(unsigned a, unsigned (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ unsigned transpose8(unsigned x) {
+    unsigned y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+template <class T>
+__device__ __forceinline__ void mma(float (&c)[4], const unsigned (&a)[4], unsigned b0, unsigned b1) {
+    if constexpr (std::is_same<T, __half>::value)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+            "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+            "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two values rounded and packed (x low), and what the rounding left, rounded and packed.
+template <class T>
+__device__ __forceinline__ void split2(float x, float y, unsigned* hi, unsigned* lo) {
+    const T hx = from_float<T>(x), hy = from_float<T>(y);
+    const T lx = from_float<T>(x - to_float(hx)), ly = from_float<T>(y - to_float(hy));
+    T h[2] = {hx, hy}, l[2] = {lx, ly};
+    *hi = *reinterpret_cast<unsigned*>(h);
+    *lo = *reinterpret_cast<unsigned*>(l);
+}
+__device__ __forceinline__ float max_rows(float x) {     // over the lanes of one column
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+}
+__device__ __forceinline__ float sum_rows(float x) {
+    x += __shfl_xor_sync(0xffffffffu, x, 4);
+    x += __shfl_xor_sync(0xffffffffu, x, 8);
+    return x + __shfl_xor_sync(0xffffffffu, x, 16);
+}
+
+// NH: columns of 8 query heads.  Of a warp's 32 lanes, lane = 4 g + t.
+template <class Type, int DIM, int NH>
+struct Mma {
+    using T = Type;
+    static constexpr int DP = DIM, RUN = 16, STAGES = DIM == 64 ? 6 : 3, HEADS = 8 * NH;
+    static_assert(kRound == 8, "a dump is one column of heads");
+    static constexpr int KS = DP / 16;                   // steps over dim
+    static constexpr float kShift = std::is_same<T, __half>::value ? 12.0f : 0.0f;
+    unsigned q[NH][KS][2];                               // head g (+ 8), dims 2t, 2t+1; 2t+8, 2t+9
+    float o[NH][KS][4];                                  // dims g (0, 1), g+8 (2, 3), heads 2t, 2t+1
+    float top[NH][2], sum[NH][2];                        // heads 2t, 2t+1
+
+    __device__ __forceinline__ void begin(const T* query, long long head_stride, int heads, int dim) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+            const T* qp = query + (h * 8 + g) * head_stride;
+            top[h][0] = top[h][1] = kNegInf;
+            sum[h][0] = sum[h][1] = 0.0f;
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int d = s * 16 + half * 8 + 2 * t;
+                    T two[2] = {from_float<T>(0.0f), from_float<T>(0.0f)};
+                    if (h * 8 + g < heads && d < dim) {
+                        two[0] = qp[d];
+                        two[1] = qp[d + 1];
+                    }
+                    q[h][s][half] = *reinterpret_cast<unsigned*>(two);
+                }
+                o[h][s][0] = o[h][s][1] = o[h][s][2] = o[h][s][3] = 0.0f;
+            }
+        }
+    }
+
+    __device__ __forceinline__ void step(const char* stage, int j, int end, float scale) {
+        const int lane = threadIdx.x & 31, g = lane >> 2;
+        float s[NH][4];                                  // positions g (0, 1), g+8 (2, 3)
+#pragma unroll
+        for (int h = 0; h < NH; ++h) s[h][0] = s[h][1] = s[h][2] = s[h][3] = 0.0f;
+        {
+            const int r = lane & 15;
+            const unsigned row = smem_addr(stage) + r * DP * 2;
+#pragma unroll
+            for (int x = 0; x < KS; ++x) {
+                unsigned a[4];
+                load_matrix(row + (((2 * x + (lane >> 4)) ^ (r & 7)) << 4), a);
+#pragma unroll
+                for (int h = 0; h < NH; ++h) mma<T>(s[h], a, q[h][x][0], q[h][x][1]);
+            }
+        }
+        bool grew = false;
+        float up[NH][2];
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[h][e] *= scale;
+                if (j + g + (e >> 1) * 8 >= end) s[h][e] = kNegInf;
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                up[h][e] = fmaxf(top[h][e], max_rows(fmaxf(s[h][e], s[h][e + 2])));
+                grew = grew || up[h][e] > top[h][e];
+            }
+        }
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+            for (int h = 0; h < NH; ++h)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float w = up[h][e] > top[h][e] ? exp2f(top[h][e] - up[h][e]) : 1.0f;
+                    sum[h][e] *= w;
+#pragma unroll
+                    for (int x = 0; x < KS; ++x) {
+                        o[h][x][e] *= w;
+                        o[h][x][e + 2] *= w;
+                    }
+                    top[h][e] = up[h][e];
+                }
+        }
+        unsigned hi[NH][2], lo[NH][2];
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float base = top[h][e] == kNegInf ? 0.0f : top[h][e] - kShift;
+                s[h][e] = exp2f(s[h][e] - base);
+                s[h][e + 2] = exp2f(s[h][e + 2] - base);
+                sum[h][e] += s[h][e] + s[h][e + 2];
+            }
+            split2<T>(s[h][0], s[h][1], &hi[h][0], &lo[h][0]);
+            split2<T>(s[h][2], s[h][3], &hi[h][1], &lo[h][1]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                hi[h][e] = transpose8(hi[h][e]);
+                lo[h][e] = transpose8(lo[h][e]);
+            }
+        }
+        {
+            const int r = (lane & 7) + ((lane >> 4) << 3);
+            const unsigned row = smem_addr(stage) + (RUN + r) * DP * 2;
+#pragma unroll
+            for (int x = 0; x < KS; ++x) {
+                unsigned a[4];
+                load_matrix_t(row + (((2 * x + ((lane >> 3) & 1)) ^ (r & 7)) << 4), a);
+#pragma unroll
+                for (int h = 0; h < NH; ++h) {
+                    mma<T>(o[h][x], a, hi[h][0], hi[h][1]);
+                    mma<T>(o[h][x], a, lo[h][0], lo[h][1]);
+                }
+            }
+        }
+    }
+
+    __device__ __forceinline__ void dump(float* m, float* s, float* out, int first, int heads,
+                                         int dim) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+            if (h * 8 != first) continue;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int head = 2 * t + e;              // of this dump
+                const float all = sum_rows(sum[h][e]);
+                if (first + head >= heads) continue;
+                if (g == 0) {
+                    m[head] = top[h][e] - kShift;
+                    s[head] = all;
+                }
+#pragma unroll
+                for (int x = 0; x < KS; ++x)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int d = x * 16 + half * 8 + g;
+                        if (d < dim) out[head * dim + d] = o[h][x][e + 2 * half];
+                    }
+            }
+        }
+    }
+};
+
+template <class T>
+gs_status launch_type(const AttnParams& p, int blocks, gs_stream stream) {
+    if (p.c.dim <= 64)
+        return p.part <= 8 ? launch_policy<Mma<T, 64, 1>>(p, blocks, stream)
+                           : launch_policy<Mma<T, 64, 2>>(p, blocks, stream);
+    if (p.c.dim <= 128)
+        return p.part <= 8 ? launch_policy<Mma<T, 128, 1>>(p, blocks, stream)
+                           : launch_policy<Mma<T, 128, 2>>(p, blocks, stream);
+    return launch_policy<Mma<T, 256, 1>>(p, blocks, stream);
+}
+
+}  // namespace
+
+// 16 query heads in one pass; 8 for rows over 256 bytes, whose output would not fit the
+// registers.  Rings of 96 KB a block (192 KB for rows over 256 bytes).
+Serves mma_serves(int dim) {
+    constexpr int tile = Layout<Mma<__half, 64, 1>>::kTile;
+    return dim <= 128 ? Serves{tile, 16, 2} : Serves{tile, 8, 1};
+}
+
+gs_status launch_mma(int dtype, const AttnParams& p, int blocks, gs_stream stream) {
+    return dtype == GS_DTYPE_BF16 ? launch_type<__nv_bfloat16>(p, blocks, stream)
+                                  : launch_type<__half>(p, blocks, stream);
+}
+
+}  // namespace gs_decode
