@@ -23,7 +23,7 @@ struct Fp32 {
     float q[HEADS][E], o[HEADS][E], top[HEADS], sum[HEADS];
 
     __device__ __forceinline__ void begin(const float* query, long long head_stride, int heads,
-                                          int dim) {
+                                          int dim, bool) {
         const int sub = threadIdx.x & 7;
 #pragma unroll
         for (int h = 0; h < HEADS; ++h) {
@@ -38,7 +38,7 @@ struct Fp32 {
         }
     }
 
-    __device__ __forceinline__ void step(const char* stage, int j, int end, float scale) {
+    __device__ __forceinline__ void step(const char* stage, int lo, int hi, float scale) {
         const int sub = threadIdx.x & 7, group = (threadIdx.x >> 3) & 3;
         float s[U][HEADS];
 #pragma unroll
@@ -66,11 +66,11 @@ struct Fp32 {
             for (int u = 0; u < U; ++u) {
 #pragma unroll
                 for (int d = 1; d < 8; d <<= 1) s[u][h] += __shfl_xor_sync(0xffffffffu, s[u][h], d);
-                s[u][h] = j + u * 4 + group < end ? s[u][h] * scale : kNegInf;
+                s[u][h] = u * 4 + group >= lo && u * 4 + group < hi ? s[u][h] * scale : kNegInf;
                 up = fmaxf(up, s[u][h]);
             }
             if (up > top[h]) {
-                const float w = exp2f(top[h] - up);      // 0 at the first position
+                const float w = pow2(top[h] - up);      // 0 at the first position
                 sum[h] *= w;
 #pragma unroll
                 for (int e = 0; e < E; ++e) o[h][e] *= w;
@@ -79,7 +79,7 @@ struct Fp32 {
             const float base = up == kNegInf ? 0.0f : up;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                s[u][h] = exp2f(s[u][h] - base);
+                s[u][h] = pow2(s[u][h] - base);
                 sum[h] += s[u][h];
             }
         }
@@ -101,13 +101,14 @@ struct Fp32 {
         }
     }
 
-    __device__ __forceinline__ void dump(float* m, float* s, float* out, int, int heads, int dim) {
+    __device__ __forceinline__ void dump(float* m, float* s, float* out, int pitch, int, int heads,
+                                         int dim) {
         const int lane = threadIdx.x & 31, sub = lane & 7, group = lane >> 3;
 #pragma unroll
         for (int h = 0; h < HEADS; ++h) {
             float up = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 8));
             up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 16));
-            const float w = exp2f(top[h] - (up == kNegInf ? 0.0f : up));
+            const float w = pow2(top[h] - (up == kNegInf ? 0.0f : up));
             float all = sum[h] * w;
             all += __shfl_xor_sync(0xffffffffu, all, 8);
             all += __shfl_xor_sync(0xffffffffu, all, 16);
@@ -126,7 +127,7 @@ struct Fp32 {
                 }
                 const int d = (sub + 8 * i) * 4;
                 if (group == 0 && h < heads && d < dim)
-                    *reinterpret_cast<float4*>(out + h * dim + d) = make_float4(x[0], x[1], x[2], x[3]);
+                    *reinterpret_cast<float4*>(out + h * pitch + d) = make_float4(x[0], x[1], x[2], x[3]);
             }
         }
     }
@@ -150,7 +151,7 @@ gs_status launch_fp32(const AttnParams& p, int blocks, gs_stream stream) {
 namespace {
 
 struct Plan {
-    int part, parts, blocks;
+    int part, parts, blocks, run;
     long long counters, slots;            // words of the workspace
 };
 
@@ -166,13 +167,14 @@ gs_status plan_of(const gs_paged_attention_args* a, Plan* plan) {
     if (a->batch > GS_MAX_SEQS || a->q_heads > (1 << 16)) return GS_ERR_UNSUPPORTED;
     const int group = a->q_heads / c->kv_heads;
     const Serves by = c->dtype == GS_DTYPE_F32 ? fp32_serves(c->dim) : mma_serves(c->dim);
+    plan->run = by.tile / kWarps;
     plan->parts = (group + by.heads - 1) / by.heads;
     plan->part = (group + plan->parts - 1) / plan->parts;
     long long most = static_cast<long long>(c->cols) * c->page;
-    const long long visible = static_cast<long long>(a->window) + a->sinks;
+    const long long visible = static_cast<long long>(a->window) + a->sinks + 2 * by.tile;   // whole runs
     if (a->window > 0 && visible < most) most = visible;
     const long long items = static_cast<long long>(a->batch) * c->kv_heads * plan->parts;
-    const long long tiles = items * ((most + by.tile - 1) / by.tile);
+    const long long tiles = items * ((most + by.tile - 1) / by.tile + 1);         // units
     if (tiles > 0x7fffffffll || items > 0x3fffffffll) return GS_ERR_UNSUPPORTED;
     // What is resident at once, no more blocks than tiles.
     const long long full = static_cast<long long>(by.per_sm) * sm_count();
@@ -241,6 +243,14 @@ extern "C" gs_status gs_paged_attention(const gs_paged_attention_args* args, gs_
                     (args->new_batch_stride * es) % 16 == 0 && (args->new_head_stride * es) % 16 == 0;
     p.out_aligned = aligned(args->out, 4 * es) && args->out_batch_stride % 4 == 0 &&
                     args->out_head_stride % 4 == 0;
+    p.q_aligned = aligned(args->q, 2 * es) && args->q_batch_stride % 2 == 0 && args->q_head_stride % 2 == 0;
+    // Division by the page size: with s = ceil(log2 page), mul = 2^32 (2^s - page) / page + 1.
+    p.page_shift = 0;
+    while ((1u << p.page_shift) < static_cast<unsigned>(p.c.page)) ++p.page_shift;
+    p.page_mul = static_cast<unsigned>(
+        (((1ull << p.page_shift) - static_cast<unsigned>(p.c.page)) << 32) / static_cast<unsigned>(p.c.page) + 1);
+    p.page_runs = p.c.page % plan.run == 0;
+    p.dim_mul = (1u << 20) / static_cast<unsigned>(p.c.dim) + 1;
     p.scale_log2 = args->scale * kLog2e;
     p.window = args->window;
     p.sinks = args->sinks;

@@ -30,6 +30,7 @@ namespace gs_decode {
 
 constexpr int kWarps = 4;                 // warps of a block
 constexpr int kThreads = 32 * kWarps;
+constexpr int kLeast = 1;                 // units a block takes at least
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -46,6 +47,10 @@ struct AttnParams {
     long long new_batch, new_head;
     int new_aligned;                      // k_new and v_new rows lie on 16 bytes
     int out_aligned;                      // out rows lie on 4 elements
+    int q_aligned;                        // q rows lie on 2 elements
+    unsigned page_mul, page_shift;        // position / page = (mulhi(position, mul) + position) >> shift
+    int page_runs;                        // a page holds whole runs: a run lies in one page
+    unsigned dim_mul;                     // x / dim = x * mul >> 20, for x < 8 dim
     float scale_log2;                     // scale * log2 e: scores are kept in powers of two
     int window, sinks;
     void* out;
@@ -61,11 +66,16 @@ __host__ __device__ inline long long slot_size(int part, int dim) {
     return slot_head(part) + static_cast<long long>(part) * dim;
 }
 
-// A row's visible positions: j < sinks is position j, else position j + gap.
+// A row's visible positions, numbered in runs that begin at multiples of RUN in the sequence
+// too: the sinks are 0 .. sinks - 1, the window begins at number `turn` (a multiple of RUN)
+// with position `from` (the multiple of RUN at or below its first).  Numbers in between, and
+// positions from .. first - 1, are not visible.  Without a window all but n and len are 0.
 struct Row {
-    int seq, n, sinks, gap, len;          // len: tokens of the sequence (0: nothing to read)
+    int seq, n, len;                      // n: numbers in all (0: nothing to read); len: tokens
+    int sinks, turn, from, first;
 };
 
+template <int RUN>
 __device__ __forceinline__ Row row_of(const AttnParams& p, int b, unsigned* bad) {
     Row r;
     r.seq = p.seq != nullptr ? p.seq[b] : b;
@@ -82,107 +92,119 @@ __device__ __forceinline__ Row row_of(const AttnParams& p, int b, unsigned* bad)
         }
     }
     r.n = r.len;
-    r.sinks = 0;
-    r.gap = 0;
-    if (p.window > 0 && r.len > p.window) {
-        const int first = r.len - p.window;
-        r.sinks = p.sinks < first ? p.sinks : first;
-        r.gap = first - r.sinks;
-        r.n = r.sinks + p.window;
+    r.sinks = r.turn = r.from = r.first = 0;
+    if (p.window > 0 && r.len - p.window > p.sinks) {
+        r.first = r.len - p.window;
+        r.from = r.first / RUN * RUN;
+        r.sinks = p.sinks;
+        r.turn = (p.sinks + RUN - 1) / RUN * RUN;
+        r.n = r.turn + (r.len - r.from);
     }
     return r;
 }
 
-__device__ __forceinline__ int position(const Row& r, int j) {
-    return j < r.sinks ? j : j + r.gap;
-}
-
-// The split of all tiles: the first `more` blocks take each + 1, the others each.
+// The split of all units: the first `more` blocks take each + 1, the others each.
 struct Split {
     int blocks, each, more;
 
     __device__ __forceinline__ int first_of(int block) const {
         return block * each + min(block, more);
     }
-    __device__ __forceinline__ int block_of(int tile) const {
+    __device__ __forceinline__ int block_of(int unit) const {
         const int edge = more * (each + 1);
-        return tile < edge ? tile / (each + 1) : more + (tile - edge) / each;
+        return unit < edge ? unit / (each + 1) : more + (unit - edge) / each;
     }
 };
 
-// A place in the sequence of tiles.
-template <int TILE>
+// A place in the sequence of units: a tile is a unit, and every (row, head group) has one more
+// after its tiles for what beginning and ending a segment costs.
+template <int RUN>
 struct Cursor {
+    static constexpr int TILE = kWarps * RUN;
     Row row;
     int b, tiles;                         // row; tiles of one head group of it
-    int base;                             // number of its first tile
+    int base;                             // number of its first unit
     int hg, tile;                         // head group (head * parts + part); tile of it
 
     __device__ __forceinline__ void take_row(const AttnParams& p, int row_number) {
         unsigned bad = 0;
         b = row_number;
-        row = row_of(p, b, &bad);
+        row = row_of<RUN>(p, b, &bad);
         tiles = (row.n + TILE - 1) / TILE;
     }
+    __device__ __forceinline__ int item() const { return base + hg * (tiles + 1); }
+    __device__ __forceinline__ int unit() const { return item() + tile; }
+    // To the next tile; past the last one, unit() is past every block's end.
     __device__ __forceinline__ void next(const AttnParams& p) {
         if (++tile < tiles) return;
         tile = 0;
         const int hp = p.c.heads * p.parts;
         if (++hg < hp) return;
         hg = 0;
-        base += tiles * hp;
+        base += (tiles + 1) * hp;
         do {
-            if (b + 1 >= p.batch) return; // past the last tile: not used any more
+            if (b + 1 >= p.batch) return;
             take_row(p, b + 1);
         } while (tiles == 0);
     }
 };
 
-// This block's tiles [t, t1) and the cursor at t.  Every warp finds them by itself.
-template <int TILE>
-__device__ __forceinline__ void find_work(const AttnParams& p, Split* split, int* t, int* t1,
-                                          Cursor<TILE>* at) {
+template <int RUN>
+__device__ __forceinline__ int units_of(const AttnParams& p, int b, unsigned* bad) {
+    const int n = row_of<RUN>(p, b, bad).n;
+    return n > 0 ? (n + kWarps * RUN - 1) / (kWarps * RUN) + 1 : 0;
+}
+
+// The end of this block's units and the cursor at its first tile; false where it has none.
+// Every warp finds them by itself.
+template <int RUN>
+__device__ __forceinline__ bool find_work(const AttnParams& p, Split* split, int* end,
+                                          Cursor<RUN>* at) {
     const int lane = threadIdx.x & 31;
     const int hp = p.c.heads * p.parts;
     unsigned bad = 0;
     int all = 0;
-    for (int b = lane; b < p.batch; b += 32) all += (row_of(p, b, &bad).n + TILE - 1) / TILE;
+    for (int b = lane; b < p.batch; b += 32) all += units_of<RUN>(p, b, &bad);
     all = __reduce_add_sync(0xffffffffu, all);
     if (blockIdx.x == 0 && threadIdx.x < 32) flag(p.c.status, bad);
     const int total = all * hp;
-    split->blocks = min(total, static_cast<int>(gridDim.x));
-    *t = *t1 = 0;
-    if (static_cast<int>(blockIdx.x) >= split->blocks) return;
+    split->blocks = min((total + kLeast - 1) / kLeast, static_cast<int>(gridDim.x));
+    if (static_cast<int>(blockIdx.x) >= split->blocks) return false;
     split->each = total / split->blocks;
     split->more = total - split->each * split->blocks;
-    *t = split->first_of(blockIdx.x);
-    *t1 = split->first_of(blockIdx.x + 1);
-    const int want = *t / hp;             // tile of the rows' own count
+    const int first = split->first_of(blockIdx.x);
+    *end = split->first_of(blockIdx.x + 1);
+    const int want = first / hp;          // unit of the rows' own count
     int before = 0;
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
         const int b = b0 + lane;
-        const int tiles = b < p.batch ? (row_of(p, b, &bad).n + TILE - 1) / TILE : 0;
-        const int sum = __reduce_add_sync(0xffffffffu, tiles);
+        const int units = b < p.batch ? units_of<RUN>(p, b, &bad) : 0;
+        const int sum = __reduce_add_sync(0xffffffffu, units);
         if (before + sum <= want) {
             before += sum;
             continue;
         }
-        int inc = tiles;
+        int inc = units;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int o = __shfl_up_sync(0xffffffffu, inc, d);
             if (lane >= d) inc += o;
         }
         const unsigned past = __ballot_sync(0xffffffffu, before + inc > want);
-        const int first = __ffs(past) - 1;
-        before += __shfl_sync(0xffffffffu, inc - tiles, first);
-        at->take_row(p, b0 + first);
+        const int found = __ffs(past) - 1;
+        before += __shfl_sync(0xffffffffu, inc - units, found);
+        at->take_row(p, b0 + found);
         break;
     }
     at->base = before * hp;
-    const int into = *t - at->base;
-    at->hg = into / at->tiles;
-    at->tile = into - at->hg * at->tiles;
+    const int into = first - at->base;
+    at->hg = into / (at->tiles + 1);
+    at->tile = into - at->hg * (at->tiles + 1);
+    if (at->tile == at->tiles) {          // the unit after the tiles
+        --at->tile;
+        at->next(p);
+    }
+    return at->unit() < *end;
 }
 
 // ---- asynchronous copies --------------------------------------------------------------------
@@ -198,6 +220,13 @@ __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_gr
 template <int N>
 __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// 2^x (results below 2^-126 are 0).
+__device__ __forceinline__ float pow2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // ---- outputs --------------------------------------------------------------------------------
@@ -229,7 +258,7 @@ template <class T>
 __device__ __forceinline__ void put_empty_rows(const AttnParams& p) {
     unsigned bad = 0;
     for (int b = blockIdx.x * kWarps + (threadIdx.x >> 5); b < p.batch; b += gridDim.x * kWarps) {
-        if (row_of(p, b, &bad).n > 0) continue;
+        if (row_of<8>(p, b, &bad).len > 0) continue;
         for (int x = 4 * (threadIdx.x & 31); x < p.q_heads * p.c.dim; x += 128) {
             const int h = x / p.c.dim, d = x - h * p.c.dim;
             put_out<T>(p, b, h, d, make_float4(0.0f, 0.0f, 0.0f, 0.0f), 0.0f);
@@ -247,7 +276,7 @@ __device__ __forceinline__ void join_parts(const float (&m)[N], const float (&s)
 #pragma unroll
     for (int i = 0; i < N; ++i) up = fmaxf(up, m[i]);
     const float base = up == kNegInf ? 0.0f : up;
-    const float w = exp2f(*top - base);
+    const float w = pow2(*top - base);
     *sum *= w;
     acc->x *= w;
     acc->y *= w;
@@ -255,7 +284,7 @@ __device__ __forceinline__ void join_parts(const float (&m)[N], const float (&s)
     acc->w *= w;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const float f = exp2f(m[i] - base);
+        const float f = pow2(m[i] - base);
         *sum = fmaf(s[i], f, *sum);
         acc->x = fmaf(o[i].x, f, acc->x);
         acc->y = fmaf(o[i].y, f, acc->y);
@@ -269,11 +298,11 @@ __device__ __forceinline__ void join_parts(const float (&m)[N], const float (&s)
 // A policy P has
 //   T, DP (dim rounded up), RUN (positions of a warp's share of a tile), STAGES, HEADS (most
 //   query heads of a part), and registers of its own;
-//   begin(q, head_stride, heads, dim): takes the query heads, empties max, sum and output;
-//   step(stage, j, end, scale): the run in `stage` (K rows, then V rows), whose first row is
-//     position j; rows from `end` on are not there;
-//   dump(m, s, o, first, heads, dim): leaves reference, sum and output (not divided) of heads
-//     first .. first + kRound - 1 (below heads) in shared memory.
+//   begin(q, head_stride, heads, dim, aligned): takes the query heads, empties max, sum, output;
+//   step(stage, lo, hi, scale): the run in `stage` (K rows, then V rows), of which rows
+//     lo .. hi - 1 are visible;
+//   dump(m, s, o, pitch, first, heads, dim): leaves reference, sum and output (not divided) of
+//     heads first .. first + kRound - 1 (below heads) in shared memory.
 constexpr int kRound = 8;                 // query heads that meet in shared memory at a time
 template <class P>
 struct Layout {
@@ -283,16 +312,20 @@ struct Layout {
     static constexpr int kStage = 2 * kHalf;
     static constexpr int kWarp = P::STAGES * kStage;
     static constexpr int kRing = kWarps * kWarp;
+    // Values between two heads of a dump: 4 more than dim, so that the lanes of a store, which
+    // hold 8 dims of 4 even (or odd) heads, meet different banks.
+    static __host__ __device__ constexpr int pitch(int dim) { return dim + 4; }
     static int smem(int part, int dim) {
-        return kRing + 4 * kWarps * (part < kRound ? part : kRound) * dim;
+        return kRing + 4 * kWarps * (part < kRound ? part : kRound) * pitch(dim);
     }
 };
 
-// What a warp's copies of one tile need, found one tile ahead: of position j of its run (lane
-// j), the page and the row in it.
+// What a warp's copies of one run need, found one tile ahead.
 struct Pending {
-    int page, row;
-    int kind;                                            // 0: zeros, 1: cached, 2: new token
+    int page, row;                                       // of row 0 of the run (lane r: of row r,
+                                                         // where runs cross pages)
+    int lo, hi;                                          // visible rows
+    int fresh;                                           // the row of the new token, or -1
     int b, hg;
 };
 
@@ -304,11 +337,13 @@ attention_kernel(const __grid_constant__ AttnParams p) {
     constexpr int V = 16 / static_cast<int>(sizeof(T));  // values of a 16-byte piece
     constexpr int CH = L::kRow / 16;                     // pieces of a row
     constexpr int STAGES = P::STAGES, RUN = P::RUN, TILE = L::kTile;
+    static_assert(CH <= 64 && RUN % 8 == 0, "a lane copies one or two pieces of a row");
     extern __shared__ __align__(128) char smem[];
-    float* const so = reinterpret_cast<float*>(smem + L::kRing);     // [kWarps][kRound or part heads][dim]
+    float* const so = reinterpret_cast<float*>(smem + L::kRing);     // [kWarps][kRound or part heads][pitch]
     __shared__ int turn;
     __shared__ float sm[kWarps][kRound], ss[kWarps][kRound];
-    const int gap = min(p.part, kRound) * p.c.dim;       // between the warps' outputs
+    const int pitch = L::pitch(p.c.dim);
+    const int gap = min(p.part, kRound) * pitch;      // between the warps' outputs
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int dim = p.c.dim, hp = p.c.heads * p.parts;
     char* const ring = smem + warp * L::kWarp;
@@ -320,61 +355,97 @@ attention_kernel(const __grid_constant__ AttnParams p) {
     }
     grid_wait();
     grid_trigger();
-    put_empty_rows<T>(p);
     Split split;
-    Cursor<TILE> cur;
-    int t, t1;
-    find_work<TILE>(p, &split, &t, &t1, &cur);
-    if (t >= t1) return;
-    const int t0 = t;
+    Cursor<RUN> cur;
+    int end;
+    if (!find_work<RUN>(p, &split, &end, &cur)) {
+        put_empty_rows<T>(p);
+        return;
+    }
+    const int begin = cur.unit();
 
-    auto look_up = [&](const Cursor<TILE>& c) {
+    // A lane copies piece c0 of every RPS-th row from r0 on (with rows of more than 32 pieces, two
+    // pieces of every row).
+    constexpr int RPS = CH < 32 ? 32 / CH : 1;
+    const int r0 = CH < 32 ? lane / CH : 0, c0 = CH < 32 ? lane % CH : lane;
+    const long long to_v = p.c.v - p.c.k;                // bytes from K to V
+    const long long row_step = p.c.token_stride * RPS * static_cast<int>(sizeof(T));
+
+    // The run of number j: its first position and visible rows.
+    auto look_up = [&](const Cursor<RUN>& c) {
         Pending w;
         w.b = c.b;
         w.hg = c.hg;
-        w.page = w.row = w.kind = 0;
-        const int j = c.tile * TILE + warp * RUN + (lane & (RUN - 1));
-        if (j < c.row.n) {
-            const int pos = position(c.row, j);
-            const int col = pos / p.c.page;
-            w.row = pos - col * p.c.page;
+        const int j = c.tile * TILE + warp * RUN;
+        const bool sink = j < c.row.turn;
+        const int pos = sink ? j : j - c.row.turn + c.row.from;
+        w.lo = sink ? 0 : max(0, c.row.first - pos);
+        w.hi = min(RUN, (sink ? c.row.sinks : c.row.len) - pos);
+        w.fresh = p.k_new != nullptr && !sink && c.row.len - 1 - pos < RUN ? c.row.len - 1 - pos : -1;
+        w.page = w.row = 0;
+        const int r = p.page_runs ? 0 : lane & (RUN - 1);
+        if (p.page_runs ? w.hi > 0 : r >= w.lo && r < w.hi) {
+            const unsigned at = static_cast<unsigned>(pos + r);
+            const unsigned col = (__umulhi(at, p.page_mul) + at) >> p.page_shift;
+            w.row = static_cast<int>(at - col * static_cast<unsigned>(p.c.page));
             w.page = p.c.table[static_cast<long long>(c.row.seq) * p.c.cols + col];
-            w.kind = p.k_new != nullptr && pos == c.row.len - 1 ? 2 : 1;
         }
         return w;
     };
     auto load = [&](const Pending& w, int slot) {
+        if (w.hi <= 0) return;                           // past the end
         const int head = p.parts == 1 ? w.hg : w.hg / p.parts;
-        const long long head_at = p.layer * p.c.layer_stride + head * p.c.head_stride;
         const bool ok = w.page >= 0 && w.page < p.c.pages;
-        long long off = head_at;
-        int size = 0;                                    // what the row's copies read of 16 bytes
-        if (w.kind != 0) {
-            if (ok) off += w.page * p.c.page_stride + w.row * p.c.token_stride;
-            else if (lane < RUN) flag(p.c.status, GS_DEV_BAD_SEQ);
-            size = w.kind == 2 ? -1 : ok ? 16 : 0;
-        }
+        const char* const from = p.c.k + (p.layer * p.c.layer_stride + head * p.c.head_stride +
+                                          (ok ? w.page * p.c.page_stride + w.row * p.c.token_stride : 0)) *
+                                             static_cast<int>(sizeof(T));
         const unsigned stage = ring_at + slot * L::kStage;
-        const T* const kc = reinterpret_cast<const T*>(p.c.k);
-        const T* const vc = reinterpret_cast<const T*>(p.c.v);
+        if (p.page_runs) {
+            if (!ok) flag(p.c.status, GS_DEV_BAD_SEQ);
+            const char* src = from + (r0 * p.c.token_stride + c0 * V) * static_cast<int>(sizeof(T));
+            const unsigned dst = stage + r0 * L::kRow;
 #pragma unroll
-        for (int x = 0; x < RUN * CH / 32; ++x) {
-            const int r = (x * 32 + lane) / CH, c = (x * 32 + lane) % CH;
-            const long long o = __shfl_sync(0xffffffffu, off, r) + c * V;
-            const int sz = __shfl_sync(0xffffffffu, size, r);
-            const unsigned dst = stage + r * L::kRow + ((c ^ (r & 7)) << 4);
-            if (c * V < dim && sz >= 0) {
-                copy_async(dst, kc + o, sz);
-                copy_async(dst + L::kHalf, vc + o, sz);
+            for (int x = 0; x < RUN / RPS; ++x) {
+                const int r = x * RPS + r0;
+                // (c ^ (r & 7): r0 is below RPS, a power of two)
+                const unsigned to = dst + x * RPS * L::kRow + (((c0 ^ r0) ^ (x * RPS & 7)) << 4);
+                const int size = ok && r >= w.lo && r < w.hi ? 16 : 0;
+                if (r != w.fresh) {
+                    if (c0 * V < dim) {
+                        copy_async(to, src, size);
+                        copy_async(to + L::kHalf, src + to_v, size);
+                    }
+                    if (CH > 32 && (c0 + 32) * V < dim) {
+                        copy_async(to + 512, src + 512, size);
+                        copy_async(to + 512 + L::kHalf, src + 512 + to_v, size);
+                    }
+                }
+                src += row_step;
+            }
+        } else {
+            const bool mine = (lane & (RUN - 1)) >= w.lo && (lane & (RUN - 1)) < w.hi;
+            if (mine && !ok) flag(p.c.status, GS_DEV_BAD_SEQ);
+            const long long at = from - p.c.k;
+            const int size = mine && ok ? 16 : 0;
+#pragma unroll
+            for (int x = 0; x < RUN * CH / 32; ++x) {
+                const int r = (x * 32 + lane) / CH, c = (x * 32 + lane) % CH;
+                const char* src = p.c.k + __shfl_sync(0xffffffffu, at, r) + 16 * c;
+                const int sz = __shfl_sync(0xffffffffu, size, r);
+                const unsigned to = stage + r * L::kRow + ((c ^ (r & 7)) << 4);
+                if (c * V < dim && r != w.fresh) {
+                    copy_async(to, src, sz);
+                    copy_async(to + L::kHalf, src + to_v, sz);
+                }
             }
         }
-        const unsigned fresh = __ballot_sync(0xffffffffu, lane < RUN && w.kind == 2);
-        if (fresh != 0u) {                               // the new token's row comes from k_new, v_new
-            const int r = __ffs(fresh) - 1;
-            const long long o = __shfl_sync(0xffffffffu, off, r);
-            const bool store = __shfl_sync(0xffffffffu, ok ? 1 : 0, r) != 0 && w.hg == head * p.parts;
-            for (int c = lane; c < CH; c += 32) {
-                if (c * V >= dim) break;
+        if (w.fresh >= 0) {                              // the new token's row comes from k_new, v_new
+            const int r = w.fresh;
+            const long long row = (from - p.c.k) + (p.page_runs ? r * p.c.token_stride * static_cast<int>(sizeof(T)) : 0);
+            const int from_lane = p.page_runs ? 0 : r;
+            const long long at = __shfl_sync(0xffffffffu, row, from_lane);
+            const bool store = __shfl_sync(0xffffffffu, ok ? 1 : 0, from_lane) != 0 && w.hg == head * p.parts;
+            for (int c = lane; c * V < dim; c += 32) {
                 const long long n = w.b * p.new_batch + head * p.new_head + c * V;
                 const uint4 k = load16_any(static_cast<const T*>(p.k_new) + n, p.new_aligned != 0);
                 const uint4 v = load16_any(static_cast<const T*>(p.v_new) + n, p.new_aligned != 0);
@@ -382,74 +453,81 @@ attention_kernel(const __grid_constant__ AttnParams p) {
                 *reinterpret_cast<uint4*>(to) = k;
                 *reinterpret_cast<uint4*>(to + L::kHalf) = v;
                 if (store) {
-                    *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.c.k) + o + c * V) = k;
-                    *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.c.v) + o + c * V) = v;
+                    *reinterpret_cast<uint4*>(p.c.k + at + 16 * c) = k;
+                    *reinterpret_cast<uint4*>(p.c.v + at + 16 * c) = v;
                 }
             }
         }
     };
 
-    Cursor<TILE> ahead = cur;
+    Cursor<RUN> ahead = cur;
     Pending next[STAGES];
 #pragma unroll
     for (int i = 0; i < STAGES; ++i) {
-        if (t + i < t1) {
+        next[i].hi = 0;
+        if (ahead.unit() < end) {
             next[i] = look_up(ahead);
             ahead.next(p);
         }
     }
 #pragma unroll
     for (int i = 0; i < STAGES - 1; ++i) {
-        if (t + i < t1) load(next[i], i);
+        load(next[i], i);
         copy_commit();
     }
     Pending pending = next[STAGES - 1];
+    put_empty_rows<T>(p);
     int slot = 0;
     P work;
     bool fresh = true;
-    for (; t < t1; ++t) {
+    while (cur.unit() < end) {
         const int head = p.parts == 1 ? cur.hg : cur.hg / p.parts;
         const int part = cur.hg - head * p.parts;
         const int first_head = head * p.group + part * p.part;
         const int heads = min(p.part, p.group - part * p.part);
         if (fresh) {
             work.begin(static_cast<const T*>(p.q) + cur.b * p.q_batch + first_head * p.q_head,
-                       p.q_head, heads, dim);
+                       p.q_head, heads, dim, p.q_aligned != 0);
             fresh = false;
         }
         copy_wait<STAGES - 2>();
         __syncwarp();
-        if (t + STAGES - 1 < t1) load(pending, slot == 0 ? STAGES - 1 : slot - 1);
+        load(pending, slot == 0 ? STAGES - 1 : slot - 1);
         copy_commit();
-        if (t + STAGES < t1) {
+        pending.hi = 0;
+        if (ahead.unit() < end) {
             pending = look_up(ahead);
             ahead.next(p);
         }
         const int j = cur.tile * TILE + warp * RUN;
-        if (j < cur.row.n) work.step(ring + slot * L::kStage, j, cur.row.n, p.scale_log2);
+        const bool sink = j < cur.row.turn;
+        const int pos = sink ? j : j - cur.row.turn + cur.row.from;
+        const int hi = min(RUN, (sink ? cur.row.sinks : cur.row.len) - pos);
+        if (hi > 0)
+            work.step(ring + slot * L::kStage, sink ? 0 : max(0, cur.row.first - pos), hi, p.scale_log2);
         slot = slot + 1 == STAGES ? 0 : slot + 1;
 
-        if (t + 1 == t1 || cur.tile + 1 == cur.tiles) {  // the segment's end
-            const int a = cur.base + cur.hg * cur.tiles; // the item's first tile
-            const bool whole = a >= t0 && a + cur.tiles <= t1;
+        if (cur.unit() + 1 == end || cur.tile + 1 == cur.tiles) {    // the segment's end
+            const int a = cur.item();
+            const bool whole = a >= begin && a + cur.tiles <= end;
             const int item = cur.b * hp + cur.hg;
             const long long size = slot_size(p.part, dim);
             // Slot 0 of a block for the segment it begins with, slot 1 for a later one.
-            float* const mine = p.slots + (2 * blockIdx.x + (a <= t0 ? 0 : 1)) * size;
+            float* const mine = p.slots + (2 * blockIdx.x + (a <= begin ? 0 : 1)) * size;
 #pragma unroll
             for (int h0 = 0; h0 < P::HEADS; h0 += kRound) {
                 if (h0 >= heads) break;
-                work.dump(sm[warp], ss[warp], so + warp * gap, h0, heads, dim);
+                work.dump(sm[warp], ss[warp], so + warp * gap, pitch, h0, heads, dim);
                 __syncthreads();
                 for (int x = 4 * threadIdx.x; x < min(kRound, heads - h0) * dim; x += 4 * kThreads) {
-                    const int h = x / dim;
+                    const int h = static_cast<int>(x * p.dim_mul >> 20);
                     float m[kWarps], s[kWarps], top = kNegInf, sum = 0.0f;
                     float4 o[kWarps], acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
                     for (int w = 0; w < kWarps; ++w) {
                         m[w] = sm[w][h];
                         s[w] = ss[w][h];
-                        o[w] = *reinterpret_cast<const float4*>(so + w * gap + x);
+                        o[w] = *reinterpret_cast<const float4*>(so + w * gap + h * pitch + (x - h * dim));
                     }
                     join_parts(m, s, o, &top, &sum, &acc);
                     if (whole) {
@@ -478,7 +556,8 @@ attention_kernel(const __grid_constant__ AttnParams p) {
                 }
                 __syncthreads();
                 if (turn != 0) {
-                    const float* first = p.slots + (2 * lo + (a == split.first_of(lo) ? 0 : 1)) * size;
+                    // (block lo begins with this item where its first unit is the item's, or the one before it)
+                    const float* first = p.slots + (2 * lo + (split.first_of(lo) >= a - 1 ? 0 : 1)) * size;
                     const float* rest = p.slots + 2 * static_cast<long long>(lo) * size;
                     for (int x = 4 * threadIdx.x; x < heads * dim; x += 4 * kThreads) {
                         const int h = x / dim;

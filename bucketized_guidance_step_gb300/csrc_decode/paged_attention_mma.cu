@@ -46,11 +46,19 @@ __device__ __forceinline__ void mma(float (&c)[4], const unsigned (&a)[4], unsig
 // Two values rounded and packed (x low), and what the rounding left, rounded and packed.
 template <class T>
 __device__ __forceinline__ void split2(float x, float y, unsigned* hi, unsigned* lo) {
-    const T hx = from_float<T>(x), hy = from_float<T>(y);
-    const T lx = from_float<T>(x - to_float(hx)), ly = from_float<T>(y - to_float(hy));
-    T h[2] = {hx, hy}, l[2] = {lx, ly};
-    *hi = *reinterpret_cast<unsigned*>(h);
-    *lo = *reinterpret_cast<unsigned*>(l);
+    if constexpr (std::is_same<T, __half>::value) {
+        const __half2 h = __floats2half2_rn(x, y);
+        const float2 f = __half22float2(h);
+        const __half2 l = __floats2half2_rn(x - f.x, y - f.y);
+        *hi = *reinterpret_cast<const unsigned*>(&h);
+        *lo = *reinterpret_cast<const unsigned*>(&l);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        *hi = *reinterpret_cast<const unsigned*>(&h);
+        const __nv_bfloat162 l = __floats2bfloat162_rn(x - __uint_as_float(*hi << 16),
+                                                       y - __uint_as_float(*hi & 0xffff0000u));
+        *lo = *reinterpret_cast<const unsigned*>(&l);
+    }
 }
 __device__ __forceinline__ float max_rows(float x) {     // over the lanes of one column
     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
@@ -75,7 +83,8 @@ struct Mma {
     float o[NH][KS][4];                                  // dims g (0, 1), g+8 (2, 3), heads 2t, 2t+1
     float top[NH][2], sum[NH][2];                        // heads 2t, 2t+1
 
-    __device__ __forceinline__ void begin(const T* query, long long head_stride, int heads, int dim) {
+    __device__ __forceinline__ void begin(const T* query, long long head_stride, int heads, int dim,
+                                          bool aligned) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
@@ -87,19 +96,23 @@ struct Mma {
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     const int d = s * 16 + half * 8 + 2 * t;
-                    T two[2] = {from_float<T>(0.0f), from_float<T>(0.0f)};
+                    unsigned two = 0u;
                     if (h * 8 + g < heads && d < dim) {
-                        two[0] = qp[d];
-                        two[1] = qp[d + 1];
+                        if (aligned) {
+                            two = *reinterpret_cast<const unsigned*>(qp + d);
+                        } else {
+                            const unsigned short* at = reinterpret_cast<const unsigned short*>(qp + d);
+                            two = at[0] | static_cast<unsigned>(at[1]) << 16;
+                        }
                     }
-                    q[h][s][half] = *reinterpret_cast<unsigned*>(two);
+                    q[h][s][half] = two;
                 }
                 o[h][s][0] = o[h][s][1] = o[h][s][2] = o[h][s][3] = 0.0f;
             }
         }
     }
 
-    __device__ __forceinline__ void step(const char* stage, int j, int end, float scale) {
+    __device__ __forceinline__ void step(const char* stage, int lo, int hi, float scale) {
         const int lane = threadIdx.x & 31, g = lane >> 2;
         float s[NH][4];                                  // positions g (0, 1), g+8 (2, 3)
 #pragma unroll
@@ -120,9 +133,11 @@ struct Mma {
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                s[h][e] *= scale;
-                if (j + g + (e >> 1) * 8 >= end) s[h][e] = kNegInf;
+            for (int e = 0; e < 4; ++e) s[h][e] *= scale;
+            if (lo > 0 || hi < RUN) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (g + (e >> 1) * 8 < lo || g + (e >> 1) * 8 >= hi) s[h][e] = kNegInf;
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -135,7 +150,7 @@ struct Mma {
             for (int h = 0; h < NH; ++h)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float w = up[h][e] > top[h][e] ? exp2f(top[h][e] - up[h][e]) : 1.0f;
+                    const float w = up[h][e] > top[h][e] ? pow2(top[h][e] - up[h][e]) : 1.0f;
                     sum[h][e] *= w;
 #pragma unroll
                     for (int x = 0; x < KS; ++x) {
@@ -145,22 +160,22 @@ struct Mma {
                     top[h][e] = up[h][e];
                 }
         }
-        unsigned hi[NH][2], lo[NH][2];
+        unsigned wh[NH][2], wl[NH][2];
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const float base = top[h][e] == kNegInf ? 0.0f : top[h][e] - kShift;
-                s[h][e] = exp2f(s[h][e] - base);
-                s[h][e + 2] = exp2f(s[h][e + 2] - base);
+                s[h][e] = pow2(s[h][e] - base);
+                s[h][e + 2] = pow2(s[h][e + 2] - base);
                 sum[h][e] += s[h][e] + s[h][e + 2];
             }
-            split2<T>(s[h][0], s[h][1], &hi[h][0], &lo[h][0]);
-            split2<T>(s[h][2], s[h][3], &hi[h][1], &lo[h][1]);
+            split2<T>(s[h][0], s[h][1], &wh[h][0], &wl[h][0]);
+            split2<T>(s[h][2], s[h][3], &wh[h][1], &wl[h][1]);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                hi[h][e] = transpose8(hi[h][e]);
-                lo[h][e] = transpose8(lo[h][e]);
+                wh[h][e] = transpose8(wh[h][e]);
+                wl[h][e] = transpose8(wl[h][e]);
             }
         }
         {
@@ -172,15 +187,15 @@ struct Mma {
                 load_matrix_t(row + (((2 * x + ((lane >> 3) & 1)) ^ (r & 7)) << 4), a);
 #pragma unroll
                 for (int h = 0; h < NH; ++h) {
-                    mma<T>(o[h][x], a, hi[h][0], hi[h][1]);
-                    mma<T>(o[h][x], a, lo[h][0], lo[h][1]);
+                    mma<T>(o[h][x], a, wh[h][0], wh[h][1]);
+                    mma<T>(o[h][x], a, wl[h][0], wl[h][1]);
                 }
             }
         }
     }
 
-    __device__ __forceinline__ void dump(float* m, float* s, float* out, int first, int heads,
-                                         int dim) {
+    __device__ __forceinline__ void dump(float* m, float* s, float* out, int pitch, int first,
+                                         int heads, int dim) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
@@ -199,7 +214,7 @@ struct Mma {
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const int d = x * 16 + half * 8 + g;
-                        if (d < dim) out[head * dim + d] = o[h][x][e + 2 * half];
+                        if (d < dim) out[head * pitch + d] = o[h][x][e + 2 * half];
                     }
             }
         }
