@@ -112,6 +112,7 @@ extend_kernel(CacheView c, const int* __restrict__ seq, const int* __restrict__ 
     __shared__ int tmp[kMeta / 32 + 1];
     __shared__ int mine;
     grid_wait();
+    grid_trigger();
     mark_first(mark, c.seqs, seq, n);
     const bool first_block = cluster_rank() == 0;
     for (int i = threadIdx.x; i < n; i += kMeta) {
@@ -180,6 +181,7 @@ fork_kernel(CacheView c, const int* __restrict__ src, const int* __restrict__ ds
     __shared__ int tmp[kMeta / 32 + 1];
     __shared__ int mine;
     grid_wait();
+    grid_trigger();
     mark_first(mark, c.seqs, dst, n);
     const bool first_block = cluster_rank() == 0;
     const int most = c.cols * c.page;
@@ -272,6 +274,7 @@ fork_kernel(CacheView c, const int* __restrict__ src, const int* __restrict__ ds
 // finds nothing to release.
 __global__ void __launch_bounds__(128) free_kernel(CacheView c, const int* __restrict__ seq, int n) {
     grid_wait();
+    grid_trigger();
     const int i = (blockIdx.x * 128 + threadIdx.x) >> 5, lane = threadIdx.x & 31;
     if (i >= n) return;
     const int s = seq[i];
@@ -304,6 +307,7 @@ compact_kernel(CacheView c, int* __restrict__ refs_out, int* __restrict__ live_o
     __shared__ int tmp[kMeta / 32 + 1];
     __shared__ int mine;
     grid_wait();
+    grid_trigger();
     int lo, hi, avail, before;
     eighth(c.pages, &lo, &hi);
     count_free(c, lo, hi, &mine, tmp, &avail, &before);
@@ -355,17 +359,18 @@ compact_kernel(CacheView c, int* __restrict__ refs_out, int* __restrict__ live_o
     cluster_sync();
 }
 
-// The listed copies: a unit of work is one page of one layer of K or V.  16-byte vectors,
-// several in flight a thread.  With `table` set, the table's entries are renumbered too
-// (compact).
-template <bool REMAP>
+// The listed copies: a warp takes one head of one page of one layer of K or V at a time, 8
+// vectors of 16 bytes a lane in flight.  DENSE: a head's rows lie next to each other.  With REMAP
+// the table's entries are renumbered too (compact).
+template <bool REMAP, bool DENSE>
 __global__ void __launch_bounds__(kCopy)
 copy_kernel(CacheView c, int es, int* __restrict__ table_out) {
     grid_wait();
-    const int count = __ldcg(c.work);
-    const Copy* copies = copies_of(c.work);
+    grid_trigger();
+    const int count = c.work[0];
+    const int4* const copies = reinterpret_cast<const int4*>(copies_of(c.work));
     if constexpr (REMAP) {
-        const int live = __ldcg(c.work + 1);
+        const int live = c.work[1];
         const int* rank_of = c.work + 4 + 4 * static_cast<long long>(c.pages > c.seqs ? c.pages : c.seqs);
         const long long cells = static_cast<long long>(c.seqs) * c.cols;
         for (long long q = static_cast<long long>(blockIdx.x) * kCopy + threadIdx.x; q < cells;
@@ -373,64 +378,93 @@ copy_kernel(CacheView c, int es, int* __restrict__ table_out) {
             int p = c.table[q];
             // Entries past a sequence's pages may hold anything: only held pages are renumbered.
             const int s = static_cast<int>(q / c.cols), j = static_cast<int>(q % c.cols);
-            if (p >= live && p < c.pages && j < pages_of(__ldcg(c.lens + s), c.page))
-                p = __ldcg(&copies[rank_of[p]].to);
+            if (p >= live && p < c.pages && j < pages_of(c.lens[s], c.page)) p = copies[rank_of[p]].y;
             table_out[q] = p;
         }
     }
+    const int lane = threadIdx.x & 31;
     const int per = c.dim * es / 16;                     // vectors of a row
-    const long long units = 2ll * count * c.layers;
-    for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-        const int4 w = __ldcg(reinterpret_cast<const int4*>(copies + u / (2 * c.layers)));
-        const int which = static_cast<int>(u % (2 * c.layers));
-        char* base = ((which & 1) != 0 ? c.v : c.k) + (which >> 1) * c.layer_stride * es;
-        const char* src = base + w.x * c.page_stride * es;
-        char* dst = base + w.y * c.page_stride * es;
-        const int vecs = c.heads * w.z * per;
-        constexpr int U = 4;
-        for (int v0 = threadIdx.x; v0 < vecs; v0 += kCopy * U) {
+    const int sides = 2 * c.layers * c.heads;            // warps' units of a copy
+    const long long units = static_cast<long long>(count) * sides;
+    const long long warps = static_cast<long long>(gridDim.x) * (kCopy / 32);
+    for (long long u = static_cast<long long>(blockIdx.x) * (kCopy / 32) + (threadIdx.x >> 5); u < units;
+         u += warps) {
+        const int i = static_cast<int>(u / sides), side = static_cast<int>(u - static_cast<long long>(i) * sides);
+        const int head = side % c.heads, which = side / c.heads;
+        const int4 w = copies[i];                        // from, to, tokens
+        char* const base = ((which & 1) != 0 ? c.v : c.k) +
+                           ((which >> 1) * c.layer_stride + head * c.head_stride) * es;
+        const char* const src = base + w.x * c.page_stride * es;
+        char* const dst = base + w.y * c.page_stride * es;
+        const int vecs = w.z * per;
+        constexpr int U = 8;
+        for (int v0 = lane; v0 < vecs; v0 += 32 * U) {
             uint4 r[U];
             long long off[U];
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const int v = v0 + i * kCopy;
+            for (int x = 0; x < U; ++x) {
+                const int v = v0 + x * 32;
                 if (v < vecs) {
-                    const int row = v / per;
-                    const int head = row / w.z;
-                    off[i] = (head * c.head_stride + (row - head * w.z) * c.token_stride) * es +
-                             16ll * (v - row * per);
-                    r[i] = __ldcs(reinterpret_cast<const uint4*>(src + off[i]));
+                    if (DENSE) {
+                        off[x] = 16ll * v;
+                    } else {
+                        const int row = v / per;
+                        off[x] = row * c.token_stride * es + 16ll * (v - row * per);
+                    }
+                    r[x] = __ldcs(reinterpret_cast<const uint4*>(src + off[x]));
                 }
             }
 #pragma unroll
-            for (int i = 0; i < U; ++i)
-                if (v0 + i * kCopy < vecs) __stcs(reinterpret_cast<uint4*>(dst + off[i]), r[i]);
+            for (int x = 0; x < U; ++x)
+                if (v0 + x * 32 < vecs) __stcs(reinterpret_cast<uint4*>(dst + off[x]), r[x]);
         }
     }
 }
 
-// New tokens' K and V into one layer: a warp a token and K or V, 16 bytes a lane.
+// New tokens' K and V into one layer: a warp a token.  The token's first vectors are asked for
+// before its place is looked up.
 template <class T>
 __global__ void __launch_bounds__(kCopy)
 write_kernel(CacheView c, int layer, const T* __restrict__ k, const T* __restrict__ v,
              long long token_stride, long long head_stride, int src_aligned, int tokens,
              const int* __restrict__ seq, const int* __restrict__ start, int n) {
+    extern __shared__ int first[];                       // [n + 1]: start
     grid_wait();
+    grid_trigger();
     const int lane = threadIdx.x & 31;
-    const long long w = (static_cast<long long>(blockIdx.x) * kCopy + threadIdx.x) >> 5;
-    const int t = static_cast<int>(w >> 1);
-    if (t >= tokens || t < start[0] || t >= start[n]) return;
+    const int t = static_cast<int>((static_cast<long long>(blockIdx.x) * kCopy + threadIdx.x) >> 5);
+    constexpr int E = 16 / static_cast<int>(sizeof(T)), U = 4;
+    const int per = c.dim / E, vecs = c.heads * per;     // vectors of a row; of a token's K
+    const T* const ks = k + t * token_stride;
+    const T* const vs = v + t * token_stride;
+    uint4 kr[U], vr[U];
+    int head[U], x[U];
+    auto fetch = [&](int q0) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int q = q0 + i * 32;
+            if (q >= vecs || t >= tokens) continue;
+            head[i] = q / per;
+            x[i] = (q - head[i] * per) * E;
+            kr[i] = load16_any(ks + head[i] * head_stride + x[i], src_aligned != 0);
+            vr[i] = load16_any(vs + head[i] * head_stride + x[i], src_aligned != 0);
+        }
+    };
+    fetch(lane);
+    for (int i = threadIdx.x; i <= n; i += kCopy) first[i] = start[i];
+    __syncthreads();
+    if (t >= tokens || t < first[0] || t >= first[n]) return;
     int lo = 0, hi = n;                                  // the last i with start[i] <= t
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (start[mid] <= t) lo = mid; else hi = mid;
+        if (first[mid] <= t) lo = mid; else hi = mid;
     }
     const int s = seq[lo];
     bool ok = s >= 0 && s < c.seqs;
     long long pos = -1;
     if (ok) {
         const int len = c.lens[s];
-        pos = static_cast<long long>(len) - (start[lo + 1] - t);
+        pos = static_cast<long long>(len) - (first[lo + 1] - t);
         ok = pos >= 0 && len <= c.cols * c.page;
     }
     int p = -1;
@@ -442,15 +476,17 @@ write_kernel(CacheView c, int layer, const T* __restrict__ k, const T* __restric
         if (lane == 0) flag(c.status, GS_DEV_BAD_SEQ);
         return;
     }
-    constexpr int E = 16 / sizeof(T);
-    const T* src = ((w & 1) != 0 ? v : k) + t * token_stride;
-    T* dst = reinterpret_cast<T*>((w & 1) != 0 ? c.v : c.k) + layer * c.layer_stride +
-             p * c.page_stride + (pos % c.page) * c.token_stride;
-    const int per = c.dim / E;
-    for (int q = lane; q < c.heads * per; q += 32) {
-        const int head = q / per, x = (q - head * per) * E;
-        *reinterpret_cast<uint4*>(dst + head * c.head_stride + x) =
-            load16_any(src + head * head_stride + x, src_aligned != 0);
+    const long long at = layer * c.layer_stride + p * c.page_stride + (pos % c.page) * c.token_stride;
+    T* const kd = reinterpret_cast<T*>(c.k) + at;
+    T* const vd = reinterpret_cast<T*>(c.v) + at;
+    for (int q0 = lane; q0 < vecs; q0 += 32 * U) {
+        if (q0 != lane) fetch(q0);
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (q0 + i * 32 >= vecs) continue;
+            *reinterpret_cast<uint4*>(kd + head[i] * c.head_stride + x[i]) = kr[i];
+            *reinterpret_cast<uint4*>(vd + head[i] * c.head_stride + x[i]) = vr[i];
+        }
     }
 }
 
@@ -473,15 +509,18 @@ gs_status check_workspace(const gs_kv_cache* c) {
     return GS_OK;
 }
 
+// `most` copies at most; the list's length is on the device.
 template <bool REMAP>
 gs_status launch_copies(const CacheView& c, int dtype, long long most, int* table_out,
                         gs_stream stream) {
-    long long blocks = most * 2 * c.layers;
+    long long blocks = (most * 2 * c.layers * c.heads + kCopy / 32 - 1) / (kCopy / 32);
     const long long full = static_cast<long long>(sm_count()) * 8;
     if (blocks > full) blocks = full;
-    if (blocks < 1) blocks = 1;
-    return launch(copy_kernel<REMAP>, dim3(static_cast<unsigned>(blocks)), kCopy, 0, 1, stream, c,
-                  static_cast<int>(elem_size(dtype)), table_out);
+    const dim3 grid(static_cast<unsigned>(blocks));
+    const int es = static_cast<int>(elem_size(dtype));
+    return c.token_stride == c.dim || c.page == 1
+               ? launch(copy_kernel<REMAP, true>, grid, kCopy, 0, 1, stream, c, es, table_out)
+               : launch(copy_kernel<REMAP, false>, grid, kCopy, 0, 1, stream, c, es, table_out);
 }
 
 }  // namespace
@@ -564,20 +603,21 @@ extern "C" gs_status gs_kv_write(const gs_kv_cache* cache, int32_t layer, const 
         return GS_ERR_INVALID_ARG;
     const int vec = aligned(k, 16) && aligned(v, 16) && (token_stride * es) % 16 == 0 &&
                     (head_stride * es) % 16 == 0;
-    const long long blocks = (2ll * tokens * 32 + kCopy - 1) / kCopy;
+    const long long blocks = (32ll * tokens + kCopy - 1) / kCopy;
+    const int smem = 4 * (n + 1);
     const dim3 grid(static_cast<unsigned>(blocks));
     switch (cache->dtype) {
         case GS_DTYPE_F32:
-            return launch(write_kernel<float>, grid, kCopy, 0, 1, stream, c, layer,
+            return launch(write_kernel<float>, grid, kCopy, smem, 1, stream, c, layer,
                           static_cast<const float*>(k), static_cast<const float*>(v), token_stride,
                           head_stride, vec, tokens, seq, start, n);
         case GS_DTYPE_BF16:
-            return launch(write_kernel<__nv_bfloat16>, grid, kCopy, 0, 1, stream, c, layer,
+            return launch(write_kernel<__nv_bfloat16>, grid, kCopy, smem, 1, stream, c, layer,
                           static_cast<const __nv_bfloat16*>(k),
                           static_cast<const __nv_bfloat16*>(v), token_stride, head_stride, vec,
                           tokens, seq, start, n);
         default:
-            return launch(write_kernel<__half>, grid, kCopy, 0, 1, stream, c, layer,
+            return launch(write_kernel<__half>, grid, kCopy, smem, 1, stream, c, layer,
                           static_cast<const __half*>(k), static_cast<const __half*>(v),
                           token_stride, head_stride, vec, tokens, seq, start, n);
     }

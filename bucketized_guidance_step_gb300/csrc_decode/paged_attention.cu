@@ -12,12 +12,12 @@
 namespace gs_decode {
 namespace {
 
-// NV: 16-byte pieces of a row that a lane holds.  The query heads and the output of a part take
-// 64 registers each.
-template <int NV>
+// NV: 16-byte pieces of a row that a lane holds; H: query heads of a part, for whose values and
+// output a lane has 4 NV H registers each.
+template <int NV, int H>
 struct Fp32 {
     using T = float;
-    static constexpr int DP = 32 * NV, RUN = 8, STAGES = NV <= 2 ? 6 : 3, HEADS = 16 / NV;
+    static constexpr int DP = 32 * NV, RUN = 8, STAGES = NV <= 2 ? 6 : 3, HEADS = H;
     static constexpr int E = 4 * NV, U = RUN / 4;
     static_assert(HEADS <= kRound, "one dump");
     float q[HEADS][E], o[HEADS][E], top[HEADS], sum[HEADS];
@@ -135,17 +135,23 @@ struct Fp32 {
 
 }  // namespace
 
-// Rings of 96 KB a block (192 KB for rows over 512 bytes).
+// Most heads of a part: 64 registers for their values.  Rings of 96 KB a block (192 KB for rows
+// over 512 bytes).
 Serves fp32_serves(int dim) {
-    if (dim <= 64) return {Layout<Fp32<2>>::kTile, Fp32<2>::HEADS, 2};
-    if (dim <= 128) return {Layout<Fp32<4>>::kTile, Fp32<4>::HEADS, 2};
-    return {Layout<Fp32<8>>::kTile, Fp32<8>::HEADS, 1};
+    if (dim <= 64) return {Layout<Fp32<2, 8>>::kTile, 8, 2};
+    if (dim <= 128) return {Layout<Fp32<4, 4>>::kTile, 4, 2};
+    return {Layout<Fp32<8, 2>>::kTile, 2, 1};
 }
 
+// Parts of one or two heads have instances of their own: an instance computes for all its heads.
 gs_status launch_fp32(const AttnParams& p, int blocks, gs_stream stream) {
-    if (p.c.dim <= 64) return launch_policy<Fp32<2>>(p, blocks, stream);
-    if (p.c.dim <= 128) return launch_policy<Fp32<4>>(p, blocks, stream);
-    return launch_policy<Fp32<8>>(p, blocks, stream);
+    if (p.c.dim <= 64)
+        return p.part <= 2 ? launch_policy<Fp32<2, 2>>(p, blocks, stream)
+                           : launch_policy<Fp32<2, 8>>(p, blocks, stream);
+    if (p.c.dim <= 128)
+        return p.part <= 2 ? launch_policy<Fp32<4, 2>>(p, blocks, stream)
+                           : launch_policy<Fp32<4, 4>>(p, blocks, stream);
+    return launch_policy<Fp32<8, 2>>(p, blocks, stream);
 }
 
 namespace {
