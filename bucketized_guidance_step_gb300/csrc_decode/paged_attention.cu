@@ -22,19 +22,27 @@ struct Fp32 {
     static_assert(HEADS <= kRound, "one dump");
     float q[HEADS][E], o[HEADS][E], top[HEADS], sum[HEADS];
 
-    __device__ __forceinline__ void begin(const float* query, long long head_stride, int heads,
+    static constexpr bool AHEAD = false;
+
+    __device__ __forceinline__ void fetch(const float* query, long long head_stride, int heads,
                                           int dim, bool) {
         const int sub = threadIdx.x & 7;
+#pragma unroll
+        for (int h = 0; h < HEADS; ++h)
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int d = (sub + 8 * (e / 4)) * 4 + e % 4;
+                q[h][e] = h < heads && d < dim ? query[h * head_stride + d] : 0.0f;
+            }
+    }
+
+    __device__ __forceinline__ void begin() {
 #pragma unroll
         for (int h = 0; h < HEADS; ++h) {
             top[h] = kNegInf;
             sum[h] = 0.0f;
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int d = (sub + 8 * (e / 4)) * 4 + e % 4;
-                q[h][e] = h < heads && d < dim ? query[h * head_stride + d] : 0.0f;
-                o[h][e] = 0.0f;
-            }
+            for (int e = 0; e < E; ++e) o[h][e] = 0.0f;
         }
     }
 
@@ -101,8 +109,7 @@ struct Fp32 {
         }
     }
 
-    __device__ __forceinline__ void dump(float* m, float* s, float* out, int pitch, int, int heads,
-                                         int dim) {
+    __device__ __forceinline__ void dump(float* out, int pitch, int, int heads, int dim) {
         const int lane = threadIdx.x & 31, sub = lane & 7, group = lane >> 3;
 #pragma unroll
         for (int h = 0; h < HEADS; ++h) {
@@ -113,8 +120,8 @@ struct Fp32 {
             all += __shfl_xor_sync(0xffffffffu, all, 8);
             all += __shfl_xor_sync(0xffffffffu, all, 16);
             if (lane == 0 && h < heads) {
-                m[h] = up;
-                s[h] = all;
+                out[h * pitch + dim] = up;
+                out[h * pitch + dim + 1] = all;
             }
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -231,7 +238,8 @@ extern "C" gs_status gs_paged_attention(const gs_paged_attention_args* args, gs_
     if (args->workspace == nullptr || !aligned(args->workspace, 16) ||
         args->workspace_bytes < 4 * (plan.counters + plan.slots))
         return GS_ERR_INVALID_ARG;
-    p.layer = args->layer;
+    p.c.k += args->layer * p.c.layer_stride * es;
+    p.c.v += args->layer * p.c.layer_stride * es;
     p.batch = args->batch;
     p.seq = args->seq;
     p.q_heads = args->q_heads;

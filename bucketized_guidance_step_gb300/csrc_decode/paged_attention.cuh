@@ -30,13 +30,12 @@ namespace gs_decode {
 
 constexpr int kWarps = 4;                 // warps of a block
 constexpr int kThreads = 32 * kWarps;
-constexpr int kLeast = 1;                 // units a block takes at least
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct AttnParams {
     CacheView c;
-    int layer, batch;
+    int batch;                            // c.k and c.v are the layer's
     const int* seq;
     int q_heads, group;                   // query heads; of one kv head
     int parts, part;                      // head groups of a kv head; query heads of one
@@ -49,7 +48,9 @@ struct AttnParams {
     int out_aligned;                      // out rows lie on 4 elements
     int q_aligned;                        // q rows lie on 2 elements
     unsigned page_mul, page_shift;        // position / page = (mulhi(position, mul) + position) >> shift
+    int dumps;                            // places for a segment's end in shared memory: 1 or 2
     int page_runs;                        // a page holds whole runs: a run lies in one page
+    int whole_runs;                       // and a row fills the pieces that lanes copy (dim is DP)
     unsigned dim_mul;                     // x / dim = x * mul >> 20, for x < 8 dim
     float scale_log2;                     // scale * log2 e: scores are kept in powers of two
     int window, sinks;
@@ -75,21 +76,20 @@ struct Row {
     int sinks, turn, from, first;
 };
 
+// The row of sequence `seq` with what lens[seq] holds (0 for a sequence outside the cache).
 template <int RUN>
-__device__ __forceinline__ Row row_of(const AttnParams& p, int b, unsigned* bad) {
+__device__ __forceinline__ Row row_from(const AttnParams& p, int seq, int len, unsigned* bad) {
     Row r;
-    r.seq = p.seq != nullptr ? p.seq[b] : b;
-    r.len = 0;
-    if (r.seq < 0 || r.seq >= p.c.seqs) {
+    r.seq = seq;
+    r.len = len;
+    if (seq < 0 || seq >= p.c.seqs) {
         *bad |= GS_DEV_BAD_SEQ;
-        r.seq = 0;
-    } else {
-        r.len = p.c.lens[r.seq];
-        const int most = p.c.cols * p.c.page;
-        if (r.len < 0 || r.len > most) {
-            *bad |= GS_DEV_BAD_SEQ;
-            r.len = r.len < 0 ? 0 : most;
-        }
+        r.seq = r.len = 0;
+    }
+    const int most = p.c.cols * p.c.page;
+    if (r.len < 0 || r.len > most) {
+        *bad |= GS_DEV_BAD_SEQ;
+        r.len = r.len < 0 ? 0 : most;
     }
     r.n = r.len;
     r.sinks = r.turn = r.from = r.first = 0;
@@ -101,6 +101,11 @@ __device__ __forceinline__ Row row_of(const AttnParams& p, int b, unsigned* bad)
         r.n = r.turn + (r.len - r.from);
     }
     return r;
+}
+template <int RUN>
+__device__ __forceinline__ Row row_of(const AttnParams& p, int b, unsigned* bad) {
+    const int seq = p.seq != nullptr ? p.seq[b] : b;
+    return row_from<RUN>(p, seq, seq >= 0 && seq < p.c.seqs ? p.c.lens[seq] : 0, bad);
 }
 
 // The split of all units: the first `more` blocks take each + 1, the others each.
@@ -150,9 +155,8 @@ struct Cursor {
 };
 
 template <int RUN>
-__device__ __forceinline__ int units_of(const AttnParams& p, int b, unsigned* bad) {
-    const int n = row_of<RUN>(p, b, bad).n;
-    return n > 0 ? (n + kWarps * RUN - 1) / (kWarps * RUN) + 1 : 0;
+__device__ __forceinline__ int units_in(const Row& r) {
+    return r.n > 0 ? (r.n + kWarps * RUN - 1) / (kWarps * RUN) + 1 : 0;
 }
 
 // The end of this block's units and the cursor at its first tile; false where it has none.
@@ -162,39 +166,67 @@ __device__ __forceinline__ bool find_work(const AttnParams& p, Split* split, int
                                           Cursor<RUN>* at) {
     const int lane = threadIdx.x & 31;
     const int hp = p.c.heads * p.parts;
+    // 32 rows at a time, eight such loads in flight; lane i keeps the sum of `per` of them from
+    // per * i on, then the lanes are summed up.
+    const int groups = (p.batch + 31) / 32, per = (groups + 31) / 32;
     unsigned bad = 0;
-    int all = 0;
-    for (int b = lane; b < p.batch; b += 32) all += units_of<RUN>(p, b, &bad);
-    all = __reduce_add_sync(0xffffffffu, all);
+    int mine = 0;
+    constexpr int N = 8;
+    for (int g0 = 0; g0 < groups; g0 += N) {
+        int seq[N], len[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int b = (g0 + i) * 32 + lane;
+            seq[i] = b < p.batch && p.seq != nullptr ? p.seq[b] : b;
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int b = (g0 + i) * 32 + lane;
+            len[i] = b < p.batch && seq[i] >= 0 && seq[i] < p.c.seqs ? p.c.lens[seq[i]] : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (g0 + i >= groups) break;
+            const int b = (g0 + i) * 32 + lane;
+            const int sum = __reduce_add_sync(
+                0xffffffffu, b < p.batch ? units_in<RUN>(row_from<RUN>(p, seq[i], len[i], &bad)) : 0);
+            if ((g0 + i) / per == lane) mine += sum;
+        }
+    }
     if (blockIdx.x == 0 && threadIdx.x < 32) flag(p.c.status, bad);
-    const int total = all * hp;
-    split->blocks = min((total + kLeast - 1) / kLeast, static_cast<int>(gridDim.x));
+    int upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += o;
+    }
+    const int total = __shfl_sync(0xffffffffu, upto, 31) * hp;
+    split->blocks = min(total, static_cast<int>(gridDim.x));
     if (static_cast<int>(blockIdx.x) >= split->blocks) return false;
     split->each = total / split->blocks;
     split->more = total - split->each * split->blocks;
     const int first = split->first_of(blockIdx.x);
     *end = split->first_of(blockIdx.x + 1);
     const int want = first / hp;          // unit of the rows' own count
-    int before = 0;
-    for (int b0 = 0; b0 < p.batch; b0 += 32) {
-        const int b = b0 + lane;
-        const int units = b < p.batch ? units_of<RUN>(p, b, &bad) : 0;
-        const int sum = __reduce_add_sync(0xffffffffu, units);
-        if (before + sum <= want) {
-            before += sum;
-            continue;
-        }
-        int inc = units;
+    const int found = __ffs(__ballot_sync(0xffffffffu, upto > want)) - 1;
+    int before = __shfl_sync(0xffffffffu, upto - mine, found);
+    // The same for the found lane's rows, 32 at a time.
+    for (int row = found * per * 32;; row += 32) {
+        const int units = row + lane < p.batch ? units_in<RUN>(row_of<RUN>(p, row + lane, &bad)) : 0;
+        upto = units;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, inc, d);
-            if (lane >= d) inc += o;
+            const int o = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += o;
         }
-        const unsigned past = __ballot_sync(0xffffffffu, before + inc > want);
-        const int found = __ffs(past) - 1;
-        before += __shfl_sync(0xffffffffu, inc - units, found);
-        at->take_row(p, b0 + found);
-        break;
+        const unsigned past = __ballot_sync(0xffffffffu, before + upto > want);
+        if (past != 0u) {
+            const int i = __ffs(past) - 1;
+            before += __shfl_sync(0xffffffffu, upto - units, i);
+            at->take_row(p, row + i);
+            break;
+        }
+        before += __shfl_sync(0xffffffffu, upto, 31);
     }
     at->base = before * hp;
     const int into = first - at->base;
@@ -298,11 +330,14 @@ __device__ __forceinline__ void join_parts(const float (&m)[N], const float (&s)
 // A policy P has
 //   T, DP (dim rounded up), RUN (positions of a warp's share of a tile), STAGES, HEADS (most
 //   query heads of a part), and registers of its own;
-//   begin(q, head_stride, heads, dim, aligned): takes the query heads, empties max, sum, output;
+//   AHEAD: fetch may be called during the segment before;
+//   fetch(q, head_stride, heads, dim, aligned): reads the query heads of a segment;
+//   begin(): takes them into use, empties max, sum and output;
 //   step(stage, lo, hi, scale): the run in `stage` (K rows, then V rows), of which rows
 //     lo .. hi - 1 are visible;
-//   dump(m, s, o, pitch, first, heads, dim): leaves reference, sum and output (not divided) of
-//     heads first .. first + kRound - 1 (below heads) in shared memory.
+//   dump(o, pitch, first, heads, dim): leaves of heads first .. first + kRound - 1 (below heads)
+//     the output (not divided), the reference and the sum in shared memory: a head's row of
+//     pitch values is dim outputs, reference, sum.
 constexpr int kRound = 8;                 // query heads that meet in shared memory at a time
 template <class P>
 struct Layout {
@@ -312,11 +347,11 @@ struct Layout {
     static constexpr int kStage = 2 * kHalf;
     static constexpr int kWarp = P::STAGES * kStage;
     static constexpr int kRing = kWarps * kWarp;
-    // Values between two heads of a dump: 4 more than dim, so that the lanes of a store, which
-    // hold 8 dims of 4 even (or odd) heads, meet different banks.
+    // Values between two heads of a dump: 4 more than dim (the reference, the sum, two unused), so
+    // that the lanes of a store, which hold 8 dims of 4 even (or odd) heads, meet different banks.
     static __host__ __device__ constexpr int pitch(int dim) { return dim + 4; }
-    static int smem(int part, int dim) {
-        return kRing + 4 * kWarps * (part < kRound ? part : kRound) * pitch(dim);
+    static int dump(int part, int dim) {                 // bytes
+        return 4 * kWarps * (part < kRound ? part : kRound) * pitch(dim);
     }
 };
 
@@ -339,11 +374,11 @@ attention_kernel(const __grid_constant__ AttnParams p) {
     constexpr int STAGES = P::STAGES, RUN = P::RUN, TILE = L::kTile;
     static_assert(CH <= 64 && RUN % 8 == 0, "a lane copies one or two pieces of a row");
     extern __shared__ __align__(128) char smem[];
-    float* const so = reinterpret_cast<float*>(smem + L::kRing);     // [kWarps][kRound or part heads][pitch]
+    float* so = reinterpret_cast<float*>(smem + L::kRing);           // [kWarps][kRound or part heads][pitch]
     __shared__ int turn;
-    __shared__ float sm[kWarps][kRound], ss[kWarps][kRound];
     const int pitch = L::pitch(p.c.dim);
-    const int gap = min(p.part, kRound) * pitch;      // between the warps' outputs
+    const int gap = min(p.part, kRound) * pitch;         // between the warps' dumps
+    int other = p.dumps == 2 ? kWarps * gap : 0;         // from this dump's place to the next one's
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int dim = p.c.dim, hp = p.c.heads * p.parts;
     char* const ring = smem + warp * L::kWarp;
@@ -369,6 +404,7 @@ attention_kernel(const __grid_constant__ AttnParams p) {
     constexpr int RPS = CH < 32 ? 32 / CH : 1;
     const int r0 = CH < 32 ? lane / CH : 0, c0 = CH < 32 ? lane % CH : lane;
     const long long to_v = p.c.v - p.c.k;                // bytes from K to V
+    const long long lane_at = (r0 * p.c.token_stride + c0 * V) * static_cast<int>(sizeof(T));
     const long long row_step = p.c.token_stride * RPS * static_cast<int>(sizeof(T));
 
     // The run of number j: its first position and visible rows.
@@ -396,13 +432,26 @@ attention_kernel(const __grid_constant__ AttnParams p) {
         if (w.hi <= 0) return;                           // past the end
         const int head = p.parts == 1 ? w.hg : w.hg / p.parts;
         const bool ok = w.page >= 0 && w.page < p.c.pages;
-        const char* const from = p.c.k + (p.layer * p.c.layer_stride + head * p.c.head_stride +
+        const char* const from = p.c.k + (head * p.c.head_stride +
                                           (ok ? w.page * p.c.page_stride + w.row * p.c.token_stride : 0)) *
                                              static_cast<int>(sizeof(T));
         const unsigned stage = ring_at + slot * L::kStage;
-        if (p.page_runs) {
+        if (CH <= 32 && p.whole_runs && ok && w.lo == 0 && w.hi == RUN && w.fresh < 0) {
+            // The usual run: all rows, in one page, every piece.
+            const char* ks = from + lane_at;
+            const char* vs = ks + to_v;
+            const unsigned dst = stage + r0 * L::kRow;
+#pragma unroll
+            for (int x = 0; x < RUN / RPS; ++x) {
+                const unsigned to = dst + x * RPS * L::kRow + (((c0 ^ r0) << 4) ^ (x * RPS & 7) << 4);
+                copy_async(to, ks, 16);
+                copy_async(to + L::kHalf, vs, 16);
+                ks += row_step;
+                vs += row_step;
+            }
+        } else if (p.page_runs) {
             if (!ok) flag(p.c.status, GS_DEV_BAD_SEQ);
-            const char* src = from + (r0 * p.c.token_stride + c0 * V) * static_cast<int>(sizeof(T));
+            const char* src = from + lane_at;
             const unsigned dst = stage + r0 * L::kRow;
 #pragma unroll
             for (int x = 0; x < RUN / RPS; ++x) {
@@ -479,16 +528,25 @@ attention_kernel(const __grid_constant__ AttnParams p) {
     put_empty_rows<T>(p);
     int slot = 0;
     P work;
-    bool fresh = true;
+    bool fresh = true, fetched = false;
     while (cur.unit() < end) {
         const int head = p.parts == 1 ? cur.hg : cur.hg / p.parts;
         const int part = cur.hg - head * p.parts;
         const int first_head = head * p.group + part * p.part;
         const int heads = min(p.part, p.group - part * p.part);
         if (fresh) {
-            work.begin(static_cast<const T*>(p.q) + cur.b * p.q_batch + first_head * p.q_head,
-                       p.q_head, heads, dim, p.q_aligned != 0);
-            fresh = false;
+            const T* const q = static_cast<const T*>(p.q) + cur.b * p.q_batch;
+            if (!fetched) work.fetch(q + first_head * p.q_head, p.q_head, heads, dim, p.q_aligned != 0);
+            work.begin();
+            fresh = fetched = false;
+            // The next segment's query heads, where it belongs to the same row.
+            if (P::AHEAD && cur.hg + 1 < hp && cur.item() + cur.tiles + 1 < end) {
+                const int next_head = p.parts == 1 ? cur.hg + 1 : (cur.hg + 1) / p.parts;
+                const int next_part = cur.hg + 1 - next_head * p.parts;
+                work.fetch(q + (next_head * p.group + next_part * p.part) * p.q_head, p.q_head,
+                           min(p.part, p.group - next_part * p.part), dim, p.q_aligned != 0);
+                fetched = true;
+            }
         }
         copy_wait<STAGES - 2>();
         __syncwarp();
@@ -517,7 +575,7 @@ attention_kernel(const __grid_constant__ AttnParams p) {
 #pragma unroll
             for (int h0 = 0; h0 < P::HEADS; h0 += kRound) {
                 if (h0 >= heads) break;
-                work.dump(sm[warp], ss[warp], so + warp * gap, pitch, h0, heads, dim);
+                work.dump(so + warp * gap, pitch, h0, heads, dim);
                 __syncthreads();
                 for (int x = 4 * threadIdx.x; x < min(kRound, heads - h0) * dim; x += 4 * kThreads) {
                     const int h = static_cast<int>(x * p.dim_mul >> 20);
@@ -525,9 +583,11 @@ attention_kernel(const __grid_constant__ AttnParams p) {
                     float4 o[kWarps], acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
                     for (int w = 0; w < kWarps; ++w) {
-                        m[w] = sm[w][h];
-                        s[w] = ss[w][h];
-                        o[w] = *reinterpret_cast<const float4*>(so + w * gap + h * pitch + (x - h * dim));
+                        const float* from = so + w * gap + h * pitch;
+                        const float2 f = *reinterpret_cast<const float2*>(from + dim);
+                        m[w] = f.x;
+                        s[w] = f.y;
+                        o[w] = *reinterpret_cast<const float4*>(from + (x - h * dim));
                     }
                     join_parts(m, s, o, &top, &sum, &acc);
                     if (whole) {
@@ -541,7 +601,11 @@ attention_kernel(const __grid_constant__ AttnParams p) {
                         }
                     }
                 }
-                __syncthreads();                         // before the next dump
+                // The next dump overwrites this one, or (two places) the one before it, which every
+                // thread was done with before the barrier above.
+                if (other == 0) __syncthreads();
+                so += other;
+                other = -other;
             }
             if (!whole) {
                 const int lo = split.block_of(a);
@@ -596,10 +660,17 @@ attention_kernel(const __grid_constant__ AttnParams p) {
 
 template <class P>
 gs_status launch_policy(const AttnParams& p, int blocks, gs_stream stream) {
-    const int smem = Layout<P>::smem(p.part, p.c.dim);
+    // Two places for a segment's end where the block then still shares an SM as the ring wants it
+    // (228 KB an SM, 1 KB a block for the system).
+    const int dump = Layout<P>::dump(p.part, p.c.dim);
+    const int most = Layout<P>::kRing <= 96 * 1024 ? 113 * 1024 - 64 : 227 * 1024 - 64;
+    AttnParams a = p;
+    a.dumps = Layout<P>::kRing + 2 * dump <= most ? 2 : 1;
+    a.whole_runs = p.page_runs && p.c.dim == P::DP;
+    const int smem = Layout<P>::kRing + a.dumps * dump;
     if (!allow_smem<attention_kernel<P>>(smem)) return GS_ERR_CUDA;
     return launch(attention_kernel<P>, dim3(static_cast<unsigned>(blocks)), kThreads, smem, 1,
-                  stream, p);
+                  stream, a);
 }
 
 // How a policy's kernel serves a head dimension: positions of a tile, most query heads of a

@@ -10,8 +10,8 @@
 //
 // The weights 2^(s - m) enter the second product as two 16-bit numbers, hi + lo: with hi alone
 // the rounding of the weights would add as much error as the rounding of the output.  The sum
-// of the weights is taken before they are rounded.  For fp16 the weights are scaled by 2^12
-// (the reference of the softmax is m - 12), so that small ones stay clear of fp16's subnormals.
+// of the weights is taken before they are rounded.  For fp16 the weights are scaled by 2^11
+// (the reference of the softmax is m - 11), so that small ones stay clear of fp16's subnormals.
 #include "paged_attention.cuh"
 
 namespace gs_decode {
@@ -78,34 +78,61 @@ struct Mma {
     static constexpr int DP = DIM, RUN = 16, STAGES = DIM == 64 ? 6 : 3, HEADS = 8 * NH;
     static_assert(kRound == 8, "a dump is one column of heads");
     static constexpr int KS = DP / 16;                   // steps over dim
-    static constexpr float kShift = std::is_same<T, __half>::value ? 12.0f : 0.0f;
+    static constexpr float kShift = std::is_same<T, __half>::value ? 11.0f : 0.0f;
+    static constexpr float kSlack = std::is_same<T, __half>::value ? 4.0f : 8.0f;    // 2^(11 + 4) fits fp16
     unsigned q[NH][KS][2];                               // head g (+ 8), dims 2t, 2t+1; 2t+8, 2t+9
     float o[NH][KS][4];                                  // dims g (0, 1), g+8 (2, 3), heads 2t, 2t+1
     float top[NH][2], sum[NH][2];                        // heads 2t, 2t+1
+    bool empty;                                          // no run yet: o and sum are 0
 
-    __device__ __forceinline__ void begin(const T* query, long long head_stride, int heads, int dim,
+    // The next segment's query heads wait in registers where there is room for them.
+    static constexpr bool AHEAD = NH == 1 && DP <= 128;
+    unsigned next[AHEAD ? KS : 1][2];
+
+    __device__ __forceinline__ void fetch(const T* query, long long head_stride, int heads, int dim,
                                           bool aligned) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        const bool usual = aligned && dim == DP;
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-            const T* qp = query + (h * 8 + g) * head_stride;
+            const unsigned short* const qp =
+                reinterpret_cast<const unsigned short*>(query + (h * 8 + g) * head_stride + 2 * t);
+            const bool here = h * 8 + g < heads;
+            if (usual) {
+#pragma unroll
+                for (int s = 0; s < KS; ++s)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)
+                        keep(h, s, half, here ? *reinterpret_cast<const unsigned*>(qp + s * 16 + half * 8) : 0u);
+            } else {
+#pragma unroll
+                for (int s = 0; s < KS; ++s)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int d = s * 16 + half * 8;
+                        const bool in = here && d < dim;
+                        const unsigned low = in ? qp[d] : 0u, high = in ? qp[d + 1] : 0u;
+                        keep(h, s, half, low | high << 16);
+                    }
+            }
+        }
+    }
+    __device__ __forceinline__ void keep(int h, int s, int half, unsigned two) {
+        if constexpr (AHEAD) next[s][half] = two;
+        else q[h][s][half] = two;
+    }
+
+    __device__ __forceinline__ void begin() {
+        empty = true;
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
             top[h][0] = top[h][1] = kNegInf;
             sum[h][0] = sum[h][1] = 0.0f;
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int d = s * 16 + half * 8 + 2 * t;
-                    unsigned two = 0u;
-                    if (h * 8 + g < heads && d < dim) {
-                        if (aligned) {
-                            two = *reinterpret_cast<const unsigned*>(qp + d);
-                        } else {
-                            const unsigned short* at = reinterpret_cast<const unsigned short*>(qp + d);
-                            two = at[0] | static_cast<unsigned>(at[1]) << 16;
-                        }
-                    }
-                    q[h][s][half] = two;
+                if constexpr (AHEAD) {
+                    q[h][s][0] = next[s][0];
+                    q[h][s][1] = next[s][1];
                 }
                 o[h][s][0] = o[h][s][1] = o[h][s][2] = o[h][s][3] = 0.0f;
             }
@@ -114,52 +141,60 @@ struct Mma {
 
     __device__ __forceinline__ void step(const char* stage, int lo, int hi, float scale) {
         const int lane = threadIdx.x & 31, g = lane >> 2;
-        float s[NH][4];                                  // positions g (0, 1), g+8 (2, 3)
+        float s[NH][4], odd[NH][4];                      // positions g (0, 1), g+8 (2, 3)
 #pragma unroll
-        for (int h = 0; h < NH; ++h) s[h][0] = s[h][1] = s[h][2] = s[h][3] = 0.0f;
+        for (int h = 0; h < NH; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[h][e] = odd[h][e] = 0.0f;
         {
             const int r = lane & 15;
             const unsigned row = smem_addr(stage) + r * DP * 2;
 #pragma unroll
-            for (int x = 0; x < KS; ++x) {
-                unsigned a[4];
+            for (int x = 0; x < KS; x += 2) {            // two sums, for shorter chains
+                unsigned a[4], b[4];
                 load_matrix(row + (((2 * x + (lane >> 4)) ^ (r & 7)) << 4), a);
+                load_matrix(row + (((2 * x + 2 + (lane >> 4)) ^ (r & 7)) << 4), b);
 #pragma unroll
-                for (int h = 0; h < NH; ++h) mma<T>(s[h], a, q[h][x][0], q[h][x][1]);
+                for (int h = 0; h < NH; ++h) {
+                    mma<T>(s[h], a, q[h][x][0], q[h][x][1]);
+                    mma<T>(odd[h], b, q[h][x + 1][0], q[h][x + 1][1]);
+                }
             }
         }
-        bool grew = false;
-        float up[NH][2];
+        // The reference `top` is the largest score so far, or up to 2^kSlack below it: it moves only
+        // when a score passes it by more, so that most runs need no maximum over the lanes.
+        bool over = false;
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[h][e] *= scale;
+            for (int e = 0; e < 4; ++e) s[h][e] = (s[h][e] + odd[h][e]) * scale;
             if (lo > 0 || hi < RUN) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     if (g + (e >> 1) * 8 < lo || g + (e >> 1) * 8 >= hi) s[h][e] = kNegInf;
             }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                up[h][e] = fmaxf(top[h][e], max_rows(fmaxf(s[h][e], s[h][e + 2])));
-                grew = grew || up[h][e] > top[h][e];
-            }
+            for (int e = 0; e < 4; ++e) over = over || s[h][e] > top[h][e & 1] + kSlack;
         }
-        if (__any_sync(0xffffffffu, grew)) {
+        if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
             for (int h = 0; h < NH; ++h)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float w = up[h][e] > top[h][e] ? pow2(top[h][e] - up[h][e]) : 1.0f;
-                    sum[h][e] *= w;
+                    const float up = fmaxf(top[h][e], max_rows(fmaxf(s[h][e], s[h][e + 2])));
+                    if (!empty) {
+                        const float w = up > top[h][e] ? pow2(top[h][e] - up) : 1.0f;
+                        sum[h][e] *= w;
 #pragma unroll
-                    for (int x = 0; x < KS; ++x) {
-                        o[h][x][e] *= w;
-                        o[h][x][e + 2] *= w;
+                        for (int x = 0; x < KS; ++x) {
+                            o[h][x][e] *= w;
+                            o[h][x][e + 2] *= w;
+                        }
                     }
-                    top[h][e] = up[h][e];
+                    top[h][e] = up;
                 }
         }
+        empty = false;
         unsigned wh[NH][2], wl[NH][2];
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
@@ -194,8 +229,7 @@ struct Mma {
         }
     }
 
-    __device__ __forceinline__ void dump(float* m, float* s, float* out, int pitch, int first,
-                                         int heads, int dim) {
+    __device__ __forceinline__ void dump(float* out, int pitch, int first, int heads, int dim) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
@@ -206,16 +240,18 @@ struct Mma {
                 const float all = sum_rows(sum[h][e]);
                 if (first + head >= heads) continue;
                 if (g == 0) {
-                    m[head] = top[h][e] - kShift;
-                    s[head] = all;
+                    out[head * pitch + dim] = top[h][e] - kShift;
+                    out[head * pitch + dim + 1] = all;
                 }
+                float* const to = out + head * pitch + g;
+                if (dim == DP) {
 #pragma unroll
-                for (int x = 0; x < KS; ++x)
+                    for (int x = 0; x < 2 * KS; ++x) to[x * 8] = o[h][x / 2][e + 2 * (x & 1)];
+                } else {
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int d = x * 16 + half * 8 + g;
-                        if (d < dim) out[head * pitch + d] = o[h][x][e + 2 * half];
-                    }
+                    for (int x = 0; x < 2 * KS; ++x)
+                        if (x * 8 < dim) to[x * 8] = o[h][x / 2][e + 2 * (x & 1)];
+                }
             }
         }
     }
