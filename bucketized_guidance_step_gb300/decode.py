@@ -95,24 +95,26 @@ def status_from_word(word: int) -> int:
 
 
 class Call:
-    """A checked call on fixed buffers: ``call()`` launches it on the current stream."""
+    """A checked call on fixed buffers: ``call()`` launches it on the current stream.
+
+    The call keeps its tensors and its workspace alive; keep the call until its work is done
+    where that runs on another stream than the tensors were made on, or in a captured graph.
+    Two calls in flight at once need a ``Call`` each (a workspace serves one at a time)."""
 
     def __init__(self, name: str, args, device, keep):
+        import torch
         self._name = name
         self._fn = getattr(load(), name)
         self._args = args                       # ctypes values, the stream excepted
         self._keep = keep                       # tensors and structs behind the pointers
         self._device = device.index
+        # The handle alone: torch.cuda.current_stream() builds a Stream object around it (1 us).
+        self._stream = torch._C._cuda_getCurrentRawStream
 
     def __call__(self) -> None:
-        status = self._fn(*self._args, _current_stream(self._device))
+        status = self._fn(*self._args, self._stream(self._device))
         if status != gs.GS_OK:
             raise GSError(self._name, status)
-
-
-def _current_stream(device: int) -> int:
-    import torch
-    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _ptr(t, name: str, device, dtype=None, shape=None, contiguous: bool = True) -> Optional[int]:
