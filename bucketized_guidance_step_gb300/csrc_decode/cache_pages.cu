@@ -32,19 +32,44 @@ inline long long copy_slots(const gs_kv_cache* c) {
 
 __device__ __forceinline__ int pages_of(int len, int page) { return (len + page - 1) / page; }
 
-// The free pages of this block's eighth, and what the whole cluster has: avail = all free
-// pages, before = those of the lower blocks.  Contains two cluster barriers; `mine` is read by
-// the other blocks until the second.
-__device__ __forceinline__ void count_free(const CacheView& c, int lo, int hi, int* mine, int* tmp,
+// Which pages of this block's eighth [lo, hi) are free.  A thread has every kMeta-th; it keeps the
+// first 32 of them, so that they are read once.
+struct Eighth {
+    int lo, hi;
+    unsigned kept;
+
+    __device__ __forceinline__ bool read(const CacheView& c, int p) const {
+        return p < hi && __ldcg(c.refs + p) == 0;
+    }
+    __device__ __forceinline__ int count(const CacheView& c) {
+        int n = 0;
+        kept = 0u;
+#pragma unroll 4
+        for (int k = 0; lo + k * kMeta < hi; ++k) {
+            const bool f = read(c, lo + k * kMeta + static_cast<int>(threadIdx.x));
+            if (k < 32 && f) kept |= 1u << k;
+            n += f ? 1 : 0;
+        }
+        return n;
+    }
+    // Page k of this thread (before anything of the eighth beyond the pages already asked about
+    // is handed out).
+    __device__ __forceinline__ bool free_at(const CacheView& c, int k) const {
+        return k < 32 ? (kept >> k & 1u) != 0u : read(c, lo + k * kMeta + static_cast<int>(threadIdx.x));
+    }
+};
+
+// Counts the free pages: avail = of the whole cluster, before = of the lower blocks.  Contains
+// two cluster barriers; `mine` is read by the other blocks until the second.
+__device__ __forceinline__ void count_free(const CacheView& c, Eighth* e, int* mine, int* tmp,
                                            int* avail, int* before) {
-    int n = 0;
-    for (int p = lo + static_cast<int>(threadIdx.x); p < hi; p += kMeta)
-        n += __ldcg(c.refs + p) == 0 ? 1 : 0;
+    const long long rank = cluster_rank();
+    e->lo = static_cast<int>(c.pages * rank / kCluster);
+    e->hi = static_cast<int>(c.pages * (rank + 1) / kCluster);
     int total;
-    block_scan<kMeta>(n, tmp, &total);
+    block_scan<kMeta>(e->count(c), tmp, &total);
     if (threadIdx.x == 0) *mine = total;
     cluster_sync();
-    const unsigned rank = cluster_rank();
     int a = 0, b = 0;
 #pragma unroll
     for (unsigned r = 0; r < kCluster; ++r) {
@@ -57,13 +82,6 @@ __device__ __forceinline__ void count_free(const CacheView& c, int lo, int hi, i
     cluster_sync();
 }
 
-// The eighth [lo, hi) of block `rank`.
-__device__ __forceinline__ void eighth(int n, int* lo, int* hi) {
-    const long long rank = cluster_rank();
-    *lo = static_cast<int>(n * rank / kCluster);
-    *hi = static_cast<int>(n * (rank + 1) / kCluster);
-}
-
 // The last i in [0, n) with at[i] <= r (at rises, at[0] = 0).
 __device__ __forceinline__ int owner_of(const int* at, int n, int r) {
     int lo = 0, hi = n;
@@ -74,15 +92,16 @@ __device__ __forceinline__ int owner_of(const int* at, int n, int r) {
     return lo;
 }
 
-// at[i] = the sum of need[0 .. i), held at `cap` at most; returns the sum of all, held likewise.
-__device__ __forceinline__ int prefix_of(const int* need, int* at, int n, int cap,
-                                         long long* tmp) {
+// at[i] = the sum of need(0) .. need(i - 1), held at `cap` at most; returns the sum of all, held
+// likewise.  Ends with a barrier.
+template <class F>
+__device__ __forceinline__ int prefix_of(F need, int* at, int n, int cap, long long* tmp) {
     long long carry = 0;
     for (int i0 = 0; i0 < n; i0 += kMeta) {
         const int i = i0 + static_cast<int>(threadIdx.x);
         long long total;
         const long long ex =
-            carry + block_scan<kMeta>(i < n ? static_cast<long long>(need[i]) : 0ll, tmp, &total);
+            carry + block_scan<kMeta>(i < n ? static_cast<long long>(need(i)) : 0ll, tmp, &total);
         if (i < n) at[i] = static_cast<int>(ex < cap ? ex : cap);
         carry += total;
     }
@@ -90,12 +109,14 @@ __device__ __forceinline__ int prefix_of(const int* need, int* at, int n, int ca
     return static_cast<int>(carry < cap ? carry : cap);
 }
 
-// First entry of the list that names each sequence (kNone: none).  Ends with a barrier.
-__device__ __forceinline__ void mark_first(int* mark, int seqs, const int* list, int n) {
+// Takes the list into shared memory and finds the first entry that names each sequence (kNone:
+// none).  Ends with a barrier.
+__device__ __forceinline__ void mark_first(int* mark, int seqs, const int* list, int* kept, int n) {
     for (int s = threadIdx.x; s < seqs; s += kMeta) mark[s] = kNone;
     __syncthreads();
     for (int i = threadIdx.x; i < n; i += kMeta) {
         const int s = list[i];
+        kept[i] = s;
         if (s >= 0 && s < seqs) atomicMin(mark + s, i);
     }
     __syncthreads();
@@ -108,15 +129,16 @@ extend_kernel(CacheView c, const int* __restrict__ seq, const int* __restrict__ 
     int* need = mark + c.seqs;           // [n] pages wanted
     int* held = need + n;                // [n] pages held, -1: not to be served
     int* at = held + n;                  // [n] pages wanted by the entries before
+    int* ids = at + n;                   // [n] seq
     __shared__ long long tmp64[kMeta / 32 + 1];
     __shared__ int tmp[kMeta / 32 + 1];
     __shared__ int mine;
     grid_wait();
     grid_trigger();
-    mark_first(mark, c.seqs, seq, n);
+    mark_first(mark, c.seqs, seq, ids, n);
     const bool first_block = cluster_rank() == 0;
     for (int i = threadIdx.x; i < n; i += kMeta) {
-        const int s = seq[i];
+        const int s = ids[i];
         const int more = add != nullptr ? add[i] : 1;
         int want = 0, have = -1;
         if (s >= 0 && s < c.seqs && mark[s] == i && more >= 0) {
@@ -137,23 +159,23 @@ extend_kernel(CacheView c, const int* __restrict__ seq, const int* __restrict__ 
         held[i] = have;
     }
     __syncthreads();
-    const int total = prefix_of(need, at, n, c.pages + 1, tmp64);
+    const int total = prefix_of([&](int i) { return need[i]; }, at, n, c.pages + 1, tmp64);
     int avail = 0;
     if (total > 0) {
-        int lo, hi, rank;
-        eighth(c.pages, &lo, &hi);
-        count_free(c, lo, hi, &mine, tmp, &avail, &rank);
+        int rank;
+        Eighth e;
+        count_free(c, &e, &mine, tmp, &avail, &rank);
         const int end = total < avail ? total : avail;
-        for (int p0 = lo; p0 < hi && rank < end; p0 += kMeta) {
-            const int p = p0 + static_cast<int>(threadIdx.x);
-            const int is_free = p < hi && __ldcg(c.refs + p) == 0 ? 1 : 0;
+        for (int k = 0; e.lo + k * kMeta < e.hi && rank < end; ++k) {
+            const int p = e.lo + k * kMeta + static_cast<int>(threadIdx.x);
+            const int is_free = e.free_at(c, k) ? 1 : 0;
             int found;
             const int r = rank + block_scan<kMeta>(is_free, tmp, &found);
             rank += found;
             if (is_free && r < end) {
                 const int i = owner_of(at, n, r);
                 if (at[i] + need[i] <= avail) {
-                    c.table[static_cast<long long>(seq[i]) * c.cols + held[i] + (r - at[i])] = p;
+                    c.table[static_cast<long long>(ids[i]) * c.cols + held[i] + (r - at[i])] = p;
                     c.refs[p] = 1;
                 }
             }
@@ -164,7 +186,7 @@ extend_kernel(CacheView c, const int* __restrict__ seq, const int* __restrict__ 
     for (int i = cluster_rank() * kMeta + threadIdx.x; i < n; i += kCluster * kMeta) {
         if (held[i] < 0) continue;
         if (need[i] == 0 || at[i] + need[i] <= avail)
-            c.lens[seq[i]] += add != nullptr ? add[i] : 1;
+            c.lens[ids[i]] += add != nullptr ? add[i] : 1;
         else
             flag(c.status, GS_DEV_NO_PAGE);
     }
@@ -175,29 +197,34 @@ fork_kernel(CacheView c, const int* __restrict__ src, const int* __restrict__ ds
     extern __shared__ int smem[];
     int* mark = smem;                    // [seqs]
     int* from = mark + c.seqs;           // [n] length of src, -1: pair refused
-    int* need = from + n;                // [n] 1: src's last page is partly filled
-    int* at = need + n;                  // [n]
+    int* old = from + n;                 // [n] length of dst
+    int* at = old + n;                   // [n] pairs before that need a page
+    int* srcs = at + n;                  // [n]
+    int* dsts = srcs + n;                // [n]
     __shared__ long long tmp64[kMeta / 32 + 1];
     __shared__ int tmp[kMeta / 32 + 1];
     __shared__ int mine;
     grid_wait();
     grid_trigger();
-    mark_first(mark, c.seqs, dst, n);
+    mark_first(mark, c.seqs, dst, dsts, n);
     const bool first_block = cluster_rank() == 0;
     const int most = c.cols * c.page;
     for (int i = threadIdx.x; i < n; i += kMeta) {
-        const int s = src[i], d = dst[i];
-        int len = -1;
+        const int s = src[i], d = dsts[i];
+        int len = -1, was = 0;
         if (s >= 0 && s < c.seqs && d >= 0 && d < c.seqs && mark[d] == i && mark[s] == kNone) {
             len = __ldcg(c.lens + s);
-            const int old = __ldcg(c.lens + d);
-            if (len < 0 || len > most || old < 0 || old > most) len = -1;
+            was = __ldcg(c.lens + d);
+            if (len < 0 || len > most || was < 0 || was > most) len = -1;
         }
         if (len < 0 && first_block) flag(c.status, GS_DEV_BAD_SEQ);
         from[i] = len;
-        need[i] = len > 0 && len % c.page != 0 ? 1 : 0;
+        old[i] = was;
+        srcs[i] = s;
     }
     __syncthreads();
+    // A pair needs a page where src's last page is partly filled.
+    auto need = [&](int i) { return from[i] > 0 && from[i] % c.page != 0 ? 1 : 0; };
     const int total = prefix_of(need, at, n, c.pages + 1, tmp64);
     // Release what the destinations hold, share the sources' full pages.
     const int self = cluster_rank() * kMeta + threadIdx.x;
@@ -205,41 +232,44 @@ fork_kernel(CacheView c, const int* __restrict__ src, const int* __restrict__ ds
     for (long long q = self; q < cells; q += kCluster * kMeta) {
         const int i = static_cast<int>(q / c.cols), j = static_cast<int>(q % c.cols);
         if (from[i] < 0) continue;
-        if (j < pages_of(__ldcg(c.lens + dst[i]), c.page)) {
-            const int p = __ldcg(c.table + static_cast<long long>(dst[i]) * c.cols + j);
+        const bool release = j < pages_of(old[i], c.page), share = j < from[i] / c.page;
+        int p = 0, r = 0;
+        if (release) p = __ldcg(c.table + static_cast<long long>(dsts[i]) * c.cols + j);
+        if (share) r = __ldcg(c.table + static_cast<long long>(srcs[i]) * c.cols + j);
+        if (release) {
             if (p >= 0 && p < c.pages) atomicSub(c.refs + p, 1);
             else flag(c.status, GS_DEV_BAD_SEQ);
         }
-        if (j < from[i] / c.page) {
-            const int p = __ldcg(c.table + static_cast<long long>(src[i]) * c.cols + j);
-            if (p >= 0 && p < c.pages) atomicAdd(c.refs + p, 1);
+        if (share) {
+            if (r >= 0 && r < c.pages) atomicAdd(c.refs + r, 1);
             else flag(c.status, GS_DEV_BAD_SEQ);
         }
     }
     cluster_sync();
     int avail = 0;
     if (total > 0) {
-        int lo, hi, rank;
-        eighth(c.pages, &lo, &hi);
-        count_free(c, lo, hi, &mine, tmp, &avail, &rank);
+        int rank;
+        Eighth e;
+        count_free(c, &e, &mine, tmp, &avail, &rank);
         const int end = total < avail ? total : avail;
-        for (int p0 = lo; p0 < hi && rank < end; p0 += kMeta) {
-            const int p = p0 + static_cast<int>(threadIdx.x);
-            const int is_free = p < hi && __ldcg(c.refs + p) == 0 ? 1 : 0;
+        for (int k = 0; e.lo + k * kMeta < e.hi && rank < end; ++k) {
+            const int p = e.lo + k * kMeta + static_cast<int>(threadIdx.x);
+            const int is_free = e.free_at(c, k) ? 1 : 0;
             int found;
             const int r = rank + block_scan<kMeta>(is_free, tmp, &found);
             rank += found;
             if (is_free && r < end) {
                 const int i = owner_of(at, n, r);
                 const int col = from[i] / c.page;
-                const int last = __ldcg(c.table + static_cast<long long>(src[i]) * c.cols + col);
+                const int last = __ldcg(c.table + static_cast<long long>(srcs[i]) * c.cols + col);
                 Copy w;
                 w.from = last;
                 w.to = p;
                 w.tokens = last >= 0 && last < c.pages ? from[i] % c.page : 0;
+                if (w.tokens == 0) flag(c.status, GS_DEV_BAD_SEQ);
                 w.pad = 0;
                 copies_of(c.work)[r] = w;
-                c.table[static_cast<long long>(dst[i]) * c.cols + col] = p;
+                c.table[static_cast<long long>(dsts[i]) * c.cols + col] = p;
                 c.refs[p] = 1;
             }
         }
@@ -249,20 +279,20 @@ fork_kernel(CacheView c, const int* __restrict__ src, const int* __restrict__ ds
         const int i = static_cast<int>(q / c.cols), j = static_cast<int>(q % c.cols);
         if (from[i] < 0) continue;
         const int full = from[i] / c.page;
-        const bool served = need[i] == 0 || at[i] < avail;
+        const bool served = need(i) == 0 || at[i] < avail;
         if (j == 0) {
-            c.lens[dst[i]] = served ? from[i] : 0;
+            c.lens[dsts[i]] = served ? from[i] : 0;
             if (!served) flag(c.status, GS_DEV_NO_PAGE);
         }
-        int* to = c.table + static_cast<long long>(dst[i]) * c.cols + j;
+        int* to = c.table + static_cast<long long>(dsts[i]) * c.cols + j;
         int p = -1;
         if (j < full) {
-            p = __ldcg(c.table + static_cast<long long>(src[i]) * c.cols + j);
+            p = __ldcg(c.table + static_cast<long long>(srcs[i]) * c.cols + j);
             if (!served) {
                 if (p >= 0 && p < c.pages) atomicSub(c.refs + p, 1);
                 p = -1;
             }
-        } else if (j == full && need[i] != 0 && served) {
+        } else if (j == full && need(i) != 0 && served) {
             continue;                    // the page taken above
         }
         *to = p;
@@ -308,9 +338,10 @@ compact_kernel(CacheView c, int* __restrict__ refs_out, int* __restrict__ live_o
     __shared__ int mine;
     grid_wait();
     grid_trigger();
-    int lo, hi, avail, before;
-    eighth(c.pages, &lo, &hi);
-    count_free(c, lo, hi, &mine, tmp, &avail, &before);
+    int avail, before;
+    Eighth e;
+    count_free(c, &e, &mine, tmp, &avail, &before);
+    const int lo = e.lo, hi = e.hi;
     const int live = c.pages - avail;
     Copy* copies = copies_of(c.work);
     int* rank_of = c.work + 4 + 4 * static_cast<long long>(c.pages > c.seqs ? c.pages : c.seqs);
@@ -543,7 +574,7 @@ extern "C" gs_status gs_pages_extend(const gs_kv_cache* cache, const int32_t* se
     if (st != GS_OK) return st;
     if (n == 0) return GS_OK;
     if (seq == nullptr) return GS_ERR_INVALID_ARG;
-    const int smem = 4 * (c.seqs + 3 * n);
+    const int smem = 4 * (c.seqs + 4 * n);
     if (!allow_smem<extend_kernel>(smem)) return GS_ERR_CUDA;
     return launch(extend_kernel, dim3(kCluster), kMeta, smem, kCluster, stream, c, seq, add, n);
 }
@@ -557,7 +588,7 @@ extern "C" gs_status gs_pages_fork(const gs_kv_cache* cache, const int32_t* src,
     if (src == nullptr || dst == nullptr) return GS_ERR_INVALID_ARG;
     st = check_workspace(cache);
     if (st != GS_OK) return st;
-    const int smem = 4 * (c.seqs + 3 * n);
+    const int smem = 4 * (c.seqs + 5 * n);
     if (!allow_smem<fork_kernel>(smem)) return GS_ERR_CUDA;
     st = launch(fork_kernel, dim3(kCluster), kMeta, smem, kCluster, stream, c, src, dst, n);
     if (st != GS_OK) return st;
