@@ -496,7 +496,7 @@ write_kernel(CacheView c, int layer, const T* __restrict__ k, const T* __restric
     if (ok) {
         const int len = c.lens[s];
         pos = static_cast<long long>(len) - (first[lo + 1] - t);
-        ok = pos >= 0 && len <= c.cols * c.page;
+        ok = pos >= 0 && pos < len && len <= c.cols * c.page;
     }
     int p = -1;
     if (ok) {

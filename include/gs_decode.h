@@ -161,8 +161,10 @@ typedef struct gs_paged_attention_args {
     int64_t out_batch_stride, out_head_stride;
     float*  lse;                /* device float[batch][q_heads] or NULL                   */
     void*   workspace;          /* device, gs_paged_attention_workspace bytes, 16-byte
-                                   aligned, all 0 before its first use; the call leaves
-                                   what the next one needs                                */
+                                   aligned, all 0 before its first use; a call leaves it
+                                   ready for calls of the same sizes (batch, heads, dim,
+                                   dtype, cols, page, window, sinks) - zero it again
+                                   before one of others                                   */
     int64_t workspace_bytes;
 } gs_paged_attention_args;
 
@@ -173,7 +175,7 @@ gs_status gs_paged_attention_workspace(const gs_paged_attention_args* args, int6
  * (0 <= j < lens; with a window: j < sinks or j >= lens - window):
  *   s_j = scale * q . k_j,  m = max_j s_j,  out = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m),
  *   lse = m + ln sum_j e^(s_j - m).
- * Sums, maxima and the output's accumulator are fp32; in the tensor-core kernel the weights
+ * Sums, maxima and the output's accumulator are fp32; for 16-bit caches the weights
  * e^(s_j - m) enter the product with V as a sum of two 16-bit numbers.  A row of length 0
  * gives out = 0 and lse = -inf.  Rows of a page past the sequence's length are never used,
  * whatever they hold.  Results do not depend on the grid's timing: the parts of a split
@@ -182,7 +184,8 @@ gs_status gs_paged_attention_workspace(const gs_paged_attention_args* args, int6
  * outside the pool: its rows read as zeros; a length past the table: cut).
  * Errors: as the page calls', and GS_ERR_INVALID_ARG for q_heads not a multiple of kv_heads,
  * layer outside the cache, k_new without v_new, window or sinks < 0, sinks without window,
- * a scale that is not finite.
+ * a scale that is not finite; GS_ERR_UNSUPPORTED also where batch * q_heads * cols * page / 32
+ * passes 2^31.
  */
 gs_status gs_paged_attention(const gs_paged_attention_args* args, gs_stream stream);
 
@@ -227,7 +230,9 @@ typedef struct gs_guided_logits_args {
     float*   logprob;           /* device float[batch] or NULL: z[token] - ln sum e^z     */
     uint32_t* dev_status;
     void*    workspace;         /* device, gs_guided_logits_workspace bytes, 16-byte
-                                   aligned, all 0 before its first use                    */
+                                   aligned, all 0 before its first use; a call leaves it
+                                   ready for calls of the same batch, vocab, dtype and
+                                   streams given - zero it again before one of others     */
     int64_t  workspace_bytes;
 } gs_guided_logits_args;
 
@@ -251,7 +256,8 @@ gs_status gs_guided_logits_workspace(const gs_guided_logits_args* args, int64_t*
  * missing uncond (scale not 1: GS_DEV_NEED_UNCOND) is not written, but for its token (-1).
  * Errors: GS_ERR_INVALID_ARG (NULL cond, sizes, strides, unknown dtype, tokens without
  * tokens_len, no output at all, workspace too small, step outside the table),
- * GS_ERR_UNSUPPORTED (batch over GS_MAX_SEQS), GS_ERR_CUDA.
+ * GS_ERR_UNSUPPORTED (batch over GS_MAX_SEQS, vocab over 2^28), GS_ERR_CUDA.  No output may
+ * overlap an input or another output.
  */
 gs_status gs_guided_logits(const gs_guided_logits_args* args, gs_stream stream);
 

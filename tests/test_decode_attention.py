@@ -268,3 +268,29 @@ def test_offsets_past_32_bits():
     cache = decode.PagedCache(k, k, table, torch.tensor([150], dtype=torch.int32).cuda(), refs)
     q = queries(cache, 1, 4)
     check(cache, 0, q, *run(cache, q, layer=0))
+
+
+@pytest.mark.parametrize("dtype,window", [(BF16, 0), (F32, 0), (F16, 40)])
+def test_many_rows(dtype, window):
+    """More rows than a warp's first look at the lengths takes, a third of them empty."""
+    g = torch.Generator().manual_seed(11)
+    lens = torch.randint(-60, 130, (1100,), generator=g).clamp(min=0).tolist()
+    cache = build(lens, dtype=dtype, dim=32, heads=1, page=8, seed=12, layers=1)
+    q = queries(cache, 1100, 3)
+    check(cache, 0, q, *run(cache, q, layer=0, window=window), window=window)
+    order = torch.randperm(1100, generator=g)
+    check(cache, 0, q, *run(cache, q, layer=0, window=window, seq=order.int().cuda()), rows=order.tolist(), window=window)
+
+
+def test_calls_on_one_workspace_leave_it_ready():
+    """The same prepared call again and again, lengths changing between: counts of arrived parts
+    start from zero each time."""
+    cache = build([3000, 10, 700, 0], dtype=BF16, dim=64, page=32, seed=3)
+    q = queries(cache, 4, 8)
+    out, lse = torch.empty_like(q), torch.empty((4, 16), device="cuda")
+    call = cache.prepare_attention(q, 1, out=out, lse=lse)
+    for lens in ([3000, 10, 700, 0], [1, 0, 0, 0], [2999, 1, 64, 0], [65, 9, 640, 0], [3000, 10, 700, 0]):
+        cache.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        for _ in range(3):
+            call()
+        check(cache, 1, q, out, lse)

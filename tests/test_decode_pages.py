@@ -170,3 +170,33 @@ def test_refusals_of_the_binding():
         decode.PagedCache(b.k[:, :1].expand(-1, 40, -1, -1, -1), b.v, b.table, b.lens, b.refs)
     with pytest.raises(decode.GSError):
         decode.PagedCache(*(x[..., :4].contiguous() for x in (b.k, b.v)), b.table, b.lens, b.refs)
+
+
+def test_a_pool_of_many_pages():
+    """More pages than the bookkeeping keeps in registers (8 blocks x 512 threads x 32)."""
+    pages = 150000
+    b = Both(pages=pages, page=1, dim=8, heads=1, layers=1, seqs=5, cols=70000)
+    b.extend([0, 1], [60000, 65000])
+    b.check()
+    b.fork([0, 1], [2, 3])                         # all pages full: shared only
+    b.free([0])
+    b.extend([4], [24999])
+    b.check()
+    b.extend([0], [2])                             # one page is left
+    b.check()
+    assert b.pool.no_page
+    b.free([1, 3])
+    b.cache.compact()
+    b.pool.compact()
+    b.check()
+
+
+def test_write_of_ranges_that_do_not_rise_stays_in_its_sequence():
+    b = Both(dtype=F32, dim=16)
+    b.extend([0, 1], [9, 3])
+    k = torch.randn((12, 3, 16)).cuda()
+    before = b.k.clone()
+    b.cache.write(0, k, k, b.dev([0, 1]), b.dev([0, 12, 4]))
+    torch.cuda.synchronize()
+    changed = (b.k != before).any(dim=4).any(dim=2)[0].nonzero()[:, 0]
+    assert set(changed.tolist()) <= set(b.table[0, :2].tolist()) and int(b.status) == decode.GS_DEV_BAD_SEQ
