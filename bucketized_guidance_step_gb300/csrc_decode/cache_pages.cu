@@ -545,7 +545,7 @@ template <bool REMAP>
 gs_status launch_copies(const CacheView& c, int dtype, long long most, int* table_out,
                         gs_stream stream) {
     long long blocks = (most * 2 * c.layers * c.heads + kCopy / 32 - 1) / (kCopy / 32);
-    const long long full = static_cast<long long>(sm_count()) * 8;
+    const long long full = static_cast<long long>(sm_count()) * 32;
     if (blocks > full) blocks = full;
     const dim3 grid(static_cast<unsigned>(blocks));
     const int es = static_cast<int>(elem_size(dtype));
