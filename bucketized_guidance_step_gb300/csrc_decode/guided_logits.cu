@@ -307,9 +307,16 @@ logits_kernel(const __grid_constant__ LogitParams p) {
                 const int t = i * kLogitThreads + static_cast<int>(threadIdx.x);
                 if (t < known && held[i] >= low && held[i] < end) f(t, held[i] - origin);
             }
-            for (int t = HELD * kLogitThreads + threadIdx.x; t < known; t += kLogitThreads) {
-                const int v = __ldg(tokens + t);
-                if (v >= low && v < end) f(t, v - origin);
+            for (int t0 = HELD * kLogitThreads + threadIdx.x; t0 < known; t0 += HELD * kLogitThreads) {
+                int v[HELD];
+#pragma unroll
+                for (int i = 0; i < HELD; ++i) {
+                    const int t = t0 + i * kLogitThreads;
+                    v[i] = t < known ? __ldg(tokens + t) : -1;
+                }
+#pragma unroll
+                for (int i = 0; i < HELD; ++i)
+                    if (v[i] >= low && v[i] < end) f(t0 + i * kLogitThreads, v[i] - origin);
             }
         };
         bool any = false;
@@ -538,14 +545,13 @@ gs_status cut_of(const gs_guided_logits_args* a, Cut* cut) {
     cut->stage = stage;
     const long long history = a->tokens != nullptr ? a->tokens_stride : 0;
     // As many chunks of a row as make the call's blocks resident at once; chunks are whole pieces
-    // of a warp, and of a block at least.  kMaxChunk bounds the counts a block may hold.
+    // of a warp, and of a block at least.  kMaxChunk bounds the counts a block may hold (64 KB).
     const long long slots = static_cast<long long>(kPerSm) * sm_count();
     long long chunks = a->batch > 0 ? slots / a->batch : 1;
     if (chunks < 1) chunks = 1;
     long long chunk = (a->vocab + 3 + chunks - 1) / chunks;
     if (chunk < kStride) chunk = kStride;
     if (chunk > kMaxChunk) chunk = kMaxChunk;
-    if (history > 4096 && chunk > 4096) chunk = 4096;
     chunk = (chunk + kPiece - 1) / kPiece * kPiece;
     cut->chunk = static_cast<int>(chunk);
     cut->chunks = static_cast<int>((a->vocab + 3 + chunk - 1) / chunk);      // (a row may begin 3 early)
