@@ -5,6 +5,11 @@
 // powers of two, and o += 2^(s - m) v, all in fp32.  Eight lanes hold a row (a 16-byte piece
 // every eighth), so a warp works on four positions at a time; each group of eight lanes keeps
 // a maximum, sum and output of its own, and they meet at the segment's end.
+//
+// What bounds it: 16 rows of 4096 tokens with 32 query and 8 kv heads of dim 128 (537 MB) take
+// 94 us, 84 % of the measured copy rate; 8 rows of 333 .. 3001 with 8 and 4 heads of 96 (45 MB)
+// 18.9 us, 35 %: the call's fixed part, and five or six tiles a block in a row, whose multiply-adds
+// two warps a scheduler do not hide.
 #include <cmath>
 
 #include "paged_attention.cuh"
@@ -150,7 +155,8 @@ Serves fp32_serves(int dim) {
     return {Layout<Fp32<8, 2>>::kTile, 2, 1};
 }
 
-// Parts of one or two heads have instances of their own: an instance computes for all its heads.
+// Parts of one or two heads have instances of their own: an instance computes for all its heads
+// (8 rows of 333 .. 3001 tokens, groups of 2, dim 96: 18.9 us, and 22.0 us in the instance of 4).
 gs_status launch_fp32(const AttnParams& p, int blocks, gs_stream stream) {
     if (p.c.dim <= 64)
         return p.part <= 2 ? launch_policy<Fp32<2, 2>>(p, blocks, stream)

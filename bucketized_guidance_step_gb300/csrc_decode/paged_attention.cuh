@@ -21,7 +21,24 @@
 // pieces of a row are permuted by the row's number (piece c of row r lies at c ^ (r & 7)),
 // which keeps the reads of 8 rows free of bank conflicts.
 //
-// Visible positions are numbered 0 .. n-1 without gaps: the first `sinks`, then the window.
+// Visible positions are numbered 0 .. n-1: the first `sinks`, then the window (struct Row).
+//
+// What bounds it, on a GB300 (graph replay, inputs not in L2; bf16, dim 128, 32 query and 8 kv
+// heads unless said): HBM where rows are long: 2 rows of 200001 .. 262143 tokens (2.02 GB) take
+// 301 us, 99 % of the measured copy rate, 16 rows of 8192 161 us (98 %).  Below that a call's
+// fixed part shows, about 9 us: lengths, table and first rows are three DRAM latencies in a
+// chain (4.5 us), the last segment's end, its count and the join 3 to 5 us.  32 rows of 2048
+// tokens: 48 us (82 %), 32 ragged ones of 1 .. 4099: 50 us (81 %).  Where segments are a tile
+// long, what beginning and ending one costs is not hidden any more: 1032 rows of 64 tokens 75 us
+// (56 %), 258 rows of 256 53 us (77 %).  The smallest calls (2 rows of 125 and 250 tokens) take
+// 7.5 us.  Counters (ncu, the ragged rows): DRAM reads 277.7 MB of 277.7 required, tensor pipe
+// 9.5 %, 8 warps an SM.
+//
+// Measured and not kept: finding the places of 32 tiles at once, a tile a lane (48 -> 51 us at 32
+// rows of 2048: the work moves between the copies of two tiles); three blocks an SM with rings of
+// two stages (48 -> 51); blocks of at least 2, 3 or 4 units for small calls (7.4 -> 8.1, 10.1,
+// 10.9 us at the smallest: a tile more in a row costs more than a part more to join); joining in
+// two passes, weights first (7.5 -> 9.7 us).
 #pragma once
 
 #include "decode_common.cuh"
@@ -122,7 +139,8 @@ struct Split {
 };
 
 // A place in the sequence of units: a tile is a unit, and every (row, head group) has one more
-// after its tiles for what beginning and ending a segment costs.
+// after its tiles for what beginning and ending a segment costs (without it the blocks of short
+// rows end late: 58 against 52 us for 32 rows of 1 .. 4099 tokens).
 template <int RUN>
 struct Cursor {
     static constexpr int TILE = kWarps * RUN;
@@ -437,7 +455,9 @@ attention_kernel(const __grid_constant__ AttnParams p) {
                                              static_cast<int>(sizeof(T));
         const unsigned stage = ring_at + slot * L::kStage;
         if (CH <= 32 && p.whole_runs && ok && w.lo == 0 && w.hi == RUN && w.fresh < 0) {
-            // The usual run: all rows, in one page, every piece.
+            // The usual run: all rows, in one page, every piece (48.1 us against 48.7 without this
+            // case and 49.3 by rows of any page, 32 rows of 2048 tokens; 75.2, 78.2 and 81.6 for
+            // 1032 of 64).
             const char* ks = from + lane_at;
             const char* vs = ks + to_v;
             const unsigned dst = stage + r0 * L::kRow;
@@ -660,8 +680,9 @@ attention_kernel(const __grid_constant__ AttnParams p) {
 
 template <class P>
 gs_status launch_policy(const AttnParams& p, int blocks, gs_stream stream) {
-    // Two places for a segment's end where the block then still shares an SM as the ring wants it
-    // (228 KB an SM, 1 KB a block for the system).
+    // Two places for a segment's end (which saves a barrier: 7.6 -> 7.5 us for the smallest calls,
+    // 75.8 -> 75.1 for 1032 rows of 64 tokens) where the block then still shares an SM as the ring
+    // wants it (228 KB an SM, 1 KB a block for the system); else one.
     const int dump = Layout<P>::dump(p.part, p.c.dim);
     const int most = Layout<P>::kRing <= 96 * 1024 ? 113 * 1024 - 64 : 227 * 1024 - 64;
     AttnParams a = p;

@@ -8,6 +8,10 @@
 // The warp-wide mma.sync is used rather than tcgen05: a tile has 8 or 16 columns, each byte of
 // K and V is used for a few operations only, and the time goes to reading them from HBM.
 //
+// Heads that fill one column of 8 take the instance of one (48 us against 50.5 us in the instance
+// of two, 32 rows of 2048 tokens, groups of 4), more the instance of two, which reads K and V once
+// (36.9 us against 42.7 us in two parts of 8, groups of 16 and 4 kv heads).
+//
 // The weights 2^(s - m) enter the second product as two 16-bit numbers, hi + lo: with hi alone
 // the rounding of the weights would add as much error as the rounding of the output.  The sum
 // of the weights is taken before they are rounded.  For fp16 the weights are scaled by 2^11
