@@ -130,7 +130,7 @@ __device__ __forceinline__ void mark_first(int* mark, int seqs, const int* list,
 }
 
 __global__ void __launch_bounds__(kMeta)
-extend_kernel(CacheView c, const int* __restrict__ seq, const int* __restrict__ add, int n) {
+extend_kernel(CacheView c, const int* seq, const int* add, int n) {
     extern __shared__ int smem[];
     int* mark = smem;                    // [seqs]
     int* need = mark + c.seqs;           // [n] pages wanted
@@ -200,7 +200,7 @@ extend_kernel(CacheView c, const int* __restrict__ seq, const int* __restrict__ 
 }
 
 __global__ void __launch_bounds__(kMeta)
-fork_kernel(CacheView c, const int* __restrict__ src, const int* __restrict__ dst, int n) {
+fork_kernel(CacheView c, const int* src, const int* dst, int n) {
     extern __shared__ int smem[];
     int* mark = smem;                    // [seqs]
     int* from = mark + c.seqs;           // [n] length of src, -1: pair refused
@@ -309,7 +309,7 @@ fork_kernel(CacheView c, const int* __restrict__ src, const int* __restrict__ ds
 
 // One warp a listed sequence.  Its length is taken once (atomicExch), so that a second listing
 // finds nothing to release.
-__global__ void __launch_bounds__(128) free_kernel(CacheView c, const int* __restrict__ seq, int n) {
+__global__ void __launch_bounds__(128) free_kernel(CacheView c, const int* seq, int n) {
     grid_wait();
     grid_trigger();
     const int i = (blockIdx.x * 128 + threadIdx.x) >> 5, lane = threadIdx.x & 31;
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(128) free_kernel(CacheView c, const int* __res
 // k-th highest held page (n - 1 - held pages before it = k).  The counts of the moved pages go
 // through the list, so that refs_out may be refs.
 __global__ void __launch_bounds__(kMeta)
-compact_kernel(CacheView c, int* __restrict__ refs_out, int* __restrict__ live_out) {
+compact_kernel(CacheView c, int* refs_out, int* live_out) {
     __shared__ int tmp[kMeta / 32 + 1];
     __shared__ int mine;
     grid_wait();
@@ -369,6 +369,8 @@ compact_kernel(CacheView c, int* __restrict__ refs_out, int* __restrict__ live_o
                 copies[k].pad = count;
                 rank_of[p] = k;
                 ++moved;
+            } else if (p >= live) {
+                rank_of[p] = -1;                                // free: no table should name it
             }
         }
     }
@@ -403,7 +405,7 @@ compact_kernel(CacheView c, int* __restrict__ refs_out, int* __restrict__ live_o
 // the table's entries are renumbered too (compact).
 template <bool REMAP, bool DENSE>
 __global__ void __launch_bounds__(kCopy)
-copy_kernel(CacheView c, int es, int* __restrict__ table_out) {
+copy_kernel(CacheView c, int es, int* table_out) {
     grid_wait();
     grid_trigger();
     const int count = c.work[0];
@@ -417,7 +419,11 @@ copy_kernel(CacheView c, int es, int* __restrict__ table_out) {
             int p = c.table[q];
             // Entries past a sequence's pages may hold anything: only held pages are renumbered.
             const int s = static_cast<int>(q / c.cols), j = static_cast<int>(q % c.cols);
-            if (p >= live && p < c.pages && j < pages_of(c.lens[s], c.page)) p = copies[rank_of[p]].y;
+            if (p >= live && p < c.pages && j < pages_of(c.lens[s], c.page)) {
+                const int k = rank_of[p];
+                if (k >= 0) p = copies[k].y;
+                else flag(c.status, GS_DEV_BAD_SEQ);
+            }
             table_out[q] = p;
         }
     }
@@ -464,9 +470,9 @@ copy_kernel(CacheView c, int es, int* __restrict__ table_out) {
 // before its place is looked up.
 template <class T>
 __global__ void __launch_bounds__(kCopy)
-write_kernel(CacheView c, int layer, const T* __restrict__ k, const T* __restrict__ v,
+write_kernel(CacheView c, int layer, const T* k, const T* v,
              long long token_stride, long long head_stride, int src_aligned, int tokens,
-             const int* __restrict__ seq, const int* __restrict__ start, int n) {
+             const int* seq, const int* start, int n) {
     extern __shared__ int first[];                       // [n + 1]: start
     grid_wait();
     grid_trigger();

@@ -127,7 +127,8 @@ inline bool allow_smem(int bytes) {
 
 // Every decode kernel is launched with programmatic stream serialization: its blocks may be
 // placed before the stream's previous kernel ends, and wait for it (grid_wait) before they
-// touch memory.
+// touch memory.  (So no kernel has read-only pointers - restrict, __ldg - whose loads a compiler
+// may move above the wait.)
 template <class... P, class... A>
 inline gs_status launch(void (*kernel)(P...), dim3 grid, int threads, int smem, int cluster,
                         gs_stream stream, A... args) {

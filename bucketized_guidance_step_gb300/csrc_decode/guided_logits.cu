@@ -260,7 +260,7 @@ logits_kernel(const __grid_constant__ LogitParams p) {
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
         const int t = i * kLogitThreads + static_cast<int>(threadIdx.x);
-        held[i] = t < room ? __ldg(tokens + t) : -1;
+        held[i] = t < room ? tokens[t] : -1;
     }
 
     // The row's settings.
@@ -324,7 +324,7 @@ logits_kernel(const __grid_constant__ LogitParams p) {
 #pragma unroll
                 for (int i = 0; i < HELD; ++i) {
                     const int t = t0 + i * kLogitThreads;
-                    v[i] = t < known ? __ldg(tokens + t) : -1;
+                    v[i] = t < known ? tokens[t] : -1;
                 }
 #pragma unroll
                 for (int i = 0; i < HELD; ++i)
@@ -361,8 +361,8 @@ logits_kernel(const __grid_constant__ LogitParams p) {
     auto fetch_mask = [&](int v) {
         if (mask == nullptr || v >= end) return;
         const int w = max(v, 0) >> 5;
-        allow_lo = __ldg(mask + w);
-        if (MIS && v >= 0 && (v & 31) > 24 && (w + 1) * 32 < p.vocab) allow_hi = __ldg(mask + w + 1);
+        allow_lo = mask[w];
+        if (MIS && v >= 0 && (v & 31) > 24 && (w + 1) * 32 < p.vocab) allow_hi = mask[w + 1];
     };
     fetch_mask(start + lane * kPer);
 

@@ -230,6 +230,7 @@ __device__ __forceinline__ bool find_work(const AttnParams& p, Split* split, int
     int before = __shfl_sync(0xffffffffu, upto - mine, found);
     // The same for the found lane's rows, 32 at a time.
     for (int row = found * per * 32;; row += 32) {
+        if (row >= p.batch) return false;                // (lengths that change during the call)
         const int units = row + lane < p.batch ? units_in<RUN>(row_of<RUN>(p, row + lane, &bad)) : 0;
         upto = units;
 #pragma unroll

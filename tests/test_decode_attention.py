@@ -104,6 +104,13 @@ def test_types_and_head_sizes(dtype, dim):
     check(cache, 1, q, *run(cache, q))
 
 
+@pytest.mark.parametrize("dim", [4, 12, 20, 100, 252])
+def test_head_sizes_of_a_few_fp32_values(dim):
+    cache = build([0, 1, 9, 70, 300], dim=dim, dtype=F32, heads=3, page=7, seed=dim)
+    q = queries(cache, 5, 5)
+    check(cache, 1, q, *run(cache, q))
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("heads,group", [(1, 1), (1, 16), (3, 5), (2, 8), (5, 3), (1, 33), (16, 1), (2, 12)])
 def test_head_layouts(dtype, heads, group):

@@ -200,3 +200,15 @@ def test_write_of_ranges_that_do_not_rise_stays_in_its_sequence():
     torch.cuda.synchronize()
     changed = (b.k != before).any(dim=4).any(dim=2)[0].nonzero()[:, 0]
     assert set(changed.tolist()) <= set(b.table[0, :2].tolist()) and int(b.status) == decode.GS_DEV_BAD_SEQ
+
+
+def test_compact_leaves_an_entry_that_names_a_free_page():
+    b = Both(pages=8, page=4)
+    b.extend([0, 1], [4, 8])                       # pages 0; 1, 2
+    b.table[1, 1] = 7                              # (a state that no call makes)
+    b.refs[0] = 0
+    table, refs = torch.empty_like(b.table), torch.empty_like(b.refs)
+    b.cache.compact(table_out=table, refs_out=refs)
+    torch.cuda.synchronize()
+    assert table[1, :2].tolist() == [1, 7] and int(b.status) == decode.GS_DEV_BAD_SEQ
+    assert refs.tolist() == [1, 1, 0, 0, 0, 0, 0, 0]
