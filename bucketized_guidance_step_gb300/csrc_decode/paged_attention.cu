@@ -22,7 +22,10 @@ namespace {
 template <int NV, int H>
 struct Fp32 {
     using T = float;
-    static constexpr int DP = 32 * NV, RUN = 8, STAGES = NV <= 2 ? 6 : 3, HEADS = H;
+    static constexpr int DP = 32 * NV, RUN = 8, HEADS = H;
+    // Blocks on an SM as registers allow; rings of 64, 96 or 192 KB.
+    static constexpr int PER_SM = NV > 4 ? 1 : NV > 2 || H > 4 ? 2 : 3;
+    static constexpr int STAGES = NV > 2 ? 3 : PER_SM == 3 ? 4 : 6;
     static constexpr int E = 4 * NV, U = RUN / 4;
     static_assert(HEADS <= kRound, "one dump");
     float q[HEADS][E], o[HEADS][E], top[HEADS], sum[HEADS];
@@ -145,26 +148,28 @@ struct Fp32 {
     }
 };
 
-}  // namespace
 
-// Most heads of a part: 64 registers for their values.  Rings of 96 KB a block (192 KB for rows
-// over 512 bytes).
-Serves fp32_serves(int dim) {
-    if (dim <= 64) return {Layout<Fp32<2, 8>>::kTile, 8, 2};
-    if (dim <= 128) return {Layout<Fp32<4, 4>>::kTile, 4, 2};
-    return {Layout<Fp32<8, 2>>::kTile, 2, 1};
+// An instance computes for all its heads, so small groups have instances of their own: groups of 2
+// with dim 96 (8 rows of 333 .. 3001 tokens) take 18.9 us, and 22.0 us in the instance of 4; groups
+// of 4 with dim 64 (32 rows of 2048) 66 us, and 107 us in the instance of 8, whose registers allow
+// two blocks an SM instead of three; groups of 8 109 us, and 127 us in two parts of 4.
+template <class F>
+auto with_instance(int dim, int group, F f) {
+    if (dim <= 64) return group <= 2 ? f(Fp32<2, 2>()) : group <= 4 ? f(Fp32<2, 4>()) : f(Fp32<2, 8>());
+    if (dim <= 128) return group <= 2 ? f(Fp32<4, 2>()) : f(Fp32<4, 4>());
+    return f(Fp32<8, 2>());
 }
 
-// Parts of one or two heads have instances of their own: an instance computes for all its heads
-// (8 rows of 333 .. 3001 tokens, groups of 2, dim 96: 18.9 us, and 22.0 us in the instance of 4).
+}  // namespace
+
+Serves fp32_serves(int dim, int group) {
+    return with_instance(dim, group, [&](auto policy) { return serves_by<decltype(policy)>(group); });
+}
+
 gs_status launch_fp32(const AttnParams& p, int blocks, gs_stream stream) {
-    if (p.c.dim <= 64)
-        return p.part <= 2 ? launch_policy<Fp32<2, 2>>(p, blocks, stream)
-                           : launch_policy<Fp32<2, 8>>(p, blocks, stream);
-    if (p.c.dim <= 128)
-        return p.part <= 2 ? launch_policy<Fp32<4, 2>>(p, blocks, stream)
-                           : launch_policy<Fp32<4, 4>>(p, blocks, stream);
-    return launch_policy<Fp32<8, 2>>(p, blocks, stream);
+    return with_instance(p.c.dim, p.group, [&](auto policy) {
+        return launch_policy<decltype(policy)>(p, blocks, stream);
+    });
 }
 
 namespace {
@@ -185,10 +190,10 @@ gs_status plan_of(const gs_paged_attention_args* a, Plan* plan) {
         return GS_ERR_INVALID_ARG;
     if (a->batch > GS_MAX_SEQS || a->q_heads > (1 << 16)) return GS_ERR_UNSUPPORTED;
     const int group = a->q_heads / c->kv_heads;
-    const Serves by = c->dtype == GS_DTYPE_F32 ? fp32_serves(c->dim) : mma_serves(c->dim);
+    const Serves by = c->dtype == GS_DTYPE_F32 ? fp32_serves(c->dim, group) : mma_serves(c->dim, group);
     plan->run = by.tile / kWarps;
-    plan->parts = (group + by.heads - 1) / by.heads;
-    plan->part = (group + plan->parts - 1) / plan->parts;
+    plan->parts = by.parts;
+    plan->part = by.part;
     long long most = static_cast<long long>(c->cols) * c->page;
     const long long visible = static_cast<long long>(a->window) + a->sinks + 2 * by.tile;   // whole runs
     if (a->window > 0 && visible < most) most = visible;

@@ -184,31 +184,35 @@ __device__ __forceinline__ bool find_work(const AttnParams& p, Split* split, int
                                           Cursor<RUN>* at) {
     const int lane = threadIdx.x & 31;
     const int hp = p.c.heads * p.parts;
-    // 32 rows at a time, eight such loads in flight; lane i keeps the sum of `per` of them from
-    // per * i on, then the lanes are summed up.
     const int groups = (p.batch + 31) / 32, per = (groups + 31) / 32;
     unsigned bad = 0;
     int mine = 0;
-    constexpr int N = 8;
-    for (int g0 = 0; g0 < groups; g0 += N) {
-        int seq[N], len[N];
+    if (groups == 1) {                                   // a row a lane
+        if (lane < p.batch) mine = units_in<RUN>(row_of<RUN>(p, lane, &bad));
+    } else {
+        // 32 rows at a time, eight such loads in flight; lane i keeps the sum of `per` of them from
+        // per * i on, then the lanes are summed up.
+        constexpr int N = 8;
+        for (int g0 = 0; g0 < groups; g0 += N) {
+            int seq[N], len[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int b = (g0 + i) * 32 + lane;
-            seq[i] = b < p.batch && p.seq != nullptr ? p.seq[b] : b;
-        }
+            for (int i = 0; i < N; ++i) {
+                const int b = (g0 + i) * 32 + lane;
+                seq[i] = b < p.batch && p.seq != nullptr ? p.seq[b] : b;
+            }
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int b = (g0 + i) * 32 + lane;
-            len[i] = b < p.batch && seq[i] >= 0 && seq[i] < p.c.seqs ? p.c.lens[seq[i]] : 0;
-        }
+            for (int i = 0; i < N; ++i) {
+                const int b = (g0 + i) * 32 + lane;
+                len[i] = b < p.batch && seq[i] >= 0 && seq[i] < p.c.seqs ? p.c.lens[seq[i]] : 0;
+            }
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            if (g0 + i >= groups) break;
-            const int b = (g0 + i) * 32 + lane;
-            const int sum = __reduce_add_sync(
-                0xffffffffu, b < p.batch ? units_in<RUN>(row_from<RUN>(p, seq[i], len[i], &bad)) : 0);
-            if ((g0 + i) / per == lane) mine += sum;
+            for (int i = 0; i < N; ++i) {
+                if (g0 + i >= groups) break;
+                const int b = (g0 + i) * 32 + lane;
+                const int sum = __reduce_add_sync(
+                    0xffffffffu, b < p.batch ? units_in<RUN>(row_from<RUN>(p, seq[i], len[i], &bad)) : 0);
+                if ((g0 + i) / per == lane) mine += sum;
+            }
         }
     }
     if (blockIdx.x == 0 && threadIdx.x < 32) flag(p.c.status, bad);
@@ -227,25 +231,29 @@ __device__ __forceinline__ bool find_work(const AttnParams& p, Split* split, int
     *end = split->first_of(blockIdx.x + 1);
     const int want = first / hp;          // unit of the rows' own count
     const int found = __ffs(__ballot_sync(0xffffffffu, upto > want)) - 1;
-    int before = __shfl_sync(0xffffffffu, upto - mine, found);
-    // The same for the found lane's rows, 32 at a time.
-    for (int row = found * per * 32;; row += 32) {
-        if (row >= p.batch) return false;                // (lengths that change during the call)
-        const int units = row + lane < p.batch ? units_in<RUN>(row_of<RUN>(p, row + lane, &bad)) : 0;
-        upto = units;
+    int before = __shfl_sync(0xffffffffu, upto - mine, found);       // (groups == 1: found is the row)
+    if (groups == 1) {
+        at->take_row(p, found);
+    } else {
+        // The same for the found lane's rows, 32 at a time.
+        for (int row = found * per * 32;; row += 32) {
+            if (row >= p.batch) return false;                // (lengths that change during the call)
+            const int units = row + lane < p.batch ? units_in<RUN>(row_of<RUN>(p, row + lane, &bad)) : 0;
+            upto = units;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, upto, d);
-            if (lane >= d) upto += o;
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, upto, d);
+                if (lane >= d) upto += o;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, before + upto > want);
+            if (past != 0u) {
+                const int i = __ffs(past) - 1;
+                before += __shfl_sync(0xffffffffu, upto - units, i);
+                at->take_row(p, row + i);
+                break;
+            }
+            before += __shfl_sync(0xffffffffu, upto, 31);
         }
-        const unsigned past = __ballot_sync(0xffffffffu, before + upto > want);
-        if (past != 0u) {
-            const int i = __ffs(past) - 1;
-            before += __shfl_sync(0xffffffffu, upto - units, i);
-            at->take_row(p, row + i);
-            break;
-        }
-        before += __shfl_sync(0xffffffffu, upto, 31);
     }
     at->base = before * hp;
     const int into = first - at->base;
@@ -347,8 +355,8 @@ __device__ __forceinline__ void join_parts(const float (&m)[N], const float (&s)
 
 // ---- the kernel -----------------------------------------------------------------------------
 // A policy P has
-//   T, DP (dim rounded up), RUN (positions of a warp's share of a tile), STAGES, HEADS (most
-//   query heads of a part), and registers of its own;
+//   T, DP (dim rounded up), RUN (positions of a warp's share of a tile), STAGES, PER_SM (blocks
+//   on an SM), HEADS (most query heads of a part), and registers of its own;
 //   AHEAD: fetch may be called during the segment before;
 //   fetch(q, head_stride, heads, dim, aligned): reads the query heads of a segment;
 //   begin(): takes them into use, empties max, sum and output;
@@ -384,7 +392,7 @@ struct Pending {
 };
 
 template <class P>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, P::PER_SM)
 attention_kernel(const __grid_constant__ AttnParams p) {
     using T = typename P::T;
     using L = Layout<P>;
@@ -682,10 +690,11 @@ attention_kernel(const __grid_constant__ AttnParams p) {
 template <class P>
 gs_status launch_policy(const AttnParams& p, int blocks, gs_stream stream) {
     // Two places for a segment's end (which saves a barrier: 7.6 -> 7.5 us for the smallest calls,
-    // 75.8 -> 75.1 for 1032 rows of 64 tokens) where the block then still shares an SM as the ring
-    // wants it (228 KB an SM, 1 KB a block for the system); else one.
+    // 75.8 -> 75.1 for 1032 rows of 64 tokens) where PER_SM blocks then still share an SM (228 KB,
+    // 1 KB a block for the system); else one.
     const int dump = Layout<P>::dump(p.part, p.c.dim);
-    const int most = Layout<P>::kRing <= 96 * 1024 ? 113 * 1024 - 64 : 227 * 1024 - 64;
+    constexpr int most = 228 * 1024 / P::PER_SM - 1024 - 64;
+    static_assert(Layout<P>::kRing < most, "the ring fits");
     AttnParams a = p;
     a.dumps = Layout<P>::kRing + 2 * dump <= most ? 2 : 1;
     a.whole_runs = p.page_runs && p.c.dim == P::DP;
@@ -695,13 +704,18 @@ gs_status launch_policy(const AttnParams& p, int blocks, gs_stream stream) {
                   stream, a);
 }
 
-// How a policy's kernel serves a head dimension: positions of a tile, most query heads of a
-// part, blocks resident on an SM.
+// How the query heads of a kv head (group) are served: positions of a tile, parts of the group
+// and heads of a part, blocks resident on an SM.
 struct Serves {
-    int tile, heads, per_sm;
+    int tile, parts, part, per_sm;
 };
-Serves fp32_serves(int dim);
-Serves mma_serves(int dim);
+template <class P>
+Serves serves_by(int group) {
+    const int parts = (group + P::HEADS - 1) / P::HEADS;
+    return {Layout<P>::kTile, parts, (group + parts - 1) / parts, P::PER_SM};
+}
+Serves fp32_serves(int dim, int group);
+Serves mma_serves(int dim, int group);
 gs_status launch_fp32(const AttnParams& p, int blocks, gs_stream stream);
 gs_status launch_mma(int dtype, const AttnParams& p, int blocks, gs_stream stream);
 

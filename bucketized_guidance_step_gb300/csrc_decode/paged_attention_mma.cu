@@ -79,7 +79,8 @@ __device__ __forceinline__ float sum_rows(float x) {
 template <class Type, int DIM, int NH>
 struct Mma {
     using T = Type;
-    static constexpr int DP = DIM, RUN = 16, STAGES = DIM == 64 ? 6 : 3, HEADS = 8 * NH;
+    static constexpr int DP = DIM, RUN = 16, HEADS = 8 * NH;
+    static constexpr int STAGES = DIM == 64 ? 4 : 3, PER_SM = DIM == 64 ? 3 : DIM == 128 ? 2 : 1;
     static_assert(kRound == 8, "a dump is one column of heads");
     static constexpr int KS = DP / 16;                   // steps over dim
     static constexpr float kShift = std::is_same<T, __half>::value ? 11.0f : 0.0f;
@@ -261,29 +262,28 @@ struct Mma {
     }
 };
 
-template <class T>
-gs_status launch_type(const AttnParams& p, int blocks, gs_stream stream) {
-    if (p.c.dim <= 64)
-        return p.part <= 8 ? launch_policy<Mma<T, 64, 1>>(p, blocks, stream)
-                           : launch_policy<Mma<T, 64, 2>>(p, blocks, stream);
-    if (p.c.dim <= 128)
-        return p.part <= 8 ? launch_policy<Mma<T, 128, 1>>(p, blocks, stream)
-                           : launch_policy<Mma<T, 128, 2>>(p, blocks, stream);
-    return launch_policy<Mma<T, 256, 1>>(p, blocks, stream);
+// The instance for a head dimension and a group of query heads.  As many blocks on an SM as
+// registers and rings allow: rows of up to 128 bytes take three with rings of four stages (2 rows
+// of 200000 tokens, 32/8 heads of 64: 129 us, and 143 us with two blocks and six stages, 153 us
+// with four and three), rows of up to 256 bytes two with three.  Rows over that take 8 query heads
+// at a time: the output of 16 would not fit the registers.
+template <class T, class F>
+auto with_instance(int dim, int group, F f) {
+    if (dim <= 64) return group <= 8 ? f(Mma<T, 64, 1>()) : f(Mma<T, 64, 2>());
+    if (dim <= 128) return group <= 8 ? f(Mma<T, 128, 1>()) : f(Mma<T, 128, 2>());
+    return f(Mma<T, 256, 1>());
 }
 
 }  // namespace
 
-// 16 query heads in one pass; 8 for rows over 256 bytes, whose output would not fit the
-// registers.  Rings of 96 KB a block (192 KB for rows over 256 bytes).
-Serves mma_serves(int dim) {
-    constexpr int tile = Layout<Mma<__half, 64, 1>>::kTile;
-    return dim <= 128 ? Serves{tile, 16, 2} : Serves{tile, 8, 1};
+Serves mma_serves(int dim, int group) {
+    return with_instance<__half>(dim, group, [&](auto policy) { return serves_by<decltype(policy)>(group); });
 }
 
 gs_status launch_mma(int dtype, const AttnParams& p, int blocks, gs_stream stream) {
-    return dtype == GS_DTYPE_BF16 ? launch_type<__nv_bfloat16>(p, blocks, stream)
-                                  : launch_type<__half>(p, blocks, stream);
+    const auto run = [&](auto policy) { return launch_policy<decltype(policy)>(p, blocks, stream); };
+    return dtype == GS_DTYPE_BF16 ? with_instance<__nv_bfloat16>(p.c.dim, p.group, run)
+                                  : with_instance<__half>(p.c.dim, p.group, run);
 }
 
 }  // namespace gs_decode
