@@ -30,7 +30,7 @@ struct Fp32 {
     static_assert(HEADS <= kRound, "one dump");
     float q[HEADS][E], o[HEADS][E], top[HEADS], sum[HEADS];
 
-    static constexpr bool AHEAD = false;
+    static constexpr bool AHEAD = false, FULL = NV <= 4, PARTIAL = NV <= 4;
 
     __device__ __forceinline__ void fetch(const float* query, long long head_stride, int heads,
                                           int dim, bool) {

@@ -67,7 +67,6 @@ struct AttnParams {
     unsigned page_mul, page_shift;        // position / page = (mulhi(position, mul) + position) >> shift
     int dumps;                            // places for a segment's end in shared memory: 1 or 2
     int page_runs;                        // a page holds whole runs: a run lies in one page
-    int whole_runs;                       // and a row fills the pieces that lanes copy (dim is DP)
     unsigned dim_mul;                     // x / dim = x * mul >> 20, for x < 8 dim
     float scale_log2;                     // scale * log2 e: scores are kept in powers of two
     int window, sinks;
@@ -357,6 +356,9 @@ __device__ __forceinline__ void join_parts(const float (&m)[N], const float (&s)
 // A policy P has
 //   T, DP (dim rounded up), RUN (positions of a warp's share of a tile), STAGES, PER_SM (blocks
 //   on an SM), HEADS (most query heads of a part), and registers of its own;
+//   FULL, PARTIAL: runs of rows that fill DP, or do not, have copies of their own (48.1 us against
+//     48.7 without for 32 rows of 2048 tokens with 32/8 heads of 128, and 49.3 where a run may cross
+//     pages; 75.2, 78.2 and 81.6 for 1032 rows of 64 tokens);
 //   AHEAD: fetch may be called during the segment before;
 //   fetch(q, head_stride, heads, dim, aligned): reads the query heads of a segment;
 //   begin(): takes them into use, empties max, sum and output;
@@ -463,21 +465,27 @@ attention_kernel(const __grid_constant__ AttnParams p) {
                                           (ok ? w.page * p.c.page_stride + w.row * p.c.token_stride : 0)) *
                                              static_cast<int>(sizeof(T));
         const unsigned stage = ring_at + slot * L::kStage;
-        if (CH <= 32 && p.whole_runs && ok && w.lo == 0 && w.hi == RUN && w.fresh < 0) {
-            // The usual run: all rows, in one page, every piece (48.1 us against 48.7 without this
-            // case and 49.3 by rows of any page, 32 rows of 2048 tokens; 75.2, 78.2 and 81.6 for
-            // 1032 of 64).
+        const bool usual = p.page_runs && ok && w.lo == 0 && w.hi == RUN && w.fresh < 0;
+        // The usual run: all rows, in one page.
+        auto copy_rows = [&](bool mine) {
             const char* ks = from + lane_at;
             const char* vs = ks + to_v;
             const unsigned dst = stage + r0 * L::kRow;
 #pragma unroll
             for (int x = 0; x < RUN / RPS; ++x) {
                 const unsigned to = dst + x * RPS * L::kRow + (((c0 ^ r0) << 4) ^ (x * RPS & 7) << 4);
-                copy_async(to, ks, 16);
-                copy_async(to + L::kHalf, vs, 16);
+                if (mine) {
+                    copy_async(to, ks, 16);
+                    copy_async(to + L::kHalf, vs, 16);
+                }
                 ks += row_step;
                 vs += row_step;
             }
+        };
+        if (P::FULL && usual && dim == P::DP) {
+            copy_rows(true);
+        } else if (P::PARTIAL && usual && dim != P::DP) {
+            copy_rows(c0 * V < dim);
         } else if (p.page_runs) {
             if (!ok) flag(p.c.status, GS_DEV_BAD_SEQ);
             const char* src = from + lane_at;
@@ -697,7 +705,6 @@ gs_status launch_policy(const AttnParams& p, int blocks, gs_stream stream) {
     static_assert(Layout<P>::kRing < most, "the ring fits");
     AttnParams a = p;
     a.dumps = Layout<P>::kRing + 2 * dump <= most ? 2 : 1;
-    a.whole_runs = p.page_runs && p.c.dim == P::DP;
     const int smem = Layout<P>::kRing + a.dumps * dump;
     if (!allow_smem<attention_kernel<P>>(smem)) return GS_ERR_CUDA;
     return launch(attention_kernel<P>, dim3(static_cast<unsigned>(blocks)), kThreads, smem, 1,

@@ -75,14 +75,15 @@ __device__ __forceinline__ float sum_rows(float x) {
     return x + __shfl_xor_sync(0xffffffffu, x, 16);
 }
 
-// NH: columns of 8 query heads.  Of a warp's 32 lanes, lane = 4 g + t.
-template <class Type, int DIM, int NH>
+// NH: columns of 8 query heads; STEPS: of 16 dims.  Of a warp's 32 lanes, lane = 4 g + t.
+template <class Type, int DIM, int NH, int STEPS = DIM / 16>
 struct Mma {
     using T = Type;
     static constexpr int DP = DIM, RUN = 16, HEADS = 8 * NH;
     static constexpr int STAGES = DIM == 64 ? 4 : 3, PER_SM = DIM == 64 ? 3 : DIM == 128 ? 2 : 1;
     static_assert(kRound == 8, "a dump is one column of heads");
-    static constexpr int KS = DP / 16;                   // steps over dim
+    static constexpr int KS = STEPS;                     // steps of 16 over dim
+    static constexpr bool FULL = KS * 16 == DP, PARTIAL = !FULL;
     static constexpr float kShift = std::is_same<T, __half>::value ? 11.0f : 0.0f;
     static constexpr float kSlack = std::is_same<T, __half>::value ? 4.0f : 8.0f;    // 2^(11 + 4) fits fp16
     unsigned q[NH][KS][2];                               // head g (+ 8), dims 2t, 2t+1; 2t+8, 2t+9
@@ -97,7 +98,7 @@ struct Mma {
     __device__ __forceinline__ void fetch(const T* query, long long head_stride, int heads, int dim,
                                           bool aligned) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-        const bool usual = aligned && dim == DP;
+        const bool usual = aligned && dim == 16 * KS;
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
             const unsigned short* const qp =
@@ -249,7 +250,7 @@ struct Mma {
                     out[head * pitch + dim + 1] = all;
                 }
                 float* const to = out + head * pitch + g;
-                if (dim == DP) {
+                if (dim == 16 * KS) {
 #pragma unroll
                     for (int x = 0; x < 2 * KS; ++x) to[x * 8] = o[h][x / 2][e + 2 * (x & 1)];
                 } else {
@@ -265,11 +266,14 @@ struct Mma {
 // The instance for a head dimension and a group of query heads.  As many blocks on an SM as
 // registers and rings allow: rows of up to 128 bytes take three with rings of four stages (2 rows
 // of 200000 tokens, 32/8 heads of 64: 129 us, and 143 us with two blocks and six stages, 153 us
-// with four and three), rows of up to 256 bytes two with three.  Rows over that take 8 query heads
+// with four and three), rows of up to 256 bytes two with three.  Dims of up to 96 lie in rows of
+// 256 bytes, but for their products (32 rows of 2048 tokens, 32/8 heads of 96: 39.3 us, and 42.4 us
+// with the products of 128).  Rows over that take 8 query heads
 // at a time: the output of 16 would not fit the registers.
 template <class T, class F>
 auto with_instance(int dim, int group, F f) {
     if (dim <= 64) return group <= 8 ? f(Mma<T, 64, 1>()) : f(Mma<T, 64, 2>());
+    if (dim <= 96) return group <= 8 ? f(Mma<T, 128, 1, 6>()) : f(Mma<T, 128, 2, 6>());
     if (dim <= 128) return group <= 8 ? f(Mma<T, 128, 1>()) : f(Mma<T, 128, 2>());
     return f(Mma<T, 256, 1>());
 }

@@ -97,7 +97,7 @@ def run(cache, q, layer=1, **kw):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])
-@pytest.mark.parametrize("dim", [8, 16, 24, 64, 80, 96, 128, 136, 192, 256])
+@pytest.mark.parametrize("dim", [8, 16, 24, 64, 80, 96, 104, 128, 136, 192, 256])
 def test_types_and_head_sizes(dtype, dim):
     cache = build([0, 1, 5, 16, 17, 70, 131], dim=dim, dtype=dtype, seed=dim)
     q = queries(cache, 7, 2)
