@@ -312,13 +312,19 @@ logits_kernel(const __grid_constant__ LogitParams p) {
         for (int i = threadIdx.x; i < words; i += kLogitThreads) bits[i] = 0u;
         __syncthreads();
         const int low = max(origin, 0);
-        // Calls f(t, token - origin) for the history's tokens in this chunk.
-        auto each_token = [&](auto f) {
+        // Of the tokens held, the place in the chunk; -1 elsewhere.
+        bool any = false;
 #pragma unroll
-            for (int i = 0; i < HELD; ++i) {
-                const int t = i * kLogitThreads + static_cast<int>(threadIdx.x);
-                if (t < known && held[i] >= low && held[i] < end) f(t, held[i] - origin);
+        for (int i = 0; i < HELD; ++i) {
+            const int t = i * kLogitThreads + static_cast<int>(threadIdx.x);
+            held[i] = t < known && held[i] >= low && held[i] < end ? held[i] - origin : -1;
+            if (held[i] >= 0) {
+                atomicOr(bits + (held[i] >> 5), 1u << (held[i] & 31));
+                any = true;
             }
+        }
+        // Calls f(t, token - origin) for the other tokens in the chunk.
+        auto each_other = [&](auto f) {
             for (int t0 = HELD * kLogitThreads + threadIdx.x; t0 < known; t0 += HELD * kLogitThreads) {
                 int v[HELD];
 #pragma unroll
@@ -331,27 +337,32 @@ logits_kernel(const __grid_constant__ LogitParams p) {
                     if (v[i] >= low && v[i] < end) f(t0 + i * kLogitThreads, v[i] - origin);
             }
         };
-        bool any = false;
-        each_token([&](int, int b) {
+        each_other([&](int, int b) {
             atomicOr(bits + (b >> 5), 1u << (b & 31));
             any = true;
         });
         said = __syncthreads_or(any ? 1 : 0) != 0;
         if (said) {
-            int before = 0;
-            for (int i0 = 0; i0 < words; i0 += kLogitThreads) {
-                const int i = i0 + static_cast<int>(threadIdx.x);
-                int total;
-                const int r = before + block_scan<kLogitThreads>(i < words ? __popc(bits[i]) : 0, scan, &total);
-                if (i < words) rank[i] = r;
-                before += total;
-            }
-            for (int i = threadIdx.x; i < before; i += kLogitThreads) count[i] = 0u;
+            // The words' ranks, two words a thread; the counts from 0.
+            static_assert(kMaxChunk / 32 <= 2 * kLogitThreads, "two words a thread");
+            const int i = 2 * static_cast<int>(threadIdx.x);
+            const int n0 = i < words ? __popc(bits[i]) : 0, n1 = i + 1 < words ? __popc(bits[i + 1]) : 0;
+            int total;
+            const int r = block_scan<kLogitThreads>(n0 + n1, scan, &total);
+            if (i < words) rank[i] = r;
+            if (i + 1 < words) rank[i + 1] = r + n0;
+            for (int x = threadIdx.x; x < total; x += kLogitThreads) count[x] = 0u;
             __syncthreads();
-            each_token([&](int t, int b) {
+            auto add = [&](int t, int b) {
                 if (t >= prompt)
                     atomicAdd(count + rank[b >> 5] + __popc(bits[b >> 5] & ((1u << (b & 31)) - 1u)), 1u);
-            });
+            };
+            if (any) {
+#pragma unroll
+                for (int k = 0; k < HELD; ++k)
+                    if (held[k] >= 0) add(k * kLogitThreads + static_cast<int>(threadIdx.x), held[k]);
+                each_other(add);
+            }
             __syncthreads();
         }
     }
