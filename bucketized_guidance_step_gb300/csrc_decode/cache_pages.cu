@@ -12,7 +12,7 @@
 // host knowing the list's length.  It is bound by HBM: each byte is read once and written once.
 //
 // Measured on a GB300 (graph replay): 64 forks of 32 layers of 8 heads of 64 x 128 bf16 pages, half
-// filled (426 MB read and written), 75.5 us, of which the copies take 64 (98 % of the measured copy
+// filled (426 MB read and written), 75.4 us, of which the copies take 65 (97 % of the measured copy
 // rate); compacting 1024 of 4096 pages of 4 layers (537 MB) 87 us (91 %); 24 prompts of 12.8k
 // tokens in all freed, extended and written in 2 layers (210 MB) 46 us (67 %): 37 of them the two
 // writes, 8 the bookkeeping.  That is a chain of DRAM latencies (list, lengths, tables, counts) and

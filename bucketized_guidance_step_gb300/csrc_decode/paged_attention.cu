@@ -8,7 +8,7 @@
 //
 // What bounds it: 16 rows of 4096 tokens with 32 query and 8 kv heads of dim 128 (537 MB) take
 // 94 us, 84 % of the measured copy rate; 8 rows of 333 .. 3001 with 8 and 4 heads of 96 (45 MB)
-// 18.9 us, 35 %: the call's fixed part, and five or six tiles a block in a row, whose multiply-adds
+// 17.2 us, 39 %: the call's fixed part, and five or six tiles a block in a row, whose multiply-adds
 // two warps a scheduler do not hide.
 #include <cmath>
 
@@ -150,7 +150,7 @@ struct Fp32 {
 
 
 // An instance computes for all its heads, so small groups have instances of their own: groups of 2
-// with dim 96 (8 rows of 333 .. 3001 tokens) take 18.9 us, and 22.0 us in the instance of 4; groups
+// with dim 96 (8 rows of 333 .. 3001 tokens) took 18.9 us, and 22.0 us in the instance of 4; groups
 // of 4 with dim 64 (32 rows of 2048) 66 us, and 107 us in the instance of 8, whose registers allow
 // two blocks an SM instead of three; groups of 8 109 us, and 127 us in two parts of 4.
 template <class F>

@@ -31,8 +31,8 @@
 // tokens: 48 us (82 %), 32 ragged ones of 1 .. 4099: 50 us (81 %).  Where segments are a tile
 // long, what beginning and ending one costs is not hidden any more: 1032 rows of 64 tokens 75 us
 // (56 %), 258 rows of 256 53 us (77 %).  The smallest calls (2 rows of 125 and 250 tokens) take
-// 7.5 us.  Counters (ncu, the ragged rows): DRAM reads 277.7 MB of 277.7 required, tensor pipe
-// 9.5 %, 8 warps an SM.
+// 6.7 us.  Counters (ncu, the ragged rows): DRAM reads 277.7 MB of 277.7 required, tensor pipe
+// 9.6 %, 8 warps an SM.
 //
 // Measured and not kept: finding the places of 32 tiles at once, a tile a lane (48 -> 51 us at 32
 // rows of 2048: the work moves between the copies of two tiles); three blocks an SM with rings of
