@@ -25,7 +25,7 @@
 //
 // What bounds it, on a GB300 (graph replay, inputs not in L2; bf16, dim 128, 32 query and 8 kv
 // heads unless said): HBM where rows are long: 2 rows of 200001 .. 262143 tokens (2.02 GB) take
-// 301 us, 99 % of the measured copy rate, 16 rows of 8192 161 us (98 %).  Below that a call's
+// 301 us, 99 % of the measured copy rate, 32 rows of 8192 161 us (98 %).  Below that a call's
 // fixed part shows, about 9 us: lengths, table and first rows are three DRAM latencies in a
 // chain (4.5 us), the last segment's end, its count and the join 3 to 5 us.  32 rows of 2048
 // tokens: 48 us (82 %), 32 ragged ones of 1 .. 4099: 50 us (81 %).  Where segments are a tile

@@ -212,3 +212,16 @@ def test_compact_leaves_an_entry_that_names_a_free_page():
     torch.cuda.synchronize()
     assert table[1, :2].tolist() == [1, 7] and int(b.status) == decode.GS_DEV_BAD_SEQ
     assert refs.tolist() == [1, 1, 0, 0, 0, 0, 0, 0]
+
+
+def test_write_of_more_prompts_than_a_block_has_threads():
+    rng = np.random.default_rng(8)
+    b = Both(pages=6000, page=4, dim=8, heads=1, layers=1, seqs=5000, cols=3)
+    seq = rng.permutation(5000)[:4999].tolist()
+    add = rng.integers(0, 4, 4999).tolist()
+    b.extend(seq, add)
+    start = np.concatenate([[0], np.cumsum(add)]).tolist()
+    k = torch.randn((start[-1], 1, 8), generator=torch.Generator().manual_seed(1)).to(BF16).cuda()
+    b.cache.write(0, k, -k, b.dev(seq), b.dev(start))
+    b.pool.write(0, k.double().cpu().numpy(), -k.double().cpu().numpy(), seq, start)
+    b.check()
