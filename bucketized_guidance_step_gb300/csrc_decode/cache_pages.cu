@@ -12,7 +12,7 @@
 // host knowing the list's length.  It is bound by HBM: each byte is read once and written once.
 //
 // Measured on a GB300 (graph replay): 64 forks of 32 layers of 8 heads of 64 x 128 bf16 pages, half
-// filled (426 MB read and written), 75.4 us, of which the copies take 65 (97 % of the measured copy
+// filled (426 MB read and written), 76.3 us, of which the copies take 65 (97 % of the measured copy
 // rate); compacting 1024 of 4096 pages of 4 layers (537 MB) 87 us (91 %); 24 prompts of 12.8k
 // tokens in all freed, extended and written in 2 layers (210 MB) 46 us (67 %): 37 of them the two
 // writes, 8 the bookkeeping.  That is a chain of DRAM latencies (list, lengths, tables, counts) and
@@ -399,8 +399,12 @@ compact_kernel(CacheView c, int* refs_out, int* live_out) {
     cluster_sync();
 }
 
-// The listed copies: a warp takes one head of one page of one layer of K or V at a time, 8
-// vectors of 16 bytes a lane in flight.  DENSE: a head's rows lie next to each other (64 forks
+constexpr int kUnit = 512;               // vectors a copying warp takes at a time, at most: 8 KB (a
+                                         // head's page whole: 33 us instead of 15 for a few of 128 KB)
+__host__ __device__ inline int pieces_of(int vecs) { return (vecs + kUnit - 1) / kUnit; }
+
+// The listed copies: a warp takes up to 512 vectors of 16 bytes (kUnit) of one head of one page of
+// one layer of K or V at a time, 8 a lane in flight.  DENSE: a head's rows lie next to each other (64 forks
 // 75.5 us, and 80.5 us by rows; compacting 86.9 and 91.8).  With REMAP
 // the table's entries are renumbered too (compact).
 template <bool REMAP, bool DENSE>
@@ -429,21 +433,24 @@ copy_kernel(CacheView c, int es, int* table_out) {
     }
     const int lane = threadIdx.x & 31;
     const int per = c.dim * es / 16;                     // vectors of a row
-    const int sides = 2 * c.layers * c.heads;            // warps' units of a copy
-    const long long units = static_cast<long long>(count) * sides;
+    const int pieces = pieces_of(c.page * per);          // of a head's page
+    const long long sides = 2ll * c.layers * c.heads * pieces;           // warps' units of a copy
+    const long long units = count * sides;
     const long long warps = static_cast<long long>(gridDim.x) * (kCopy / 32);
     for (long long u = static_cast<long long>(blockIdx.x) * (kCopy / 32) + (threadIdx.x >> 5); u < units;
          u += warps) {
-        const int i = static_cast<int>(u / sides), side = static_cast<int>(u - static_cast<long long>(i) * sides);
-        const int head = side % c.heads, which = side / c.heads;
+        const int i = static_cast<int>(u / sides);
+        const long long side = u - i * sides;
+        const int piece = static_cast<int>(side % pieces), row_of_heads = static_cast<int>(side / pieces);
+        const int head = row_of_heads % c.heads, which = row_of_heads / c.heads;
         const int4 w = copies[i];                        // from, to, tokens
         char* const base = ((which & 1) != 0 ? c.v : c.k) +
                            ((which >> 1) * c.layer_stride + head * c.head_stride) * es;
         const char* const src = base + w.x * c.page_stride * es;
         char* const dst = base + w.y * c.page_stride * es;
-        const int vecs = w.z * per;
+        const int vecs = min(w.z * per, (piece + 1) * kUnit);
         constexpr int U = 8;
-        for (int v0 = lane; v0 < vecs; v0 += 32 * U) {
+        for (int v0 = piece * kUnit + lane; v0 < vecs; v0 += 32 * U) {
             uint4 r[U];
             long long off[U];
 #pragma unroll
@@ -466,8 +473,8 @@ copy_kernel(CacheView c, int es, int* table_out) {
     }
 }
 
-// New tokens' K and V into one layer: a warp a token.  The token's first vectors are asked for
-// before its place is looked up.
+// New tokens' K and V into one layer: a warp takes up to 128 vectors of K, and of V, of one token.
+// They are asked for before the token's place is looked up.
 template <class T>
 __global__ void __launch_bounds__(kCopy)
 write_kernel(CacheView c, int layer, const T* k, const T* v,
@@ -477,25 +484,25 @@ write_kernel(CacheView c, int layer, const T* k, const T* v,
     grid_wait();
     grid_trigger();
     const int lane = threadIdx.x & 31;
-    const int t = static_cast<int>((static_cast<long long>(blockIdx.x) * kCopy + threadIdx.x) >> 5);
     constexpr int E = 16 / static_cast<int>(sizeof(T)), U = 4;
     const int per = c.dim / E, vecs = c.heads * per;     // vectors of a row; of a token's K
+    const int parts = (vecs + 32 * U - 1) / (32 * U);
+    const unsigned unit = blockIdx.x * (kCopy / 32) + (threadIdx.x >> 5);
+    const int t = parts == 1 ? static_cast<int>(unit) : static_cast<int>(unit / parts);
+    const int q0 = static_cast<int>(unit - static_cast<unsigned>(t * parts)) * 32 * U + lane;
     const T* const ks = k + t * token_stride;
     const T* const vs = v + t * token_stride;
     uint4 kr[U], vr[U];
     int head[U], x[U];
-    auto fetch = [&](int q0) {
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int q = q0 + i * 32;
-            if (q >= vecs || t >= tokens) continue;
-            head[i] = q / per;
-            x[i] = (q - head[i] * per) * E;
-            kr[i] = load16_any(ks + head[i] * head_stride + x[i], src_aligned != 0);
-            vr[i] = load16_any(vs + head[i] * head_stride + x[i], src_aligned != 0);
-        }
-    };
-    fetch(lane);
+    for (int i = 0; i < U; ++i) {
+        const int q = q0 + i * 32;
+        if (q >= vecs || t >= tokens) continue;
+        head[i] = q / per;
+        x[i] = (q - head[i] * per) * E;
+        kr[i] = load16_any(ks + head[i] * head_stride + x[i], src_aligned != 0);
+        vr[i] = load16_any(vs + head[i] * head_stride + x[i], src_aligned != 0);
+    }
     for (int i = threadIdx.x; i <= n; i += kCopy) first[i] = start[i];
     __syncthreads();
     if (t >= tokens || t < first[0] || t >= first[n]) return;
@@ -524,14 +531,11 @@ write_kernel(CacheView c, int layer, const T* k, const T* v,
     const long long at = layer * c.layer_stride + p * c.page_stride + (pos % c.page) * c.token_stride;
     T* const kd = reinterpret_cast<T*>(c.k) + at;
     T* const vd = reinterpret_cast<T*>(c.v) + at;
-    for (int q0 = lane; q0 < vecs; q0 += 32 * U) {
-        if (q0 != lane) fetch(q0);
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            if (q0 + i * 32 >= vecs) continue;
-            *reinterpret_cast<uint4*>(kd + head[i] * c.head_stride + x[i]) = kr[i];
-            *reinterpret_cast<uint4*>(vd + head[i] * c.head_stride + x[i]) = vr[i];
-        }
+    for (int i = 0; i < U; ++i) {
+        if (q0 + i * 32 >= vecs) continue;
+        *reinterpret_cast<uint4*>(kd + head[i] * c.head_stride + x[i]) = kr[i];
+        *reinterpret_cast<uint4*>(vd + head[i] * c.head_stride + x[i]) = vr[i];
     }
 }
 
@@ -558,11 +562,14 @@ gs_status check_workspace(const gs_kv_cache* c) {
 template <bool REMAP>
 gs_status launch_copies(const CacheView& c, int dtype, long long most, int* table_out,
                         gs_stream stream) {
-    long long blocks = (most * 2 * c.layers * c.heads + kCopy / 32 - 1) / (kCopy / 32);
-    const long long full = static_cast<long long>(sm_count()) * 32;
+    const int es = static_cast<int>(elem_size(dtype));
+    const long long units = most * 2 * c.layers * c.heads * pieces_of(c.page * (c.dim * es / 16));
+    long long blocks = (units + kCopy / 32 - 1) / (kCopy / 32);
+    // Fewer blocks an SM leave the last units to a few warps (64 forks of the case above: 77.8 us at
+    // 8, 76.3 at 16, 75.5 at 32), more cost the call that has nothing to copy (compact: 6.7, 8.0, 10.4).
+    const long long full = static_cast<long long>(sm_count()) * 16;
     if (blocks > full) blocks = full;
     const dim3 grid(static_cast<unsigned>(blocks));
-    const int es = static_cast<int>(elem_size(dtype));
     return c.token_stride == c.dim || c.page == 1
                ? launch(copy_kernel<REMAP, true>, grid, kCopy, 0, 1, stream, c, es, table_out)
                : launch(copy_kernel<REMAP, false>, grid, kCopy, 0, 1, stream, c, es, table_out);
@@ -648,7 +655,9 @@ extern "C" gs_status gs_kv_write(const gs_kv_cache* cache, int32_t layer, const 
         return GS_ERR_INVALID_ARG;
     const int vec = aligned(k, 16) && aligned(v, 16) && (token_stride * es) % 16 == 0 &&
                     (head_stride * es) % 16 == 0;
-    const long long blocks = (32ll * tokens + kCopy - 1) / kCopy;
+    const long long parts = (c.heads * (c.dim * es / 16) + 127) / 128;   // warps a token
+    const long long blocks = (32ll * tokens * parts + kCopy - 1) / kCopy;
+    if (tokens * parts > 0x7ffffff0ll) return GS_ERR_UNSUPPORTED;
     const int smem = 4 * (n + 1);
     const dim3 grid(static_cast<unsigned>(blocks));
     switch (cache->dtype) {
