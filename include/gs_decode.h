@@ -63,7 +63,8 @@ typedef struct gs_kv_cache {
     int64_t layer_stride, page_stride, head_stride, token_stride;
                                 /* each a multiple of 16 bytes; no two (layer, page, head,
                                    token) rows overlap                                    */
-    int32_t seqs, cols;         /* sequences (<= GS_MAX_SEQS); pages a sequence can hold  */
+    int32_t seqs, cols;         /* sequences (<= GS_MAX_SEQS); pages a sequence can hold
+                                   (cols * page <= 2^30)                                  */
     int32_t* table;             /* device int32[seqs][cols]                               */
     int32_t* lens;              /* device int32[seqs]                                     */
     int32_t* refs;              /* device int32[pages]                                    */

@@ -87,6 +87,7 @@ CACHE_REFUSALS = [
     ("token_stride", 68, gs.GS_ERR_UNSUPPORTED), ("head_stride", -64, gs.GS_ERR_INVALID_ARG),
     ("token_stride", 32, gs.GS_ERR_INVALID_ARG), ("seqs", 0, gs.GS_ERR_INVALID_ARG),
     ("seqs", 8193, gs.GS_ERR_UNSUPPORTED), ("cols", 1 << 28, gs.GS_ERR_UNSUPPORTED),
+    ("cols", (1 << 26) + 1, gs.GS_ERR_UNSUPPORTED),
 ]
 
 
