@@ -30,15 +30,10 @@ constexpr int kCopy = 256;               // threads of a copy block
 constexpr int kNone = 0x7fffffff;
 constexpr int kOnePages = 1024, kOneCells = 512;     // of a pool and a list that one block keeps
 
-// Workspace: [0] the number of copies, [4 ..] the copies as (from, to, tokens, -),
-// then (compact) a word a page: the rank of a moved page.
 struct Copy {
     int from, to, tokens, pad;
 };
 __device__ __forceinline__ Copy* copies_of(int* work) { return reinterpret_cast<Copy*>(work + 4); }
-inline long long copy_slots(const gs_kv_cache* c) {
-    return c->pages > c->seqs ? c->pages : c->seqs;
-}
 
 __device__ __forceinline__ int pages_of(int len, int page) { return (len + page - 1) / page; }
 
@@ -175,7 +170,10 @@ extend_kernel(CacheView c, const int* seq, const int* add, int n) {
             if (len < 0 || len > c.cols * c.page) {
                 if (first_block) flag(c.status, GS_DEV_BAD_SEQ);
             } else if (total > static_cast<long long>(c.cols) * c.page) {
-                if (first_block) flag(c.status, GS_DEV_NO_PAGE);
+                if (first_block) {
+                    flag(c.status, GS_DEV_NO_PAGE);
+                    c.refused[s] = len + 1;
+                }
             } else {
                 have = pages_of(len, c.page);
                 want = pages_of(static_cast<int>(total), c.page) - have;
@@ -213,10 +211,14 @@ extend_kernel(CacheView c, const int* seq, const int* add, int n) {
     }
     for (int i = rank_in<BLOCKS>() * kMeta + threadIdx.x; i < n; i += BLOCKS * kMeta) {
         if (held[i] < 0) continue;
-        if (need[i] == 0 || at[i] + need[i] <= avail)
-            c.lens[ids[i]] += add != nullptr ? add[i] : 1;
-        else
+        const int s = ids[i], more = add != nullptr ? add[i] : 1;
+        if (need[i] == 0 || at[i] + need[i] <= avail) {
+            c.lens[s] += more;
+            if (more > 0) c.refused[s] = 0;
+        } else {
+            c.refused[s] = c.lens[s] + 1;
             flag(c.status, GS_DEV_NO_PAGE);
+        }
     }
 }
 
@@ -538,19 +540,24 @@ write_kernel(CacheView c, int layer, const T* k, const T* v,
     }
     const int s = seq[lo];
     bool ok = s >= 0 && s < c.seqs;
+    unsigned why = GS_DEV_BAD_SEQ;
     long long pos = -1;
     if (ok) {
-        const int len = c.lens[s];
+        const int len = c.lens[s], mark = c.refused[s];
         pos = static_cast<long long>(len) - (first[lo + 1] - t);
         ok = pos >= 0 && pos < len && len <= c.cols * c.page;
+        if (ok && was_refused(mark, len)) {              // these are tokens that it held before
+            ok = false;
+            why = GS_DEV_NO_PAGE;
+        }
     }
     int p = -1;
     if (ok) {
         p = c.table[static_cast<long long>(s) * c.cols + pos / c.page];
-        ok = p >= 0 && p < c.pages;
+        ok = p >= 0 && p < c.pages && __ldcg(c.refs + p) <= 1;      // never into a shared page
     }
     if (!ok) {
-        if (lane == 0) flag(c.status, GS_DEV_BAD_SEQ);
+        if (lane == 0) flag(c.status, why);
         return;
     }
     const long long at = layer * c.layer_stride + p * c.page_stride + (pos % c.page) * c.token_stride;
@@ -564,22 +571,11 @@ write_kernel(CacheView c, int layer, const T* k, const T* v,
     }
 }
 
-long long workspace_need(const gs_kv_cache* c) {
-    return 4 * (4 + 4 * copy_slots(c) + static_cast<long long>(c->pages));
-}
-
 gs_status check_call(const gs_kv_cache* cache, int32_t n, CacheView* view) {
     const gs_status st = check_cache(cache, view);
     if (st != GS_OK) return st;
     if (n < 0) return GS_ERR_INVALID_ARG;
     if (n > GS_MAX_SEQS) return GS_ERR_UNSUPPORTED;
-    return GS_OK;
-}
-
-gs_status check_workspace(const gs_kv_cache* c) {
-    if (c->workspace == nullptr || !aligned(c->workspace, 16) ||
-        c->workspace_bytes < workspace_need(c))
-        return GS_ERR_INVALID_ARG;
     return GS_OK;
 }
 
@@ -621,10 +617,12 @@ extern "C" gs_status gs_pages_workspace(const gs_kv_cache* cache, int64_t* bytes
 extern "C" gs_status gs_pages_extend(const gs_kv_cache* cache, const int32_t* seq,
                                      const int32_t* add, int32_t n, gs_stream stream) {
     CacheView c;
-    const gs_status st = check_call(cache, n, &c);
+    gs_status st = check_call(cache, n, &c);
     if (st != GS_OK) return st;
     if (n == 0) return GS_OK;
     if (seq == nullptr) return GS_ERR_INVALID_ARG;
+    st = check_workspace(cache);
+    if (st != GS_OK) return st;
     const int smem = 4 * (c.seqs + 4 * n);
     if (one_block(c, n)) {
         if (!allow_smem<extend_kernel<1>>(smem)) return GS_ERR_CUDA;
@@ -682,10 +680,12 @@ extern "C" gs_status gs_kv_write(const gs_kv_cache* cache, int32_t layer, const 
                                  int32_t tokens, const int32_t* seq, const int32_t* start,
                                  int32_t n, gs_stream stream) {
     CacheView c;
-    const gs_status st = check_call(cache, n, &c);
+    gs_status st = check_call(cache, n, &c);
     if (st != GS_OK) return st;
     if (layer < 0 || layer >= c.layers || tokens < 0) return GS_ERR_INVALID_ARG;
     if (n == 0 || tokens == 0) return GS_OK;
+    st = check_workspace(cache);
+    if (st != GS_OK) return st;
     const long long es = elem_size(cache->dtype);
     if (k == nullptr || v == nullptr || seq == nullptr || start == nullptr ||
         !aligned(k, es) || !aligned(v, es) || token_stride < 0 || head_stride < 0)

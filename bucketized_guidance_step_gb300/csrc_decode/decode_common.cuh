@@ -35,7 +35,31 @@ struct CacheView {
     int* refs;
     unsigned* status;
     int* work;
+    int* refused;                         // [seqs] of the workspace, see below; null without one
 };
+
+// A cache's workspace, in words: [0] the number of copies a call asks for, [1] held pages, [4 ..]
+// the copies as (from, to, tokens, -), then a word a page (compact: the rank of a moved page), then
+// a word a sequence: what gs_pages_extend refused it last.  That word is the sequence's length + 1
+// at the time (0: nothing), so that it says nothing of a sequence whose length has changed since.
+inline long long copy_slots(const gs_kv_cache* c) {
+    return c->pages > c->seqs ? c->pages : c->seqs;
+}
+inline long long refused_at(const gs_kv_cache* c) {
+    return 4 + 4 * copy_slots(c) + static_cast<long long>(c->pages);
+}
+inline long long workspace_need(const gs_kv_cache* c) {
+    return 4 * (refused_at(c) + c->seqs);
+}
+inline gs_status check_workspace(const gs_kv_cache* c) {
+    if (c->workspace == nullptr || !aligned(c->workspace, 16) ||
+        c->workspace_bytes < workspace_need(c))
+        return GS_ERR_INVALID_ARG;
+    return GS_OK;
+}
+// Whether gs_pages_extend left the sequence at this length: its last positions were not given to
+// the tokens that come.
+__device__ __forceinline__ bool was_refused(int mark, int len) { return mark == len + 1; }
 
 // Sizes alone (what a workspace depends on).
 inline gs_status check_cache_sizes(const gs_kv_cache* c) {
@@ -86,6 +110,7 @@ inline gs_status check_cache(const gs_kv_cache* c, CacheView* out) {
     out->refs = c->refs;
     out->status = c->dev_status;
     out->work = static_cast<int*>(c->workspace);
+    out->refused = out->work != nullptr ? out->work + refused_at(c) : nullptr;
     return GS_OK;
 }
 

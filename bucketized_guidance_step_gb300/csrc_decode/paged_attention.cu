@@ -234,6 +234,7 @@ extern "C" gs_status gs_paged_attention(const gs_paged_attention_args* args, gs_
     if (args->layer < 0 || args->layer >= p.c.layers) return GS_ERR_INVALID_ARG;
     if (args->seq == nullptr && args->batch > p.c.seqs) return GS_ERR_INVALID_ARG;
     if ((args->k_new == nullptr) != (args->v_new == nullptr)) return GS_ERR_INVALID_ARG;
+    if (args->k_new != nullptr && check_workspace(args->cache) != GS_OK) return GS_ERR_INVALID_ARG;
     if (!std::isfinite(args->scale)) return GS_ERR_INVALID_ARG;
     if (args->batch == 0) return GS_OK;
     if (args->q == nullptr || args->out == nullptr || !aligned(args->q, es) ||

@@ -390,7 +390,7 @@ struct Pending {
                                                          // where runs cross pages)
     int lo, hi;                                          // visible rows
     int fresh;                                           // the row of the new token, or -1
-    int b, hg;
+    int b, hg, seq;
 };
 
 template <class P>
@@ -441,6 +441,7 @@ attention_kernel(const __grid_constant__ AttnParams p) {
         Pending w;
         w.b = c.b;
         w.hg = c.hg;
+        w.seq = c.row.seq;
         const int j = c.tile * TILE + warp * RUN;
         const bool sink = j < c.row.turn;
         const int pos = sink ? j : j - c.row.turn + c.row.from;
@@ -530,17 +531,29 @@ attention_kernel(const __grid_constant__ AttnParams p) {
             const long long row = (from - p.c.k) + (p.page_runs ? r * p.c.token_stride * static_cast<int>(sizeof(T)) : 0);
             const int from_lane = p.page_runs ? 0 : r;
             const long long at = __shfl_sync(0xffffffffu, row, from_lane);
-            const bool store = __shfl_sync(0xffffffffu, ok ? 1 : 0, from_lane) != 0 && w.hg == head * p.parts;
+            const int page = __shfl_sync(0xffffffffu, ok ? w.page : -1, from_lane);
+            // If the position is the token's own: the sequence got it by its last extension, and
+            // the page is not shared.  Else the row is read from the cache as any other.  (Asked for
+            // beside the row, so that it costs no latency of its own.)
+            const int len = p.c.lens[w.seq], mark = p.c.refused[w.seq];
+            const int holders = page >= 0 ? p.c.refs[page] : 0;
             for (int c = lane; c * V < dim; c += 32) {
                 const long long n = w.b * p.new_batch + head * p.new_head + c * V;
                 const uint4 k = load16_any(static_cast<const T*>(p.k_new) + n, p.new_aligned != 0);
                 const uint4 v = load16_any(static_cast<const T*>(p.v_new) + n, p.new_aligned != 0);
-                char* to = ring + slot * L::kStage + r * L::kRow + ((c ^ (r & 7)) << 4);
-                *reinterpret_cast<uint4*>(to) = k;
-                *reinterpret_cast<uint4*>(to + L::kHalf) = v;
-                if (store) {
-                    *reinterpret_cast<uint4*>(p.c.k + at + 16 * c) = k;
-                    *reinterpret_cast<uint4*>(p.c.v + at + 16 * c) = v;
+                const int off = slot * L::kStage + r * L::kRow + ((c ^ (r & 7)) << 4);
+                if (holders <= 1 && !was_refused(mark, len)) {
+                    *reinterpret_cast<uint4*>(ring + off) = k;
+                    *reinterpret_cast<uint4*>(ring + off + L::kHalf) = v;
+                    if (page >= 0 && w.hg == head * p.parts) {
+                        *reinterpret_cast<uint4*>(p.c.k + at + 16 * c) = k;
+                        *reinterpret_cast<uint4*>(p.c.v + at + 16 * c) = v;
+                    }
+                } else {
+                    const int size = page >= 0 ? 16 : 0;
+                    copy_async(ring_at + off, p.c.k + at + 16 * c, size);
+                    copy_async(ring_at + off + L::kHalf, p.c.v + at + 16 * c, size);
+                    if (c == 0) flag(p.c.status, was_refused(mark, len) ? GS_DEV_NO_PAGE : GS_DEV_BAD_SEQ);
                 }
             }
         }

@@ -159,10 +159,12 @@ class PagedCache:
     k, v: [layers, pages, kv_heads, page, dim], fp32, bf16 or fp16, the same strides (any
     order of the first four dimensions: a permuted view serves), the last dimension dense,
     every row on 16 bytes. table: int32 [seqs, cols], lens: int32 [seqs], refs: int32 [pages]
-    (lens and refs start as zeros). status: int32 [1], device flags OR-ed in.
+    (lens and refs start as zeros). status: int32 [1], device flags OR-ed in. workspace: int32,
+    made (zeros) where none is given; caches over one table (k and v of a layer each, say) pass the
+    first one's .workspace, as it also keeps which sequences the last extension refused.
     """
 
-    def __init__(self, k, v, table, lens, refs, *, status=None):
+    def __init__(self, k, v, table, lens, refs, *, status=None, workspace=None):
         import torch
         if k.dim() != 5 or tuple(k.shape) != tuple(v.shape) or k.dtype != v.dtype:
             raise ValueError("k and v must be [layers, pages, kv_heads, page, dim] alike")
@@ -187,12 +189,16 @@ class PagedCache:
         d.dev_status = _ptr(status, "status", dev, torch.int32)
         n = ctypes.c_int64(0)
         gs._check("gs_pages_workspace", lib.gs_pages_workspace(ctypes.byref(d), ctypes.byref(n)))
-        work = torch.empty((n.value + 3) // 4, dtype=torch.int32, device=dev)
-        d.workspace, d.workspace_bytes = work.data_ptr(), work.numel() * 4
+        if workspace is None:
+            workspace = torch.zeros((n.value + 3) // 4, dtype=torch.int32, device=dev)
+        elif workspace.numel() * 4 < n.value:
+            raise ValueError(f"workspace must hold {(n.value + 3) // 4} words")
+        d.workspace, d.workspace_bytes = _ptr(workspace, "workspace", dev, torch.int32), workspace.numel() * 4
         self.k, self.v, self.table, self.lens, self.refs, self.status = k, v, table, lens, refs, status
+        self.workspace = workspace
         self.device = dev
         self._desc = d
-        self._keep = (k, v, table, lens, refs, status, work)
+        self._keep = (k, v, table, lens, refs, status, workspace)
 
     def _call(self, name, args, *keep) -> Call:
         return Call(name, (ctypes.byref(self._desc),) + args, self.device, (self, self._desc) + keep)

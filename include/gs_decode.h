@@ -69,8 +69,10 @@ typedef struct gs_kv_cache {
     int32_t* lens;              /* device int32[seqs]                                     */
     int32_t* refs;              /* device int32[pages]                                    */
     uint32_t* dev_status;       /* device uint32 or NULL: GS_DEV_* bits OR-ed in          */
-    void*    workspace;         /* device, gs_pages_workspace bytes, 16-byte aligned; its
-                                   contents need not be kept or set                       */
+    void*    workspace;         /* device, gs_pages_workspace bytes, 16-byte aligned, all 0
+                                   before its first use: it keeps which sequences the last
+                                   gs_pages_extend refused (descriptions that share a table
+                                   share it too)                                          */
     int64_t  workspace_bytes;
 } gs_kv_cache;
 
@@ -82,8 +84,10 @@ gs_status gs_pages_workspace(const gs_kv_cache* cache, int64_t* bytes);
  * gs_pages_extend -- room for add[i] more tokens of sequence seq[i]: takes the pages that
  * the longer sequences need and adds to their lengths.  Free pages are taken lowest number
  * first, in the order of the list.  Entry i is served when the needs of all entries up to
- * and including it fit the free pages (an entry that needs none always is) and its row of the table; else it is left as it
- * is and GS_DEV_NO_PAGE is set.  An id outside the cache, a negative add and the second
+ * and including it fit the free pages (an entry that needs none always is) and its row of the
+ * table; else it is left as it is, GS_DEV_NO_PAGE is set, and nothing is stored for the
+ * sequence (gs_kv_write, the append of gs_paged_attention) until an extension by one token or
+ * more is served or its length is another.  An id outside the cache, a negative add and the second
  * listing of a sequence are skipped (GS_DEV_BAD_SEQ).
  *
  * seq: device int32[n].  add: device int32[n], or NULL (one token each).
@@ -126,8 +130,9 @@ gs_status gs_pages_compact(const gs_kv_cache* cache, int32_t* table_out, int32_t
 /*
  * gs_kv_write -- store the K and V of new tokens in one layer: rows start[i] .. start[i+1]-1
  * of k and v are the last start[i+1] - start[i] tokens of sequence seq[i] (after
- * gs_pages_extend).  Rows that would lie before the sequence's first token are skipped
- * (GS_DEV_BAD_SEQ), as are rows outside 0 .. tokens-1.
+ * gs_pages_extend).  Rows that would lie before the sequence's first token or in a page that
+ * other sequences share are skipped (GS_DEV_BAD_SEQ), as are rows outside 0 .. tokens-1 and the
+ * rows of a sequence whose last extension was refused (GS_DEV_NO_PAGE).
  *
  * k, v: device, storage dtype, [tokens][kv_heads][dim] with the strides given (elements;
  * dim has stride 1; any alignment).  seq: device int32[n].  start: device int32[n+1], rising.
@@ -141,7 +146,7 @@ gs_status gs_kv_write(const gs_kv_cache* cache, int32_t layer, const void* k, co
 /* ------------------------------------------------------------------------ */
 
 typedef struct gs_paged_attention_args {
-    const gs_kv_cache* cache;   /* its workspace and refs are not used                    */
+    const gs_kv_cache* cache;   /* its workspace is used where k_new is given             */
     int32_t layer;
     int32_t batch;              /* query rows (<= GS_MAX_SEQS)                             */
     const int32_t* seq;         /* device int32[batch]: row b reads sequence seq[b] (rows
@@ -153,7 +158,10 @@ typedef struct gs_paged_attention_args {
     int64_t q_batch_stride, q_head_stride;
     const void* k_new;          /* device, cache dtype, [batch][kv_heads][dim], or NULL:   */
     const void* v_new;          /* stored at the sequence's last position (lens - 1) and
-                                   attended to from there; both or neither                */
+                                   attended to from there; both or neither.  Where that
+                                   position is not the new token's (its extension was
+                                   refused, or other sequences share the page), nothing is
+                                   stored and the row attends over what the cache holds   */
     int64_t new_batch_stride, new_head_stride;
     float   scale;              /* of the scores (usually dim ** -0.5); finite            */
     int32_t window;             /* 0: every position; else the last `window` ...          */
@@ -182,7 +190,8 @@ gs_status gs_paged_attention_workspace(const gs_paged_attention_args* args, int6
  * whatever they hold.  Results do not depend on the grid's timing: the parts of a split
  * sequence are joined in their order.
  * Device-found: GS_DEV_BAD_SEQ (a sequence id outside the cache: as length 0; a page id
- * outside the pool: its rows read as zeros; a length past the table: cut).
+ * outside the pool: its rows read as zeros; a length past the table: cut; a new token whose
+ * page other sequences share), GS_DEV_NO_PAGE (a new token whose extension was refused).
  * Errors: as the page calls', and GS_ERR_INVALID_ARG for q_heads not a multiple of kv_heads,
  * layer outside the cache, k_new without v_new, window or sinks < 0, sinks without window,
  * a scale that is not finite; GS_ERR_UNSUPPORTED also where batch * q_heads * cols * page / 32
