@@ -4,7 +4,8 @@ A ``PagedCache`` describes a key-value cache in the caller's tensors; its method
 calls on it. ``guided_logits`` turns a step's logits into the next tokens. Every call has a
 ``prepare_*`` form that checks the arguments once and returns a ``Call``: calling it launches
 the same work again on the same buffers (their contents may change, their addresses may not),
-on ``torch.cuda.current_stream()``, as a sampler's loop or a CUDA graph's capture does.
+on their device and its ``torch.cuda.current_stream()``, as a sampler's loop or a CUDA graph's
+capture does.
 
 As in ``gs``, the arithmetic is the library's; a missing library raises ``GSLibraryError``.
 """
@@ -108,11 +109,19 @@ class Call:
         self._args = args                       # ctypes values, the stream excepted
         self._keep = keep                       # tensors and structs behind the pointers
         self._device = device.index
+        # The library launches on the current device: a stream's handle does not name one (the
+        # default stream's is 0 on each).
+        self._current = torch._C._cuda_getDevice
+        self._guard = torch.cuda.device
         # The handle alone: torch.cuda.current_stream() builds a Stream object around it (1 us).
         self._stream = torch._C._cuda_getCurrentRawStream
 
     def __call__(self) -> None:
-        status = self._fn(*self._args, self._stream(self._device))
+        if self._current() == self._device:
+            status = self._fn(*self._args, self._stream(self._device))
+        else:
+            with self._guard(self._device):
+                status = self._fn(*self._args, self._stream(self._device))
         if status != gs.GS_OK:
             raise GSError(self._name, status)
 
@@ -323,7 +332,8 @@ def _zeroed(fn: str, args, device):
     """The workspace that `fn` asks for, zeroed and entered into args."""
     import torch
     n = ctypes.c_int64(0)
-    gs._check(fn, getattr(load(), fn)(ctypes.byref(args), ctypes.byref(n)))
+    with torch.cuda.device(device):
+        gs._check(fn, getattr(load(), fn)(ctypes.byref(args), ctypes.byref(n)))
     work = torch.zeros(max(1, (n.value + 3) // 4), dtype=torch.int32, device=device)
     args.workspace, args.workspace_bytes = work.data_ptr(), work.numel() * 4
     return work
