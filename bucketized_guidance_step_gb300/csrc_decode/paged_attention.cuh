@@ -532,20 +532,22 @@ attention_kernel(const __grid_constant__ AttnParams p) {
             const int from_lane = p.page_runs ? 0 : r;
             const long long at = __shfl_sync(0xffffffffu, row, from_lane);
             const int page = __shfl_sync(0xffffffffu, ok ? w.page : -1, from_lane);
-            // If the position is the token's own: the sequence got it by its last extension, and
-            // the page is not shared.  Else the row is read from the cache as any other.  (Asked for
-            // beside the row, so that it costs no latency of its own.)
+            // If the position is the token's own: the sequence got it by its last extension, its
+            // length was not cut, and its page is in the pool and not shared.  Else the row is read
+            // from the cache as any other.  (Asked for beside the row, so that it costs no latency
+            // of its own.)
             const int len = p.c.lens[w.seq], mark = p.c.refused[w.seq];
-            const int holders = page >= 0 ? p.c.refs[page] : 0;
+            const int holders = page >= 0 ? p.c.refs[page] : 2;
+            const bool own = holders <= 1 && len <= p.c.cols * p.c.page && !was_refused(mark, len);
             for (int c = lane; c * V < dim; c += 32) {
                 const long long n = w.b * p.new_batch + head * p.new_head + c * V;
                 const uint4 k = load16_any(static_cast<const T*>(p.k_new) + n, p.new_aligned != 0);
                 const uint4 v = load16_any(static_cast<const T*>(p.v_new) + n, p.new_aligned != 0);
                 const int off = slot * L::kStage + r * L::kRow + ((c ^ (r & 7)) << 4);
-                if (holders <= 1 && !was_refused(mark, len)) {
+                if (own) {
                     *reinterpret_cast<uint4*>(ring + off) = k;
                     *reinterpret_cast<uint4*>(ring + off + L::kHalf) = v;
-                    if (page >= 0 && w.hg == head * p.parts) {
+                    if (w.hg == head * p.parts) {
                         *reinterpret_cast<uint4*>(p.c.k + at + 16 * c) = k;
                         *reinterpret_cast<uint4*>(p.c.v + at + 16 * c) = v;
                     }

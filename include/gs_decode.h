@@ -160,8 +160,9 @@ typedef struct gs_paged_attention_args {
     const void* v_new;          /* stored at the sequence's last position (lens - 1) and
                                    attended to from there; both or neither.  Where that
                                    position is not the new token's (its extension was
-                                   refused, or other sequences share the page), nothing is
-                                   stored and the row attends over what the cache holds   */
+                                   refused, the length was cut, or the page is shared or
+                                   outside the pool), nothing is stored and the row attends
+                                   over what the cache holds                              */
     int64_t new_batch_stride, new_head_stride;
     float   scale;              /* of the scores (usually dim ** -0.5); finite            */
     int32_t window;             /* 0: every position; else the last `window` ...          */
@@ -190,8 +191,8 @@ gs_status gs_paged_attention_workspace(const gs_paged_attention_args* args, int6
  * whatever they hold.  Results do not depend on the grid's timing: the parts of a split
  * sequence are joined in their order.
  * Device-found: GS_DEV_BAD_SEQ (a sequence id outside the cache: as length 0; a page id
- * outside the pool: its rows read as zeros; a length past the table: cut; a new token whose
- * page other sequences share), GS_DEV_NO_PAGE (a new token whose extension was refused).
+ * outside the pool: its rows read as zeros; a length past the table: cut, and no new token
+ * stored; a new token whose page other sequences share), GS_DEV_NO_PAGE (a new token whose extension was refused).
  * Errors: as the page calls', and GS_ERR_INVALID_ARG for q_heads not a multiple of kv_heads,
  * layer outside the cache, k_new without v_new, window or sinks < 0, sinks without window,
  * a scale that is not finite; GS_ERR_UNSUPPORTED also where batch * q_heads * cols * page / 32

@@ -1,0 +1,36 @@
+"""States that no call makes and lists that fit nothing: flagged, and nothing else is touched (GPU)."""
+
+import pytest
+import torch
+
+from bucketized_guidance_step_gb300 import decode
+from tests.test_decode_refused_stores import BF16, attend, make, new_tokens, word
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("page", [5, 16])
+@pytest.mark.parametrize("length", [2 ** 20, 2 ** 31 - 1])
+def test_append_past_the_table_stores_nothing(page, length):
+    """The row is cut to what the table can hold; its last token there is not the new one's place."""
+    c = make(3, page, 1, 2)
+    c.extend(c.refs.new_tensor([0]), c.refs.new_tensor([2 * page]))
+    plain, before = attend(c, [0], 3), (c.k.clone(), c.v.clone())
+    assert word(c) == 0
+    c.lens.fill_(length)
+    got = attend(c, [0], 3, *new_tokens(1, BF16))
+    assert torch.equal(c.k, before[0]) and torch.equal(c.v, before[1]) and word(c) == decode.GS_DEV_BAD_SEQ
+    assert torch.equal(got[0], plain[0]) and torch.equal(got[1], plain[1])
+
+
+@pytest.mark.parametrize("page", [5, 16])
+def test_append_to_a_page_outside_the_pool_reads_zeros(page):
+    """As without the append: rows of such a page read as zeros, the new token's too."""
+    c = make(3, page, 1, 2)
+    c.extend(c.refs.new_tensor([0]), c.refs.new_tensor([page + 2]))
+    c.table[0, 1] = 7
+    plain, before = attend(c, [0], 3), (c.k.clone(), c.v.clone())
+    assert word(c) == decode.GS_DEV_BAD_SEQ
+    got = attend(c, [0], 3, *new_tokens(1, BF16))
+    assert torch.equal(c.k, before[0]) and torch.equal(c.v, before[1]) and word(c) == decode.GS_DEV_BAD_SEQ
+    assert torch.equal(got[0], plain[0]) and torch.equal(got[1], plain[1])
