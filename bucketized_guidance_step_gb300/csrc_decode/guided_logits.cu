@@ -514,6 +514,7 @@ logits_kernel(const __grid_constant__ LogitParams p) {
             __threadfence();
         }
         if (__shfl_sync(0xffffffffu, last, 0) == 0) return;
+        __syncwarp();                                    // thread 0's fence holds for all lanes
         Part all = no_part();
         for (int c0 = 0; c0 < p.chunks; c0 += 32) {      // in the order of the chunks
             const int c = c0 + static_cast<int>(threadIdx.x);
