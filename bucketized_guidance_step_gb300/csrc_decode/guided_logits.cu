@@ -558,6 +558,7 @@ gs_status cut_of(const gs_guided_logits_args* a, Cut* cut) {
     if (a == nullptr || a->batch < 0 || a->vocab < 1 || a->tokens_stride < 0 || !known_dtype(a->dtype))
         return GS_ERR_INVALID_ARG;
     if (a->batch > GS_MAX_SEQS || a->vocab > (1 << 28)) return GS_ERR_UNSUPPORTED;
+    if (a->tokens != nullptr && a->tokens_stride > (1ll << 30)) return GS_ERR_UNSUPPORTED;   // (t0 + 2048 is an int)
     const int in = a->dtype == GS_DTYPE_F32 ? Stream<float, true>::size() : Stream<__half, true>::size();
     int stage = in;
     cut->off_uncond = stage;

@@ -219,7 +219,7 @@ typedef struct gs_guided_logits_args {
     const float* bias;          /* device float[.][vocab] or NULL                         */
     int64_t bias_stride;        /* elements between rows; 0 = one row for all             */
     const int32_t* tokens;      /* device int32[batch][tokens_stride] or NULL: history     */
-    int64_t tokens_stride;      /* >= 0: entries a row holds                               */
+    int64_t tokens_stride;      /* >= 0, <= 2^30: entries a row holds                      */
     const int32_t* tokens_len;  /* device int32[batch]: prompt and output tokens in a row;
                                    entries outside 0 .. vocab-1 are passed over           */
     const int32_t* prompt_len;  /* device int32[batch] or NULL (= 0)                      */
@@ -267,8 +267,8 @@ gs_status gs_guided_logits_workspace(const gs_guided_logits_args* args, int64_t*
  * missing uncond (scale not 1: GS_DEV_NEED_UNCOND) is not written, but for its token (-1).
  * Errors: GS_ERR_INVALID_ARG (NULL cond, sizes, strides, unknown dtype, tokens without
  * tokens_len, no output at all, workspace too small, step outside the table),
- * GS_ERR_UNSUPPORTED (batch over GS_MAX_SEQS, vocab over 2^28), GS_ERR_CUDA.  No output may
- * overlap an input or another output.
+ * GS_ERR_UNSUPPORTED (batch over GS_MAX_SEQS, vocab over 2^28, tokens_stride over 2^30),
+ * GS_ERR_CUDA.  No output may overlap an input or another output.
  */
 gs_status gs_guided_logits(const gs_guided_logits_args* args, gs_stream stream);
 
