@@ -69,6 +69,7 @@ inline gs_status check_cache_sizes(const gs_kv_cache* c) {
         return GS_ERR_INVALID_ARG;
     if (c->seqs > GS_MAX_SEQS || c->pages > (1 << 28) || c->page > (1 << 20) || c->kv_heads > (1 << 16) ||
         static_cast<long long>(c->cols) * c->page > (1ll << 30) ||
+        static_cast<long long>(c->layers) * c->kv_heads > (1ll << 30) ||
         static_cast<long long>(c->kv_heads) * c->page * c->dim > (1ll << 30))
         return GS_ERR_UNSUPPORTED;
     if (c->dim > 256 || (c->dim * elem_size(c->dtype)) % 16 != 0) return GS_ERR_UNSUPPORTED;

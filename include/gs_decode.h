@@ -55,7 +55,8 @@ extern "C" {
 typedef struct gs_kv_cache {
     int32_t dtype;              /* GS_DTYPE_*                                             */
     int32_t layers, pages;      /* >= 1                                                   */
-    int32_t kv_heads, page;     /* >= 1; page = tokens a page holds                       */
+    int32_t kv_heads, page;     /* >= 1; page = tokens a page holds; layers * kv_heads <=
+                                   2^30                                                   */
     int32_t dim;                /* head dimension: dim * element size a multiple of 16
                                    bytes, dim <= 256                                      */
     void*   k;                  /* device, 16-byte aligned                                */
