@@ -331,8 +331,8 @@ fork_kernel(CacheView c, const int* src, const int* dst, int n) {
     sync_all<BLOCKS>();                      // no block ends while another reads its count
 }
 
-// One warp a listed sequence.  Its length is taken once (atomicExch), so that a second listing
-// finds nothing to release.
+// One warp a listed sequence.  Its length is taken once (atomicCAS), so that a second listing
+// finds nothing to release; one outside its range stays.
 __global__ void __launch_bounds__(128) free_kernel(CacheView c, const int* seq, int n) {
     grid_wait();
     grid_trigger();
@@ -344,12 +344,15 @@ __global__ void __launch_bounds__(128) free_kernel(CacheView c, const int* seq, 
         return;
     }
     int len = 0;
-    if (lane == 0) len = atomicExch(c.lens + s, 0);
-    len = __shfl_sync(0xffffffffu, len, 0);
-    if (len < 0 || len > c.cols * c.page) {
-        if (lane == 0) flag(c.status, GS_DEV_BAD_SEQ);
-        return;
+    if (lane == 0) {
+        len = c.lens[s];
+        if (len < 0 || len > c.cols * c.page) {
+            flag(c.status, GS_DEV_BAD_SEQ);
+            len = 0;
+        }
+        if (len > 0 && atomicCAS(c.lens + s, len, 0) != len) len = 0;
     }
+    len = __shfl_sync(0xffffffffu, len, 0);
     const int held = pages_of(len, c.page);
     int* row = c.table + static_cast<long long>(s) * c.cols;
     for (int j = lane; j < held; j += 32) {

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from bucketized_guidance_step_gb300 import decode
+from tests.test_decode_pages import Both
 from tests.test_decode_refused_stores import BF16, attend, make, new_tokens, word
 
 pytestmark = pytest.mark.gpu
@@ -34,3 +35,21 @@ def test_append_to_a_page_outside_the_pool_reads_zeros(page):
     got = attend(c, [0], 3, *new_tokens(1, BF16))
     assert torch.equal(c.k, before[0]) and torch.equal(c.v, before[1]) and word(c) == decode.GS_DEV_BAD_SEQ
     assert torch.equal(got[0], plain[0]) and torch.equal(got[1], plain[1])
+
+
+@pytest.mark.parametrize("length", [-1, -2 ** 31, 33, 2 ** 31 - 1])
+def test_free_leaves_a_sequence_whose_length_is_none(length):
+    b = Both(page=8, cols=4)
+    b.extend([0, 1], [20, 9])
+    table, refs = b.table.clone(), b.refs.clone()
+    b.lens[0] = length
+    b.cache.free(b.dev([0, 1, 0]))
+    torch.cuda.synchronize()
+    assert b.lens.tolist()[:2] == [length, 0] and int(b.status) == decode.GS_DEV_BAD_SEQ
+    refs[table[1, :2].long()] = 0
+    table[1, :2] = -1
+    assert torch.equal(b.table, table) and torch.equal(b.refs, refs)
+    b.lens[0] = 20                                     # put right, it can be freed
+    b.cache.free(b.dev([0]))
+    torch.cuda.synchronize()
+    assert not b.refs.any() and (b.table == -1).all() and not b.lens.any()
