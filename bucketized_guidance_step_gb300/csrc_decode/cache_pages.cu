@@ -535,6 +535,7 @@ write_kernel(CacheView c, int layer, const T* k, const T* v,
     }
     for (int i = threadIdx.x; i <= n; i += kCopy) first[i] = start[i];
     __syncthreads();
+    if (unit == 0 && lane == 0 && (first[0] < 0 || first[n] > tokens)) flag(c.status, GS_DEV_BAD_SEQ);
     if (t >= tokens || t < first[0] || t >= first[n]) return;
     int lo = 0, hi = n;                                  // the last i with start[i] <= t
     while (hi - lo > 1) {

@@ -132,8 +132,9 @@ gs_status gs_pages_compact(const gs_kv_cache* cache, int32_t* table_out, int32_t
  * gs_kv_write -- store the K and V of new tokens in one layer: rows start[i] .. start[i+1]-1
  * of k and v are the last start[i+1] - start[i] tokens of sequence seq[i] (after
  * gs_pages_extend).  Rows that would lie before the sequence's first token or in a page that
- * other sequences share are skipped (GS_DEV_BAD_SEQ), as are rows outside 0 .. tokens-1 and the
- * rows of a sequence whose last extension was refused (GS_DEV_NO_PAGE).
+ * other sequences share, and rows outside 0 .. tokens-1, are skipped (GS_DEV_BAD_SEQ), as are
+ * the rows of a sequence whose last extension was refused (GS_DEV_NO_PAGE).  tokens = 0 does
+ * nothing.
  *
  * k, v: device, storage dtype, [tokens][kv_heads][dim] with the strides given (elements;
  * dim has stride 1; any alignment).  seq: device int32[n].  start: device int32[n+1], rising.

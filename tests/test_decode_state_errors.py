@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from bucketized_guidance_step_gb300 import decode
-from tests.test_decode_pages import Both
+from tests.test_decode_pages import F32, Both
 from tests.test_decode_refused_stores import BF16, attend, make, new_tokens, word
 
 pytestmark = pytest.mark.gpu
@@ -53,3 +53,19 @@ def test_free_leaves_a_sequence_whose_length_is_none(length):
     b.cache.free(b.dev([0]))
     torch.cuda.synchronize()
     assert not b.refs.any() and (b.table == -1).all() and not b.lens.any()
+
+
+@pytest.mark.parametrize("start", [[0, 3, 6], [-2, 3, 5], [-1, 1, 9]])
+def test_write_flags_rows_that_are_not_there(start):
+    """Rows below 0 or from `tokens` on: skipped and flagged, the others stored."""
+    b = Both(dtype=F32, dim=16)
+    b.extend([0, 1], [12, 12])
+    k = torch.randn((5, 3, 16), generator=torch.Generator().manual_seed(1)).cuda()
+    want = b.k.clone()
+    for i in range(2):
+        for t in range(max(start[i], 0), min(start[i + 1], 5)):
+            pos = 12 - (start[i + 1] - t)
+            want[0, int(b.table[i, pos // 8]), :, pos % 8] = k[t]
+    b.cache.write(0, k, k, b.dev([0, 1]), b.dev(start))
+    torch.cuda.synchronize()
+    assert torch.equal(b.k, want) and int(b.status) == decode.GS_DEV_BAD_SEQ
