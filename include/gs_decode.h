@@ -258,10 +258,12 @@ gs_status gs_guided_logits_workspace(const gs_guided_logits_args* args, int64_t*
  *                                        where cond is; z = cond exactly at s = 1 (uncond is
  *                                        then not read) or without uncond
  *   z = z + bias
- *   z = z > 0 ? z / repetition : z * repetition          for tokens of the history
+ *   z = z > 0 ? z * (1 / repetition) : z * repetition    for tokens of the history (the
+ *                                        reciprocal rounded; z / repetition for repetitions
+ *                                        outside 2^-40 .. 2^40, where it could overflow)
  *   z = z - (frequency * count + presence)               for tokens said count > 0 times
  *                                        in the output part of the history
- *   z = z / temperature                                  (temperature > 0)
+ *   z = z / temperature                                  (temperature > 0; correctly rounded)
  *   z = -inf                                             where the mask forbids v
  * token = the lowest index of the largest z (+ noise); NaN is never chosen.  A row with no
  * z above -inf gives token -1, logprob -inf and GS_DEV_EMPTY_ROW.
