@@ -156,18 +156,33 @@ struct Cursor {
     }
     __device__ __forceinline__ int item() const { return base + hg * (tiles + 1); }
     __device__ __forceinline__ int unit() const { return item() + tile; }
-    // To the next tile; past the last one, unit() is past every block's end.
-    __device__ __forceinline__ void next(const AttnParams& p) {
+    // To the next tile; where that is not below `end` (the block's), unit() is not either.
+    __device__ __forceinline__ void next(const AttnParams& p, int end) {
         if (++tile < tiles) return;
         tile = 0;
         const int hp = p.c.heads * p.parts;
         if (++hg < hp) return;
         hg = 0;
         base += (tiles + 1) * hp;
-        do {
-            if (b + 1 >= p.batch) return;
-            take_row(p, b + 1);
-        } while (tiles == 0);
+        if (base >= end || b + 1 >= p.batch) return;
+        take_row(p, b + 1);
+        while (tiles == 0) {              // empty rows: the next one that is not, 128 at a look
+            const int lane = threadIdx.x & 31;
+            unsigned live[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int at = b + 1 + i * 32 + lane;
+                const int s = at < p.batch ? (p.seq != nullptr ? p.seq[at] : at) : -1;
+                live[i] = __ballot_sync(0xffffffffu, s >= 0 && s < p.c.seqs && p.c.lens[s] > 0);
+            }
+            int past = 0;                 // rows before the live one
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (past == i * 32) past += live[i] != 0u ? __ffs(live[i]) - 1 : 32;
+            if (b + 1 + past >= p.batch) return;         // (lengths that change during the call)
+            if (past < 128) take_row(p, b + 1 + past);
+            else b += 128;
+        }
     }
 };
 
@@ -260,7 +275,7 @@ __device__ __forceinline__ bool find_work(const AttnParams& p, Split* split, int
     at->tile = into - at->hg * (at->tiles + 1);
     if (at->tile == at->tiles) {          // the unit after the tiles
         --at->tile;
-        at->next(p);
+        at->next(p, *end);
     }
     return at->unit() < *end;
 }
@@ -568,7 +583,7 @@ attention_kernel(const __grid_constant__ AttnParams p) {
         next[i].hi = 0;
         if (ahead.unit() < end) {
             next[i] = look_up(ahead);
-            ahead.next(p);
+            ahead.next(p, end);
         }
     }
 #pragma unroll
@@ -607,7 +622,7 @@ attention_kernel(const __grid_constant__ AttnParams p) {
         pending.hi = 0;
         if (ahead.unit() < end) {
             pending = look_up(ahead);
-            ahead.next(p);
+            ahead.next(p, end);
         }
         const int j = cur.tile * TILE + warp * RUN;
         const bool sink = j < cur.row.turn;
@@ -705,7 +720,7 @@ attention_kernel(const __grid_constant__ AttnParams p) {
             }
             fresh = true;
         }
-        cur.next(p);
+        cur.next(p, end);
     }
     copy_wait<0>();
 }
