@@ -310,7 +310,7 @@ class PagedCache:
         a.scale = float(D) ** -0.5 if scale is None else float(scale)
         a.window, a.sinks = int(window), int(sinks)
         a.lse = _ptr(lse, "lse", dev, torch.float32, (B, Hq))
-        work = _zeroed("gs_paged_attention_workspace", a, dev)
+        work = _zeroed("gs_paged_attention_workspace", a, dev, B * Hq)
         return Call("gs_paged_attention", (ctypes.byref(a),), dev,
                     (self, d, a, q, out, lse, seq, k_new, v_new, work))
 
@@ -328,13 +328,14 @@ class PagedCache:
         return out
 
 
-def _zeroed(fn: str, args, device):
-    """The workspace that `fn` asks for, zeroed and entered into args."""
+def _zeroed(fn: str, args, device, words: Optional[int] = None):
+    """The workspace that `fn` asks for, its first `words` zeroed (None: all), entered into args."""
     import torch
     n = ctypes.c_int64(0)
     with torch.cuda.device(device):
         gs._check(fn, getattr(load(), fn)(ctypes.byref(args), ctypes.byref(n)))
-    work = torch.zeros(max(1, (n.value + 3) // 4), dtype=torch.int32, device=device)
+    work = torch.empty(max(1, (n.value + 3) // 4), dtype=torch.int32, device=device)
+    work[:words].zero_()
     args.workspace, args.workspace_bytes = work.data_ptr(), work.numel() * 4
     return work
 
@@ -418,7 +419,7 @@ def prepare_guided_logits(logits=None, *, uncond=None, cond=None, stacked=None, 
     if out is None and token is None and logprob is None:
         raise ValueError("pass out, token or logprob")
     a.dev_status = _ptr(status, "status", dev, i32)
-    work = _zeroed("gs_guided_logits_workspace", a, dev)
+    work = _zeroed("gs_guided_logits_workspace", a, dev, B)
     return Call("gs_guided_logits", (ctypes.byref(a),), dev,
                 (a, uncond, cond, step_idx, scale_lut, bias, tokens, tokens_len, prompt_len,
                  repetition, frequency, presence, temperature, mask, mask_present, noise, out,

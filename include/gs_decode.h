@@ -173,10 +173,11 @@ typedef struct gs_paged_attention_args {
     int64_t out_batch_stride, out_head_stride;
     float*  lse;                /* device float[batch][q_heads] or NULL                   */
     void*   workspace;          /* device, gs_paged_attention_workspace bytes, 16-byte
-                                   aligned, all 0 before its first use; a call leaves it
-                                   ready for calls of the same sizes (batch, heads, dim,
-                                   dtype, cols, page, window, sinks) - zero it again
-                                   before one of others                                   */
+                                   aligned; its first batch * q_heads int32 words are 0
+                                   before its first use (the rest may hold anything); a
+                                   call leaves it ready for calls of the same sizes
+                                   (batch, heads, dim, dtype, cols, page, window, sinks) -
+                                   zero those words again before one of others            */
     int64_t workspace_bytes;
 } gs_paged_attention_args;
 
@@ -243,9 +244,11 @@ typedef struct gs_guided_logits_args {
     float*   logprob;           /* device float[batch] or NULL: z[token] - ln sum e^z     */
     uint32_t* dev_status;
     void*    workspace;         /* device, gs_guided_logits_workspace bytes, 16-byte
-                                   aligned, all 0 before its first use; a call leaves it
-                                   ready for calls of the same batch, vocab, dtype and
-                                   streams given - zero it again before one of others     */
+                                   aligned; its first batch int32 words are 0 before its
+                                   first use (the rest may hold anything); a call leaves
+                                   it ready for calls of the same batch, vocab, dtype and
+                                   streams given - zero those words again before one of
+                                   others                                                 */
     int64_t  workspace_bytes;
 } gs_guided_logits_args;
 
