@@ -313,6 +313,7 @@ fork_kernel(CacheView c, const int* src, const int* dst, int n) {
         const bool served = need(i) == 0 || at[i] < avail;
         if (j == 0) {
             c.lens[dsts[i]] = served ? from[i] : 0;
+            c.refused[dsts[i]] = 0;
             if (!served) flag(c.status, GS_DEV_NO_PAGE);
         }
         int* to = c.table + static_cast<long long>(dsts[i]) * c.cols + j;
@@ -349,6 +350,8 @@ __global__ void __launch_bounds__(128) free_kernel(CacheView c, const int* seq, 
         if (len < 0 || len > c.cols * c.page) {
             flag(c.status, GS_DEV_BAD_SEQ);
             len = 0;
+        } else if (c.refused != nullptr) {
+            c.refused[s] = 0;
         }
         if (len > 0 && atomicCAS(c.lens + s, len, 0) != len) len = 0;
     }

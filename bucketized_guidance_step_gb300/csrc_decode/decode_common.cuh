@@ -35,7 +35,7 @@ struct CacheView {
     int* refs;
     unsigned* status;
     int* work;
-    int* refused;                         // [seqs] of the workspace, see below; null without one
+    int* refused;                         // [seqs] of the workspace, see below; null where that is too small
 };
 
 // A cache's workspace, in words: [0] the number of copies a call asks for, [1] held pages, [4 ..]
@@ -111,7 +111,7 @@ inline gs_status check_cache(const gs_kv_cache* c, CacheView* out) {
     out->refs = c->refs;
     out->status = c->dev_status;
     out->work = static_cast<int*>(c->workspace);
-    out->refused = out->work != nullptr ? out->work + refused_at(c) : nullptr;
+    out->refused = check_workspace(c) == GS_OK ? out->work + refused_at(c) : nullptr;
     return GS_OK;
 }
 

@@ -88,7 +88,7 @@ gs_status gs_pages_workspace(const gs_kv_cache* cache, int64_t* bytes);
  * and including it fit the free pages (an entry that needs none always is) and its row of the
  * table; else it is left as it is, GS_DEV_NO_PAGE is set, and nothing is stored for the
  * sequence (gs_kv_write, the append of gs_paged_attention) until an extension by one token or
- * more is served or its length is another.  An id outside the cache, a negative add and the second
+ * more is served, it is freed or forked onto, or its length is another.  An id outside the cache, a negative add and the second
  * listing of a sequence are skipped (GS_DEV_BAD_SEQ).
  *
  * seq: device int32[n].  add: device int32[n], or NULL (one token each).

@@ -196,3 +196,23 @@ def test_caches_over_one_table_share_a_workspace():
     assert word(a) == decode.GS_DEV_NO_PAGE and not b.k.any() and not b.v.any()
     with pytest.raises(ValueError):
         decode.PagedCache(b.k, b.v, a.table, a.lens, a.refs, workspace=a.workspace[:-1])
+
+
+@pytest.mark.parametrize("how", ["free", "fork"])
+def test_a_refusal_ends_with_the_sequence(how):
+    """Freed, or forked onto, and given the same length again by other means: it is another one."""
+    c = make(3, 8, 2, 2)
+    c.extend(dev([0, 1]), dev([8, 16]))
+    c.extend(dev([0]), dev([9]))
+    assert word(c) == decode.GS_DEV_NO_PAGE
+    if how == "free":
+        c.free(dev([0]))
+    else:
+        c.free(dev([1]))
+        c.fork(dev([1]), dev([0]))
+    assert not c.lens[0] and word(c) == 0
+    c.table[0, 0], c.lens[0], c.refs[0] = 0, 8, 1
+    k, v = new_tokens(8, BF16)
+    c.write(1, k, v, dev([0]), dev([0, 8]))
+    assert word(c) == 0
+    assert torch.equal(c.k[1, 0], k.transpose(0, 1)) and torch.equal(c.v[1, 0], v.transpose(0, 1))
