@@ -2,11 +2,12 @@
 //
 // The bookkeeping of one call (which pages are free, who gets which) is small: a few words
 // a sequence and one word a page.  It runs in one block where both are few (one_block), else in
-// one cluster of 8 blocks, so that the count of
-// every page is read once, by eighths, without a grid-wide pass: each block counts the free
-// pages of its eighth, the counts are exchanged through distributed shared memory, and each
-// block then hands out its own free pages by rank.  The rank of a free page decides which
-// entry of the list takes it, so the outcome does not depend on timing.
+// one cluster of 8 blocks, so that the counts of the pages are read by eighths, without a
+// grid-wide pass: each block counts the free pages of its eighth, the numbers are exchanged
+// through distributed shared memory, and each block then hands out its own free pages by rank.
+// The rank of a free page decides which entry of the list takes it, so the outcome does not
+// depend on timing.  (A thread keeps what it read of its first 32 pages; pages beyond them are
+// read a second time, and a compaction reads every count three times.)
 //
 // The copies (fork: the filled rows of a partly filled page; compact: whole pages) are a
 // second kernel over a list that the first one leaves in the workspace, launched without the
@@ -14,11 +15,11 @@
 //
 // Measured on a GB300 (graph replay): 64 forks of 32 layers of 8 heads of 64 x 128 bf16 pages, half
 // filled (426 MB read and written), 76.3 us, of which the copies take 65 (97 % of the measured copy
-// rate); compacting 1024 of 4096 pages of 4 layers (537 MB) 87 us (91 %); 24 prompts of 12.8k
-// tokens in all freed, extended and written in 2 layers (210 MB) 46 us (67 %): 37 of them the two
-// writes, 8 the bookkeeping.  That is a chain of DRAM latencies (list, lengths, tables, counts) and
-// of cluster barriers: a fork or an extension of a few pages
-// takes 4 to 6 us.
+// rate); compacting 1024 of 4096 pages of 4 layers (537 MB) 88 us (90 %); 24 prompts of 12.8k
+// tokens in all freed, extended and written in 2 layers (210 MB) 48 us (64 %): 39 of them the two
+// writes, of which looking whether a page is shared before storing into it is 1, 8 the
+// bookkeeping.  That is a chain of DRAM latencies (list, lengths, tables, counts) and of cluster
+// barriers: a fork or an extension of a few pages takes 4 to 6 us.
 #include "decode_common.cuh"
 
 namespace gs_decode {

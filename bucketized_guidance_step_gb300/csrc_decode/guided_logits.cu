@@ -3,10 +3,12 @@
 // log-probability, in one pass over the vocabulary.
 //
 // A block takes one chunk of one row; chunks are cut so that all blocks of the call are
-// resident at once (what a block does once - settings, history, joining - costs about 4 us and
-// is then paid once an SM's slot).  Each warp streams 256 logits at a time through a buffer of
-// its own in shared memory, by 16-byte asynchronous copies: once a piece is in registers the
-// next one's copies are issued, and then the piece is worked on.
+// resident at once where a chunk then holds 16384 logits at most (what a block does once -
+// settings, history, joining - costs about 4 us and is then paid once an SM's slot).  Larger
+// calls have several waves of such blocks (67 rows of 131072 25.8 us, 68 27.5, 128 47.9, 256 83.3).
+// Each warp streams 256 logits at a time through a buffer of its own in shared memory, by 16-byte
+// asynchronous copies: once a piece is in registers the next one's copies are issued, and then
+// the piece is worked on.
 //
 // Rows need no alignment: groups of 8 logits are laid so that the output is written in 16-byte
 // vectors, the inputs are copied as the aligned vectors that cover them, and a lane shifts its
@@ -24,12 +26,14 @@
 // them in the order of the chunks.
 //
 // What bounds it, on a GB300 (graph replay, inputs not in L2): 64 rows of 131072 fp32 logits
-// without extras (67 MB) take 16 us, 62 % of the measured copy rate; bf16 with guidance, histories
-// of up to 2048 tokens, mask, bias and noise (102 MB) 26 us, 58 %: 70 instructions a logit at half
+// without extras (67 MB) take 16.3 us, 61 % of the measured copy rate; bf16 with guidance, histories
+// of up to 2048 tokens, mask, bias and noise (102 MB) 26 us, 58 %: 67 instructions a logit at half
 // of the issue slots, 5 us of settings, counting and joining, and as the blocks are cut evenly
-// some SMs have four and some three.  Histories cost 4.5 us at 2048 tokens, 10 at 8192 and 45 at
-// 32768 (every block of a row counts its whole history).  One row of 16384 takes 5.9 us: five
-// latencies in a chain.
+// some SMs have four and some three.  Histories cost 4.5 us at 2048 tokens, 10 at 8192 and 36 at
+// 32768 (every block of a row counts its whole history, and the counts' shared memory costs
+// blocks on an SM, which the cut does not look at).  The instances for rows off 16 bytes are held
+// to 64 registers for four blocks an SM and spill 12 to 64 bytes.  One row of 16384 takes 6.0 us:
+// five latencies in a chain.
 //
 // Measured and not kept: logits held in registers instead of a buffer (45 us, and 29 us at four
 // blocks an SM, for the 64 rows above), a count a logit instead of a bitmap (32 KB a block), two

@@ -7,8 +7,8 @@
 // a maximum, sum and output of its own, and they meet at the segment's end.
 //
 // What bounds it: 16 rows of 4096 tokens with 32 query and 8 kv heads of dim 128 (537 MB) take
-// 94 us, 84 % of the measured copy rate; 8 rows of 333 .. 3001 with 8 and 4 heads of 96 (45 MB)
-// 17.2 us, 39 %: the call's fixed part, and five or six tiles a block in a row, whose multiply-adds
+// 92 us, 86 % of the measured copy rate; 8 rows of 333 .. 3001 with 8 and 4 heads of 96 (45 MB)
+// 17.1 us, 39 %: the call's fixed part, and five or six tiles a block in a row, whose multiply-adds
 // two warps a scheduler do not hide.
 #include <cmath>
 
@@ -151,8 +151,9 @@ struct Fp32 {
 
 // An instance computes for all its heads, so small groups have instances of their own: groups of 2
 // with dim 96 (8 rows of 333 .. 3001 tokens) took 18.9 us, and 22.0 us in the instance of 4; groups
-// of 4 with dim 64 (32 rows of 2048) 66 us, and 107 us in the instance of 8, whose registers allow
-// two blocks an SM instead of three; groups of 8 109 us, and 127 us in two parts of 4.
+// of 4 with dim 64 (32 rows of 2048) 61 us, and 107 us in the instance of 8, whose registers allow
+// two blocks an SM instead of three (the instance of 4 is held to 168 registers for the third
+// and spills 40 to 64 bytes); groups of 8 107 us, and 127 us in two parts of 4.
 template <class F>
 auto with_instance(int dim, int group, F f) {
     if (dim <= 64) return group <= 2 ? f(Fp32<2, 2>()) : group <= 4 ? f(Fp32<2, 4>()) : f(Fp32<2, 8>());

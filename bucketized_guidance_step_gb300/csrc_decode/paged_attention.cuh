@@ -28,10 +28,11 @@
 // 301 us, 99 % of the measured copy rate, 32 rows of 8192 161 us (98 %).  Below that a call's
 // fixed part shows, about 9 us: lengths, table and first rows are three DRAM latencies in a
 // chain (4.5 us), the last segment's end, its count and the join 3 to 5 us.  32 rows of 2048
-// tokens: 48 us (82 %), 32 ragged ones of 1 .. 4099: 50 us (81 %).  Where segments are a tile
-// long, what beginning and ending one costs is not hidden any more: 1032 rows of 64 tokens 75 us
-// (56 %), 258 rows of 256 53 us (77 %).  The smallest calls (2 rows of 125 and 250 tokens) take
-// 6.7 us.  Counters (ncu, the ragged rows): DRAM reads 277.7 MB of 277.7 required, tensor pipe
+// tokens: 48 us (83 %), 32 ragged ones of 1 .. 4099 with new tokens: 52 us (79 %).  Where segments
+// are a tile long, what beginning and ending one costs is not hidden any more: 1032 rows of 64
+// tokens 75 us (57 %), 258 rows of 256 53 us (77 %).  The smallest calls (2 rows of 125 and 250
+// tokens, with new tokens) take 6.9 us.  Looking where a new token may be stored is 2 to 4 % of a
+// call with new tokens (49.7 us without it for the ragged rows).  Counters (ncu, the ragged rows): DRAM reads 277.7 MB of 277.7 required, tensor pipe
 // 9.6 %, 8 warps an SM.
 //
 // Measured and not kept: finding the places of 32 tiles at once, a tile a lane (48 -> 51 us at 32

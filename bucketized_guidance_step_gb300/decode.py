@@ -100,7 +100,9 @@ class Call:
 
     The call keeps its tensors and its workspace alive; keep the call until its work is done
     where that runs on another stream than the tensors were made on, or in a captured graph.
-    Two calls in flight at once need a ``Call`` each (a workspace serves one at a time)."""
+    A workspace serves one call at a time: two calls of attention or logits in flight at once need
+    a ``Call`` each, and calls on one cache's pages, whose workspace is the cache's, are ordered
+    by the caller whatever their ``Call`` objects."""
 
     def __init__(self, name: str, args, device, keep):
         import torch
