@@ -22,11 +22,12 @@ from .gs import GSError, _dtype_code
 # ---- constants mirrored from include/gs_decode.h -------------------------------
 GS_DEV_NO_PAGE, GS_DEV_BAD_SEQ, GS_DEV_EMPTY_ROW = 16, 32, 64
 GS_MAX_SEQS = 8192
+GS_CHUNK_COUNTERS = 1024
 
 EXPORTS = ("gs_pages_workspace", "gs_pages_extend", "gs_pages_fork", "gs_pages_free",
            "gs_pages_compact", "gs_kv_write", "gs_paged_attention_workspace",
-           "gs_paged_attention", "gs_guided_logits_workspace", "gs_guided_logits",
-           "gs_decode_status_from_word")
+           "gs_paged_attention", "gs_chunk_attention_workspace", "gs_chunk_attention",
+           "gs_guided_logits_workspace", "gs_guided_logits", "gs_decode_status_from_word")
 
 _I32, _I64, _P, _F = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
 
@@ -45,6 +46,15 @@ class PagedAttentionArgs(ctypes.Structure):
                 ("q_head_stride", _I64), ("k_new", _P), ("v_new", _P),
                 ("new_batch_stride", _I64), ("new_head_stride", _I64), ("scale", _F),
                 ("window", _I32), ("sinks", _I32), ("out", _P), ("out_batch_stride", _I64),
+                ("out_head_stride", _I64), ("lse", _P), ("workspace", _P),
+                ("workspace_bytes", _I64)]
+
+
+class ChunkAttentionArgs(ctypes.Structure):
+    _fields_ = [("cache", ctypes.POINTER(KVCacheDesc)), ("layer", _I32), ("tokens", _I32),
+                ("n", _I32), ("seq", _P), ("start", _P), ("q_heads", _I32), ("q", _P),
+                ("q_token_stride", _I64), ("q_head_stride", _I64), ("scale", _F),
+                ("window", _I32), ("sinks", _I32), ("out", _P), ("out_token_stride", _I64),
                 ("out_head_stride", _I64), ("lse", _P), ("workspace", _P),
                 ("workspace_bytes", _I64)]
 
@@ -81,6 +91,8 @@ def load() -> ctypes.CDLL:
         lib.gs_kv_write.argtypes = [cache, _I32, _P, _P, _I64, _I64, _I32, _P, _P, _I32, _P]
         lib.gs_paged_attention_workspace.argtypes = [ctypes.POINTER(PagedAttentionArgs), _P]
         lib.gs_paged_attention.argtypes = [ctypes.POINTER(PagedAttentionArgs), _P]
+        lib.gs_chunk_attention_workspace.argtypes = [ctypes.POINTER(ChunkAttentionArgs), _P]
+        lib.gs_chunk_attention.argtypes = [ctypes.POINTER(ChunkAttentionArgs), _P]
         lib.gs_guided_logits_workspace.argtypes = [ctypes.POINTER(GuidedLogitsArgs), _P]
         lib.gs_guided_logits.argtypes = [ctypes.POINTER(GuidedLogitsArgs), _P]
         lib.gs_decode_status_from_word.argtypes = [ctypes.c_uint32]
@@ -327,6 +339,46 @@ class PagedCache:
         if out is None:
             out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         self.prepare_attention(q, layer, out=out, **kw)()
+        return out
+
+    def prepare_chunk_attention(self, q, layer: int, seq, start, *, scale: Optional[float] = None,
+                                window: int = 0, sinks: int = 0, out=None, lse=None) -> Call:
+        import torch
+        d, dev, dt = self._desc, self.device, self.k.dtype
+        if q.dim() != 3 or q.shape[2] != d.dim:
+            raise ValueError(f"q must be [tokens, q_heads, {d.dim}]")
+        T, Hq, D = q.shape
+        if out is None or tuple(out.shape) != tuple(q.shape):
+            raise ValueError("out must have the shape of q")
+        a = ChunkAttentionArgs()
+        a.cache = ctypes.pointer(d)
+        a.layer, a.tokens, a.q_heads, a.n = int(layer), T, Hq, seq.numel()
+        a.seq, a.start = self._list(seq, "seq"), self._list(start, "start", a.n + 1)
+        for name, t in (("q", q), ("out", out)):
+            _last_dense(t, name)
+        _no_overlap(out, "out")
+        a.q, a.out = _ptr(q, "q", dev, dt, contiguous=False), _ptr(out, "out", dev, dt, contiguous=False)
+        a.q_token_stride, a.q_head_stride = _stride(q, 0), _stride(q, 1)
+        a.out_token_stride, a.out_head_stride = _stride(out, 0), _stride(out, 1)
+        a.scale = float(D) ** -0.5 if scale is None else float(scale)
+        a.window, a.sinks = int(window), int(sinks)
+        a.lse = _ptr(lse, "lse", dev, torch.float32, (T, Hq))
+        work = _zeroed("gs_chunk_attention_workspace", a, dev, GS_CHUNK_COUNTERS)
+        return Call("gs_chunk_attention", (ctypes.byref(a),), dev, (self, d, a, q, out, lse, seq, start, work))
+
+    def chunk_attention(self, q, layer: int, seq, start, *, out=None, **kw):
+        """gs_chunk_attention: rows start[i] .. start[i+1]-1 of q [tokens, q_heads, dim] are the last
+        tokens of sequence seq[i], whose K and V the cache's layer holds; each attends over the
+        positions up to its own. Returns out.
+
+        seq: int32 [n], start: int32 [n + 1]; scale (default dim ** -0.5); window and sinks: only the
+        last `window` positions up to the row's own and the first `sinks`; lse: fp32 [tokens, q_heads],
+        receives the log-sum-exp of the scaled scores. Rows of no entry are left as they were (zeros,
+        where out is made here)."""
+        import torch
+        if out is None:
+            out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+        self.prepare_chunk_attention(q, layer, seq, start, out=out, **kw)()
         return out
 
 

@@ -204,6 +204,65 @@ gs_status gs_paged_attention_workspace(const gs_paged_attention_args* args, int6
 gs_status gs_paged_attention(const gs_paged_attention_args* args, gs_stream stream);
 
 /* ------------------------------------------------------------------------ */
+/* Attention of chunks of new tokens.                                        */
+/* ------------------------------------------------------------------------ */
+
+/* Words of a chunk attention's workspace that are 0 before its first use. */
+#define GS_CHUNK_COUNTERS 1024
+
+typedef struct gs_chunk_attention_args {
+    const gs_kv_cache* cache;
+    int32_t layer;
+    int32_t tokens;             /* rows of q and out                                       */
+    int32_t n;                  /* entries: chunks of the call (<= GS_MAX_SEQS)            */
+    const int32_t* seq;         /* device int32[n]: entry i reads sequence seq[i]          */
+    const int32_t* start;       /* device int32[n+1], rising: its rows are start[i] ..
+                                   start[i+1]-1                                           */
+    int32_t q_heads;            /* a multiple of kv_heads: query head h reads kv head
+                                   h / (q_heads / kv_heads)                               */
+    const void* q;              /* device, cache dtype, [tokens][q_heads][dim]            */
+    int64_t q_token_stride, q_head_stride;
+    float   scale;              /* of the scores (usually dim ** -0.5); finite            */
+    int32_t window;             /* 0: every earlier position; else the last `window` ...  */
+    int32_t sinks;              /* ... and the first `sinks` positions                    */
+    void*   out;                /* device, cache dtype, [tokens][q_heads][dim]            */
+    int64_t out_token_stride, out_head_stride;
+    float*  lse;                /* device float[tokens][q_heads] or NULL                  */
+    void*   workspace;          /* device, gs_chunk_attention_workspace bytes, 16-byte
+                                   aligned; its first GS_CHUNK_COUNTERS int32 words are 0
+                                   before its first use (the rest may hold anything); a
+                                   call leaves it ready for any other chunk attention that
+                                   it is large enough for                                 */
+    int64_t workspace_bytes;
+} gs_chunk_attention_args;
+
+gs_status gs_chunk_attention_workspace(const gs_chunk_attention_args* args, int64_t* bytes);
+
+/*
+ * gs_chunk_attention -- prompts, and chunks of them or of drafted tokens: the rows of entry i are
+ * the last m = start[i+1] - start[i] tokens of sequence seq[i], whose K and V the cache holds
+ * (after gs_pages_extend and gs_kv_write).  The row of position t = lens - m + (its number in the
+ * entry) attends over the positions j of its sequence with j <= t and, with a window, j < sinks or
+ * j > t - window:
+ *   s_j = scale * q . k_j,  M = max_j s_j,  out = sum_j e^(s_j - M) v_j / sum_j e^(s_j - M),
+ *   lse = M + ln sum_j e^(s_j - M).
+ * Sums, maxima and the output's accumulator are fp32; for 16-bit caches the weights e^(s_j - M)
+ * enter the product with V rounded to the cache's type.  A row before its sequence's first token
+ * (m > lens) gives out = 0 and lse = -inf.  Rows that no entry has (behind start[n], say) are left as
+ * they were.  Rows of a page past the sequence's length are never used, whatever they hold.  Several
+ * entries may read one sequence.  Results do not depend on the grid's timing.
+ * Device-found: GS_DEV_BAD_SEQ (a sequence id outside the cache: as length 0; a page id outside the
+ * pool: its rows read as zeros; a length past the table: cut; rows before the first token; an entry
+ * whose rows do not rise or pass 0 .. tokens: skipped).  Entries whose rows overlap leave either's
+ * results there.
+ * Errors: GS_ERR_INVALID_ARG (NULL pointers, sizes, q_heads not a multiple of kv_heads, layer outside
+ * the cache, window or sinks < 0, sinks without window, a scale that is not finite, workspace too
+ * small), GS_ERR_UNSUPPORTED (the cache's limits, n over GS_MAX_SEQS, tokens * q_heads over 2^30, n *
+ * kv_heads over 2^28), GS_ERR_CUDA.  tokens = 0 or n = 0 does nothing.
+ */
+gs_status gs_chunk_attention(const gs_chunk_attention_args* args, gs_stream stream);
+
+/* ------------------------------------------------------------------------ */
 /* Guided logits.                                                            */
 /* ------------------------------------------------------------------------ */
 
