@@ -242,21 +242,6 @@ gs_status launch_chunk_fp32(const ChunkParams& p, int blocks, gs_stream stream) 
     return launch_as<float, 256, 32>(p, blocks, stream);
 }
 
-// (16-bit caches go the same way.)
-ChunkShape chunk_mma_shape(int) { return {kRows, sm_count()}; }
-
-template <class T>
-static gs_status launch_16(const ChunkParams& p, int blocks, gs_stream stream) {
-    if (p.c.dim <= 64) return launch_as<T, 64, 64>(p, blocks, stream);
-    if (p.c.dim <= 128) return launch_as<T, 128, 64>(p, blocks, stream);
-    return launch_as<T, 256, 32>(p, blocks, stream);
-}
-
-gs_status launch_chunk_mma(int dtype, const ChunkParams& p, const gs_kv_cache*, int blocks, gs_stream stream) {
-    if (dtype == GS_DTYPE_BF16) return launch_16<__nv_bfloat16>(p, blocks, stream);
-    return launch_16<__half>(p, blocks, stream);
-}
-
 namespace {
 
 struct Plan {
@@ -357,5 +342,5 @@ extern "C" gs_status gs_chunk_attention(const gs_chunk_attention_args* args, gs_
     p.slot_count = plan.slots;
     p.slot_rows = plan.rows;
     if (args->cache->dtype == GS_DTYPE_F32) return launch_chunk_fp32(p, plan.shape.blocks, stream);
-    return launch_chunk_mma(args->cache->dtype, p, args->cache, plan.shape.blocks, stream);
+    return launch_chunk_mma(args->cache->dtype, p, plan.shape.blocks, stream);
 }

@@ -412,7 +412,6 @@ struct ChunkShape {
 ChunkShape chunk_fp32_shape(int dim);
 ChunkShape chunk_mma_shape(int dim);
 gs_status launch_chunk_fp32(const ChunkParams& p, int blocks, gs_stream stream);
-gs_status launch_chunk_mma(int dtype, const ChunkParams& p, const gs_kv_cache* cache, int blocks,
-                           gs_stream stream);
+gs_status launch_chunk_mma(int dtype, const ChunkParams& p, int blocks, gs_stream stream);
 
 }  // namespace gs_decode
