@@ -27,7 +27,8 @@ GS_CHUNK_COUNTERS = 1024
 EXPORTS = ("gs_pages_workspace", "gs_pages_extend", "gs_pages_fork", "gs_pages_free",
            "gs_pages_compact", "gs_kv_write", "gs_paged_attention_workspace",
            "gs_paged_attention", "gs_chunk_attention_workspace", "gs_chunk_attention",
-           "gs_guided_logits_workspace", "gs_guided_logits", "gs_decode_status_from_word")
+           "gs_guided_logits_workspace", "gs_guided_logits", "gs_sample",
+           "gs_decode_status_from_word")
 
 _I32, _I64, _P, _F = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
 
@@ -71,6 +72,13 @@ class GuidedLogitsArgs(ctypes.Structure):
                 ("workspace_bytes", _I64)]
 
 
+class SampleArgs(ctypes.Structure):
+    _fields_ = [("batch", _I32), ("vocab", _I32), ("dtype", _I32), ("logits", _P),
+                ("row_stride", _I64), ("temperature", _P), ("top_k", _P), ("top_p", _P),
+                ("min_p", _P), ("noise", _P), ("noise_stride", _I64), ("token", _P),
+                ("logprob", _P), ("dev_status", _P)]
+
+
 _ready = False
 _lock = threading.Lock()
 
@@ -95,6 +103,7 @@ def load() -> ctypes.CDLL:
         lib.gs_chunk_attention.argtypes = [ctypes.POINTER(ChunkAttentionArgs), _P]
         lib.gs_guided_logits_workspace.argtypes = [ctypes.POINTER(GuidedLogitsArgs), _P]
         lib.gs_guided_logits.argtypes = [ctypes.POINTER(GuidedLogitsArgs), _P]
+        lib.gs_sample.argtypes = [ctypes.POINTER(SampleArgs), _P]
         lib.gs_decode_status_from_word.argtypes = [ctypes.c_uint32]
         for f in EXPORTS:
             getattr(lib, f).restype = _I32
@@ -499,3 +508,49 @@ def guided_logits(logits=None, **kw):
         kw["logprob"] = torch.empty(B, dtype=torch.float32, device=src.device)
     prepare_guided_logits(logits, **kw)()
     return kw.get("out"), kw.get("token"), kw.get("logprob")
+
+
+def prepare_sample(logits, *, temperature=None, top_k=None, top_p=None, min_p=None, noise=None,
+                   token=None, logprob=None, status=None) -> Call:
+    import torch
+    if logits.dim() != 2:
+        raise ValueError("logits must be [batch, vocab]")
+    B, V = logits.shape
+    dev, f32, i32 = logits.device, torch.float32, torch.int32
+    a = SampleArgs()
+    a.batch, a.vocab, a.dtype = B, V, _dtype_code(logits)
+    _last_dense(logits, "logits")
+    if _stride(logits, 0) < V and B > 1:
+        raise ValueError("the rows of the logits overlap")
+    a.logits, a.row_stride = _ptr(logits, "logits", dev, contiguous=False), _stride(logits, 0)
+    a.temperature = _ptr(temperature, "temperature", dev, f32, (B,))
+    a.top_k = _ptr(top_k, "top_k", dev, i32, (B,))
+    a.top_p = _ptr(top_p, "top_p", dev, f32, (B,))
+    a.min_p = _ptr(min_p, "min_p", dev, f32, (B,))
+    if noise is not None:
+        if noise.dim() != 2 or noise.shape[0] not in (1, B) or noise.shape[1] != V:
+            raise ValueError(f"noise must be [1 or {B}, {V}]")
+        _last_dense(noise, "noise")
+        a.noise, a.noise_stride = _ptr(noise, "noise", dev, f32, contiguous=False), _stride(noise, 0)
+    if token is None and logprob is None:
+        raise ValueError("pass token or logprob")
+    a.token = _ptr(token, "token", dev, i32, (B,))
+    a.logprob = _ptr(logprob, "logprob", dev, f32, (B,))
+    a.dev_status = _ptr(status, "status", dev, i32)
+    return Call("gs_sample", (ctypes.byref(a),), dev,
+                (a, logits, temperature, top_k, top_p, min_p, noise, token, logprob, status))
+
+
+def sample(logits, **kw):
+    """gs_sample: the next tokens from a step's logits and given random numbers; returns (token, logprob).
+
+    logits: [B, V], fp32, bf16 or fp16 (the z of guided_logits serves). temperature (<= 0 greedy),
+    top_p and min_p: fp32 [B], top_k: int32 [B]; tokens are kept by top_k, then top_p of what that left,
+    then min_p. noise: fp32 [1 or B, V], added where the token is chosen (Gumbel noise draws from what is
+    kept). token: int32 [B], logprob: fp32 [B] (both made if neither is given). status: int32 [1]."""
+    import torch
+    if kw.get("token") is None and kw.get("logprob") is None:
+        kw["token"] = torch.empty(logits.shape[0], dtype=torch.int32, device=logits.device)
+        kw["logprob"] = torch.empty(logits.shape[0], dtype=torch.float32, device=logits.device)
+    prepare_sample(logits, **kw)()
+    return kw.get("token"), kw.get("logprob")

@@ -338,6 +338,47 @@ gs_status gs_guided_logits_workspace(const gs_guided_logits_args* args, int64_t*
  */
 gs_status gs_guided_logits(const gs_guided_logits_args* args, gs_stream stream);
 
+/* ------------------------------------------------------------------------ */
+/* Sampling.                                                                 */
+/* ------------------------------------------------------------------------ */
+
+typedef struct gs_sample_args {
+    int32_t batch, vocab;       /* >= 1 (batch <= GS_MAX_SEQS)                             */
+    int32_t dtype;              /* GS_DTYPE_*: of the logits                              */
+    const void* logits;         /* device [batch][vocab]; gs_guided_logits' out serves     */
+    int64_t row_stride;         /* elements between rows, >= vocab                        */
+    const float* temperature;   /* device float[batch] or NULL (= 1); <= 0: greedy         */
+    const int32_t* top_k;       /* device int32[batch] or NULL; <= 0: every token          */
+    const float* top_p;         /* device float[batch] or NULL; >= 1: every token          */
+    const float* min_p;         /* device float[batch] or NULL; <= 0: every token          */
+    const float* noise;         /* device float[.][vocab] or NULL: added to z where the token
+                                   is chosen (Gumbel noise draws from what is kept); not
+                                   for greedy rows                                        */
+    int64_t noise_stride;       /* elements between rows; 0 = one row for all             */
+    int32_t* token;             /* device int32[batch] or NULL                            */
+    float*   logprob;           /* device float[batch] or NULL                            */
+    uint32_t* dev_status;
+} gs_sample_args;
+
+/*
+ * gs_sample -- for every row, with z = logits / temperature (fp32, correctly rounded; greedy rows: z
+ * = logits), weights e^z, and tokens in the order of falling z (ties: rising index):
+ *   top_k   the first top_k tokens are kept,
+ *   top_p   of these the shortest beginning whose weights reach top_p of their sum (a token is kept
+ *           where the sum of those before it is below; the first one always),
+ *   min_p   of these those with at least min_p times the largest weight (those of the largest z
+ *           always).
+ * token = the lowest index of the largest z (+ noise) among what is kept, logprob = z[token] - ln sum
+ * e^z over what is kept.  Logits of -inf and NaN are not kept, and noise of NaN is never chosen; where
+ * nothing is left, token = -1, logprob = -inf and GS_DEV_EMPTY_ROW is set.  Of logits of +inf each has
+ * the same weight and the others have none.  Sums of weights decide in units of 2^-40 of the largest
+ * weight, the weights themselves are good to about 2^-21.
+ * Errors: GS_ERR_INVALID_ARG (NULL logits, sizes, strides, unknown dtype, neither token nor logprob),
+ * GS_ERR_UNSUPPORTED (batch over GS_MAX_SEQS, vocab over 2^28), GS_ERR_CUDA.  batch = 0 does nothing.
+ * No output may overlap an input or another output.
+ */
+gs_status gs_sample(const gs_sample_args* args, gs_stream stream);
+
 /* The status of a device status word of these calls: GS_ERR_INVALID_ARG for GS_DEV_BAD_SEQ,
    GS_ERR_CAPACITY for GS_DEV_NO_PAGE, GS_ERR_UNSUPPORTED for GS_DEV_EMPTY_ROW, else
    gs_status_from_word. */
