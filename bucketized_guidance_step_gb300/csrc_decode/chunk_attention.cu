@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         if (it.kind == 2) {
             if (tid == 0) ok = chunk_wait_parts(p.work + kChunkHead + it.tile, it.need);
             __syncthreads();
-            if (ok) chunk_join<T>(p, it, tid, kThreads, 0.0f);
+            if (ok) chunk_join<T>(p, it, tid >> 5, kThreads / 32, 0.0f);
             else if (tid == 0) flag(p.c.status, GS_DEV_TIMEOUT);
             __syncthreads();
             continue;

@@ -35,6 +35,7 @@ struct ChunkParams {
     const void* q;
     long long q_token, q_head;
     int q_aligned, out_aligned;           // rows lie on 16 bytes
+    int q_boxes;                          // TMA brings the queries
     float scale_log2;                     // |scale| * log2 e (1 where scale is 0)
     float q_sign;                         // what queries are multiplied with: 1, -1 or 0
     int window, sinks;
@@ -146,6 +147,7 @@ struct ChunkItem {
     int need;                             // its count once all parts are there
     int tile;                             // its count's number
     int at;                               // kind 2: first row of the piece in the tile
+    int steps;                            // of the tensor cores' kernel
 };
 
 // The cut, found by every block alike: WIDTH of its THREADS threads take the entries.  A tile's
@@ -367,41 +369,62 @@ __device__ __forceinline__ T* chunk_out(const ChunkParams& p, const ChunkItem& i
     return static_cast<T*>(p.out) + token * p.out_token + h * p.out_head;
 }
 
-// Joins a piece of a tile: the parts of a row are weighted to their common reference, in their order.
-// `lanes` threads (whole warps) take part, this one is number `me`; a warp has four rows at a time, eight
-// lanes each. lift: what the sums are scaled by, in powers of two.
+// Joins a piece of a tile: the parts of a row are weighted to their common reference.  A warp a row: a
+// lane looks at every 32nd part's reference and sum, then has four neighbouring dims of all parts, eight of
+// them in flight (a thread that went through the parts one by one took 150 us for 38 parts of 132 rows).
+// lift: what the sums are scaled by, in powers of two.
 template <class T>
-__device__ __forceinline__ void chunk_join(const ChunkParams& p, const ChunkItem& it, int me, int lanes,
+__device__ __forceinline__ void chunk_join(const ChunkParams& p, const ChunkItem& it, int warp, int warps,
                                            float lift) {
-    const int dim = p.c.dim, sub = me & 7;
+    const int dim = p.c.dim, lane = threadIdx.x & 31;
     const long long words = chunk_slot_words(p.slot_rows, dim);
-    for (int x = me >> 3; x < it.rows; x += lanes >> 3) {
+    const float* const first = p.slots + it.slot * words;
+    for (int x = warp; x < it.rows; x += warps) {
         const int r = it.at + x;
-        const float* const slot = p.slots + it.slot * words;
         float top = kNegInf;
-        for (int k = 0; k < it.parts; ++k) top = fmaxf(top, __ldcg(slot + k * words + r));
+        for (int k = lane; k < it.parts; k += 32) top = fmaxf(top, __ldcg(first + k * words + r));
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
         const float base = top == kNegInf ? 0.0f : top;
         float sum = 0.0f;
-        for (int k = 0; k < it.parts; ++k)
-            sum = fmaf(__ldcg(slot + k * words + p.slot_rows + r), chunk_pow2(__ldcg(slot + k * words + r) - base), sum);
-        const float by = sum > 0.0f ? 1.0f / sum : sum;  // a NaN stays one
         float* lse;
         T* const to = chunk_out<T>(p, it, it.row + r, &lse);
-        for (int d = 4 * sub; d < dim; d += 32) {
+        for (int d0 = 0; d0 < dim; d0 += 128) {
+            const int d = d0 + 4 * lane;
             float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-            for (int k = 0; k < it.parts; ++k) {
-                const float w = chunk_pow2(__ldcg(slot + k * words + r) - base);
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(
-                    slot + k * words + 2 * p.slot_rows + static_cast<long long>(r) * dim + d));
-                o.x = fmaf(v.x, w, o.x);
-                o.y = fmaf(v.y, w, o.y);
-                o.z = fmaf(v.z, w, o.z);
-                o.w = fmaf(v.w, w, o.w);
+            for (int k0 = 0; k0 < it.parts; k0 += 32) {
+                float w = 0.0f;
+                if (k0 + lane < it.parts) {
+                    const float* const slot = first + (k0 + lane) * words + r;
+                    w = chunk_pow2(__ldcg(slot) - base);
+                    if (d0 == 0) sum = fmaf(__ldcg(slot + p.slot_rows), w, sum);
+                }
+                const int n = min(32, it.parts - k0);
+                const float* from = first + k0 * words + 2 * p.slot_rows + static_cast<long long>(r) * dim + d;
+                for (int k = 0; k < n; k += 8) {
+                    float4 v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        v[i] = k + i < n && d < dim ? __ldcg(reinterpret_cast<const float4*>(from + (k + i) * words))
+                                                    : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float f = __shfl_sync(0xffffffffu, w, k + i);
+                        o.x = fmaf(v[i].x, f, o.x);
+                        o.y = fmaf(v[i].y, f, o.y);
+                        o.z = fmaf(v[i].z, f, o.z);
+                        o.w = fmaf(v[i].w, f, o.w);
+                    }
+                }
             }
-            chunk_put4<T>(p, to + d, make_float4(o.x * by, o.y * by, o.z * by, o.w * by));
+            if (d0 == 0) {
+#pragma unroll
+                for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+            }
+            const float by = sum > 0.0f ? 1.0f / sum : sum;          // a NaN stays one
+            if (d < dim) chunk_put4<T>(p, to + d, make_float4(o.x * by, o.y * by, o.z * by, o.w * by));
         }
-        if (sub == 0 && lse != nullptr) *lse = sum == 0.0f ? kNegInf : (top + log2f(sum) - lift) * kChunkLn2;
+        if (lane == 0 && lse != nullptr) *lse = sum == 0.0f ? kNegInf : (top + log2f(sum) - lift) * kChunkLn2;
     }
 }
 
@@ -412,6 +435,6 @@ struct ChunkShape {
 ChunkShape chunk_fp32_shape(int dim);
 ChunkShape chunk_mma_shape(int dim);
 gs_status launch_chunk_fp32(const ChunkParams& p, int blocks, gs_stream stream);
-gs_status launch_chunk_mma(int dtype, const ChunkParams& p, int blocks, gs_stream stream);
+gs_status launch_chunk_mma(int dtype, ChunkParams& p, int blocks, gs_stream stream);
 
 }  // namespace gs_decode

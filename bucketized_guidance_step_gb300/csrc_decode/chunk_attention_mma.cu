@@ -3,13 +3,14 @@
 //
 // A block works on two tiles of 128 query rows at a time (one for heads of over 128 dims), which share
 // every unit of keys and values.  Of its warps
-//   one takes items from the queue and brings units: K and V in turn through a ring of stages in
-//     shared memory, as many units ahead as the ring has room, over the ends of items;
-//   one issues the products: S = Q K^T of 128 rows and the unit's positions into tensor memory, and
-//     O += P V from there;
+//   one takes items from the queue and brings their queries and units by TMA: K and V in turn through a
+//     ring of stages in shared memory, as many units ahead as the ring has room, over the ends of items;
+//   one issues the products, in steps of 64 positions: S = Q K^T into one of a tile's two places in tensor
+//     memory, and O += P V from there;
 //   four a tile have a row a thread: they read S, keep the softmax's reference and sum, write the
 //     weights P over S as 16-bit numbers, and at the item's end read O and store it.
-// While one tile's rows take their softmax, the tensor cores work for the other.
+// The scores of a step are there before the weights of the last one are done: the rows' threads never
+// wait for the tensor cores, but where those are what bounds the kernel.
 //
 // With s the scores in powers of two (times scale log2 e), the weights are 2^(s - m + kLift) with a
 // reference m that is the row's largest score so far, or up to kSlack below: O and the sum are
@@ -107,6 +108,41 @@ __device__ __forceinline__ void load_box(unsigned dst, const CUtensorMap* map, i
         : "memory");
 }
 
+__device__ __forceinline__ void load_box3(unsigned dst, const CUtensorMap* map, int x, int head, int token,
+                                          unsigned bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<unsigned long long>(map)), "r"(x), "r"(head), "r"(token), "r"(bar)
+        : "memory");
+}
+
+// Two fp32 numbers in a register pair.
+__device__ __forceinline__ unsigned long long pair_of(float lo, float hi) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void split_pair(unsigned long long p, float* lo, float* hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(p));
+}
+__device__ __forceinline__ unsigned long long fma_pair(unsigned long long a, unsigned long long b,
+                                                       unsigned long long c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ unsigned long long add_pair(unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 __device__ __forceinline__ void mma_fence_after() {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
@@ -130,6 +166,12 @@ __device__ __forceinline__ void mma_ts(unsigned d, unsigned a, unsigned long lon
         "r"(a), "l"(b), "r"(what), "r"(add)
         : "memory");
 }
+__device__ __forceinline__ bool elect_one() {
+    unsigned yes;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+    return yes != 0u;
+}
 // The barrier gets an arrival once all products issued so far are done.
 __device__ __forceinline__ void mma_commit(unsigned bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"l"(
@@ -150,7 +192,14 @@ __device__ __forceinline__ void tmem_load(unsigned at, float* f) {
           "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(at));
 }
-__device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Waits for the loads into x: what uses x comes after it (the loads' outputs alone would not tell the
+// compiler so).
+template <int N>
+__device__ __forceinline__ void tmem_wait_load(float (&x)[N]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+f"(x[i]));
+}
 __device__ __forceinline__ void tmem_store32(unsigned at, const float* f) {
     const unsigned* r = reinterpret_cast<const unsigned*>(f);
     asm volatile(
@@ -205,17 +254,19 @@ struct Weights<__half> {
 };
 
 // ---- shapes -----------------------------------------------------------------------------------
+constexpr int kStep = 64;                 // positions of a step
 template <int DP>
 struct Shape {
     static constexpr int TILES = DP > 128 ? 1 : 2;       // tiles of 128 rows
     static constexpr int KT = DP > 128 ? 64 : 128;       // positions of a unit
+    static constexpr int STEPS = KT / kStep;             // steps of a unit
     static constexpr int Q = 128 * DP * 2, STAGE = KT * DP * 2;      // bytes
     static constexpr int STAGES = DP == 64 ? 8 : 5;
     static constexpr int GROUP = 128 * TILES;            // threads with a row
     static constexpr int THREADS = GROUP + 64, WIDTH = 128;
-    // Tensor memory: S of each tile (later P, in the last half of S), then O of each.
-    static constexpr int P = KT / 2, O = 256;
-    static_assert(TILES * KT <= O && O + TILES * DP <= 512, "tensor memory");
+    // Tensor memory: two places of S for each tile (P in the last half of the place), then O of each.
+    static constexpr int P = kStep / 2, O = 256;
+    static_assert(TILES * 2 * kStep <= O && O + TILES * DP <= 512, "tensor memory");
     using Cut = ChunkCut<128 * TILES, 128, KT, THREADS, WIDTH>;
 };
 
@@ -227,9 +278,10 @@ struct alignas(1024) Smem {
     unsigned char ring[S::STAGES][S::STAGE];
     unsigned long long full[S::STAGES], empty[S::STAGES];
     unsigned long long item_full[kItems], item_empty[kItems];
-    unsigned long long q_full[2], s_full[2], p_full[2], o_full[2], tile_meet[2], both_meet, tail, drain;
+    unsigned long long q_full[2], q_empty[2], s_full[2][2], p_full[2][2], o_full[2][2];
+    unsigned long long tile_meet[2], both_meet, tail, drain;
     ChunkItem items[kItems];
-    int dead, seeded[2], hot[2];
+    int dead, seeded[2], hot[2][2];
     unsigned tmem;
     typename S::Cut::Shared plan;
 };
@@ -249,7 +301,7 @@ __device__ __noinline__ bool give_out(unsigned char* v, unsigned o_at, int dim, 
             for (int i = 0; i < 32; ++i) o[i] = 0.0f;
         } else {
             tmem_load(o_at + d0, o);
-            tmem_wait_load();
+            tmem_wait_load(o);
         }
         for (int r = 0; r < valid; ++r) {
             if (!((r >= lo || r < sinks) && r < hi)) continue;
@@ -280,7 +332,7 @@ __device__ __noinline__ bool give_out(unsigned char* v, unsigned o_at, int dim, 
 template <class T, int DP>
 __global__ void __launch_bounds__(Shape<DP>::THREADS, 1)
 chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUtensorMap k_map,
-                 const __grid_constant__ CUtensorMap v_map) {
+                 const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap q_map) {
     using S = Shape<DP>;
     using W = Weights<T>;
     constexpr int KT = S::KT, TILES = S::TILES;
@@ -301,12 +353,16 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
             bar_init(smem_at(&s.item_empty[i]), S::GROUP + 1);
         }
         for (int i = 0; i < 2; ++i) {
-            bar_init(smem_at(&s.q_full[i]), 128);
-            bar_init(smem_at(&s.s_full[i]), 1);
-            bar_init(smem_at(&s.p_full[i]), 128);
-            bar_init(smem_at(&s.o_full[i]), 1);
+            bar_init(smem_at(&s.q_full[i]), 1);
+            bar_init(smem_at(&s.q_empty[i]), 1);
+            bar_init(smem_at(&s.s_full[i][0]), 1);
+            bar_init(smem_at(&s.s_full[i][1]), 1);
+            bar_init(smem_at(&s.p_full[i][0]), 128);
+            bar_init(smem_at(&s.p_full[i][1]), 128);
+            bar_init(smem_at(&s.o_full[i][0]), 1);
+            bar_init(smem_at(&s.o_full[i][1]), 1);
             bar_init(smem_at(&s.tile_meet[i]), 128);
-            s.hot[i] = 0;
+            s.hot[i][0] = s.hot[i][1] = 0;
         }
         bar_init(smem_at(&s.both_meet), S::GROUP);
         bar_init(smem_at(&s.tail), 1);
@@ -332,16 +388,14 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
     cut.find(p);                          // (ends with a barrier)
     mma_fence_after();
     const unsigned tmem = s.tmem;
-    int stage = 0;                        // the ring: stage, and the parity of its use
-    unsigned turn = 0;
-    unsigned loads = 0;                   // loader: stages filled
-
     if (loader) {
         const int halves = (dim + 63) / 64;
         const int page_rows = min(p.c.page, KT);
         const unsigned box = page_rows * 128;
         const int pages = units.per > 0 ? 1 : KT / p.c.page, boxes = pages * halves;
-        unsigned tails = 0, bad = 0;
+        unsigned tails = 0, bad = 0, q_turn = 3u;        // (q_turn: a bit a tile)
+        int stage = 0;                    // the ring: stage, and the parity of its use
+        unsigned turn = 0;
         bool go = true;
         for (int n = 0; go;) {
             const int slot = n & 1;
@@ -352,6 +406,14 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
                     it = cut.item(p, atomicAdd(p.work, 1));
                 } while (it.kind != 0 && it.rows == 0);
                 if (bar_wait(smem_at(&s.item_empty[slot]), ((n >> 1) & 1) ^ 1, &s.dead)) {
+                    // (the last unit's second step may have no position that some row sees)
+                    it.steps = (it.hi - it.lo) * S::STEPS;
+                    if (S::STEPS == 2 && it.kind == 1 && it.hi > it.lo) {
+                        int c, r;
+                        const int at = units.first(it.span.unit(it.hi - 1), &c, &r);
+                        const int last = it.e.len - it.e.m + (it.row + it.rows - 1) / p.group;
+                        if (min(c, last + 1 - at) <= kStep) --it.steps;
+                    }
                     s.items[slot] = it;
                     kind = it.kind;
                     bar_arrive(smem_at(&s.item_full[slot]));
@@ -367,6 +429,8 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
             const ChunkItem& it = s.items[slot];
             const int head = it.head, len = it.e.len, lo = it.lo, hi = it.hi;
             const ChunkSpan span = it.span;
+            const int tiles = TILES == 2 && it.rows > 128 ? 2 : 1;
+            const int q_token = it.e.row + it.row / p.group;
             const int* const table = p.c.table + static_cast<long long>(it.e.seq) * p.c.cols;
             // Box `lane` of a unit, its page one unit ahead.
             auto page_of = [&](int at, int x) {
@@ -406,7 +470,20 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
                                  ok ? page : p.c.pages, bar);
                     }
                     if (live > 32) page = lane < boxes ? page_of(at, lane) : -2;
-                    ++loads;
+                    if (kv == 0 && u == lo && p.q_boxes != 0) {          // the queries, once the last item's are done with
+                        for (int w = 0; w < tiles && go; ++w) {
+                            go = warp_wait(smem_at(&s.q_empty[w]), q_turn >> w & 1, &s.dead);
+                            q_turn ^= 1u << w;
+                            if (!go) break;
+                            const unsigned q_bar = smem_at(&s.q_full[w]);
+                            if (lane == 0) bar_expect(q_bar, halves * 128 * 128);
+                            __syncwarp();
+                            if (lane < halves)
+                                load_box3(smem_at(s.q[w]) + lane * (128 * 128), &q_map, lane * 64, head * p.group,
+                                          q_token + w * (128 / p.group), q_bar);
+                        }
+                        if (!go) break;
+                    }
                     if (tail) {
                         if (!warp_wait(bar, tails & 1, &s.dead)) {
                             go = false;
@@ -437,99 +514,128 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
             while (chunk_clock() - t0 < 10ull * 1000ull * 1000ull) __nanosleep(10000);
         }
     } else if (issuer) {
-        if (lane == 0) {
-            const unsigned kind = 1u << 4 | W::kType << 7 | W::kType << 10 | (128u >> 4) << 24;
-            const unsigned what_s = kind | static_cast<unsigned>(KT >> 3) << 17;
-            const unsigned what_o = kind | 1u << 16 | static_cast<unsigned>((dim + 15) / 16 * 2) << 17;
-            const int steps = (dim + 15) / 16;
-            unsigned q_turn = 0, p_turn = 0;
-            bool go = true;
-            for (int n = 0; go; ++n) {
-                const int slot = n & 1;
-                if (!bar_wait(smem_at(&s.item_full[slot]), (n >> 1) & 1, &s.dead)) break;
-                const int item = s.items[slot].kind, rows = s.items[slot].rows;
-                const int count = s.items[slot].hi - s.items[slot].lo;
-                bar_arrive(smem_at(&s.item_empty[slot]));
-                if (item == 0) break;
-                if (item == 2 || count == 0) continue;
-                const int tiles = TILES == 2 && rows > 128 ? 2 : 1;
-                auto scores = [&](int w, unsigned k) {
-                    const unsigned q = smem_at(s.q[w]);
-                    for (int i = 0; i < steps; ++i)
-                        mma_ss(tmem + w * KT, matrix_at(q + (i >> 2) * (128 * 128) + (i & 3) * 32, 16),
-                               matrix_at(k + (i >> 2) * (KT * 128) + (i & 3) * 32, 16), what_s, i > 0);
-                };
-                if (!(go = bar_wait(smem_at(&s.full[stage]), turn, &s.dead))) break;
-                for (int w = 0; w < tiles && go; ++w) {
-                    go = bar_wait(smem_at(&s.q_full[w]), q_turn >> w & 1, &s.dead);
-                    q_turn ^= 1u << w;
-                    if (!go) break;
-                    mma_fence_after();
-                    scores(w, smem_at(s.ring[stage]));
-                    mma_commit(smem_at(&s.s_full[w]));
+        // The whole warp goes through the loop, so that what the instructions are given is the same in all
+        // lanes; one of them issues.
+        const unsigned kind = 1u << 4 | W::kType << 7 | W::kType << 10 | (128u >> 4) << 24;
+        const unsigned what_s = kind | static_cast<unsigned>(kStep >> 3) << 17;
+        const unsigned what_o = kind | 1u << 16 | static_cast<unsigned>((dim + 15) / 16 * 2) << 17;
+        const int steps = (dim + 15) / 16;
+        const bool one = elect_one();
+        const unsigned long long q_at = matrix_at(smem_at(s.q[0]), 16);
+        const unsigned long long k_at = matrix_at(smem_at(s.ring[0]), 16);
+        const unsigned long long v_at = matrix_at(smem_at(s.ring[0]), KT * 128);
+        unsigned q_turn = 0;
+        bool go = true;
+        unsigned done[2] = {0, 0};        // steps of each tile's rows so far
+        unsigned ring = 0;                // stages gone through
+        auto stage_of = [&](unsigned n) { return n % S::STAGES; };
+        auto filled = [&](unsigned n) {
+            return warp_wait(smem_at(&s.full[n % S::STAGES]), n / S::STAGES & 1, &s.dead);
+        };
+        // Scores of step `step` of the item from stage `at`.
+        auto scores = [&](int w, unsigned step, unsigned at) {
+            if (!one) return;
+            const unsigned place = done[w] + step & 1;
+            const unsigned long long q = q_at + w * (S::Q / 16);
+            const unsigned long long k = k_at + at * (S::STAGE / 16) + step % S::STEPS * (kStep * 128 / 16);
+#pragma unroll
+            for (int i = 0; i < DP / 16; ++i)
+                if (i < steps)
+                    mma_ss(tmem + (w * 2 + place) * kStep, q + ((i >> 2) * (128 * 128) + (i & 3) * 32) / 16,
+                           k + ((i >> 2) * (KT * 128) + (i & 3) * 32) / 16, what_s, i > 0);
+            mma_commit(smem_at(&s.s_full[w][place]));
+        };
+        for (int n = 0; go; ++n) {
+            const int slot = n & 1;
+            if (!warp_wait(smem_at(&s.item_full[slot]), (n >> 1) & 1, &s.dead)) break;
+            const int item = s.items[slot].kind, rows = s.items[slot].rows;
+            const unsigned count = s.items[slot].hi - s.items[slot].lo, total = s.items[slot].steps;
+            __syncwarp();
+            if (one) bar_arrive(smem_at(&s.item_empty[slot]));
+            if (item == 0) break;
+            if (item == 2 || count == 0) continue;
+            const int tiles = TILES == 2 && rows > 128 ? 2 : 1;
+            // K of unit u is stage ring + 2 u, V the one after.
+            unsigned known = 0;           // stages of the item that are known to be there
+            auto have = [&](unsigned n) {
+                while (known <= n && go) {
+                    go = filled(ring + known);
+                    ++known;
                 }
-                if (!go) break;
-                mma_commit(smem_at(&s.empty[stage]));
-                for (int u = 0; u < count && go; ++u) {
-                    if (++stage == S::STAGES) {
-                        stage = 0;
-                        turn ^= 1;
-                    }
-                    const int v_stage = stage;
-                    if (!(go = bar_wait(smem_at(&s.full[stage]), turn, &s.dead))) break;
-                    const bool more = u + 1 < count;
-                    if (more) {
-                        if (++stage == S::STAGES) {
-                            stage = 0;
-                            turn ^= 1;
-                        }
-                    }
-                    for (int w = 0; w < tiles && go; ++w) {
-                        go = bar_wait(smem_at(&s.p_full[w]), p_turn >> w & 1, &s.dead);
-                        p_turn ^= 1u << w;
+                return go;
+            };
+            // Step g's scores, and what follows from them for its stage.
+            auto score_step = [&](int w, unsigned g) {
+                scores(w, g, stage_of(ring + g / S::STEPS * 2));
+                if (one && w == tiles - 1 && (g % S::STEPS == S::STEPS - 1 || g + 1 == total))
+                    mma_commit(smem_at(&s.empty[stage_of(ring + g / S::STEPS * 2)]));
+                if (one && g + 1 == total) mma_commit(smem_at(&s.q_empty[w]));
+                __syncwarp();
+            };
+            for (unsigned g = 0; g < 2 && g < total && go; ++g) {
+                if (!have(g / S::STEPS * 2)) break;
+                for (int w = 0; w < tiles && go; ++w) {
+                    if (g == 0) {
+                        go = warp_wait(smem_at(&s.q_full[w]), q_turn >> w & 1, &s.dead);
+                        q_turn ^= 1u << w;
                         if (!go) break;
                         mma_fence_after();
-                        const unsigned v = smem_at(s.ring[v_stage]);
-                        const unsigned add = u > 0 || *static_cast<volatile int*>(&s.seeded[w]) != 0;
-                        for (int i = 0; i < KT / 16; ++i)
-                            mma_ts(tmem + S::O + w * DP, tmem + w * KT + S::P + i * 8, matrix_at(v + i * 2048, KT * 128),
-                                   what_o, add | (i > 0));
-                        mma_commit(smem_at(&s.o_full[w]));
-                        if (w == tiles - 1) mma_commit(smem_at(&s.empty[v_stage]));
-                        if (more) {
-                            if (w == 0 && !(go = bar_wait(smem_at(&s.full[stage]), turn, &s.dead))) break;
-                            scores(w, smem_at(s.ring[stage]));
-                            mma_commit(smem_at(&s.s_full[w]));
-                            if (w == tiles - 1) mma_commit(smem_at(&s.empty[stage]));
-                        }
+                    }
+                    score_step(w, g);
+                }
+            }
+            for (unsigned g = 0; g < total && go; ++g) {
+                const unsigned v_stage = stage_of(ring + g / S::STEPS * 2 + 1);
+                const bool more = g + 2 < total;
+                if (!have(g / S::STEPS * 2 + 1)) break;
+                for (int w = 0; w < tiles; ++w) {
+                    // (A place has a barrier of its own: a warp may be a step ahead of another.)
+                    const unsigned place = done[w] + g & 1;
+                    go = warp_wait(smem_at(&s.p_full[w][place]), done[w] + g >> 1 & 1, &s.dead);
+                    if (!go) break;
+                    mma_fence_after();
+                    const unsigned add = g > 0 || *static_cast<volatile int*>(&s.seeded[w]) != 0;
+                    if (one) {
+                        const unsigned long long v = v_at + v_stage * (S::STAGE / 16) + g % S::STEPS * (kStep * 128 / 16);
+#pragma unroll
+                        for (int i = 0; i < kStep / 16; ++i)
+                            mma_ts(tmem + S::O + w * DP, tmem + (w * 2 + place) * kStep + S::P + i * 8,
+                                   v + i * (2048 / 16), what_o, add | (i > 0));
+                        mma_commit(smem_at(&s.o_full[w][place]));
+                        if (w == tiles - 1 && (g % S::STEPS == S::STEPS - 1 || g + 1 == total))
+                            mma_commit(smem_at(&s.empty[v_stage]));
+                    }
+                    __syncwarp();
+                    if (more) {
+                        if (!have((g + 2) / S::STEPS * 2)) break;
+                        score_step(w, g + 2);
                     }
                 }
-                if (++stage == S::STAGES) {
-                    stage = 0;
-                    turn ^= 1;
-                }
             }
-            if (s.dead != 0) {            // products under way end before the block does
-                mma_commit(smem_at(&s.drain));
-                const unsigned long long t0 = chunk_clock();
-                while (!bar_try(smem_at(&s.drain), 0) && chunk_clock() - t0 < 10ull * 1000ull * 1000ull) {}
-            }
+            ring += 2 * count;
+            for (int w = 0; w < tiles; ++w) done[w] += total;
+        }
+        if (s.dead != 0) {                // products under way end before the block does
+            if (one) mma_commit(smem_at(&s.drain));
+            const unsigned long long t0 = chunk_clock();
+            while (!bar_try(smem_at(&s.drain), 0) && chunk_clock() - t0 < 10ull * 1000ull * 1000ull) {}
         }
         __syncwarp();
     } else if (warp < S::GROUP / 32) {
         const int w = TILES == 2 ? warp >> 2 : 0, mine = tid & 127;
         const unsigned lanes = static_cast<unsigned>((warp & 3) * 32) << 16;
-        const unsigned s_at = tmem + lanes + w * KT, o_at = tmem + lanes + S::O + w * DP;
+        const unsigned s_at = tmem + lanes + w * 2 * kStep, o_at = tmem + lanes + S::O + w * DP;
         const float scale = p.scale_log2;
-        unsigned s_turn = 0, o_turn = 0, meet_turn = 0, both_turn = 0;       // parities of the next phases
+        unsigned meet_turn = 0, both_turn = 0;                               // parities of the next phases
+        unsigned done = 0;                // steps
         int looked = 0;                   // units looked through
-        int v_stage = 0;                  // the ring as the issuer goes through it
-        unsigned v_turn = 0;
-        auto next_stage = [&] {
-            if (++v_stage == S::STAGES) {
-                v_stage = 0;
-                v_turn ^= 1;
-            }
+        unsigned ring = 0;                // stages gone through
+        // Step number `step`'s products with V are in O.  (A step's two barriers take turns with the places of
+        // S: the one before last is known to be done, so that a phase is never taken for an older one.)
+        auto added = [&](unsigned step) {
+            const bool ok = warp_wait(smem_at(&s.o_full[w][step & 1]), step >> 1 & 1, &s.dead);
+            mma_fence_after();
+            return ok;
         };
         bool go = true;
         for (int n = 0; go; ++n) {
@@ -541,13 +647,13 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
                 if (mine == 0 && !chunk_wait_parts(p.work + kChunkHead + it.tile, it.need))
                     *static_cast<volatile int*>(&s.dead) = 1;
                 if (!meet(smem_at(&s.tile_meet[w]), &meet_turn, &s.dead)) break;
-                chunk_join<T>(p, it, tid, S::GROUP, W::kLift);
+                chunk_join<T>(p, it, warp, S::GROUP / 32, W::kLift);
                 bar_arrive(smem_at(&s.item_empty[slot]));
                 continue;
             }
             const int count = it.hi - it.lo, tiles = TILES == 2 && it.rows > 128 ? 2 : 1;
             if (w >= tiles) {
-                for (int u = 0; u < 2 * count; ++u) next_stage();
+                ring += 2 * count;
                 bar_arrive(smem_at(&s.item_empty[slot]));
                 continue;
             }
@@ -555,8 +661,8 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
             const bool real = r < it.rows;
             const int from = it.e.len - it.e.m;
             const int token = row / p.group, pos = from + token;
-            if (count > 0) {
-                // The row of Q, with the scale's sign.
+            if (count > 0 && p.q_boxes == 0) {
+                // The row of Q, with the scale's sign, where TMA cannot bring it.
                 const T* const q = static_cast<const T*>(p.q) + (it.e.row + static_cast<long long>(token)) * p.q_token +
                                    (it.head * p.group + row - token * p.group) * p.q_head;
                 unsigned char* const to = s.q[w] + mine * 128;
@@ -575,31 +681,35 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
                     *reinterpret_cast<uint4*>(to + (c >> 3) * (128 * 128) + (((c & 7) ^ (mine & 7)) << 4)) = x;
                 }
                 async_fence();
-                bar_arrive(smem_at(&s.q_full[w]));
+                if (!(go = meet(smem_at(&s.tile_meet[w]), &meet_turn, &s.dead))) break;
+                if (mine == 0) bar_arrive(smem_at(&s.q_full[w]));
             }
             float top = kNegInf, sum = 0.0f;
             const int first_pos = from + it.row / p.group, last_pos = from + (it.row + it.rows - 1) / p.group;
-            for (int u = 0; u < count; ++u) {
+            const bool idle = w * 128 + (warp & 3) * 32 >= it.rows;      // none of the warp's rows is the tile's
+            const int total = it.steps;
+            for (int g = 0; g < total; ++g) {
+                const int sub = S::STEPS == 1 ? 0 : g & 1;
                 int here, in_page;
-                const int at = units.first(it.span.unit(it.lo + u), &here, &in_page);
+                const int at = units.first(it.span.unit(it.lo + g / S::STEPS), &here, &in_page);
                 const int valid = min(here, it.e.len - at);
                 // What this row sees of the unit: lo .. hi - 1, and those below sink.
                 const int hi = min(valid, pos - at + 1);
                 const int lo = p.window > 0 ? pos - p.window + 1 - at : 0;
                 const int sink = p.window > 0 ? p.sinks - at : 0;
-                next_stage();                            // to V's
                 // Whether some row of the block's tiles sees the unit in part (all threads alike).
                 const bool part = at + valid - 1 > first_pos ||
                                   (p.window > 0 && at <= last_pos - p.window && at + valid > p.sinks);
-                if (!(go = warp_wait(smem_at(&s.s_full[w]), s_turn, &s.dead))) break;
-                s_turn ^= 1;
+                const unsigned place = done + g & 1;
+                if (!(go = warp_wait(smem_at(&s.s_full[w][place]), (done + g) >> 1 & 1, &s.dead))) break;
                 mma_fence_after();
                 bool odd = false;
-                if (part) {
-                    if (!(go = warp_wait(smem_at(&s.full[v_stage]), v_turn, &s.dead))) break;
+                if (part && sub == 0) {
+                    const unsigned v_at = ring + g / S::STEPS * 2 + 1, v_stage = v_at % S::STAGES;
+                    if (!(go = warp_wait(smem_at(&s.full[v_stage]), v_at / S::STAGES & 1, &s.dead))) break;
                     unsigned hot = 0;
                     const uint4* const v = reinterpret_cast<const uint4*>(s.ring[v_stage]);
-#pragma unroll 4
+#pragma unroll 8
                     for (int x = mine; x < S::STAGE / 16; x += 128) {
                         const uint4 y = v[x];
                         hot |= ((y.x & W::kExponent) + W::kOne) | ((y.y & W::kExponent) + W::kOne) |
@@ -608,106 +718,89 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
                     // (All of a tile's threads look at all of it.)
                     ++looked;
                     if (__any_sync(0xffffffffu, (hot & 0x80008000u) != 0u) && lane == 0)
-                        *static_cast<volatile int*>(&s.hot[w]) = looked;
+                        *static_cast<volatile int*>(&s.hot[w][looked & 1]) = looked;
                     if (!(go = meet(smem_at(&s.tile_meet[w]), &meet_turn, &s.dead))) break;
-                    odd = *static_cast<volatile int*>(&s.hot[w]) == looked;
+                    odd = *static_cast<volatile int*>(&s.hot[w][looked & 1]) == looked;
+                    if (odd) {
+                        if (g > 0 && !(go = added(done + g - 1))) break;
+                        if (!(go = give_out<T, DP>(s.ring[v_stage], o_at, dim, lo, hi, sink, valid, g == 0, 128 * tiles,
+                                                   smem_at(tiles == 2 ? &s.both_meet : &s.tile_meet[w]),
+                                                   tiles == 2 ? &both_turn : &meet_turn, &s.dead)))
+                            break;
+                    }
                 }
-                if (odd) {
-                    if (u > 0 && !(go = warp_wait(smem_at(&s.o_full[w]), o_turn ^ 1, &s.dead))) break;
-                    mma_fence_after();
-                    if (!(go = give_out<T, DP>(s.ring[v_stage], o_at, dim, lo, hi, sink, valid, u == 0, 128 * tiles,
-                                               smem_at(tiles == 2 ? &s.both_meet : &s.tile_meet[w]),
-                                               tiles == 2 ? &both_turn : &meet_turn, &s.dead)))
-                        break;
-                }
-                if (u == 0 && mine == 0) s.seeded[w] = odd;
-                next_stage();                            // to the next K's
-                // S 64 columns at a time, the last ones last: they stay in registers for the weights, the
-                // others are read again (a thread with all 128 would have to spill).
-                float x[64];
-                const bool whole = __all_sync(0xffffffffu, hi >= KT && lo <= 0);
-                auto read = [&](int c0) {
-                    tmem_load(s_at + c0, x);
-                    tmem_load(s_at + c0 + 32, x + 32);
-                    tmem_wait_load();
-                    if (!whole) {
+                if (g == 0 && mine == 0) s.seeded[w] = odd;
+                if (!idle) {
+                    float x[kStep];
+                    const unsigned from_at = s_at + place * kStep;
+                    tmem_load(from_at, x);
+                    tmem_load(from_at + 32, x + 32);
+                    tmem_wait_load(x);
+                    const int c0 = sub * kStep;
+                    if (!__all_sync(0xffffffffu, hi >= c0 + kStep && lo <= c0)) {
 #pragma unroll
-                        for (int c = 0; c < 64; ++c)
+                        for (int c = 0; c < kStep; ++c)
                             if (!(c < hi - c0 && (c >= lo - c0 || c < sink - c0))) x[c] = kNegInf;
                     }
-                };
-                float up = kNegInf;
+                    float up0 = x[0], up1 = x[1];
 #pragma unroll
-                for (int c0 = 0; c0 < KT; c0 += 64) {
-                    read(c0);
-                    float up0 = up, up1 = x[1], up2 = x[2], up3 = x[3];
-                    up0 = fmaxf(up0, x[0]);
-#pragma unroll
-                    for (int c = 4; c < 64; c += 4) {
-                        up0 = fmaxf(up0, x[c]);
-                        up1 = fmaxf(up1, x[c + 1]);
-                        up2 = fmaxf(up2, x[c + 2]);
-                        up3 = fmaxf(up3, x[c + 3]);
+                    for (int c = 2; c < kStep - 2; c += 4) {
+                        up0 = max3(up0, x[c], x[c + 1]);
+                        up1 = max3(up1, x[c + 2], x[c + 3]);
                     }
-                    up = fmaxf(fmaxf(up0, up1), fmaxf(up2, up3));
-                }
-                up *= scale;
-                const bool move = up > top + W::kSlack || (top == kNegInf && up > kNegInf);
-                if (__any_sync(0xffffffffu, move)) {
-                    const float by = move ? chunk_pow2(top - up) : 1.0f;     // 0 at the first position
-                    if (move) top = up;
-                    sum *= by;
-                    if (u > 0) {
-                        if (!(go = warp_wait(smem_at(&s.o_full[w]), o_turn ^ 1, &s.dead))) break;
-                        mma_fence_after();
-                        for (int d = 0; d < dim; d += 32) {
-                            float o[32];
-                            tmem_load(o_at + d, o);
-                            tmem_wait_load();
+                    const float up = max3(max3(up0, x[kStep - 2], x[kStep - 1]), up1, kNegInf) * scale;
+                    const bool move = up > top + W::kSlack || (top == kNegInf && up > kNegInf);
+                    if (__any_sync(0xffffffffu, move)) {
+                        const float by = move ? chunk_pow2(top - up) : 1.0f;         // 0 at the first position
+                        if (move) top = up;
+                        sum *= by;
+                        if (g > 0) {
+                            if (!(go = added(done + g - 1))) break;
+                            for (int d = 0; d < dim; d += 32) {
+                                float o[32];
+                                tmem_load(o_at + d, o);
+                                tmem_wait_load(o);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] *= by;
-                            tmem_store32(o_at + d, o);
+                                for (int i = 0; i < 32; ++i) o[i] *= by;
+                                tmem_store32(o_at + d, o);
+                            }
+                            tmem_wait_store();
                         }
-                        tmem_wait_store();
                     }
-                }
-                const float base = W::kLift - (top == kNegInf ? 0.0f : top);
-                float sum1 = 0.0f, sum2 = 0.0f, sum3 = 0.0f;
+                    const float base = W::kLift - (top == kNegInf ? 0.0f : top);
+                    const unsigned long long scale2 = pair_of(scale, scale), base2 = pair_of(base, base);
+                    unsigned long long sums = 0ull, more = 0ull;
 #pragma unroll
-                for (int c0 = KT - 64; c0 >= 0; c0 -= 64) {
-                    if (c0 != KT - 64) read(c0);
-#pragma unroll
-                    for (int h = 0; h < 64; h += 32) {
+                    for (int h = 0; h < kStep; h += 32) {
                         unsigned r16[16];
 #pragma unroll
                         for (int i = 0; i < 32; i += 4) {
-                            const float a = chunk_pow2(fmaf(x[h + i], scale, base));
-                            const float b = chunk_pow2(fmaf(x[h + i + 1], scale, base));
-                            const float e = chunk_pow2(fmaf(x[h + i + 2], scale, base));
-                            const float f = chunk_pow2(fmaf(x[h + i + 3], scale, base));
-                            sum += a;
-                            sum1 += b;
-                            sum2 += e;
-                            sum3 += f;
+                            float a, b, e, f;
+                            split_pair(fma_pair(pair_of(x[h + i], x[h + i + 1]), scale2, base2), &a, &b);
+                            split_pair(fma_pair(pair_of(x[h + i + 2], x[h + i + 3]), scale2, base2), &e, &f);
+                            a = chunk_pow2(a);
+                            b = chunk_pow2(b);
+                            e = chunk_pow2(e);
+                            f = chunk_pow2(f);
+                            sums = add_pair(sums, pair_of(a, b));
+                            more = add_pair(more, pair_of(e, f));
                             r16[i / 2] = W::pack(a, b);
                             r16[i / 2 + 1] = W::pack(e, f);
                         }
-                        // (over columns of S that have been read)
-                        tmem_store16(s_at + S::P + (c0 + h) / 2, r16);
+                        tmem_store16(from_at + S::P + h / 2, r16);
                     }
+                    float a, b;
+                    split_pair(add_pair(sums, more), &a, &b);
+                    sum += a + b;
+                    tmem_wait_store();
                 }
-                sum = (sum + sum1) + (sum2 + sum3);
-                tmem_wait_store();
                 mma_fence_before();
-                bar_arrive(smem_at(&s.p_full[w]));
-                o_turn ^= 1;
+                bar_arrive(smem_at(&s.p_full[w][place]));
             }
+            ring += 2 * count;
+            done += total;
             if (!go) break;
-            // (o_turn has changed count times: the last phase's parity is its opposite.)
-            if (count > 0) {
-                if (!(go = warp_wait(smem_at(&s.o_full[w]), o_turn ^ 1, &s.dead))) break;
-                mma_fence_after();
-            }
+            if (count > 0 && !(go = added(done - 1))) break;
             float* lse = nullptr;
             T* const to = real ? chunk_out<T>(p, it, row, &lse) : nullptr;
             float* const part = p.slots + it.slot * chunk_slot_words(p.slot_rows, dim);
@@ -716,7 +809,7 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
                 float o[32];
                 if (count > 0) {
                     tmem_load(o_at + d, o);
-                    tmem_wait_load();
+                    tmem_wait_load(o);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = 0.0f;
@@ -789,31 +882,55 @@ bool encode(CUtensorMap* map, int dtype, const CacheView& c, const char* base, i
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The queries as boxes of 64 values of a tile's rows: token after token, the heads of a group.
+bool encode_q(CUtensorMap* map, int dtype, const ChunkParams& p) {
+    const auto type = dtype == GS_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.c.dim), static_cast<cuuint64_t>(p.q_heads),
+                                static_cast<cuuint64_t>(p.tokens)};
+    const long long row = 2ll * p.c.dim;
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(p.q_heads > 1 ? 2 * p.q_head : row),
+                                   static_cast<cuuint64_t>(p.tokens > 1 ? 2 * p.q_token : row)};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(p.group), static_cast<cuuint32_t>(128 / p.group)};
+    const cuuint32_t step[3] = {1, 1, 1};
+    return encoder() != nullptr &&
+           encoder()(map, type, 3, const_cast<void*>(p.q), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Maps {
+    CUtensorMap k, v, q;
+};
+
 template <class T, int DP>
-gs_status launch_as(const ChunkParams& p, const CUtensorMap& k, const CUtensorMap& v, int blocks, gs_stream stream) {
+gs_status launch_as(const ChunkParams& p, const Maps& m, int blocks, gs_stream stream) {
     constexpr int bytes = static_cast<int>(sizeof(Smem<DP>));
     if (!allow_smem<chunk_mma_kernel<T, DP>>(bytes)) return GS_ERR_CUDA;
-    return launch(chunk_mma_kernel<T, DP>, dim3(blocks), Shape<DP>::THREADS, bytes, 1, stream, p, k, v);
+    return launch(chunk_mma_kernel<T, DP>, dim3(blocks), Shape<DP>::THREADS, bytes, 1, stream, p, m.k, m.v, m.q);
 }
 
 template <class T>
-gs_status launch_type(const ChunkParams& p, const CUtensorMap& k, const CUtensorMap& v, int blocks, gs_stream stream) {
-    if (p.c.dim <= 64) return launch_as<T, 64>(p, k, v, blocks, stream);
-    if (p.c.dim <= 128) return launch_as<T, 128>(p, k, v, blocks, stream);
-    return launch_as<T, 256>(p, k, v, blocks, stream);
+gs_status launch_type(const ChunkParams& p, const Maps& m, int blocks, gs_stream stream) {
+    if (p.c.dim <= 64) return launch_as<T, 64>(p, m, blocks, stream);
+    if (p.c.dim <= 128) return launch_as<T, 128>(p, m, blocks, stream);
+    return launch_as<T, 256>(p, m, blocks, stream);
 }
 
 }  // namespace
 
 ChunkShape chunk_mma_shape(int dim) { return {dim > 128 ? 128 : 256, sm_count()}; }
 
-gs_status launch_chunk_mma(int dtype, const ChunkParams& p, int blocks, gs_stream stream) {
-    CUtensorMap k, v;
+gs_status launch_chunk_mma(int dtype, ChunkParams& p, int blocks, gs_stream stream) {
+    Maps m = {};
     const int unit = p.c.dim > 128 ? 64 : 128;
     const int rows = p.c.page < unit ? p.c.page : unit;
-    if (!encode(&k, dtype, p.c, p.c.k, rows) || !encode(&v, dtype, p.c, p.c.v, rows)) return GS_ERR_CUDA;
-    if (dtype == GS_DTYPE_BF16) return launch_type<__nv_bfloat16>(p, k, v, blocks, stream);
-    return launch_type<__half>(p, k, v, blocks, stream);
+    if (!encode(&m.k, dtype, p.c, p.c.k, rows) || !encode(&m.v, dtype, p.c, p.c.v, rows)) return GS_ERR_CUDA;
+    // TMA brings the queries as they are, in boxes that hold whole tokens of a group, from rows on 16 bytes.
+    p.q_boxes = p.q_aligned != 0 && p.q_sign > 0.0f && 128 % p.group == 0 && (p.tokens == 1 || p.q_token > 0) &&
+                (p.q_heads == 1 || p.q_head > 0);
+    if (p.q_boxes != 0 && !encode_q(&m.q, dtype, p)) return GS_ERR_CUDA;
+    if (dtype == GS_DTYPE_BF16) return launch_type<__nv_bfloat16>(p, m, blocks, stream);
+    return launch_type<__half>(p, m, blocks, stream);
 }
 
 }  // namespace gs_decode
