@@ -33,18 +33,18 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, dim = p.c.dim;
     grid_wait();
     grid_trigger();
-    Cut cut = {&plan};
+    Cut cut;
+    cut.s = &plan;
     cut.find(p);
     const ChunkUnits<KT> units(p.c.page);
     for (;;) {
-        if (tid == 0) item = cut.item(p, atomicAdd(p.work, 1));
+        if (tid == 0) item = cut.item(p);
         __syncthreads();
         const ChunkItem it = item;
         __syncthreads();
         if (it.kind == 0) break;
-        if (it.rows == 0) continue;
         if (it.kind == 2) {
-            if (tid == 0) ok = chunk_wait_parts(p.work + kChunkHead + it.tile, it.need);
+            if (tid == 0) ok = chunk_wait_parts(p.work + kChunkHead + it.share, it.need);
             __syncthreads();
             if (ok) chunk_join<T>(p, it, tid >> 5, kThreads / 32, 0.0f);
             else if (tid == 0) flag(p.c.status, GS_DEV_TIMEOUT);
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         if (it.parts > 1) {
             __threadfence();
             __syncthreads();
-            if (tid == 0) atomicAdd(p.work + kChunkHead + it.tile, 1);
+            if (tid == 0) atomicAdd(p.work + kChunkHead + it.share, 1);
         }
     }
     if (tid < 32) chunk_leave(p, cut.used());
@@ -266,11 +266,8 @@ gs_status plan_of(const gs_chunk_attention_args* a, Plan* plan) {
     plan->shape = c->dtype == GS_DTYPE_F32 ? chunk_fp32_shape(c->dim) : chunk_mma_shape(c->dim);
     const long long rows = (a->tokens * group + 7) / 8 * 8;
     plan->rows = static_cast<int>(rows < plan->shape.rows ? rows : plan->shape.rows);
-    // Tiles are cut where there are fewer than 4 a block, into parts of which all make 2 a block, and
-    // one a tile more where they do not divide; no more than a unit a part.
-    const long long tiles = c->kv_heads * (a->tokens * group / plan->shape.rows + a->n);
-    const long long most = tiles < 4ll * plan->shape.blocks ? tiles : 4ll * plan->shape.blocks;
-    plan->slots = a->tokens == 0 || a->n == 0 ? 0 : static_cast<int>(2ll * plan->shape.blocks + most);
+    if (plan->shape.blocks > kChunkShares) plan->shape.blocks = kChunkShares;
+    plan->slots = a->tokens == 0 || a->n == 0 ? 0 : 2 * plan->shape.blocks;
     return GS_OK;
 }
 
@@ -339,7 +336,6 @@ extern "C" gs_status gs_chunk_attention(const gs_chunk_attention_args* args, gs_
     p.lse = args->lse;
     p.work = static_cast<int*>(args->workspace);
     p.slots = static_cast<float*>(args->workspace) + kChunkCounters;
-    p.slot_count = plan.slots;
     p.slot_rows = plan.rows;
     if (args->cache->dtype == GS_DTYPE_F32) return launch_chunk_fp32(p, plan.shape.blocks, stream);
     return launch_chunk_mma(args->cache->dtype, p, plan.shape.blocks, stream);

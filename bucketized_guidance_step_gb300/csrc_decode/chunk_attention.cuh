@@ -8,11 +8,16 @@
 // sees are read in units of up to KT tokens: whole pages where a page has up to KT tokens, else a
 // part of one page.
 //
-// Lengths and chunks are on the device, so the cut is found there: every block sums the entries'
-// tiles and units, a pass over n entries that is a word or two a thread.  An item is a tile, or where
-// there are few tiles a run of `each` units of one; blocks take items from a queue, the longest of an
-// entry first.  The outputs of an item do not depend on who computes it or when, and the parts of a
-// tile are joined in their order by further items of the queue: results do not depend on timing.
+// Lengths and chunks are on the device, so the cut is found there: every block sums up what the tiles of
+// the call cost, a pass over n entries in closed form, and the sum is cut into as many equal shares as
+// there are blocks, each a run of neighbouring tiles and parts of tiles.  So ragged chunks and lengths
+// balance without the host knowing them, one long sequence spreads over every block, and there are two
+// parts a share at most.  A share whose edge would leave less than two units of a tile, or lies in a tile
+// of few, takes or leaves the tile whole.
+//
+// Blocks take shares from a queue, and once there are no more, the joins of the shares' parts: what waits
+// for a part waits for a block that is running.  The outputs of a share do not depend on who computes it
+// or when, and the parts of a tile are joined in a fixed order: results do not depend on timing.
 #pragma once
 
 #include "decode_common.cuh"
@@ -22,8 +27,8 @@ namespace gs_decode {
 constexpr float kChunkLog2e = 1.4426950408889634f;
 constexpr float kChunkLn2 = 0.6931471805599453f;
 constexpr int kChunkCounters = GS_CHUNK_COUNTERS;        // words of the workspace that are 0 between calls
-constexpr int kChunkHead = 4;                            // of these, before the tiles' counts
-constexpr int kChunkCut = kChunkCounters - kChunkHead;   // most tiles of a call whose tiles are cut
+constexpr int kChunkHead = 4;                            // of these, before the shares' counts
+constexpr int kChunkShares = kChunkCounters - kChunkHead;            // most shares
 constexpr unsigned long long kChunkLimitNs = 200ull * 1000ull * 1000ull;   // of a wait
 
 struct ChunkParams {
@@ -42,10 +47,10 @@ struct ChunkParams {
     void* out;
     long long out_token, out_head;
     float* lse;
-    int* work;                            // [0] the queue, [1] blocks that are done, [kChunkHead ..]
-                                          // parts of a tile that are done
-    float* slots;                         // [slot_count][slot_words]
-    int slot_count, slot_rows;            // slots; rows of one
+    int* work;                            // [0] the queue, [1] blocks that are done, [kChunkHead ..] by
+                                          // share: parts that are done of the tile it began and did not end
+    float* slots;                         // two a share: for the tile it did not begin, the one it does not end
+    int slot_rows;                        // rows of one
 };
 
 // A slot: reference[rows], sum[rows], o[rows][dim].
@@ -143,169 +148,239 @@ struct ChunkItem {
     int rows;                             // rows of it (kind 2: of the piece)
     ChunkSpan span;
     int lo, hi;                           // units lo .. hi - 1 of the span
-    int parts, slot;                      // parts of the tile; slot of this one (kind 2: of the first)
-    int need;                             // its count once all parts are there
-    int tile;                             // its count's number
+    int parts, share;                     // parts of the tile; the share that has the first
+    int slot;                             // of this part
+    int need;                             // the tile's count once all parts are there
     int at;                               // kind 2: first row of the piece in the tile
     int steps;                            // of the tensor cores' kernel
 };
 
-// The cut, found by every block alike: WIDTH of its THREADS threads take the entries.  A tile's
-// parts count once for every HALF rows of it.
+// The slot of part k of a tile that begins in `share`.
+__device__ __forceinline__ int chunk_slot(int share, int k) { return 2 * (share + k) + (k == 0); }
+
+// The cut, found by every block alike: WIDTH of its THREADS threads take the entries.  A tile's parts
+// count once for every HALF rows of it.  Costs are in 16ths of a position.
 template <int ROWS, int HALF, int KT, int THREADS, int WIDTH>
 struct ChunkCut {
-    static constexpr int kMinUnits = 4;   // of a part
+    using ll = long long;
+    static constexpr int kOver = 16 * 192;               // what a tile costs beside its positions
+    static constexpr int kFew = 8;        // units of a tile that is not cut
+    static constexpr int kLeast = 2;      // units of a part
     struct Shared {
-        int items[WIDTH], tiles[WIDTH];                  // before a thread's entries
-        long long tmp[THREADS / 32 + 1];
-        int each, total_items, total_tiles, pieces;
+        ll before[WIDTH];                 // cost before a thread's entries
+        ll tmp[THREADS / 32 + 1];
+        ll each;                          // shares: the first `more` have each + 1, the others each
+        int more, shares;
+    };
+
+    // What the tiles of a head cost: a tile whose last row sees `a` positions kOver + a, a_t = from + (t + 1)
+    // step up to `cap`.
+    struct Cost {
+        ll from, step, cap;
+        int tiles, turn;                  // tiles; those below the cap
+        __device__ __forceinline__ ll upto(int t) const {            // of the first t
+            const ll y = t < turn ? t : turn;
+            return t * static_cast<ll>(kOver) + y * from + step * (y * (y + 1) / 2) + (t - y) * cap;
+        }
     };
     Shared* s;
+    // The walk over a share's tiles (one thread's).
+    ll x0, x1, entry_at;                  // the share; cost before the entry
+    Cost cost;
+    ChunkEntry e;
+    int i, share, head, tile;
+    bool walking, joining;
+    ll first_at;                          // joining: the share's first tile, until it is passed
 
     static __device__ __forceinline__ int tiles_of(const ChunkParams& p, const ChunkEntry& e) {
-        return static_cast<int>((static_cast<long long>(e.m) * p.group + ROWS - 1) / ROWS);
+        return static_cast<int>((static_cast<ll>(e.m) * p.group + ROWS - 1) / ROWS);
     }
-    // The most units that a tile of the entry sees, or a little more.
-    static __device__ __forceinline__ int most_units(const ChunkParams& p, const ChunkUnits<KT>& u,
-                                                     const ChunkEntry& e) {
-        if (e.len == 0) return 0;
-        const int all = u.of(e.len - 1) + 1;
-        if (p.window == 0) return all;
-        const long long seen = static_cast<long long>(p.window) + ROWS / p.group + 2;
-        const long long sinks = p.sinks > 0 ? u.of(min(p.sinks, e.len) - 1) + 1 : 0;
-        const long long few = sinks + (u.per == 0 ? seen / u.span + 2 : (seen / u.page + 2) * u.per);
-        return static_cast<int>(min(static_cast<long long>(all), few));
-    }
-    static __device__ __forceinline__ int parts_of(int units, int each) {
-        return units <= each ? 1 : (units + each - 1) / each;
+    static __device__ __forceinline__ Cost cost_of(const ChunkParams& p, const ChunkEntry& e) {
+        Cost c;
+        c.tiles = tiles_of(p, e);
+        c.from = 16ll * max(0, e.len - e.m);
+        c.step = 16 * ROWS / p.group;
+        c.cap = 0x7fffffffffffll;
+        c.turn = c.tiles;
+        if (p.window > 0) {
+            c.cap = 16 * (static_cast<ll>(p.window) + p.sinks + KT) + c.step;
+            const ll below = c.cap - c.from;
+            const ll t = below <= c.step ? 0 : c.step > 0 ? (below - 1) / c.step : c.tiles;
+            if (t < c.tiles) c.turn = static_cast<int>(t);
+        }
+        return c;
     }
 
     // All threads; ends with a barrier.
     __device__ __forceinline__ void find(const ChunkParams& p) {
-        const ChunkUnits<KT> u(p.c.page);
         const int per = (p.n + WIDTH - 1) / WIDTH, i0 = threadIdx.x * per, i1 = min(p.n, i0 + per);
-        long long tiles = 0, units = 0;
+        ll mine = 0, counts = 0, all, all_counts;        // (counts: rows, and below bit 18 tiles, 1024 a thread at most)
+        int tiles = 0;
         unsigned bad = 0;
-        for (int i = i0; i < i1; ++i) {
-            const ChunkEntry e = chunk_entry(p, i, &bad);
-            const long long t = static_cast<long long>(tiles_of(p, e)) * p.c.heads;
-            tiles += t;
-            units += t * most_units(p, u, e);
+#pragma unroll 4
+        for (int k = i0; k < i1; ++k) {
+            const ChunkEntry e = chunk_entry(p, k, &bad);
+            const Cost c = cost_of(p, e);
+            tiles = static_cast<int>(min(1024ll, tiles + static_cast<ll>(c.tiles) * p.c.heads));
+            mine += c.upto(c.tiles) * p.c.heads;
+            counts += static_cast<ll>(e.m) << 18;
+        }
+        counts += tiles;
+        const ll before = block_scan<THREADS>(mine, s->tmp, &all);
+        block_scan<THREADS>(counts, s->tmp, &all_counts);
+        if (all_counts >> 18 > p.tokens) {               // entries share rows: there is no end to what they could ask for
+            bad |= GS_DEV_BAD_SEQ;
+            all = all_counts = 0;
         }
         if (blockIdx.x == 0) flag(p.c.status, bad);
-        long long all_tiles, all_units;
-        const long long before = block_scan<THREADS>(tiles, s->tmp, &all_tiles);
-        block_scan<THREADS>(units, s->tmp, &all_units);
-        const int blocks = gridDim.x;
-        int each = 0x7fffffff;
-        if (all_tiles < 4ll * blocks && all_tiles <= kChunkCut && p.slot_count > 0) {
-            const long long want = (all_units + 2ll * blocks - 1) / (2ll * blocks);
-            each = static_cast<int>(max(static_cast<long long>(kMinUnits), want));
-        }
-        long long items = 0, all_items = 0, items_before = 0;
-        for (int turn = 0; turn < 2; ++turn) {
-            items = 0;
-            for (int i = i0; i < i1; ++i) {
-                unsigned ignore = 0;
-                const ChunkEntry e = chunk_entry(p, i, &ignore);
-                items += static_cast<long long>(tiles_of(p, e)) * p.c.heads * parts_of(most_units(p, u, e), each);
-            }
-            items_before = block_scan<THREADS>(items, s->tmp, &all_items);
-            if (each == 0x7fffffff || all_items <= p.slot_count) break;
-            each = 0x7fffffff;            // (ranges that overlap, against the rules)
-        }
-        if (all_items > 0x3fffffffll) all_items = 0;     // (ranges that overlap)
-        if (threadIdx.x < WIDTH) {
-            s->items[threadIdx.x] = static_cast<int>(items_before);
-            s->tiles[threadIdx.x] = static_cast<int>(before);
-        }
+        if (threadIdx.x < WIDTH) s->before[threadIdx.x] = before;
         if (threadIdx.x == 0) {
-            s->each = each;
-            s->total_items = static_cast<int>(all_items);
-            s->total_tiles = static_cast<int>(all_tiles);
-            // Pieces of a tile for its join: about two a block in all.
-            int pieces = each == 0x7fffffff || all_tiles == 0 ? 0 : static_cast<int>(2ll * blocks / all_tiles);
-            if (pieces < 1 && each != 0x7fffffff) pieces = 1;
-            s->pieces = min(pieces, ROWS / 8);
+            // No more shares than blocks, than tiles, or than there are four units for.
+            ll n = max(all_counts & 0x3ffffll, all / (16 * 4 * KT));
+            n = min(n, static_cast<ll>(gridDim.x));
+            s->shares = static_cast<int>(n);
+            s->each = n > 0 ? all / n : 0;
+            s->more = n > 0 ? static_cast<int>(all - s->each * n) : 0;
         }
+        walking = false;
         __syncthreads();
     }
 
     // Words of the workspace that the call counts in.
-    __device__ __forceinline__ int used() const {
-        return kChunkHead + (s->pieces > 0 ? s->total_tiles : 0);
+    __device__ __forceinline__ int used() const { return kChunkHead + s->shares; }
+
+    __device__ __forceinline__ ll first_of(int n) const { return n * s->each + min(n, s->more); }
+    __device__ __forceinline__ int share_of(ll x) const {
+        const ll edge = s->more * (s->each + 1);
+        return static_cast<int>(x < edge ? x / (s->each + 1) : s->more + (x - edge) / s->each);
+    }
+    // The unit at which an edge `f` into a tile's cost cuts it.
+    static __device__ __forceinline__ int cut(int units, ll all, ll f) {
+        if (units < kFew) return 2 * f >= all ? units : 0;
+        const int u = static_cast<int>((units * f + all / 2) / all);
+        return u < kLeast ? 0 : units - u < kLeast ? units : u;
     }
 
-    // Item number j of the queue, by one thread.
-    __device__ __forceinline__ ChunkItem item(const ChunkParams& p, int j) const {
-        ChunkItem it;
-        it.kind = 0;
-        const bool join = j >= s->total_items;
-        const int* before = join ? s->tiles : s->items;
-        int x = j, piece = 0;
-        if (join) {
-            if (s->pieces == 0) return it;
-            x = j - s->total_items;
-            piece = x % s->pieces;
-            x /= s->pieces;
-            if (x >= s->total_tiles) return it;
-        }
-        int lo = 0, hi = WIDTH - 1;     // the last thread whose `before` is not above x
+    __device__ __forceinline__ void enter(const ChunkParams& p, int entry) {
+        unsigned ignore = 0;
+        i = entry;
+        e = chunk_entry(p, i, &ignore);
+        cost = cost_of(p, e);
+    }
+
+    // To the tile at cost x.
+    __device__ __forceinline__ void seek(const ChunkParams& p, ll x) {
+        int lo = 0, hi = WIDTH - 1;       // the last thread whose entries begin at x or before
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (before[mid] <= x) lo = mid;
+            if (s->before[mid] <= x) lo = mid;
             else hi = mid - 1;
         }
-        const ChunkUnits<KT> u(p.c.page);
-        const int per = (p.n + WIDTH - 1) / WIDTH, end = min(p.n, (lo + 1) * per);
-        int items = s->items[lo], tiles = s->tiles[lo];
-        unsigned ignore = 0;
-        for (int i = lo * per; i < end; ++i) {
-            const ChunkEntry e = chunk_entry(p, i, &ignore);
-            const int mine = tiles_of(p, e) * p.c.heads;
-            const int parts = parts_of(most_units(p, u, e), s->each);
-            const int past = join ? tiles + mine : items + mine * parts;
-            if (x >= past) {
-                items += mine * parts;
-                tiles += mine;
-                continue;
-            }
-            it.kind = join ? 2 : 1;
-            it.e = e;
-            const int in = join ? x - tiles : (x - items) / parts;       // tile and head, the last tile first
-            const int part = join ? 0 : x - items - in * parts;
-            const int back = in / p.c.heads;
-            it.head = in - back * p.c.heads;
-            it.row = (tiles_of(p, e) - 1 - back) * ROWS;
-            const int all = static_cast<int>(min(static_cast<long long>(ROWS),
-                                                 static_cast<long long>(e.m) * p.group - it.row));
-            it.rows = all;
-            it.tile = tiles + in;
-            const int first = e.len - e.m + it.row / p.group;
-            const int last = e.len - e.m + (it.row + all - 1) / p.group;
-            it.span = chunk_span<KT>(p, u, first, last);
-            it.parts = parts_of(it.span.count, s->each);
-            it.slot = items + in * parts + part;
-            it.need = it.parts * ((all + HALF - 1) / HALF);
-            it.lo = 0;
-            it.hi = it.span.count;
-            if (it.parts > 1) {
-                // Equal parts: part k begins at unit count * k / parts.
-                it.lo = static_cast<int>(static_cast<long long>(it.span.count) * part / it.parts);
-                it.hi = static_cast<int>(static_cast<long long>(it.span.count) * (part + 1) / it.parts);
-            }
-            it.at = 0;
-            if (join) {
-                if (it.parts == 1) it.rows = 0;
-                const int size = (ROWS + s->pieces - 1) / s->pieces;
-                it.at = piece * size;
-                it.rows = max(0, min(size, it.rows - it.at));
-            } else if (part >= it.parts) {
-                it.rows = 0;              // fewer parts than the entry's longest tile
-            }
-            return it;
+        entry_at = s->before[lo];
+        enter(p, min(p.n - 1, lo * ((p.n + WIDTH - 1) / WIDTH)));
+        ll all = cost.upto(cost.tiles);
+        while (x >= entry_at + all * p.c.heads && i + 1 < p.n) {
+            entry_at += all * p.c.heads;
+            enter(p, i + 1);
+            all = cost.upto(cost.tiles);
         }
-        return it;                        // (lengths that change during the call)
+        head = all > 0 ? static_cast<int>((x - entry_at) / all) : p.c.heads;
+        walking = head < p.c.heads;       // (else lengths have changed during the call)
+        const ll left = x - entry_at - head * all;
+        int a = 0, b = cost.tiles - 1;    // the last tile that begins at x or before
+        while (a < b) {
+            const int mid = (a + b + 1) >> 1;
+            if (cost.upto(mid) <= left) a = mid;
+            else b = mid - 1;
+        }
+        tile = a;
+    }
+    __device__ __forceinline__ ll tile_at() const {
+        return entry_at + head * cost.upto(cost.tiles) + cost.upto(tile);
+    }
+    __device__ __forceinline__ void step(const ChunkParams& p) {
+        if (++tile < cost.tiles) return;
+        tile = 0;
+        if (++head < p.c.heads) return;
+        head = 0;
+        entry_at += cost.upto(cost.tiles) * p.c.heads;
+        do {
+            if (i + 1 >= p.n) {
+                walking = false;
+                return;
+            }
+            enter(p, i + 1);
+        } while (cost.tiles == 0);
+    }
+
+    // This share's part of the tile it is at; false where it has none, or (join) nothing to join.
+    __device__ __forceinline__ bool part(const ChunkParams& p, bool join, ChunkItem* it) const {
+        const ChunkUnits<KT> u(p.c.page);
+        const ll at = tile_at(), all = cost.upto(tile + 1) - cost.upto(tile), end = at + all;
+        it->kind = 1;
+        it->e = e;
+        it->head = head;
+        it->row = tile * ROWS;
+        const int rows = static_cast<int>(min(static_cast<ll>(ROWS), static_cast<ll>(e.m) * p.group - it->row));
+        it->rows = rows;
+        const int from = e.len - e.m;
+        it->span = chunk_span<KT>(p, u, from + it->row / p.group, from + (it->row + rows - 1) / p.group);
+        const int units = it->span.count;
+        it->lo = at >= x0 ? 0 : cut(units, all, x0 - at);
+        it->hi = end <= x1 ? units : cut(units, all, x1 - at);
+        it->parts = 1;
+        it->share = share;
+        if (it->lo > 0 || it->hi < units) {
+            // The edges that cut the tile: those in it but a first and a last one that leave too little.
+            int j0 = share_of(at) + 1, j1 = share_of(end - 1);
+            if (j0 <= j1 && cut(units, all, first_of(j0) - at) == 0) ++j0;
+            if (j0 <= j1 && cut(units, all, first_of(j1) - at) == units) --j1;
+            it->parts = j1 - j0 + 2;
+            it->share = j0 - 1;
+        }
+        const int k = share - it->share;
+        it->slot = chunk_slot(it->share, k);
+        it->need = it->parts * ((rows + HALF - 1) / HALF);
+        it->at = 0;
+        if (it->lo >= it->hi && (units > 0 || at < x0)) return false;
+        if (!join) return true;
+        it->kind = 2;                     // a part's rows of the join
+        it->at = static_cast<int>(static_cast<ll>(rows) * k / it->parts);
+        it->rows = static_cast<int>(static_cast<ll>(rows) * (k + 1) / it->parts) - it->at;
+        return it->parts > 1 && it->rows > 0;
+    }
+
+    // The block's next item, by one thread; kind 0 after the last.
+    __device__ __forceinline__ ChunkItem item(const ChunkParams& p) {
+        ChunkItem it;
+        for (;;) {
+            while (walking) {
+                if (tile_at() >= x1) {
+                    walking = false;
+                    break;
+                }
+                const bool some = part(p, joining, &it);
+                if (!joining) {
+                    step(p);
+                } else {                  // only a share's first and last tile have parts elsewhere
+                    const ll was = tile_at();
+                    if (was == first_at) seek(p, x1 - 1);
+                    if (tile_at() == was) walking = false;
+                }
+                if (some) return it;
+            }
+            const int n = atomicAdd(p.work, 1);
+            if (n >= 2 * s->shares) {
+                it.kind = 0;
+                return it;
+            }
+            joining = n >= s->shares;
+            share = joining ? n - s->shares : n;
+            x0 = first_of(share);
+            x1 = first_of(share + 1);
+            seek(p, x0);
+            first_at = tile_at();
+        }
     }
 };
 
@@ -377,12 +452,13 @@ template <class T>
 __device__ __forceinline__ void chunk_join(const ChunkParams& p, const ChunkItem& it, int warp, int warps,
                                            float lift) {
     const int dim = p.c.dim, lane = threadIdx.x & 31;
-    const long long words = chunk_slot_words(p.slot_rows, dim);
-    const float* const first = p.slots + it.slot * words;
+    const long long words = 2 * chunk_slot_words(p.slot_rows, dim);              // between the slots of two shares
+    const float* const first = p.slots + it.share * words;
+    const long long begin = words / 2;    // part 0 is in its share's second slot
     for (int x = warp; x < it.rows; x += warps) {
         const int r = it.at + x;
         float top = kNegInf;
-        for (int k = lane; k < it.parts; k += 32) top = fmaxf(top, __ldcg(first + k * words + r));
+        for (int k = lane; k < it.parts; k += 32) top = fmaxf(top, __ldcg(first + k * words + (k == 0 ? begin : 0) + r));
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
         const float base = top == kNegInf ? 0.0f : top;
@@ -395,7 +471,7 @@ __device__ __forceinline__ void chunk_join(const ChunkParams& p, const ChunkItem
             for (int k0 = 0; k0 < it.parts; k0 += 32) {
                 float w = 0.0f;
                 if (k0 + lane < it.parts) {
-                    const float* const slot = first + (k0 + lane) * words + r;
+                    const float* const slot = first + (k0 + lane) * words + (k0 + lane == 0 ? begin : 0) + r;
                     w = chunk_pow2(__ldcg(slot) - base);
                     if (d0 == 0) sum = fmaf(__ldcg(slot + p.slot_rows), w, sum);
                 }
@@ -405,7 +481,8 @@ __device__ __forceinline__ void chunk_join(const ChunkParams& p, const ChunkItem
                     float4 v[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        v[i] = k + i < n && d < dim ? __ldcg(reinterpret_cast<const float4*>(from + (k + i) * words))
+                        v[i] = k + i < n && d < dim ? __ldcg(reinterpret_cast<const float4*>(
+                                                          from + (k + i) * words + (k0 + k + i == 0 ? begin : 0)))
                                                     : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {

@@ -3,8 +3,8 @@
 //
 // A block works on two tiles of 128 query rows at a time (one for heads of over 128 dims), which share
 // every unit of keys and values.  Of its warps
-//   one takes items from the queue and brings their queries and units by TMA: K and V in turn through a
-//     ring of stages in shared memory, as many units ahead as the ring has room, over the ends of items;
+//   one takes items from the queue and brings their queries and K by TMA, another brings V: in turn through
+//     a ring of stages in shared memory, as many units ahead as the ring has room, over the ends of items;
 //   one issues the products, in steps of 64 positions: S = Q K^T into one of a tile's two places in tensor
 //     memory, and O += P V from there;
 //   four a tile have a row a thread: they read S, keep the softmax's reference and sum, write the
@@ -263,7 +263,7 @@ struct Shape {
     static constexpr int Q = 128 * DP * 2, STAGE = KT * DP * 2;      // bytes
     static constexpr int STAGES = DP == 64 ? 8 : 5;
     static constexpr int GROUP = 128 * TILES;            // threads with a row
-    static constexpr int THREADS = GROUP + 64, WIDTH = 128;
+    static constexpr int THREADS = GROUP + 96, WIDTH = 128;
     // Tensor memory: two places of S for each tile (P in the last half of the place), then O of each.
     static constexpr int P = kStep / 2, O = 256;
     static_assert(TILES * 2 * kStep <= O && O + TILES * DP <= 512, "tensor memory");
@@ -341,7 +341,8 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int dim = p.c.dim;
     const ChunkUnits<KT> units(p.c.page);
-    const bool loader = warp == S::GROUP / 32, issuer = warp == S::GROUP / 32 + 1;
+    const int role = warp - S::GROUP / 32;               // below 0: rows; 0, 2: bring K, V; 1: issues
+    const bool issuer = role == 1;
 
     if (tid == 0) {
         for (int i = 0; i < S::STAGES; ++i) {
@@ -350,7 +351,7 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
         }
         for (int i = 0; i < kItems; ++i) {
             bar_init(smem_at(&s.item_full[i]), 1);
-            bar_init(smem_at(&s.item_empty[i]), S::GROUP + 1);
+            bar_init(smem_at(&s.item_empty[i]), S::GROUP + 2);
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(smem_at(&s.q_full[i]), 1);
@@ -383,29 +384,30 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
     }
     grid_wait();
     grid_trigger();
-    typename S::Cut cut = {&s.plan};
+    typename S::Cut cut;
+    cut.s = &s.plan;
     mma_fence_before();
     cut.find(p);                          // (ends with a barrier)
     mma_fence_after();
     const unsigned tmem = s.tmem;
-    if (loader) {
+    if (role == 0 || role == 2) {
+        const bool is_v = role == 2, one = elect_one();
         const int halves = (dim + 63) / 64;
-        const int page_rows = min(p.c.page, KT);
-        const unsigned box = page_rows * 128;
-        const int pages = units.per > 0 ? 1 : KT / p.c.page, boxes = pages * halves;
+        const int box = min(p.c.page, KT) * 128;         // bytes
+        const int pages = units.per > 0 ? 1 : KT / p.c.page;         // of a unit
+        const CUtensorMap* const map = is_v ? &v_map : &k_map;
+        unsigned ring = 0;                // stages gone through
         unsigned tails = 0, bad = 0, q_turn = 3u;        // (q_turn: a bit a tile)
-        int stage = 0;                    // the ring: stage, and the parity of its use
-        unsigned turn = 0;
         bool go = true;
-        for (int n = 0; go;) {
+        for (int n = 0; go; ++n) {
             const int slot = n & 1;
             int kind = 0;
-            if (lane == 0) {
-                ChunkItem it;
-                do {
-                    it = cut.item(p, atomicAdd(p.work, 1));
-                } while (it.kind != 0 && it.rows == 0);
-                if (bar_wait(smem_at(&s.item_empty[slot]), ((n >> 1) & 1) ^ 1, &s.dead)) {
+            if (is_v) {
+                if (!warp_wait(smem_at(&s.item_full[slot]), (n >> 1) & 1, &s.dead)) break;
+                kind = s.items[slot].kind;
+            } else {
+                if (lane == 0) {
+                    ChunkItem it = cut.item(p);
                     // (the last unit's second step may have no position that some row sees)
                     it.steps = (it.hi - it.lo) * S::STEPS;
                     if (S::STEPS == 2 && it.kind == 1 && it.hi > it.lo) {
@@ -414,97 +416,95 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
                         const int last = it.e.len - it.e.m + (it.row + it.rows - 1) / p.group;
                         if (min(c, last + 1 - at) <= kStep) --it.steps;
                     }
-                    s.items[slot] = it;
-                    kind = it.kind;
-                    bar_arrive(smem_at(&s.item_full[slot]));
-                } else {
-                    kind = -1;
+                    if (bar_wait(smem_at(&s.item_empty[slot]), ((n >> 1) & 1) ^ 1, &s.dead)) {
+                        s.items[slot] = it;
+                        kind = it.kind;
+                        bar_arrive(smem_at(&s.item_full[slot]));
+                    } else {
+                        kind = -1;
+                    }
                 }
+                kind = __shfl_sync(0xffffffffu, kind, 0);
+                __syncwarp();
             }
-            kind = __shfl_sync(0xffffffffu, kind, 0);
-            __syncwarp();
-            ++n;
             if (kind <= 0) break;
-            if (kind == 2) continue;
             const ChunkItem& it = s.items[slot];
             const int head = it.head, len = it.e.len, lo = it.lo, hi = it.hi;
             const ChunkSpan span = it.span;
             const int tiles = TILES == 2 && it.rows > 128 ? 2 : 1;
             const int q_token = it.e.row + it.row / p.group;
             const int* const table = p.c.table + static_cast<long long>(it.e.seq) * p.c.cols;
-            // Box `lane` of a unit, its page one unit ahead.
-            auto page_of = [&](int at, int x) {
-                const int pos = at + x / halves * p.c.page;          // page <= KT: the box's first position
-                return pos < len ? table[pos / p.c.page] : -2;
+            __syncwarp();
+            if (is_v && one) bar_arrive(smem_at(&s.item_empty[slot]));
+            if (kind == 2) continue;
+            // The page of a unit that this lane knows (and the ones 32, 64, .. further): -1 past the end.
+            auto page_of = [&](int unit, int x) {
+                const int col = units.per == 0 ? unit * pages + x : unit / units.per;
+                return x < pages && col * p.c.page < len ? table[col] : -1;
             };
-            int count, row;
-            int at = lo < hi ? units.first(span.unit(lo), &count, &row) : 0;
-            int next = lo < hi && lane < boxes ? page_of(at, lane) : -2;
-            for (int u = lo; u < hi && go; ++u) {
-                at = units.first(span.unit(u), &count, &row);
-                int page = next;
-                if (u + 1 < hi) {
-                    int c, r;
-                    const int then = units.first(span.unit(u + 1), &c, &r);
-                    next = lane < boxes ? page_of(then, lane) : -2;
-                }
+            int next = lo < hi ? page_of(span.unit(lo), lane) : -1;
+            for (int u = lo; u < hi; ++u) {
+                const int unit = span.unit(u), page = next;
+                if (u + 1 < hi) next = page_of(span.unit(u + 1), lane);          // one unit ahead
+                int count, row;
+                const int at = units.first(unit, &count, &row);
                 const int valid = min(count, len - at);
-                const int live = (units.per > 0 ? 1 : (valid + p.c.page - 1) / p.c.page) * halves;
-                for (int kv = 0; kv < 2; ++kv) {
-                    const CUtensorMap* const map = kv == 0 ? &k_map : &v_map;
-                    if (!warp_wait(smem_at(&s.empty[stage]), turn ^ 1, &s.dead)) {
-                        go = false;
-                        break;
+                const int live = units.per > 0 ? 1 : (valid + p.c.page - 1) / p.c.page;
+                const unsigned mine = ring + 2 * (u - lo) + is_v, stage = mine % S::STAGES;
+                if (!(go = warp_wait(smem_at(&s.empty[stage]), mine / S::STAGES & 1 ^ 1, &s.dead))) break;
+                // Rows past the sequence's end hold anything: of V they are taken out.
+                const bool tail = is_v && valid < count;
+                const unsigned bar = smem_at(tail ? &s.tail : &s.full[stage]);
+                if (one) bar_expect(bar, live * halves * box);
+                __syncwarp();
+                // (One lane issues: what lanes give a box each takes turns, 86 cycles a box against 30.)
+                for (int x0 = 0; x0 < live; x0 += 32) {
+                    const int id = x0 == 0 ? page : page_of(unit, x0 + lane);
+                    const bool ok = id >= 0 && id < p.c.pages;
+                    const int n_here = min(32, live - x0);
+                    if (!ok && lane < n_here) bad |= GS_DEV_BAD_SEQ;
+                    const int safe = ok ? id : p.c.pages;
+                    unsigned to = smem_at(s.ring[stage]) + x0 * box;
+                    for (int x = 0; x < n_here; ++x, to += box) {
+                        const int from = __shfl_sync(0xffffffffu, safe, x);
+                        if (one) {
+#pragma unroll
+                            for (int col = 0; col < DP / 64; ++col)
+                                if (col < halves) load_box(to + col * (KT * 128), map, col * 64, row, head, from, bar);
+                        }
                     }
-                    // Rows past the sequence's end hold anything: of V they are taken out.
-                    const bool tail = kv == 1 && valid < count;
-                    const unsigned bar = smem_at(tail ? &s.tail : &s.full[stage]);
-                    if (lane == 0) bar_expect(bar, live * box);
-                    __syncwarp();
-                    for (int x = lane; x < live; x += 32) {
-                        if (x != lane) page = page_of(at, x);
-                        const bool ok = page >= 0 && page < p.c.pages;
-                        if (!ok) bad |= GS_DEV_BAD_SEQ;
-                        const int in = x / halves, col = x - in * halves;
-                        load_box(smem_at(s.ring[stage]) + col * (KT * 128) + in * box, map, col * 64, row, head,
-                                 ok ? page : p.c.pages, bar);
-                    }
-                    if (live > 32) page = lane < boxes ? page_of(at, lane) : -2;
-                    if (kv == 0 && u == lo && p.q_boxes != 0) {          // the queries, once the last item's are done with
-                        for (int w = 0; w < tiles && go; ++w) {
-                            go = warp_wait(smem_at(&s.q_empty[w]), q_turn >> w & 1, &s.dead);
-                            q_turn ^= 1u << w;
-                            if (!go) break;
-                            const unsigned q_bar = smem_at(&s.q_full[w]);
-                            if (lane == 0) bar_expect(q_bar, halves * 128 * 128);
-                            __syncwarp();
-                            if (lane < halves)
-                                load_box3(smem_at(s.q[w]) + lane * (128 * 128), &q_map, lane * 64, head * p.group,
+                }
+                __syncwarp();
+                if (!is_v && u == lo && p.q_boxes != 0) {            // the queries, once the last item's are done with
+                    for (int w = 0; w < tiles && go; ++w) {
+                        go = warp_wait(smem_at(&s.q_empty[w]), q_turn >> w & 1, &s.dead);
+                        q_turn ^= 1u << w;
+                        if (!go) break;
+                        const unsigned q_bar = smem_at(&s.q_full[w]);
+                        if (one) {
+                            bar_expect(q_bar, halves * 128 * 128);
+                            for (int col = 0; col < halves; ++col)
+                                load_box3(smem_at(s.q[w]) + col * (128 * 128), &q_map, col * 64, head * p.group,
                                           q_token + w * (128 / p.group), q_bar);
                         }
-                        if (!go) break;
-                    }
-                    if (tail) {
-                        if (!warp_wait(bar, tails & 1, &s.dead)) {
-                            go = false;
-                            break;
-                        }
-                        ++tails;
-                        for (int x = lane; x < (KT - valid) * 8 * halves; x += 32) {
-                            const int col = x / ((KT - valid) * 8), y = x - col * ((KT - valid) * 8);
-                            *reinterpret_cast<uint4*>(s.ring[stage] + col * (KT * 128) + valid * 128 + y * 16) =
-                                make_uint4(0u, 0u, 0u, 0u);
-                        }
-                        async_fence();
                         __syncwarp();
-                        if (lane == 0) bar_arrive(smem_at(&s.full[stage]));
                     }
-                    if (++stage == S::STAGES) {
-                        stage = 0;
-                        turn ^= 1;
+                    if (!go) break;
+                }
+                if (tail) {
+                    if (!(go = warp_wait(bar, tails & 1, &s.dead))) break;
+                    ++tails;
+                    for (int x = lane; x < (KT - valid) * 8 * halves; x += 32) {
+                        const int col = x / ((KT - valid) * 8), y = x - col * ((KT - valid) * 8);
+                        *reinterpret_cast<uint4*>(s.ring[stage] + col * (KT * 128) + valid * 128 + y * 16) =
+                            make_uint4(0u, 0u, 0u, 0u);
                     }
+                    async_fence();
+                    __syncwarp();
+                    if (one) bar_arrive(smem_at(&s.full[stage]));
                 }
             }
+            ring += 2 * (hi - lo);
         }
         flag(p.c.status, bad);
         // Where a wait has run out, the boxes under way land before the block ends.
@@ -621,7 +621,7 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
             while (!bar_try(smem_at(&s.drain), 0) && chunk_clock() - t0 < 10ull * 1000ull * 1000ull) {}
         }
         __syncwarp();
-    } else if (warp < S::GROUP / 32) {
+    } else {
         const int w = TILES == 2 ? warp >> 2 : 0, mine = tid & 127;
         const unsigned lanes = static_cast<unsigned>((warp & 3) * 32) << 16;
         const unsigned s_at = tmem + lanes + w * 2 * kStep, o_at = tmem + lanes + S::O + w * DP;
@@ -644,7 +644,7 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
             const ChunkItem& it = s.items[slot];
             if (it.kind == 0) break;
             if (it.kind == 2) {
-                if (mine == 0 && !chunk_wait_parts(p.work + kChunkHead + it.tile, it.need))
+                if (mine == 0 && !chunk_wait_parts(p.work + kChunkHead + it.share, it.need))
                     *static_cast<volatile int*>(&s.dead) = 1;
                 if (!meet(smem_at(&s.tile_meet[w]), &meet_turn, &s.dead)) break;
                 chunk_join<T>(p, it, warp, S::GROUP / 32, W::kLift);
@@ -847,7 +847,7 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
                 }
                 __threadfence();
                 if (!(go = meet(smem_at(&s.tile_meet[w]), &meet_turn, &s.dead))) break;
-                if (mine == 0) atomicAdd(p.work + kChunkHead + it.tile, 1);
+                if (mine == 0) atomicAdd(p.work + kChunkHead + it.share, 1);
             } else if (real && lse != nullptr) {
                 *lse = sum == 0.0f ? kNegInf : (top + log2f(sum) - W::kLift) * kChunkLn2;
             }
