@@ -152,7 +152,6 @@ struct ChunkItem {
     int slot;                             // of this part
     int need;                             // the tile's count once all parts are there
     int at;                               // kind 2: first row of the piece in the tile
-    int steps;                            // of the tensor cores' kernel
 };
 
 // The slot of part k of a tile that begins in `share`.

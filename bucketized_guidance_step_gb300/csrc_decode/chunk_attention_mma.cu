@@ -3,10 +3,11 @@
 //
 // A block works on two tiles of 128 query rows at a time (one for heads of over 128 dims), which share
 // every unit of keys and values.  Of its warps
-//   one takes items from the queue and brings their queries and K by TMA, another brings V: in turn through
-//     a ring of stages in shared memory, as many units ahead as the ring has room, over the ends of items;
-//   one issues the products, in steps of 64 positions: S = Q K^T into one of a tile's two places in tensor
-//     memory, and O += P V from there;
+//   one takes items from the queue and brings their queries and K by TMA, another brings V: units of 64
+//     positions through a ring of stages in shared memory each, as far ahead as the ring has room, over the
+//     ends of items;
+//   one a tile issues its products: S = Q K^T into one of the tile's two places in tensor memory, and O += P V
+//     from there (the tensor cores have hardly a product waiting: while one warp waits, the other issues);
 //   four a tile have a row a thread: they read S, keep the softmax's reference and sum, write the
 //     weights P over S as 16-bit numbers, and at the item's end read O and store it.
 // The scores of a step are there before the weights of the last one are done: the rows' threads never
@@ -64,10 +65,10 @@ __device__ __forceinline__ bool bar_try(unsigned bar, unsigned parity) {
     unsigned ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(100000u)
+        : "r"(bar), "r"(parity)
         : "memory");
     return ok != 0u;
 }
@@ -149,6 +150,14 @@ __device__ __forceinline__ void mma_fence_after() {
 __device__ __forceinline__ void mma_fence_before() {
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
 }
+// A matrix in shared memory in columns of 64 values (128 bytes a row, rows permuted in groups of 8 as
+// TMA's 128-byte swizzle leaves them).  K-major: groups of 8 rows follow each other.  MN-major: `next`
+// bytes lead to the next 64 values.
+__host__ __device__ constexpr unsigned long long matrix_at(unsigned at, unsigned next) {
+    return static_cast<unsigned long long>((at & 0x3ffffu) >> 4) |
+           static_cast<unsigned long long>(next >> 4) << 16 | 64ull << 32 | 1ull << 46 | 2ull << 61;
+}
+
 // Both operands in shared memory.
 __device__ __forceinline__ void mma_ss(unsigned d, unsigned long long a, unsigned long long b, unsigned what,
                                        unsigned add) {
@@ -158,12 +167,37 @@ __device__ __forceinline__ void mma_ss(unsigned d, unsigned long long a, unsigne
         "l"(a), "l"(b), "r"(what), "r"(add)
         : "memory");
 }
-// A in tensor memory.
-__device__ __forceinline__ void mma_ts(unsigned d, unsigned a, unsigned long long b, unsigned what, unsigned add) {
+// Four neighbouring steps of 16 of a product, their descriptors made from the first one's low words within
+// one block of instructions: what is given to an instruction goes through registers of the warp, and asked
+// for one by one that takes as long as a product of 128 by 128.
+__device__ __forceinline__ void mma_ss4(unsigned d, unsigned a, unsigned b, unsigned high, unsigned what, unsigned add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(what), "r"(add)
+        "{\n\t.reg .pred p, t;\n\t.reg .b32 a1, a2, a3, b1, b2, b3;\n\t.reg .b64 x0, x1, x2, x3, y0, y1, y2, y3;\n\t"
+        "setp.ne.u32 p, %5, 0;\n\tsetp.eq.u32 t, 0, 0;\n\t"
+        "add.u32 a1, %1, 2;\n\tadd.u32 a2, %1, 4;\n\tadd.u32 a3, %1, 6;\n\t"
+        "add.u32 b1, %2, 2;\n\tadd.u32 b2, %2, 4;\n\tadd.u32 b3, %2, 6;\n\t"
+        "mov.b64 x0, {%1, %3};\n\tmov.b64 x1, {a1, %3};\n\tmov.b64 x2, {a2, %3};\n\tmov.b64 x3, {a3, %3};\n\t"
+        "mov.b64 y0, {%2, %3};\n\tmov.b64 y1, {b1, %3};\n\tmov.b64 y2, {b2, %3};\n\tmov.b64 y3, {b3, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x0, y0, %4, p;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x1, y1, %4, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x2, y2, %4, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x3, y3, %4, t;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(high), "r"(what), "r"(add)
+        : "memory");
+}
+// A in tensor memory, 8 columns a step; B 2048 bytes a step.
+__device__ __forceinline__ void mma_ts4(unsigned d, unsigned a, unsigned b, unsigned high, unsigned what, unsigned add) {
+    asm volatile(
+        "{\n\t.reg .pred p, t;\n\t.reg .b32 a1, a2, a3, b1, b2, b3;\n\t.reg .b64 y0, y1, y2, y3;\n\t"
+        "setp.ne.u32 p, %5, 0;\n\tsetp.eq.u32 t, 0, 0;\n\t"
+        "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
+        "add.u32 b1, %2, 128;\n\tadd.u32 b2, %2, 256;\n\tadd.u32 b3, %2, 384;\n\t"
+        "mov.b64 y0, {%2, %3};\n\tmov.b64 y1, {b1, %3};\n\tmov.b64 y2, {b2, %3};\n\tmov.b64 y3, {b3, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y0, %4, p;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], y1, %4, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], y2, %4, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], y3, %4, t;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(high), "r"(what), "r"(add)
         : "memory");
 }
 __device__ __forceinline__ bool elect_one() {
@@ -222,14 +256,6 @@ __device__ __forceinline__ void tmem_store16(unsigned at, const unsigned* r) {
 }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// A matrix in shared memory in columns of 64 values (128 bytes a row, rows permuted in groups of 8 as
-// TMA's 128-byte swizzle leaves them).  K-major: groups of 8 rows follow each other.  MN-major: `next`
-// bytes lead to the next 64 values.
-__device__ __forceinline__ unsigned long long matrix_at(unsigned at, unsigned next) {
-    return static_cast<unsigned long long>((at & 0x3ffffu) >> 4) |
-           static_cast<unsigned long long>(next >> 4) << 16 | 64ull << 32 | 1ull << 46 | 2ull << 61;
-}
-
 template <class T>
 struct Weights;                           // of type T: kept below 2^(kLift + kSlack)
 template <>
@@ -254,20 +280,18 @@ struct Weights<__half> {
 };
 
 // ---- shapes -----------------------------------------------------------------------------------
-constexpr int kStep = 64;                 // positions of a step
+constexpr int kUnit = 64;                 // positions of a unit
 template <int DP>
 struct Shape {
     static constexpr int TILES = DP > 128 ? 1 : 2;       // tiles of 128 rows
-    static constexpr int KT = DP > 128 ? 64 : 128;       // positions of a unit
-    static constexpr int STEPS = KT / kStep;             // steps of a unit
-    static constexpr int Q = 128 * DP * 2, STAGE = KT * DP * 2;      // bytes
-    static constexpr int STAGES = DP == 64 ? 8 : 5;
+    static constexpr int Q = 128 * DP * 2, STAGE = kUnit * DP * 2;   // bytes
+    static constexpr int K_STAGES = DP == 64 ? 10 : DP == 128 ? 5 : 3, V_STAGES = DP == 256 ? 2 : K_STAGES;
     static constexpr int GROUP = 128 * TILES;            // threads with a row
-    static constexpr int THREADS = GROUP + 96, WIDTH = 128;
+    static constexpr int THREADS = GROUP + 64 + 32 * TILES, WIDTH = 128;
     // Tensor memory: two places of S for each tile (P in the last half of the place), then O of each.
-    static constexpr int P = kStep / 2, O = 256;
-    static_assert(TILES * 2 * kStep <= O && O + TILES * DP <= 512, "tensor memory");
-    using Cut = ChunkCut<128 * TILES, 128, KT, THREADS, WIDTH>;
+    static constexpr int P = kUnit / 2, O = 256;
+    static_assert(TILES * 2 * kUnit <= O && O + TILES * DP <= 512, "tensor memory");
+    using Cut = ChunkCut<128 * TILES, 128, kUnit, THREADS, WIDTH>;
 };
 
 constexpr int kItems = 2;                 // items under way
@@ -275,11 +299,11 @@ template <int DP>
 struct alignas(1024) Smem {
     using S = Shape<DP>;
     unsigned char q[S::TILES][S::Q];
-    unsigned char ring[S::STAGES][S::STAGE];
-    unsigned long long full[S::STAGES], empty[S::STAGES];
+    unsigned char k[S::K_STAGES][S::STAGE], v[S::V_STAGES][S::STAGE];
+    unsigned long long k_full[S::K_STAGES], k_empty[S::K_STAGES], v_full[S::V_STAGES], v_empty[S::V_STAGES];
     unsigned long long item_full[kItems], item_empty[kItems];
     unsigned long long q_full[2], q_empty[2], s_full[2][2], p_full[2][2], o_full[2][2];
-    unsigned long long tile_meet[2], both_meet, tail, drain;
+    unsigned long long tile_meet[2], both_meet, tail, drain[2];
     ChunkItem items[kItems];
     int dead, seeded[2], hot[2][2];
     unsigned tmem;
@@ -308,7 +332,7 @@ __device__ __noinline__ bool give_out(unsigned char* v, unsigned o_at, int dim, 
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
                 const int d = d0 + i, c = d & 63;
-                const T x = *reinterpret_cast<const T*>(v + (d >> 6) * (S::KT * 128) + r * 128 +
+                const T x = *reinterpret_cast<const T*>(v + (d >> 6) * (kUnit * 128) + r * 128 +
                                                         (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2);
                 const float f = static_cast<float>(x);
                 if (!(fabsf(f) <= 3.4e38f)) o[i] += f;
@@ -329,29 +353,38 @@ __device__ __noinline__ bool give_out(unsigned char* v, unsigned o_at, int dim, 
     return meet(bar, turn, dead);
 }
 
+// (Apart from the kernel, whose registers are the rows'.)
+template <class C>
+__device__ __noinline__ void next_item(C* cut, const ChunkParams& p, ChunkItem* it) {
+    *it = cut->item(p);
+}
+
 template <class T, int DP>
 __global__ void __launch_bounds__(Shape<DP>::THREADS, 1)
 chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUtensorMap k_map,
                  const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap q_map) {
     using S = Shape<DP>;
     using W = Weights<T>;
-    constexpr int KT = S::KT, TILES = S::TILES;
+    constexpr int TILES = S::TILES;
     extern __shared__ __align__(1024) unsigned char raw[];
     Smem<DP>& s = *reinterpret_cast<Smem<DP>*>(raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int dim = p.c.dim;
-    const ChunkUnits<KT> units(p.c.page);
-    const int role = warp - S::GROUP / 32;               // below 0: rows; 0, 2: bring K, V; 1: issues
-    const bool issuer = role == 1;
+    const ChunkUnits<kUnit> units(p.c.page);
+    const int role = warp - S::GROUP / 32;               // below 0: rows; 0, 1: bring K, V; 2, 3: issue a tile's products
 
     if (tid == 0) {
-        for (int i = 0; i < S::STAGES; ++i) {
-            bar_init(smem_at(&s.full[i]), 1);
-            bar_init(smem_at(&s.empty[i]), 1);
+        for (int i = 0; i < S::K_STAGES; ++i) {
+            bar_init(smem_at(&s.k_full[i]), 1);
+            bar_init(smem_at(&s.k_empty[i]), TILES);
+        }
+        for (int i = 0; i < S::V_STAGES; ++i) {
+            bar_init(smem_at(&s.v_full[i]), 1);
+            bar_init(smem_at(&s.v_empty[i]), TILES);
         }
         for (int i = 0; i < kItems; ++i) {
             bar_init(smem_at(&s.item_full[i]), 1);
-            bar_init(smem_at(&s.item_empty[i]), S::GROUP + 2);
+            bar_init(smem_at(&s.item_empty[i]), S::GROUP + 1 + TILES);
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(smem_at(&s.q_full[i]), 1);
@@ -367,19 +400,19 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
         }
         bar_init(smem_at(&s.both_meet), S::GROUP);
         bar_init(smem_at(&s.tail), 1);
-        bar_init(smem_at(&s.drain), 1);
+        for (int i = 0; i < 2; ++i) bar_init(smem_at(&s.drain[i]), 1);
         s.dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (issuer) {
+    if (role == 2) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_at(&s.tmem)),
                      "r"(512u)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
-    if (units.span < KT) {                // rows of a stage that no box reaches
-        for (int x = tid; x < S::STAGES * S::STAGE / 16; x += S::THREADS)
-            reinterpret_cast<uint4*>(s.ring)[x] = make_uint4(0u, 0u, 0u, 0u);
+    if (units.span < kUnit) {             // rows of a stage that no box reaches
+        for (int x = tid; x < S::V_STAGES * S::STAGE / 16; x += S::THREADS)
+            reinterpret_cast<uint4*>(s.v)[x] = make_uint4(0u, 0u, 0u, 0u);
         async_fence();
     }
     grid_wait();
@@ -390,13 +423,20 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
     cut.find(p);                          // (ends with a barrier)
     mma_fence_after();
     const unsigned tmem = s.tmem;
-    if (role == 0 || role == 2) {
-        const bool is_v = role == 2, one = elect_one();
+    if (role == 0 || role == 1) {
+        const bool is_v = role == 1, one = elect_one();
         const int halves = (dim + 63) / 64;
-        const int box = min(p.c.page, KT) * 128;         // bytes
-        const int pages = units.per > 0 ? 1 : KT / p.c.page;         // of a unit
+        const int box = min(p.c.page, kUnit) * 128;      // bytes
+        const int pages = units.per > 0 ? 1 : kUnit / p.c.page;      // of a unit
+        const unsigned stages = is_v ? S::V_STAGES : S::K_STAGES;
+        unsigned char* const stage0 = is_v ? s.v[0] : s.k[0];
+        const unsigned full0 = smem_at(is_v ? s.v_full : s.k_full), empty0 = smem_at(is_v ? s.v_empty : s.k_empty);
         const CUtensorMap* const map = is_v ? &v_map : &k_map;
-        unsigned ring = 0;                // stages gone through
+        // Page numbers are looked up 32 at a time, a page a lane, and a batch ahead: of `batch` units, or where
+        // pages have one token of half a unit a word.
+        const int batch = pages < 32 ? 32 / pages : 1;
+        const int my_unit = pages < 32 ? lane / pages : 0, my_page = pages < 32 ? lane - my_unit * pages : lane;
+        unsigned stage = 0, turn = 1;     // of the ring; the parity of the stage's last use
         unsigned tails = 0, bad = 0, q_turn = 3u;        // (q_turn: a bit a tile)
         bool go = true;
         for (int n = 0; go; ++n) {
@@ -407,15 +447,8 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
                 kind = s.items[slot].kind;
             } else {
                 if (lane == 0) {
-                    ChunkItem it = cut.item(p);
-                    // (the last unit's second step may have no position that some row sees)
-                    it.steps = (it.hi - it.lo) * S::STEPS;
-                    if (S::STEPS == 2 && it.kind == 1 && it.hi > it.lo) {
-                        int c, r;
-                        const int at = units.first(it.span.unit(it.hi - 1), &c, &r);
-                        const int last = it.e.len - it.e.m + (it.row + it.rows - 1) / p.group;
-                        if (min(c, last + 1 - at) <= kStep) --it.steps;
-                    }
+                    ChunkItem it;
+                    next_item<typename S::Cut>(&cut, p, &it);
                     if (bar_wait(smem_at(&s.item_empty[slot]), ((n >> 1) & 1) ^ 1, &s.dead)) {
                         s.items[slot] = it;
                         kind = it.kind;
@@ -437,44 +470,69 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
             __syncwarp();
             if (is_v && one) bar_arrive(smem_at(&s.item_empty[slot]));
             if (kind == 2) continue;
-            // The page of a unit that this lane knows (and the ones 32, 64, .. further): -1 past the end.
-            auto page_of = [&](int unit, int x) {
-                const int col = units.per == 0 ? unit * pages + x : unit / units.per;
-                return x < pages && col * p.c.page < len ? table[col] : -1;
+            // This lane's page (>= 0; c.pages: outside the pool), and the unit's first row in it.
+            struct Known {
+                int page, more, row;
             };
-            int next = lo < hi ? page_of(span.unit(lo), lane) : -1;
+            auto look_up = [&](int from) {
+                Known k = {0, 0, 0};
+                const int u = from + my_unit;
+                if (u >= hi || my_unit >= batch) return k;
+                const int unit = span.unit(u);
+                int col = unit * pages + my_page;
+                if (units.per > 0) {
+                    col = unit / units.per;
+                    k.row = (unit - col * units.per) * kUnit;
+                }
+                auto page_at = [&](int c) {
+                    if (c * p.c.page >= len) return 0;
+                    const int id = table[c];
+                    if (id >= 0 && id < p.c.pages) return id;
+                    bad |= GS_DEV_BAD_SEQ;
+                    return p.c.pages;
+                };
+                k.page = page_at(col);
+                if (pages > 32) k.more = page_at(col + 32);
+                return k;
+            };
+            // The last unit may end inside.
+            int count = 0, row_ignored, valid = 0, live_last = 1;
+            if (lo < hi) {
+                const int at = units.first(span.unit(hi - 1), &count, &row_ignored);
+                valid = min(count, len - at);
+                if (units.per == 0) live_last = (valid + p.c.page - 1) / p.c.page;
+            }
+            Known now = {0, 0, 0}, next = look_up(lo);
+            int in_batch = batch;
             for (int u = lo; u < hi; ++u) {
-                const int unit = span.unit(u), page = next;
-                if (u + 1 < hi) next = page_of(span.unit(u + 1), lane);          // one unit ahead
-                int count, row;
-                const int at = units.first(unit, &count, &row);
-                const int valid = min(count, len - at);
-                const int live = units.per > 0 ? 1 : (valid + p.c.page - 1) / p.c.page;
-                const unsigned mine = ring + 2 * (u - lo) + is_v, stage = mine % S::STAGES;
-                if (!(go = warp_wait(smem_at(&s.empty[stage]), mine / S::STAGES & 1 ^ 1, &s.dead))) break;
+                if (++in_batch >= batch) {
+                    in_batch = 0;
+                    now = next;
+                    if (u + batch < hi) next = look_up(u + batch);
+                }
+                const int live = u + 1 < hi ? pages : live_last;
+                if (!(go = warp_wait(empty0 + 8 * stage, turn, &s.dead))) break;
+                unsigned char* const here = stage0 + stage * S::STAGE;
+                const unsigned full = full0 + 8 * stage;
+                if (++stage == stages) {
+                    stage = 0;
+                    turn ^= 1;
+                }
                 // Rows past the sequence's end hold anything: of V they are taken out.
-                const bool tail = is_v && valid < count;
-                const unsigned bar = smem_at(tail ? &s.tail : &s.full[stage]);
+                const bool tail = is_v && u + 1 == hi && valid < count;
+                const unsigned bar = tail ? smem_at(&s.tail) : full;
                 if (one) bar_expect(bar, live * halves * box);
-                __syncwarp();
-                // (One lane issues: what lanes give a box each takes turns, 86 cycles a box against 30.)
-                for (int x0 = 0; x0 < live; x0 += 32) {
-                    const int id = x0 == 0 ? page : page_of(unit, x0 + lane);
-                    const bool ok = id >= 0 && id < p.c.pages;
-                    const int n_here = min(32, live - x0);
-                    if (!ok && lane < n_here) bad |= GS_DEV_BAD_SEQ;
-                    const int safe = ok ? id : p.c.pages;
-                    unsigned to = smem_at(s.ring[stage]) + x0 * box;
-                    for (int x = 0; x < n_here; ++x, to += box) {
-                        const int from = __shfl_sync(0xffffffffu, safe, x);
-                        if (one) {
+                const int row = __shfl_sync(0xffffffffu, now.row, in_batch * pages & 31);
+                // (One lane issues: boxes that lanes give one each take turns, 66 cycles a box of 16 rows against 33.)
+                unsigned to = smem_at(here);
+                for (int x = 0; x < live; ++x, to += box) {
+                    const int page = __shfl_sync(0xffffffffu, x < 32 ? now.page : now.more, in_batch * pages + x & 31);
+                    if (one) {
 #pragma unroll
-                            for (int col = 0; col < DP / 64; ++col)
-                                if (col < halves) load_box(to + col * (KT * 128), map, col * 64, row, head, from, bar);
-                        }
+                        for (int col = 0; col < DP / 64; ++col)
+                            if (col < halves) load_box(to + col * (kUnit * 128), map, col * 64, row, head, page, bar);
                     }
                 }
-                __syncwarp();
                 if (!is_v && u == lo && p.q_boxes != 0) {            // the queries, once the last item's are done with
                     for (int w = 0; w < tiles && go; ++w) {
                         go = warp_wait(smem_at(&s.q_empty[w]), q_turn >> w & 1, &s.dead);
@@ -494,17 +552,16 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
                 if (tail) {
                     if (!(go = warp_wait(bar, tails & 1, &s.dead))) break;
                     ++tails;
-                    for (int x = lane; x < (KT - valid) * 8 * halves; x += 32) {
-                        const int col = x / ((KT - valid) * 8), y = x - col * ((KT - valid) * 8);
-                        *reinterpret_cast<uint4*>(s.ring[stage] + col * (KT * 128) + valid * 128 + y * 16) =
+                    for (int x = lane; x < (kUnit - valid) * 8 * halves; x += 32) {
+                        const int col = x / ((kUnit - valid) * 8), y = x - col * ((kUnit - valid) * 8);
+                        *reinterpret_cast<uint4*>(here + col * (kUnit * 128) + valid * 128 + y * 16) =
                             make_uint4(0u, 0u, 0u, 0u);
                     }
                     async_fence();
                     __syncwarp();
-                    if (one) bar_arrive(smem_at(&s.full[stage]));
+                    if (one) bar_arrive(full);
                 }
             }
-            ring += 2 * (hi - lo);
         }
         flag(p.c.status, bad);
         // Where a wait has run out, the boxes under way land before the block ends.
@@ -513,127 +570,110 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
             const unsigned long long t0 = chunk_clock();
             while (chunk_clock() - t0 < 10ull * 1000ull * 1000ull) __nanosleep(10000);
         }
-    } else if (issuer) {
-        // The whole warp goes through the loop, so that what the instructions are given is the same in all
-        // lanes; one of them issues.
-        const unsigned kind = 1u << 4 | W::kType << 7 | W::kType << 10 | (128u >> 4) << 24;
-        const unsigned what_s = kind | static_cast<unsigned>(kStep >> 3) << 17;
-        const unsigned what_o = kind | 1u << 16 | static_cast<unsigned>((dim + 15) / 16 * 2) << 17;
-        const int steps = (dim + 15) / 16;
-        const bool one = elect_one();
-        const unsigned long long q_at = matrix_at(smem_at(s.q[0]), 16);
-        const unsigned long long k_at = matrix_at(smem_at(s.ring[0]), 16);
-        const unsigned long long v_at = matrix_at(smem_at(s.ring[0]), KT * 128);
-        unsigned q_turn = 0;
-        bool go = true;
-        unsigned done[2] = {0, 0};        // steps of each tile's rows so far
-        unsigned ring = 0;                // stages gone through
-        auto stage_of = [&](unsigned n) { return n % S::STAGES; };
-        auto filled = [&](unsigned n) {
-            return warp_wait(smem_at(&s.full[n % S::STAGES]), n / S::STAGES & 1, &s.dead);
-        };
-        // Scores of step `step` of the item from stage `at`.
-        auto scores = [&](int w, unsigned step, unsigned at) {
-            if (!one) return;
-            const unsigned place = done[w] + step & 1;
-            const unsigned long long q = q_at + w * (S::Q / 16);
-            const unsigned long long k = k_at + at * (S::STAGE / 16) + step % S::STEPS * (kStep * 128 / 16);
-#pragma unroll
-            for (int i = 0; i < DP / 16; ++i)
-                if (i < steps)
-                    mma_ss(tmem + (w * 2 + place) * kStep, q + ((i >> 2) * (128 * 128) + (i & 3) * 32) / 16,
-                           k + ((i >> 2) * (KT * 128) + (i & 3) * 32) / 16, what_s, i > 0);
-            mma_commit(smem_at(&s.s_full[w][place]));
-        };
-        for (int n = 0; go; ++n) {
-            const int slot = n & 1;
-            if (!warp_wait(smem_at(&s.item_full[slot]), (n >> 1) & 1, &s.dead)) break;
-            const int item = s.items[slot].kind, rows = s.items[slot].rows;
-            const unsigned count = s.items[slot].hi - s.items[slot].lo, total = s.items[slot].steps;
-            __syncwarp();
-            if (one) bar_arrive(smem_at(&s.item_empty[slot]));
-            if (item == 0) break;
-            if (item == 2 || count == 0) continue;
-            const int tiles = TILES == 2 && rows > 128 ? 2 : 1;
-            // K of unit u is stage ring + 2 u, V the one after.
-            unsigned known = 0;           // stages of the item that are known to be there
-            auto have = [&](unsigned n) {
-                while (known <= n && go) {
-                    go = filled(ring + known);
-                    ++known;
+    } else if (role >= 2) {
+        const int w = role - 2;
+        if (elect_one()) {
+            const unsigned kind = 1u << 4 | W::kType << 7 | W::kType << 10 | (128u >> 4) << 24;
+            const unsigned what_s = kind | static_cast<unsigned>(kUnit >> 3) << 17;
+            const unsigned what_o = kind | 1u << 16 | static_cast<unsigned>((dim + 15) / 16 * 2) << 17;
+            const int steps = (dim + 15) / 16;
+            const unsigned q = static_cast<unsigned>(matrix_at(smem_at(s.q[w]), 16));
+            const unsigned k_low = static_cast<unsigned>(matrix_at(smem_at(s.k[0]), 16));
+            const unsigned v_low = static_cast<unsigned>(matrix_at(smem_at(s.v[0]), kUnit * 128));
+            constexpr unsigned high = static_cast<unsigned>(matrix_at(0, 0) >> 32);      // (the same of all)
+            const unsigned o_at = tmem + S::O + w * DP, s_at = tmem + w * 2 * kUnit;
+            unsigned q_turn = 0, done = 0;               // items and units of the tile so far
+            unsigned k_stage = 0, k_turn = 0, v_stage = 0, v_turn = 0;
+            bool go = true;
+            for (int n = 0; go; ++n) {
+                const int slot = n & 1;
+                if (!bar_wait(smem_at(&s.item_full[slot]), (n >> 1) & 1, &s.dead)) break;
+                const int item = s.items[slot].kind, rows = s.items[slot].rows;
+                const unsigned count = s.items[slot].hi - s.items[slot].lo;
+                bar_arrive(smem_at(&s.item_empty[slot]));
+                if (item == 0) break;
+                if (item == 2 || count == 0) continue;
+                const bool alone = TILES == 2 && rows <= 128;        // the tile of the two that has rows
+                if (alone && w == 1) {
+                    k_turn ^= (k_stage + count) / S::K_STAGES & 1;
+                    k_stage = (k_stage + count) % S::K_STAGES;
+                    v_turn ^= (v_stage + count) / S::V_STAGES & 1;
+                    v_stage = (v_stage + count) % S::V_STAGES;
+                    continue;
                 }
-                return go;
-            };
-            // Step g's scores, and what follows from them for its stage.
-            auto score_step = [&](int w, unsigned g) {
-                scores(w, g, stage_of(ring + g / S::STEPS * 2));
-                if (one && w == tiles - 1 && (g % S::STEPS == S::STEPS - 1 || g + 1 == total))
-                    mma_commit(smem_at(&s.empty[stage_of(ring + g / S::STEPS * 2)]));
-                if (one && g + 1 == total) mma_commit(smem_at(&s.q_empty[w]));
-                __syncwarp();
-            };
-            for (unsigned g = 0; g < 2 && g < total && go; ++g) {
-                if (!have(g / S::STEPS * 2)) break;
-                for (int w = 0; w < tiles && go; ++w) {
-                    if (g == 0) {
-                        go = warp_wait(smem_at(&s.q_full[w]), q_turn >> w & 1, &s.dead);
-                        q_turn ^= 1u << w;
-                        if (!go) break;
+                // Unit u's scores; the first ones wait for the queries.
+                auto scores = [&](unsigned u) {
+                    if (!(go = bar_wait(smem_at(&s.k_full[k_stage]), k_turn, &s.dead))) return;
+                    if (u == 0) {
+                        go = bar_wait(smem_at(&s.q_full[w]), q_turn, &s.dead);
+                        q_turn ^= 1;
+                        if (!go) return;
                         mma_fence_after();
                     }
-                    score_step(w, g);
-                }
-            }
-            for (unsigned g = 0; g < total && go; ++g) {
-                const unsigned v_stage = stage_of(ring + g / S::STEPS * 2 + 1);
-                const bool more = g + 2 < total;
-                if (!have(g / S::STEPS * 2 + 1)) break;
-                for (int w = 0; w < tiles; ++w) {
-                    // (A place has a barrier of its own: a warp may be a step ahead of another.)
-                    const unsigned place = done[w] + g & 1;
-                    go = warp_wait(smem_at(&s.p_full[w][place]), done[w] + g >> 1 & 1, &s.dead);
-                    if (!go) break;
-                    mma_fence_after();
-                    const unsigned add = g > 0 || *static_cast<volatile int*>(&s.seeded[w]) != 0;
-                    if (one) {
-                        const unsigned long long v = v_at + v_stage * (S::STAGE / 16) + g % S::STEPS * (kStep * 128 / 16);
+                    const unsigned place = done + u & 1, to = s_at + place * kUnit;
+                    const unsigned k = k_low + k_stage * (S::STAGE / 16);
 #pragma unroll
-                        for (int i = 0; i < kStep / 16; ++i)
-                            mma_ts(tmem + S::O + w * DP, tmem + (w * 2 + place) * kStep + S::P + i * 8,
-                                   v + i * (2048 / 16), what_o, add | (i > 0));
-                        mma_commit(smem_at(&s.o_full[w][place]));
-                        if (w == tiles - 1 && (g % S::STEPS == S::STEPS - 1 || g + 1 == total))
-                            mma_commit(smem_at(&s.empty[v_stage]));
+                    for (int c = 0; c < DP / 64; ++c) {
+                        if (steps >= 4 * (c + 1)) {
+                            mma_ss4(to, q + c * (128 * 128 / 16), k + c * (kUnit * 128 / 16), high, what_s, c > 0);
+                        } else {
+                            for (int i = 4 * c; i < steps; ++i)
+                                mma_ss(to, (static_cast<unsigned long long>(high) << 32) + q + c * (128 * 128 / 16) + (i & 3) * 2,
+                                       (static_cast<unsigned long long>(high) << 32) + k + c * (kUnit * 128 / 16) + (i & 3) * 2,
+                                       what_s, i > 0);
+                            break;
+                        }
                     }
-                    __syncwarp();
-                    if (more) {
-                        if (!have((g + 2) / S::STEPS * 2)) break;
-                        score_step(w, g + 2);
+                    mma_commit(smem_at(&s.s_full[w][place]));
+                    mma_commit(smem_at(&s.k_empty[k_stage]));
+                    if (alone) bar_arrive(smem_at(&s.k_empty[k_stage]));
+                    if (u + 1 == count) mma_commit(smem_at(&s.q_empty[w]));
+                    if (++k_stage == S::K_STAGES) {
+                        k_stage = 0;
+                        k_turn ^= 1;
                     }
+                };
+                scores(0);
+                if (go && count > 1) scores(1);
+                for (unsigned u = 0; u < count && go; ++u) {
+                    // (A place has a barrier of its own: a warp may be a unit ahead of another.)
+                    const unsigned place = done + u & 1;
+                    if (!(go = bar_wait(smem_at(&s.v_full[v_stage]), v_turn, &s.dead))) break;
+                    if (!(go = bar_wait(smem_at(&s.p_full[w][place]), done + u >> 1 & 1, &s.dead))) break;
+                    mma_fence_after();
+                    const unsigned add = u > 0 || *static_cast<volatile int*>(&s.seeded[w]) != 0;
+                    mma_ts4(o_at, s_at + place * kUnit + S::P, v_low + v_stage * (S::STAGE / 16), high, what_o, add);
+                    mma_commit(smem_at(&s.o_full[w][place]));
+                    mma_commit(smem_at(&s.v_empty[v_stage]));
+                    if (alone) bar_arrive(smem_at(&s.v_empty[v_stage]));
+                    if (++v_stage == S::V_STAGES) {
+                        v_stage = 0;
+                        v_turn ^= 1;
+                    }
+                    if (u + 2 < count) scores(u + 2);
                 }
+                done += count;
             }
-            ring += 2 * count;
-            for (int w = 0; w < tiles; ++w) done[w] += total;
-        }
-        if (s.dead != 0) {                // products under way end before the block does
-            if (one) mma_commit(smem_at(&s.drain));
-            const unsigned long long t0 = chunk_clock();
-            while (!bar_try(smem_at(&s.drain), 0) && chunk_clock() - t0 < 10ull * 1000ull * 1000ull) {}
+            if (s.dead != 0) {            // products under way end before the block does
+                mma_commit(smem_at(&s.drain[w]));
+                const unsigned long long t0 = chunk_clock();
+                while (!bar_try(smem_at(&s.drain[w]), 0) && chunk_clock() - t0 < 10ull * 1000ull * 1000ull) {}
+            }
         }
         __syncwarp();
     } else {
         const int w = TILES == 2 ? warp >> 2 : 0, mine = tid & 127;
         const unsigned lanes = static_cast<unsigned>((warp & 3) * 32) << 16;
-        const unsigned s_at = tmem + lanes + w * 2 * kStep, o_at = tmem + lanes + S::O + w * DP;
+        const unsigned s_at = tmem + lanes + w * 2 * kUnit, o_at = tmem + lanes + S::O + w * DP;
         const float scale = p.scale_log2;
         unsigned meet_turn = 0, both_turn = 0;                               // parities of the next phases
-        unsigned done = 0;                // steps
+        unsigned done = 0;                // units
         int looked = 0;                   // units looked through
-        unsigned ring = 0;                // stages gone through
-        // Step number `step`'s products with V are in O.  (A step's two barriers take turns with the places of
+        unsigned ring = 0;                // units gone through of the block
+        // Unit number `step`'s products with V are in O.  (The two barriers take turns with the places of
         // S: the one before last is known to be done, so that a phase is never taken for an older one.)
-        auto added = [&](unsigned step) {
-            const bool ok = warp_wait(smem_at(&s.o_full[w][step & 1]), step >> 1 & 1, &s.dead);
+        auto added = [&](unsigned unit) {
+            const bool ok = warp_wait(smem_at(&s.o_full[w][unit & 1]), unit >> 1 & 1, &s.dead);
             mma_fence_after();
             return ok;
         };
@@ -653,7 +693,7 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
             }
             const int count = it.hi - it.lo, tiles = TILES == 2 && it.rows > 128 ? 2 : 1;
             if (w >= tiles) {
-                ring += 2 * count;
+                ring += count;
                 bar_arrive(smem_at(&s.item_empty[slot]));
                 continue;
             }
@@ -687,11 +727,9 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
             float top = kNegInf, sum = 0.0f;
             const int first_pos = from + it.row / p.group, last_pos = from + (it.row + it.rows - 1) / p.group;
             const bool idle = w * 128 + (warp & 3) * 32 >= it.rows;      // none of the warp's rows is the tile's
-            const int total = it.steps;
-            for (int g = 0; g < total; ++g) {
-                const int sub = S::STEPS == 1 ? 0 : g & 1;
+            for (int u = 0; u < count; ++u) {
                 int here, in_page;
-                const int at = units.first(it.span.unit(it.lo + g / S::STEPS), &here, &in_page);
+                const int at = units.first(it.span.unit(it.lo + u), &here, &in_page);
                 const int valid = min(here, it.e.len - at);
                 // What this row sees of the unit: lo .. hi - 1, and those below sink.
                 const int hi = min(valid, pos - at + 1);
@@ -700,15 +738,15 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
                 // Whether some row of the block's tiles sees the unit in part (all threads alike).
                 const bool part = at + valid - 1 > first_pos ||
                                   (p.window > 0 && at <= last_pos - p.window && at + valid > p.sinks);
-                const unsigned place = done + g & 1;
-                if (!(go = warp_wait(smem_at(&s.s_full[w][place]), (done + g) >> 1 & 1, &s.dead))) break;
+                const unsigned place = done + u & 1;
+                if (!(go = warp_wait(smem_at(&s.s_full[w][place]), done + u >> 1 & 1, &s.dead))) break;
                 mma_fence_after();
                 bool odd = false;
-                if (part && sub == 0) {
-                    const unsigned v_at = ring + g / S::STEPS * 2 + 1, v_stage = v_at % S::STAGES;
-                    if (!(go = warp_wait(smem_at(&s.full[v_stage]), v_at / S::STAGES & 1, &s.dead))) break;
+                if (part) {
+                    const unsigned v_stage = (ring + u) % S::V_STAGES;
+                    if (!(go = warp_wait(smem_at(&s.v_full[v_stage]), (ring + u) / S::V_STAGES & 1, &s.dead))) break;
                     unsigned hot = 0;
-                    const uint4* const v = reinterpret_cast<const uint4*>(s.ring[v_stage]);
+                    const uint4* const v = reinterpret_cast<const uint4*>(s.v[v_stage]);
 #pragma unroll 8
                     for (int x = mine; x < S::STAGE / 16; x += 128) {
                         const uint4 y = v[x];
@@ -722,40 +760,39 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
                     if (!(go = meet(smem_at(&s.tile_meet[w]), &meet_turn, &s.dead))) break;
                     odd = *static_cast<volatile int*>(&s.hot[w][looked & 1]) == looked;
                     if (odd) {
-                        if (g > 0 && !(go = added(done + g - 1))) break;
-                        if (!(go = give_out<T, DP>(s.ring[v_stage], o_at, dim, lo, hi, sink, valid, g == 0, 128 * tiles,
+                        if (u > 0 && !(go = added(done + u - 1))) break;
+                        if (!(go = give_out<T, DP>(s.v[v_stage], o_at, dim, lo, hi, sink, valid, u == 0, 128 * tiles,
                                                    smem_at(tiles == 2 ? &s.both_meet : &s.tile_meet[w]),
                                                    tiles == 2 ? &both_turn : &meet_turn, &s.dead)))
                             break;
                     }
                 }
-                if (g == 0 && mine == 0) s.seeded[w] = odd;
+                if (u == 0 && mine == 0) s.seeded[w] = odd;
                 if (!idle) {
-                    float x[kStep];
-                    const unsigned from_at = s_at + place * kStep;
+                    float x[kUnit];
+                    const unsigned from_at = s_at + place * kUnit;
                     tmem_load(from_at, x);
                     tmem_load(from_at + 32, x + 32);
                     tmem_wait_load(x);
-                    const int c0 = sub * kStep;
-                    if (!__all_sync(0xffffffffu, hi >= c0 + kStep && lo <= c0)) {
+                    if (!__all_sync(0xffffffffu, hi >= kUnit && lo <= 0)) {
 #pragma unroll
-                        for (int c = 0; c < kStep; ++c)
-                            if (!(c < hi - c0 && (c >= lo - c0 || c < sink - c0))) x[c] = kNegInf;
+                        for (int c = 0; c < kUnit; ++c)
+                            if (!(c < hi && (c >= lo || c < sink))) x[c] = kNegInf;
                     }
                     float up0 = x[0], up1 = x[1];
 #pragma unroll
-                    for (int c = 2; c < kStep - 2; c += 4) {
+                    for (int c = 2; c < kUnit - 2; c += 4) {
                         up0 = max3(up0, x[c], x[c + 1]);
                         up1 = max3(up1, x[c + 2], x[c + 3]);
                     }
-                    const float up = max3(max3(up0, x[kStep - 2], x[kStep - 1]), up1, kNegInf) * scale;
+                    const float up = max3(max3(up0, x[kUnit - 2], x[kUnit - 1]), up1, kNegInf) * scale;
                     const bool move = up > top + W::kSlack || (top == kNegInf && up > kNegInf);
                     if (__any_sync(0xffffffffu, move)) {
                         const float by = move ? chunk_pow2(top - up) : 1.0f;         // 0 at the first position
                         if (move) top = up;
                         sum *= by;
-                        if (g > 0) {
-                            if (!(go = added(done + g - 1))) break;
+                        if (u > 0) {
+                            if (!(go = added(done + u - 1))) break;
                             for (int d = 0; d < dim; d += 32) {
                                 float o[32];
                                 tmem_load(o_at + d, o);
@@ -771,7 +808,7 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
                     const unsigned long long scale2 = pair_of(scale, scale), base2 = pair_of(base, base);
                     unsigned long long sums = 0ull, more = 0ull;
 #pragma unroll
-                    for (int h = 0; h < kStep; h += 32) {
+                    for (int h = 0; h < kUnit; h += 32) {
                         unsigned r16[16];
 #pragma unroll
                         for (int i = 0; i < 32; i += 4) {
@@ -797,8 +834,8 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
                 mma_fence_before();
                 bar_arrive(smem_at(&s.p_full[w][place]));
             }
-            ring += 2 * count;
-            done += total;
+            ring += count;
+            done += count;
             if (!go) break;
             if (count > 0 && !(go = added(done - 1))) break;
             float* lse = nullptr;
@@ -857,7 +894,7 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
     mma_fence_before();
     __syncthreads();
     mma_fence_after();
-    if (issuer) {
+    if (role == 2) {
         if (s.dead != 0 && lane == 0) flag(p.c.status, GS_DEV_TIMEOUT);
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
     }
@@ -922,8 +959,7 @@ ChunkShape chunk_mma_shape(int dim) { return {dim > 128 ? 128 : 256, sm_count()}
 
 gs_status launch_chunk_mma(int dtype, ChunkParams& p, int blocks, gs_stream stream) {
     Maps m = {};
-    const int unit = p.c.dim > 128 ? 64 : 128;
-    const int rows = p.c.page < unit ? p.c.page : unit;
+    const int rows = p.c.page < kUnit ? p.c.page : kUnit;
     if (!encode(&m.k, dtype, p.c, p.c.k, rows) || !encode(&m.v, dtype, p.c, p.c.v, rows)) return GS_ERR_CUDA;
     // TMA brings the queries as they are, in boxes that hold whole tokens of a group, from rows on 16 bytes.
     p.q_boxes = p.q_aligned != 0 && p.q_sign > 0.0f && 128 % p.group == 0 && (p.tokens == 1 || p.q_token > 0) &&
