@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
 #pragma unroll
             for (int i = 0; i < V; ++i) f[i] = 0.0f;
             if (r < it.rows && c * V < dim) {
-                const int t = row / p.group, h = it.head * p.group + row - t * p.group;
+                const int t = chunk_token(p, row), h = it.head * p.group + row - t * p.group;
                 const T* from = static_cast<const T*>(p.q) + (it.e.row + t) * p.q_token + h * p.q_head + c * V;
                 unpack16<T>(load16_any(from, p.q_aligned != 0), f);
             }
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
 #pragma unroll
             for (int d = 0; d < NV * 4; ++d) o[i][d] = 0.0f;
         const int from = it.e.len - it.e.m;              // position of the entry's first row
-        const int first_row = from + it.row / p.group, last_row = from + (it.row + it.rows - 1) / p.group;
+        const int first_row = from + chunk_token(p, it.row), last_row = from + chunk_token(p, it.row + it.rows - 1);
         for (int n = it.lo; n < it.hi; ++n) {
             int count, in_page;
             const int at = units.first(it.span.unit(n), &count, &in_page);
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                                 (p.window > 0 && at <= last_row - p.window && at + KT > p.sinks);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int row = it.row + ty * 4 + i, pos = from + row / p.group;
+                const int row = it.row + ty * 4 + i, pos = from + chunk_token(p, row);
                 float up = kNegInf;
                 bool seen[CPT];
 #pragma unroll
@@ -318,12 +318,19 @@ extern "C" gs_status gs_chunk_attention(const gs_chunk_attention_args* args, gs_
     p.start = args->start;
     p.q_heads = args->q_heads;
     p.group = args->q_heads / p.c.heads;
+    // Division by the group: with s = ceil(log2 group), mul = 2^32 (2^s - group) / group + 1.
+    while ((1u << p.group_shift) < static_cast<unsigned>(p.group)) ++p.group_shift;
+    p.group_mul = static_cast<unsigned>(
+        (((1ull << p.group_shift) - static_cast<unsigned>(p.group)) << 32) / static_cast<unsigned>(p.group) + 1);
+    p.tile_step = 16 * plan.shape.rows / p.group;
     p.q = args->q;
     p.q_token = args->q_token_stride;
     p.q_head = args->q_head_stride;
     p.q_aligned = aligned(args->q, 16) && (args->q_token_stride * es) % 16 == 0 && (args->q_head_stride * es) % 16 == 0;
     p.out_aligned = aligned(args->out, 16) && (args->out_token_stride * es) % 16 == 0 &&
                     (args->out_head_stride * es) % 16 == 0;
+    p.out_wide = aligned(args->out, 32) && (args->out_token_stride * es) % 32 == 0 && (args->out_head_stride * es) % 32 == 0;
+    p.slots_wide = aligned(args->workspace, 32);
     // Scores are kept in powers of two, the largest first: a negative scale turns the queries' signs,
     // and scale 0 makes them 0.
     p.scale_log2 = args->scale == 0.0f ? 1.0f : std::fabs(args->scale) * kChunkLog2e;

@@ -37,10 +37,13 @@ struct ChunkParams {
     const int* seq;
     const int* start;
     int q_heads, group;
+    unsigned group_mul, group_shift;      // x / group = (mulhi(x, mul) + x) >> shift
+    int tile_step;                        // 16ths of a position from one tile to the next
     const void* q;
     long long q_token, q_head;
     int q_aligned, out_aligned;           // rows lie on 16 bytes
     int q_boxes;                          // TMA brings the queries
+    int out_wide, slots_wide;             // out's rows, and the slots', lie on 32 bytes
     float scale_log2;                     // |scale| * log2 e (1 where scale is 0)
     float q_sign;                         // what queries are multiplied with: 1, -1 or 0
     int window, sinks;
@@ -56,6 +59,25 @@ struct ChunkParams {
 // A slot: reference[rows], sum[rows], o[rows][dim].
 __host__ __device__ inline long long chunk_slot_words(int rows, int dim) {
     return static_cast<long long>(rows) * (dim + 2);
+}
+
+__device__ __forceinline__ int chunk_token(const ChunkParams& p, int row) {
+    return static_cast<int>((__umulhi(static_cast<unsigned>(row), p.group_mul) + static_cast<unsigned>(row)) >> p.group_shift);
+}
+// x / d for quotients that are small, x >= 0 and d > 0: a quotient in 24 bits and its remainder (a division
+// of 64-bit numbers takes hundreds of cycles, and a block's first item waits for half a dozen).
+__device__ __forceinline__ long long chunk_quotient(long long x, long long d) {
+    long long q = static_cast<long long>(__fdividef(__ll2float_rn(x), __ll2float_rn(d)));
+    long long r = x - q * d;
+    while (r < 0) {
+        --q;
+        r += d;
+    }
+    while (r >= d) {
+        ++q;
+        r -= d;
+    }
+    return q;
 }
 
 struct ChunkEntry {
@@ -162,7 +184,7 @@ __device__ __forceinline__ int chunk_slot(int share, int k) { return 2 * (share 
 template <int ROWS, int HALF, int KT, int THREADS, int WIDTH>
 struct ChunkCut {
     using ll = long long;
-    static constexpr int kOver = 16 * 192;               // what a tile costs beside its positions
+    static constexpr int kOver = 16 * 288;               // what a tile costs beside its positions
     static constexpr int kFew = 8;        // units of a tile that is not cut
     static constexpr int kLeast = 2;      // units of a part
     struct Shared {
@@ -198,13 +220,13 @@ struct ChunkCut {
         Cost c;
         c.tiles = tiles_of(p, e);
         c.from = 16ll * max(0, e.len - e.m);
-        c.step = 16 * ROWS / p.group;
+        c.step = p.tile_step;
         c.cap = 0x7fffffffffffll;
         c.turn = c.tiles;
         if (p.window > 0) {
             c.cap = 16 * (static_cast<ll>(p.window) + p.sinks + KT) + c.step;
             const ll below = c.cap - c.from;
-            const ll t = below <= c.step ? 0 : c.step > 0 ? (below - 1) / c.step : c.tiles;
+            const ll t = below <= c.step ? 0 : below > c.step * c.tiles ? c.tiles : chunk_quotient(below - 1, c.step);
             if (t < c.tiles) c.turn = static_cast<int>(t);
         }
         return c;
@@ -251,12 +273,12 @@ struct ChunkCut {
     __device__ __forceinline__ ll first_of(int n) const { return n * s->each + min(n, s->more); }
     __device__ __forceinline__ int share_of(ll x) const {
         const ll edge = s->more * (s->each + 1);
-        return static_cast<int>(x < edge ? x / (s->each + 1) : s->more + (x - edge) / s->each);
+        return static_cast<int>(x < edge ? chunk_quotient(x, s->each + 1) : s->more + chunk_quotient(x - edge, s->each));
     }
     // The unit at which an edge `f` into a tile's cost cuts it.
     static __device__ __forceinline__ int cut(int units, ll all, ll f) {
         if (units < kFew) return 2 * f >= all ? units : 0;
-        const int u = static_cast<int>((units * f + all / 2) / all);
+        const int u = static_cast<int>(chunk_quotient(units * f + all / 2, all));
         return u < kLeast ? 0 : units - u < kLeast ? units : u;
     }
 
@@ -283,7 +305,7 @@ struct ChunkCut {
             enter(p, i + 1);
             all = cost.upto(cost.tiles);
         }
-        head = all > 0 ? static_cast<int>((x - entry_at) / all) : p.c.heads;
+        head = all > 0 ? static_cast<int>(min(chunk_quotient(x - entry_at, all), static_cast<ll>(p.c.heads))) : p.c.heads;
         walking = head < p.c.heads;       // (else lengths have changed during the call)
         const ll left = x - entry_at - head * all;
         int a = 0, b = cost.tiles - 1;    // the last tile that begins at x or before
@@ -323,7 +345,7 @@ struct ChunkCut {
         const int rows = static_cast<int>(min(static_cast<ll>(ROWS), static_cast<ll>(e.m) * p.group - it->row));
         it->rows = rows;
         const int from = e.len - e.m;
-        it->span = chunk_span<KT>(p, u, from + it->row / p.group, from + (it->row + rows - 1) / p.group);
+        it->span = chunk_span<KT>(p, u, from + chunk_token(p, it->row), from + chunk_token(p, it->row + rows - 1));
         const int units = it->span.count;
         it->lo = at >= x0 ? 0 : cut(units, all, x0 - at);
         it->hi = end <= x1 ? units : cut(units, all, x1 - at);
@@ -437,70 +459,103 @@ __device__ __forceinline__ void chunk_put4(const ChunkParams& p, T* to, float4 o
 // The output row of row r of an entry's head, and its place in lse.
 template <class T>
 __device__ __forceinline__ T* chunk_out(const ChunkParams& p, const ChunkItem& it, int r, float** lse) {
-    const int t = r / p.group, h = it.head * p.group + r - t * p.group;
+    const int t = chunk_token(p, r), h = it.head * p.group + r - t * p.group;
     const long long token = it.e.row + t;
     *lse = p.lse != nullptr ? p.lse + token * p.q_heads + h : nullptr;
     return static_cast<T*>(p.out) + token * p.out_token + h * p.out_head;
 }
 
-// Joins a piece of a tile: the parts of a row are weighted to their common reference.  A warp a row: a
-// lane looks at every 32nd part's reference and sum, then has four neighbouring dims of all parts, eight of
-// them in flight (a thread that went through the parts one by one took 150 us for 38 parts of 132 rows).
-// lift: what the sums are scaled by, in powers of two.
-template <class T>
-__device__ __forceinline__ void chunk_join(const ChunkParams& p, const ChunkItem& it, int warp, int warps,
-                                           float lift) {
-    const int dim = p.c.dim, lane = threadIdx.x & 31;
+// RR rows from x0 on of a join, PP parts at a time, by a warp: a lane has a part's reference and sum of a row,
+// and four neighbouring dims of all of them.
+template <class T, int PP, int RR>
+__device__ __forceinline__ void chunk_join_rows(const ChunkParams& p, const ChunkItem& it, int x0, float lift) {
+    const int dim = p.c.dim, lane = threadIdx.x & 31, rows = it.rows, parts = it.parts;
+    const int part = lane & (PP - 1), mine = min(lane / PP, RR - 1);         // this lane's part and row
     const long long words = 2 * chunk_slot_words(p.slot_rows, dim);              // between the slots of two shares
     const float* const first = p.slots + it.share * words;
     const long long begin = words / 2;    // part 0 is in its share's second slot
-    for (int x = warp; x < it.rows; x += warps) {
-        const int r = it.at + x;
-        float top = kNegInf;
-        for (int k = lane; k < it.parts; k += 32) top = fmaxf(top, __ldcg(first + k * words + (k == 0 ? begin : 0) + r));
+    auto slot = [&](int k) { return first + k * words + (k == 0 ? begin : 0); };
+    const int row = it.at + min(x0 + mine, rows - 1);
+    for (int d0 = 0; d0 < dim; d0 += 128) {
+        const int d = d0 + 4 * lane, at = d < dim ? d : 0;
+        float4 o[RR];
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        const float base = top == kNegInf ? 0.0f : top;
-        float sum = 0.0f;
-        float* lse;
-        T* const to = chunk_out<T>(p, it, it.row + r, &lse);
-        for (int d0 = 0; d0 < dim; d0 += 128) {
-            const int d = d0 + 4 * lane;
-            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            for (int k0 = 0; k0 < it.parts; k0 += 32) {
-                float w = 0.0f;
-                if (k0 + lane < it.parts) {
-                    const float* const slot = first + (k0 + lane) * words + (k0 + lane == 0 ? begin : 0) + r;
-                    w = chunk_pow2(__ldcg(slot) - base);
-                    if (d0 == 0) sum = fmaf(__ldcg(slot + p.slot_rows), w, sum);
-                }
-                const int n = min(32, it.parts - k0);
-                const float* from = first + k0 * words + 2 * p.slot_rows + static_cast<long long>(r) * dim + d;
-                for (int k = 0; k < n; k += 8) {
-                    float4 v[8];
+        for (int r = 0; r < RR; ++r) o[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float top = kNegInf, sum = 0.0f;  // of this lane's row
+        for (int k0 = 0; k0 < parts; k0 += PP) {
+            const float* const from = slot(min(k0 + part, parts - 1)) + row;
+            const float ref = __ldcg(from), weight = __ldcg(from + p.slot_rows);
+            float4 v[RR][PP];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        v[i] = k + i < n && d < dim ? __ldcg(reinterpret_cast<const float4*>(
-                                                          from + (k + i) * words + (k0 + k + i == 0 ? begin : 0)))
-                                                    : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int i = 0; i < PP; ++i)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float f = __shfl_sync(0xffffffffu, w, k + i);
-                        o.x = fmaf(v[i].x, f, o.x);
-                        o.y = fmaf(v[i].y, f, o.y);
-                        o.z = fmaf(v[i].z, f, o.z);
-                        o.w = fmaf(v[i].w, f, o.w);
-                    }
+                for (int r = 0; r < RR; ++r)
+                    v[r][i] = __ldcg(reinterpret_cast<const float4*>(
+                        slot(min(k0 + i, parts - 1)) + 2 * p.slot_rows +
+                        static_cast<long long>(it.at + min(x0 + r, rows - 1)) * dim + at));
+            float up = fmaxf(top, ref);
+#pragma unroll
+            for (int i = 1; i < PP; i <<= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, i));
+            const float base = up == kNegInf ? 0.0f : up, fade = chunk_pow2(top - base);
+            const float w = k0 + part < parts ? chunk_pow2(ref - base) : 0.0f;
+            float all = weight * w;
+#pragma unroll
+            for (int i = 1; i < PP; i <<= 1) all += __shfl_xor_sync(0xffffffffu, all, i);
+            sum = fmaf(sum, fade, all);
+            top = up;
+#pragma unroll
+            for (int r = 0; r < RR; ++r) {
+                const float f = __shfl_sync(0xffffffffu, fade, r * PP);
+                o[r].x *= f;
+                o[r].y *= f;
+                o[r].z *= f;
+                o[r].w *= f;
+#pragma unroll
+                for (int i = 0; i < PP; ++i) {
+                    const float g = __shfl_sync(0xffffffffu, w, r * PP + i);
+                    o[r].x = fmaf(v[r][i].x, g, o[r].x);
+                    o[r].y = fmaf(v[r][i].y, g, o[r].y);
+                    o[r].z = fmaf(v[r][i].z, g, o[r].z);
+                    o[r].w = fmaf(v[r][i].w, g, o[r].w);
                 }
             }
-            if (d0 == 0) {
-#pragma unroll
-                for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
-            }
-            const float by = sum > 0.0f ? 1.0f / sum : sum;          // a NaN stays one
-            if (d < dim) chunk_put4<T>(p, to + d, make_float4(o.x * by, o.y * by, o.z * by, o.w * by));
         }
-        if (lane == 0 && lse != nullptr) *lse = sum == 0.0f ? kNegInf : (top + log2f(sum) - lift) * kChunkLn2;
+        const float by = sum > 0.0f ? 1.0f / sum : sum;  // a NaN stays one
+        float* lse;
+#pragma unroll
+        for (int r = 0; r < RR; ++r) {
+            const float f = __shfl_sync(0xffffffffu, by, r * PP);
+            if (x0 + r < rows && d < dim) {
+                T* const to = chunk_out<T>(p, it, it.row + it.at + x0 + r, &lse);
+                chunk_put4<T>(p, to + d, make_float4(o[r].x * f, o[r].y * f, o[r].z * f, o[r].w * f));
+            }
+        }
+        if (d0 == 0 && part == 0 && lane < RR * PP && x0 + mine < rows && p.lse != nullptr) {
+            chunk_out<T>(p, it, it.row + row, &lse);
+            *lse = sum == 0.0f ? kNegInf : (top + log2f(sum) - lift) * kChunkLn2;
+        }
+    }
+}
+
+// Joins a piece of a tile: the parts of a row are weighted to their common reference, in their order.
+// What costs is latency, so a warp has 16 outputs a lane in flight, none under a condition (which would put
+// them one after the other): what is past the parts, rows or dims reads the last one's and counts nothing.
+// lift: what the sums are scaled by, in powers of two.
+template <class T>
+__device__ __noinline__ void chunk_join(const ChunkParams& p, const ChunkItem& it, int warp, int warps, float lift) {
+    const int each = (it.rows + warps - 1) / warps;      // rows of a warp
+    const int end = min(it.rows, (warp + 1) * each);
+    for (int x = warp * each; x < end;) {
+        if (it.parts <= 2) {
+            chunk_join_rows<T, 2, 8>(p, it, x, lift);
+            x += 8;
+        } else if (it.parts <= 4) {
+            chunk_join_rows<T, 4, 4>(p, it, x, lift);
+            x += 4;
+        } else {
+            chunk_join_rows<T, 8, 2>(p, it, x, lift);
+            x += 2;
+        }
     }
 }
 

@@ -256,6 +256,14 @@ __device__ __forceinline__ void tmem_store16(unsigned at, const unsigned* r) {
 }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// 32 bytes at once: a whole sector (with two halves of it one after the other the rows' stores took twice
+// the time).
+__device__ __forceinline__ void store32(void* to, const unsigned* r) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 template <class T>
 struct Weights;                           // of type T: kept below 2^(kLift + kSlack)
 template <>
@@ -356,7 +364,9 @@ __device__ __noinline__ bool give_out(unsigned char* v, unsigned o_at, int dim, 
 // (Apart from the kernel, whose registers are the rows'.)
 template <class C>
 __device__ __noinline__ void next_item(C* cut, const ChunkParams& p, ChunkItem* it) {
-    *it = cut->item(p);
+    C mine = *cut;
+    *it = mine.item(p);
+    *cut = mine;
 }
 
 template <class T, int DP>
@@ -465,7 +475,7 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
             const int head = it.head, len = it.e.len, lo = it.lo, hi = it.hi;
             const ChunkSpan span = it.span;
             const int tiles = TILES == 2 && it.rows > 128 ? 2 : 1;
-            const int q_token = it.e.row + it.row / p.group;
+            const int q_token = it.e.row + chunk_token(p, it.row);
             const int* const table = p.c.table + static_cast<long long>(it.e.seq) * p.c.cols;
             __syncwarp();
             if (is_v && one) bar_arrive(smem_at(&s.item_empty[slot]));
@@ -700,7 +710,7 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
             const int r = w * 128 + mine, row = it.row + r;         // of the tile, of the entry
             const bool real = r < it.rows;
             const int from = it.e.len - it.e.m;
-            const int token = row / p.group, pos = from + token;
+            const int token = chunk_token(p, row), pos = from + token;
             if (count > 0 && p.q_boxes == 0) {
                 // The row of Q, with the scale's sign, where TMA cannot bring it.
                 const T* const q = static_cast<const T*>(p.q) + (it.e.row + static_cast<long long>(token)) * p.q_token +
@@ -725,7 +735,7 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
                 if (mine == 0) bar_arrive(smem_at(&s.q_full[w]));
             }
             float top = kNegInf, sum = 0.0f;
-            const int first_pos = from + it.row / p.group, last_pos = from + (it.row + it.rows - 1) / p.group;
+            const int first_pos = from + chunk_token(p, it.row), last_pos = from + chunk_token(p, it.row + it.rows - 1);
             const bool idle = w * 128 + (warp & 3) * 32 >= it.rows;      // none of the warp's rows is the tile's
             for (int u = 0; u < count; ++u) {
                 int here, in_page;
@@ -855,23 +865,35 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
                 if (it.parts > 1) {
                     float* const keep = part + 2 * p.slot_rows + static_cast<long long>(r) * dim + d;
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        if (d + i < dim) *reinterpret_cast<float4*>(keep + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-                } else {
-#pragma unroll
                     for (int i = 0; i < 32; i += 8) {
                         if (d + i >= dim) break;
-                        uint4 y;
-                        y.x = W::pack(o[i] * by, o[i + 1] * by);
-                        y.y = W::pack(o[i + 2] * by, o[i + 3] * by);
-                        y.z = W::pack(o[i + 4] * by, o[i + 5] * by);
-                        y.w = W::pack(o[i + 6] * by, o[i + 7] * by);
-                        if (p.out_aligned) {
-                            *reinterpret_cast<uint4*>(to + d + i) = y;
+                        if (p.slots_wide != 0) {
+                            store32(keep + i, reinterpret_cast<const unsigned*>(o + i));
                         } else {
-                            const T* const e = reinterpret_cast<const T*>(&y);
+                            *reinterpret_cast<float4*>(keep + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                            *reinterpret_cast<float4*>(keep + i + 4) = make_float4(o[i + 4], o[i + 5], o[i + 6], o[i + 7]);
+                        }
+                    }
+                } else {
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) to[d + i + k] = e[k];
+                    for (int i = 0; i < 32; i += 16) {
+                        unsigned y[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) y[k] = W::pack(o[i + 2 * k] * by, o[i + 2 * k + 1] * by);
+                        if (p.out_wide != 0 && d + i + 16 <= dim) {
+                            store32(to + d + i, y);
+                            continue;
+                        }
+#pragma unroll
+                        for (int h = 0; h < 16; h += 8) {
+                            if (d + i + h >= dim) break;
+                            if (p.out_aligned != 0) {
+                                *reinterpret_cast<uint4*>(to + d + i + h) = make_uint4(y[h / 2], y[h / 2 + 1], y[h / 2 + 2], y[h / 2 + 3]);
+                            } else {
+                                const T* const e = reinterpret_cast<const T*>(y + h / 2);
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) to[d + i + h + k] = e[k];
+                            }
                         }
                     }
                 }
