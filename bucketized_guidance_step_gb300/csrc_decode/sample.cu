@@ -1,16 +1,21 @@
 // Sampling (sm_103a): temperature, top-k, top-p, min-p and the token from given random numbers.
 //
 // What the filters keep is a beginning of the row's tokens in the order of falling z (ties: rising
-// index), so it is known by its last token: a border (a value of z) and how many of the tokens with
-// just that value stay.  The border is found digit by digit in the 32-bit keys whose order is that of z:
-// a histogram of 2048, 2048 and 1024 digits counts the tokens and sums their weights e^(z - max), the
-// digits are scanned from the largest down, and the one that holds the border is looked into.  For top-k
-// the border is the k-th token, for top-p the token at which the weights reach p of their sum over what
-// top-k left.  min-p is a bound on a token's own weight, looked at last.
+// index), so it is known by its last token.  A row is a cluster's; each block streams its part once and
+// keeps the largest key of every 16-byte vector (keys are 32-bit numbers in the order of z).  Then
+//   with top-k: a histogram of these largest keys, over 2048 equal pieces of z's range, finds a z that at
+//     least k vectors reach, so at least k tokens do, and hardly more.  Only vectors that reach it are read
+//     again, and their tokens above it, a list of somewhat over k, go to the first block, which sorts them
+//     and has all it needs: the k-th token, the weights' sum, where top-p ends, min-p, the token.
+//   with top-p alone: a histogram of the weights finds the piece of z's range in which they reach p of
+//     their sum, and the tokens of that piece alone are listed and sorted; a last pass takes what is kept.
+//   with neither, the last pass alone.
+// Where a list would be longer than its place (many tokens of one z; k over 1024), the last token is found
+// digit by digit in the keys instead: histograms of 2048, 2048 and 1024 digits count the tokens or sum
+// their weights from the largest down.
 //
 // Weights are summed as whole numbers (units of 2^-40 of the largest weight): sums do not depend on the
-// order of the additions.  A row is a cluster's; its blocks keep a part of it each in shared memory, as
-// keys, and read it once.
+// order of the additions, nor does the sorted list on the order in which blocks fill it.
 #include <cmath>
 
 #include "decode_common.cuh"
@@ -18,13 +23,15 @@
 namespace gs_decode {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32, kDigits = 2048;
+constexpr int kThreads = 256, kWarps = kThreads / 32, kDigits = 2048;
 constexpr int kMaxCluster = 8;
+constexpr int kGroups = 4096;             // groups of vectors of a block, of which the largest key is kept
+constexpr int kList = 2048, kMostK = 1024;               // tokens of a list; largest top-k that goes by one
 constexpr unsigned kNone = 0x007fffffu;   // the key of -inf: such tokens, and NaN, are not kept
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
 
 struct SampleParams {
-    int batch, vocab, cluster, held;      // held: places of a block's keys in shared memory (0: not kept)
+    int batch, vocab, cluster;
     const void* logits;
     long long row_stride;
     const float* temperature;
@@ -40,23 +47,34 @@ struct SampleParams {
 
 // What a block shows to its cluster.
 struct Shown {
-    unsigned top;                         // largest key
-    unsigned long long count, weight;     // of its share of the digits
-    unsigned long long above_count, above_weight, here;  // of what lies above the found digit; its tokens
+    unsigned top, bottom;                 // largest and smallest key
+    unsigned long long all;               // of its share of the digits: tokens, or weights
+    unsigned long long above, above_weight, here;        // what lies above the found digit; its tokens
     int digit;
+    unsigned listed;                      // tokens in the first block's list
+    unsigned border;                      // the last token that is kept
+    int limit;
     unsigned ties;                        // tokens at the border
     float pick, sum;                      // best token of the block, and the weights it keeps
     int best;
     unsigned best_key;
+    unsigned long long weight;
 };
 
 struct alignas(16) Shared {
-    unsigned count[kDigits], low[kDigits], high[kDigits];
+    union {
+        unsigned long long list[kList];
+        struct {
+            unsigned low[kDigits], high[kDigits];
+        };
+    };
+    unsigned most[kGroups];
+    unsigned count[kDigits];
     unsigned long long scan[kWarps + 1];
-    unsigned long long in[kMaxCluster][2];
+    unsigned long long in[kMaxCluster];
     float f[kWarps], g[kWarps];
     int i[kWarps];
-    unsigned u[kWarps];
+    unsigned u[kWarps], v[kWarps];
     int limit;
     Shown shown;
 };
@@ -66,8 +84,6 @@ __device__ __forceinline__ float pow2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-
-static_assert(sizeof(Shared) % 16 == 0, "the keys follow it in 16-byte vectors");
 
 // Keys rise with z; NaN is below everything.
 __device__ __forceinline__ unsigned key_of(float z) {
@@ -96,59 +112,55 @@ __device__ __forceinline__ V far(const V* local, unsigned r) {
     }
 }
 
-// A block's part of its row.  Places count from the 16-byte vector that holds the row's first value.
-template <class T, bool HELD>
+// A block's part of its row: vectors v0 .. v1 - 1, counted from the 16-byte vector that holds the row's
+// first value.
+template <class T>
 struct Part {
-    static constexpr int V = 16 / static_cast<int>(sizeof(T));
+    static constexpr int V = 16 / static_cast<int>(sizeof(T)), AHEAD = 4;    // values; vectors in flight
     const T* row;
-    unsigned* keys;
-    int shift, vocab, v0, v1;             // values of the first vector that are not the row's; vectors
+    int shift, vocab, v0, v1;             // values of the first vector that are not the row's
+    int whole0, whole1;                   // vectors that are the row's entirely: whole0 .. whole1
     float hot;
 
-    __device__ __forceinline__ float settle(float z) const { return hot > 0.0f ? __fdiv_rn(z, hot) : z; }
-    // The keys of vector v (0 for what is not the row's).
-    __device__ __forceinline__ void fetch(int v, unsigned (&k)[V]) const {
-        const int at = v * V - shift;
+    __device__ __forceinline__ uint4 raw(int v) const {              // (any vector, read only if whole)
+        const int at = min(max(v, whole0), whole1);
+        return whole0 <= whole1 ? *reinterpret_cast<const uint4*>(row + static_cast<long long>(at) * V - shift)
+                                : make_uint4(0u, 0u, 0u, 0u);
+    }
+    // The keys of vector v, of which `r` is raw(v); 0 for what is not the row's.
+    __device__ __forceinline__ void keys(int v, const uint4& r, unsigned (&k)[V]) const {
         float f[V];
-        if (at >= 0 && at + V <= vocab) {
-            unpack16<T>(*reinterpret_cast<const uint4*>(row + at), f);
+        if (v >= whole0 && v <= whole1) {
+            unpack16<T>(r, f);
         } else {
+            const int at = v * V - shift;
 #pragma unroll
-            for (int i = 0; i < V; ++i) f[i] = at + i >= 0 && at + i < vocab ? static_cast<float>(row[at + i]) : __int_as_float(0x7fffffff);
+            for (int i = 0; i < V; ++i)
+                f[i] = at + i >= 0 && at + i < vocab ? static_cast<float>(row[at + i]) : __int_as_float(0x7fffffff);
+        }
+        if (hot > 0.0f && hot != 1.0f) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) f[i] = __fdiv_rn(f[i], hot);
         }
 #pragma unroll
-        for (int i = 0; i < V; ++i) k[i] = key_of(settle(f[i]));
+        for (int i = 0; i < V; ++i) k[i] = key_of(f[i]);
     }
-    __device__ __forceinline__ void load() const {
-        if constexpr (HELD) {
-            for (int v = v0 + threadIdx.x; v < v1; v += kThreads) {
-                unsigned k[V];
-                fetch(v, k);
-#pragma unroll
-                for (int i = 0; i < V; i += 4)
-                    *reinterpret_cast<uint4*>(keys + (v - v0) * V + i) = make_uint4(k[i], k[i + 1], k[i + 2], k[i + 3]);
-            }
-        }
-    }
+    __device__ __forceinline__ void fetch(int v, unsigned (&k)[V]) const { keys(v, raw(v), k); }
     // f(key, index in the row) for the thread's values.
     template <class F>
     __device__ __forceinline__ void each(F f) const {
-        if constexpr (HELD) {
-            const int n = (v1 - v0) * V / 4;
-            for (int x = threadIdx.x; x < n; x += kThreads) {
-                const uint4 k = reinterpret_cast<const uint4*>(keys)[x];
-                const int at = v0 * V + 4 * x - shift;
-                f(k.x, at);
-                f(k.y, at + 1);
-                f(k.z, at + 2);
-                f(k.w, at + 3);
-            }
-        } else {
-            for (int v = v0 + threadIdx.x; v < v1; v += kThreads) {
-                unsigned k[V];
-                fetch(v, k);
+        for (int v = v0 + threadIdx.x; v < v1; v += kThreads * AHEAD) {
+            uint4 r[AHEAD];
 #pragma unroll
-                for (int i = 0; i < V; ++i) f(k[i], v * V + i - shift);
+            for (int a = 0; a < AHEAD; ++a) r[a] = raw(v + a * kThreads);
+#pragma unroll
+            for (int a = 0; a < AHEAD; ++a) {
+                const int x = v + a * kThreads;
+                if (x >= v1) break;
+                unsigned k[V];
+                keys(x, r[a], k);
+#pragma unroll
+                for (int i = 0; i < V; ++i) f(k[i], x * V + i - shift);
             }
         }
     }
@@ -167,6 +179,117 @@ struct Weigh {
     }
 };
 
+// The pieces of z's range, from the largest down: the first is the largest z, the last whatever is 32 and
+// more below it.
+struct Pieces {
+    unsigned top;
+    float ref, scale;
+    __device__ __forceinline__ Pieces(unsigned most, unsigned least) : top(most), ref(value_of(most)) {
+        const float range = fminf(ref - value_of(least), 32.0f);
+        scale = static_cast<float>(kDigits - 2) / range;
+    }
+    __device__ __forceinline__ int of(unsigned key) const {
+        if (key == top) return 0;
+        return 1 + static_cast<int>(fminf((ref - value_of(key)) * scale, static_cast<float>(kDigits - 2)));
+    }
+};
+
+__device__ __forceinline__ void clear(unsigned* x, int n) {
+    for (int i = threadIdx.x; i < n; i += kThreads) x[i] = 0u;
+}
+
+// Adds a weight to digit d's sum.
+__device__ __forceinline__ void add_weight(Shared& s, int d, unsigned long long w) {
+    const unsigned lo = static_cast<unsigned>(w);
+    unsigned hi = static_cast<unsigned>(w >> 32);
+    if (lo != 0u) {
+        const unsigned old = atomicAdd(&s.low[d], lo);
+        if (old + lo < old) ++hi;
+    }
+    if (hi != 0u) atomicAdd(&s.high[d], hi);
+}
+
+struct Found {
+    int digit;                            // -1: the target is not reached
+    unsigned long long above, above_weight, here, all;   // (all: counts, or weights, of all digits)
+};
+
+// The digit at which the counts (BY_WEIGHT false) or weights of the cluster's histograms reach `target`,
+// which reach(all) names.  Called once the histograms are whole (a cluster barrier); ends with one.  WITH:
+// the other sum is there too.
+template <bool BY_WEIGHT, bool WITH, class R>
+__device__ Found locate(Shared& s, int digits, unsigned long long before_all, unsigned long long before_weight,
+                        int cluster, unsigned rank, R reach) {
+    // This block's share of the digits, over all blocks.
+    const int share = digits / cluster, per = (share + kThreads - 1) / kThreads;
+    constexpr int MOST = kDigits / kThreads;
+    unsigned count[MOST];
+    unsigned long long weight[MOST], counts = 0, weights = 0;
+#pragma unroll
+    for (int j = 0; j < MOST; ++j) {
+        count[j] = 0;
+        weight[j] = 0;
+        const int x = threadIdx.x * per + j;
+        if (j >= per || x >= share) continue;
+        const int d = rank * share + x;
+        for (int r = 0; r < cluster; ++r) {
+            if (!BY_WEIGHT || WITH) count[j] += far(&s.count[d], r);
+            if (BY_WEIGHT || WITH)
+                weight[j] += (static_cast<unsigned long long>(far(&s.high[d], r)) << 32) + far(&s.low[d], r);
+        }
+        counts += count[j];
+        weights += weight[j];
+    }
+    unsigned long long all, ignored;
+    unsigned long long w = 0, c = 0;      // before this thread's digits
+    if (!BY_WEIGHT || WITH) c = block_scan<kThreads>(counts, s.scan, BY_WEIGHT ? &ignored : &all);
+    if (BY_WEIGHT || WITH) w = block_scan<kThreads>(weights, s.scan, BY_WEIGHT ? &all : &ignored);
+    if (threadIdx.x == 0) {
+        s.shown.all = all;
+        s.shown.weight = BY_WEIGHT ? all : ignored;
+        s.shown.ties = static_cast<unsigned>(BY_WEIGHT ? ignored : all);
+        s.shown.digit = -1;
+    }
+    cluster_sync();
+    Found f = {-1, 0, 0, 0, 0};
+    unsigned long long earlier_w = before_weight, earlier_c = before_all;
+    for (int r = 0; r < cluster; ++r) {
+        f.all += far(&s.shown.all, r);
+        if (r < static_cast<int>(rank)) {
+            if (BY_WEIGHT || WITH) earlier_w += far(&s.shown.weight, r);
+            if (!BY_WEIGHT || WITH) earlier_c += far(&s.shown.ties, r);
+        }
+    }
+    const unsigned long long target = reach(f.all);
+    c += earlier_c;
+    w += earlier_w;
+#pragma unroll
+    for (int j = 0; j < MOST; ++j) {
+        const int x = threadIdx.x * per + j;
+        if (j >= per || x >= share) continue;
+        const unsigned long long at = BY_WEIGHT ? w : c, mine = BY_WEIGHT ? weight[j] : count[j];
+        if (at < target && at + mine >= target) {
+            s.shown.digit = static_cast<int>(rank) * share + x;
+            s.shown.above = c;
+            s.shown.above_weight = w;
+            s.shown.here = count[j];
+        }
+        c += count[j];
+        w += weight[j];
+    }
+    cluster_sync();
+    for (int r = 0; r < cluster; ++r) {
+        const int d = far(&s.shown.digit, r);
+        if (d < 0) continue;
+        f.digit = d;
+        f.above = far(&s.shown.above, r);
+        f.above_weight = far(&s.shown.above_weight, r);
+        f.here = far(&s.shown.here, r);
+    }
+    cluster_sync();
+    return f;
+}
+
 struct Border {
     unsigned key;                         // tokens above stay, and `need` of those at it (lowest indices)
     unsigned long long need;
@@ -178,92 +301,36 @@ struct Border {
 // which the sum reaches `target`), among keys >= floor.  All blocks of the cluster; ends with a cluster
 // barrier.
 template <bool BY_WEIGHT, class P>
-__device__ Border find_border(Shared& s, const P& part, const Weigh& weigh, unsigned floor,
-                              unsigned long long target, int cluster, unsigned rank) {
+__device__ __noinline__ Border find_border(Shared& s, const P& part, const Weigh& weigh, unsigned floor,
+                                           unsigned long long target, int cluster, unsigned rank) {
     Border b = {0u, 0ull, 0ull, 0ull};
     int shift = 32;
     for (int level = 0; level < 3; ++level) {
         const int bits = level == 2 ? 10 : 11, digits = 1 << bits;
         const unsigned prefix = b.key;
         shift -= bits;
-        for (int x = threadIdx.x; x < digits; x += kThreads) s.count[x] = s.low[x] = s.high[x] = 0u;
+        clear(s.count, digits);
+        clear(s.low, digits);
+        clear(s.high, digits);
         __syncthreads();
         part.each([&](unsigned key, int) {
             if (key < floor || key <= kNone) return;
             if (level > 0 && key >> (shift + bits) != prefix) return;
             const int d = digits - 1 - static_cast<int>(key >> shift & static_cast<unsigned>(digits - 1));
-            const unsigned long long w = weigh.units(key);
             atomicAdd(&s.count[d], 1u);
-            const unsigned lo = static_cast<unsigned>(w);
-            unsigned hi = static_cast<unsigned>(w >> 32);
-            if (lo != 0u) {
-                const unsigned old = atomicAdd(&s.low[d], lo);
-                if (old + lo < old) ++hi;
-            }
-            if (hi != 0u) atomicAdd(&s.high[d], hi);
+            add_weight(s, d, weigh.units(key));
         });
         cluster_sync();
-        // This block's share of the digits, over all blocks.
-        const int share = digits / cluster, per = (share + kThreads - 1) / kThreads;
-        unsigned long long count[4], weight[4], counts = 0, weights = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            count[j] = weight[j] = 0;
-            const int x = threadIdx.x * per + j;
-            if (j >= per || x >= share) continue;
-            const int d = rank * share + x;
-            for (int r = 0; r < cluster; ++r) {
-                count[j] += far(&s.count[d], r);
-                weight[j] += (static_cast<unsigned long long>(far(&s.high[d], r)) << 32) + far(&s.low[d], r);
-            }
-            counts += count[j];
-            weights += weight[j];
+        const Found f = locate<BY_WEIGHT, true>(s, digits, b.above, b.weight, cluster, rank,
+                                                [&](unsigned long long) { return target; });
+        b.key = prefix << bits;
+        b.need = 0;
+        if (f.digit >= 0) {
+            b.key |= static_cast<unsigned>(digits - 1 - f.digit);
+            b.above = f.above;
+            b.weight = f.above_weight;
+            b.need = f.here;
         }
-        unsigned long long all_count, all_weight;
-        const unsigned long long before_count = block_scan<kThreads>(counts, s.scan, &all_count);
-        const unsigned long long before_weight = block_scan<kThreads>(weights, s.scan, &all_weight);
-        if (threadIdx.x == 0) {
-            s.shown.count = all_count;
-            s.shown.weight = all_weight;
-            s.shown.digit = -1;
-        }
-        cluster_sync();
-        if (threadIdx.x < cluster) {
-            s.in[threadIdx.x][0] = far(&s.shown.count, threadIdx.x);
-            s.in[threadIdx.x][1] = far(&s.shown.weight, threadIdx.x);
-        }
-        __syncthreads();
-        unsigned long long c = b.above, w = b.weight;
-        for (unsigned r = 0; r < rank; ++r) {
-            c += s.in[r][0];
-            w += s.in[r][1];
-        }
-        c += before_count;
-        w += before_weight;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int x = threadIdx.x * per + j;
-            if (j >= per || x >= share) continue;
-            const unsigned long long at = BY_WEIGHT ? w : c, mine = BY_WEIGHT ? weight[j] : count[j];
-            if (at < target && at + mine >= target) {
-                s.shown.digit = static_cast<int>(rank) * share + x;
-                s.shown.above_count = c;
-                s.shown.above_weight = w;
-                s.shown.here = count[j];
-            }
-            c += count[j];
-            w += weight[j];
-        }
-        cluster_sync();
-        for (int r = 0; r < cluster; ++r) {
-            const int d = far(&s.shown.digit, r);
-            if (d < 0) continue;
-            b.key = prefix << bits | static_cast<unsigned>(digits - 1 - d);
-            b.above = far(&s.shown.above_count, r);
-            b.weight = far(&s.shown.above_weight, r);
-            b.need = far(&s.shown.here, r);
-        }
-        cluster_sync();
     }
     // b.need: all tokens at the border.
     if (BY_WEIGHT) {
@@ -275,41 +342,277 @@ __device__ Border find_border(Shared& s, const P& part, const Weigh& weigh, unsi
     return b;
 }
 
-template <class T, bool HELD>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant__ SampleParams p) {
+// Of the tokens at the border, those up to the index that this returns stay.  All blocks of the cluster.
+template <class P>
+__device__ __noinline__ int limit_of(Shared& s, const P& part, const Border& border, int cluster, unsigned rank) {
+    constexpr int V = P::V;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    unsigned mine = 0;
+    part.each([&](unsigned key, int) { mine += key == border.key; });
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    if (lane == 0) s.u[warp] = mine;
+    __syncthreads();
+    if (tid == 0) {
+        unsigned n = 0;
+        for (int i = 0; i < kWarps; ++i) n += s.u[i];
+        s.shown.ties = n;
+    }
+    cluster_sync();
+    unsigned long long before = 0, here = 0;
+    for (int r = 0; r < cluster; ++r) {
+        const unsigned n = far(&s.shown.ties, r);
+        if (r < static_cast<int>(rank)) before += n;
+        else if (r == static_cast<int>(rank)) here = n;
+    }
+    int limit = part.vocab;
+    if (border.need <= before) {
+        limit = -1;
+    } else if (border.need < before + here) {
+        // Its place in this block: in the order of the indices, kThreads vectors at a time.
+        unsigned left = static_cast<unsigned>(border.need - before);
+        __syncthreads();
+        if (tid == 0) s.limit = part.vocab;
+        for (int v = part.v0; v < part.v1; v += kThreads) {
+            unsigned key[V];
+            unsigned n = 0, all;
+            const bool in = v + tid < part.v1;
+            if (in) {
+                part.fetch(v + tid, key);
+#pragma unroll
+                for (int i = 0; i < V; ++i) n += key[i] == border.key;
+            }
+            unsigned at = block_scan<kThreads>(n, reinterpret_cast<unsigned*>(s.scan), &all);
+            if (in && at < left && at + n >= left) {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (key[i] == border.key && ++at == left) s.limit = (v + tid) * V + i - part.shift;
+            }
+            if (all >= left) break;
+            left -= all;
+        }
+        __syncthreads();
+        limit = s.limit;
+    }
+    cluster_sync();
+    return limit;
+}
+
+// ---- lists ---------------------------------------------------------------------------------------
+// A listed token: key above, the index's complement below, so that falling numbers are falling z, then
+// rising indices.
+__device__ __forceinline__ unsigned long long entry_of(unsigned key, int at) {
+    return static_cast<unsigned long long>(key) << 32 | ~static_cast<unsigned>(at);
+}
+// Into the block's list.  What does not fit is counted only.
+__device__ __forceinline__ void put_in_list(Shared& s, unsigned key, int at) {
+    const unsigned n = atomicAdd(&s.shown.listed, 1u);
+    if (n < kList) s.list[n] = entry_of(key, at);
+}
+// The blocks' lists in the first one's, if they fit: their tokens in all.  Called behind a cluster barrier;
+// the others' lists are read until the next.
+__device__ __forceinline__ unsigned gather_lists(Shared& s, int cluster, unsigned rank) {
+    unsigned all = 0;
+    for (int r = 0; r < cluster; ++r) all += far(&s.shown.listed, r);
+    if (rank == 0 && all <= kList) {
+        unsigned at = s.shown.listed;
+        for (int r = 1; r < cluster; ++r) {
+            const unsigned n = far(&s.shown.listed, r);
+            for (unsigned i = threadIdx.x; i < n; i += kThreads) s.list[at + i] = far(&s.list[i], r);
+            at += n;
+        }
+        __syncthreads();
+    }
+    return all;
+}
+// Falling order of the list's n entries (a block; ends with a barrier): compare and exchange in powers of two.
+__device__ __noinline__ void sort_list(unsigned long long* list, int n) {
+    int size = 64;
+    while (size < n) size <<= 1;
+    for (int i = n + threadIdx.x; i < size; i += kThreads) list[i] = 0;
+    __syncthreads();
+    for (int run = 2; run <= size; run <<= 1) {
+        for (int step = run >> 1; step > 0; step >>= 1) {
+            for (int t = threadIdx.x; t < size / 2; t += kThreads) {
+                const int i = 2 * t - (t & (step - 1));
+                const unsigned long long a = list[i], b = list[i + step];
+                if ((a < b) == ((i & run) == 0)) {
+                    list[i] = b;
+                    list[i + step] = a;
+                }
+            }
+            // (Up to 32 apart, both of a pair are in 64 entries that one warp has.)
+            if (step > 32 || (step == 1 && run >= 64)) __syncthreads();
+            else __syncwarp();
+        }
+    }
+    __syncthreads();
+}
+
+// The best of two tokens.
+__device__ __forceinline__ void better(float x, int i, unsigned key, float* pick, int* best, unsigned* best_key) {
+    if (x > *pick || (x == *pick && i < *best)) {
+        *pick = x;
+        *best = i;
+        *best_key = key;
+    }
+}
+// The block's best token and sum, in thread 0.
+__device__ __forceinline__ void join_block(Shared& s, float* pick, int* best, unsigned* best_key, float* sum) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        const float x = __shfl_xor_sync(0xffffffffu, *pick, d);
+        const int i = __shfl_xor_sync(0xffffffffu, *best, d);
+        const unsigned u = __shfl_xor_sync(0xffffffffu, *best_key, d);
+        *sum += __shfl_xor_sync(0xffffffffu, *sum, d);
+        better(x, i, u, pick, best, best_key);
+    }
+    __syncthreads();
+    if (lane == 0) {
+        s.f[warp] = *pick;
+        s.g[warp] = *sum;
+        s.i[warp] = *best;
+        s.u[warp] = *best_key;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < kWarps; ++w) {
+            *sum += s.g[w];
+            better(s.f[w], s.i[w], s.u[w], pick, best, best_key);
+        }
+    }
+}
+__device__ __forceinline__ void put_token(const SampleParams& p, int b, const Weigh& weigh, int best, unsigned best_key,
+                                          float sum) {
+    const bool none = best == 0x7fffffff;                // (noise of NaN everywhere)
+    if (none) flag(p.status, GS_DEV_EMPTY_ROW);
+    if (p.token != nullptr) p.token[b] = none ? -1 : best;
+    if (p.logprob != nullptr)
+        p.logprob[b] = none ? kNegInf : (best_key == weigh.top ? 0.0f : value_of(best_key) - weigh.ref) - logf(sum);
+}
+
+// A token stays where the sum before it is below p of all.
+__device__ __forceinline__ unsigned long long reach_of(float top_p, unsigned long long all) {
+    const double reach = ceil(static_cast<double>(fmaxf(top_p, 0.0f)) * static_cast<double>(all));
+    return max(1ull, min(all, static_cast<unsigned long long>(reach)));
+}
+
+// The first block, with all tokens that may stay in its list: the filters and the token.
+__device__ __noinline__ void finish_list(const SampleParams& p, Shared& s, const Weigh& weigh, int b, int n, int k,
+                                         float top_p, float min_p, const float* noise) {
+    sort_list(s.list, n);
+    const int kept = k > 0 ? min(k, n) : n;
+    constexpr int PER = kList / kThreads;
+    const int per = (n + kThreads - 1) / kThreads, i0 = threadIdx.x * per;
+    unsigned long long mine = 0, all, units[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        units[j] = j < per && i0 + j < kept ? weigh.units(static_cast<unsigned>(s.list[i0 + j] >> 32)) : 0;
+        mine += units[j];
+    }
+    unsigned long long before = block_scan<kThreads>(mine, s.scan, &all);
+    const unsigned long long target = top_p < 1.0f ? reach_of(top_p, all) : ~0ull;
+    float pick = kNegInf, sum = 0.0f, z[PER];
+    int best = 0x7fffffff, at[PER];
+    unsigned best_key = 0u, key[PER];
+    bool stays[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        stays[j] = j < per && i0 + j < kept;
+        const unsigned long long e = stays[j] ? s.list[i0 + j] : 0;
+        key[j] = static_cast<unsigned>(e >> 32);
+        at[j] = static_cast<int>(~static_cast<unsigned>(e));
+        const float w = stays[j] ? weigh.weight(key[j]) : 0.0f;
+        stays[j] = stays[j] && before < target && (!(w < min_p) || key[j] == weigh.top);
+        before += units[j];
+        if (stays[j]) sum += w;
+        z[j] = stays[j] && noise != nullptr ? noise[at[j]] : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+        if (stays[j]) better(value_of(key[j]) + z[j], at[j], key[j], &pick, &best, &best_key);
+    join_block(s, &pick, &best, &best_key, &sum);
+    if (threadIdx.x == 0) put_token(p, b, weigh, best, best_key, sum);
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_constant__ SampleParams p) {
     extern __shared__ __align__(16) unsigned char raw[];
     Shared& s = *reinterpret_cast<Shared*>(raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const unsigned rank = p.cluster > 1 ? cluster_rank() : 0u;
     const int b = blockIdx.x / p.cluster;
+    if (tid == 0) s.shown.listed = 0u;
+    clear(s.count, kDigits);
     grid_wait();
     grid_trigger();
-    Part<T, HELD> part;
-    constexpr int V = Part<T, HELD>::V;
+    Part<T> part;
+    constexpr int V = Part<T>::V;
     const T* const row = static_cast<const T*>(p.logits) + b * p.row_stride;
     part.shift = static_cast<int>((reinterpret_cast<unsigned long long>(row) & 15ull) / sizeof(T));
     part.row = row;
     part.vocab = p.vocab;
-    part.keys = reinterpret_cast<unsigned*>(raw + sizeof(Shared));
     part.hot = p.temperature != nullptr ? p.temperature[b] : 1.0f;
+    const int k = p.top_k != nullptr ? p.top_k[b] : 0;
+    const float top_p = p.top_p != nullptr ? p.top_p[b] : 1.0f, min_p = p.min_p != nullptr ? p.min_p[b] : 0.0f;
     const int vectors = (p.vocab + part.shift + V - 1) / V;
     part.v0 = static_cast<int>(static_cast<long long>(vectors) * rank / p.cluster);
     part.v1 = static_cast<int>(static_cast<long long>(vectors) * (rank + 1) / p.cluster);
-    part.load();
-    __syncthreads();
-    // The largest key.
-    unsigned top = 0u;
-    part.each([&](unsigned key, int) { top = max(top, key); });
+    part.whole0 = part.shift > 0 ? 1 : 0;
+    part.whole1 = (p.vocab + part.shift) / V - 1;
+    int group = 0;                        // 2^group vectors make a group
+    while ((part.v1 - part.v0 - 1) >> group >= kGroups) ++group;
+    const int groups = part.v1 > part.v0 ? ((part.v1 - part.v0 - 1) >> group) + 1 : 0;
+    // The largest key of every group, and of the row; the smallest.
+    unsigned top = 0u, bottom = 0xffffffffu;
+    constexpr int AHEAD = Part<T>::AHEAD;
+    for (int g = tid; g < groups; g += kThreads * AHEAD) {
+        unsigned most[AHEAD] = {0u, 0u, 0u, 0u};
+        for (int x = 0; x < 1 << group; ++x) {
+            uint4 r[AHEAD];
+#pragma unroll
+            for (int a = 0; a < AHEAD; ++a) r[a] = part.raw(part.v0 + ((g + a * kThreads) << group) + x);
+#pragma unroll
+            for (int a = 0; a < AHEAD; ++a) {
+                const int v = part.v0 + ((g + a * kThreads) << group) + x;
+                if (v >= part.v1) break;
+                unsigned key[V];
+                part.keys(v, r[a], key);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    most[a] = max(most[a], key[i]);
+                    bottom = min(bottom, key[i] > kNone ? key[i] : 0xffffffffu);
+                }
+            }
+        }
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) {
+            if (g + a * kThreads < groups) s.most[g + a * kThreads] = most[a];
+            top = max(top, most[a]);
+        }
+    }
     top = __reduce_max_sync(0xffffffffu, top);
-    if (lane == 0) s.u[warp] = top;
+    bottom = __reduce_min_sync(0xffffffffu, bottom);
+    if (lane == 0) {
+        s.u[warp] = top;
+        s.v[warp] = bottom;
+    }
     __syncthreads();
     if (warp == 0) {
-        const unsigned most = __reduce_max_sync(0xffffffffu, lane < kWarps ? s.u[lane] : 0u);
-        if (lane == 0) s.shown.top = most;
+        top = __reduce_max_sync(0xffffffffu, lane < kWarps ? s.u[lane] : 0u);
+        bottom = __reduce_min_sync(0xffffffffu, lane < kWarps ? s.v[lane] : 0xffffffffu);
+        if (lane == 0) {
+            s.shown.top = top;
+            s.shown.bottom = bottom;
+        }
     }
     cluster_sync();
     top = 0u;
-    for (int r = 0; r < p.cluster; ++r) top = max(top, far(&s.shown.top, r));
+    bottom = 0xffffffffu;
+    for (int r = 0; r < p.cluster; ++r) {
+        top = max(top, far(&s.shown.top, r));
+        bottom = min(bottom, far(&s.shown.bottom, r));
+    }
     if (top <= kNone) {                   // nothing to choose from
         if (rank == 0 && tid == 0) {
             if (p.token != nullptr) p.token[b] = -1;
@@ -320,135 +623,133 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
         return;
     }
     const Weigh weigh = {top, value_of(top)};
-    const int k = p.top_k != nullptr ? p.top_k[b] : 0;
-    const float top_p = p.top_p != nullptr ? p.top_p[b] : 1.0f, min_p = p.min_p != nullptr ? p.min_p[b] : 0.0f;
-    Border border = {kNone + 1u, ~0ull, 0ull, 0ull};     // everything stays
-    if (k > 0 && k < p.vocab) {
-        const Border found = find_border<false>(s, part, weigh, 0u, static_cast<unsigned long long>(k), p.cluster, rank);
-        if (found.need > 0) border = found;              // (else fewer than k tokens can be chosen)
-    }
-    if (top_p < 1.0f) {
-        // The sum over what top-k left.
-        unsigned long long mine = 0, all;
-        part.each([&](unsigned key, int) {
-            if (key > border.key || (key == border.key && border.need == ~0ull)) mine += weigh.units(key);
-        });
-        block_scan<kThreads>(mine, s.scan, &all);
-        if (tid == 0) s.shown.weight = all;
-        cluster_sync();
-        all = 0;
-        for (int r = 0; r < p.cluster; ++r) all += far(&s.shown.weight, r);
-        cluster_sync();
-        if (border.need != ~0ull) all += border.need * weigh.units(border.key);
-        // A token stays where the sum before it is below p of all.
-        const double reach = ceil(static_cast<double>(fmaxf(top_p, 0.0f)) * static_cast<double>(all));
-        const unsigned long long target = max(1ull, min(all, static_cast<unsigned long long>(reach)));
-        const Border found = find_border<true>(s, part, weigh, border.key, target, p.cluster, rank);
-        if (found.key > border.key || (found.key == border.key && found.need < border.need)) border = found;
-    }
-    // Of the tokens at the border, those up to index `limit`.
+    const Pieces pieces(top, bottom);
+    const float* const noise = p.noise != nullptr && part.hot > 0.0f ? p.noise + b * p.noise_stride : nullptr;
+    const bool by_k = k > 0 && k < p.vocab, by_p = top_p < 1.0f;
+    unsigned border = kNone + 1u;         // the last token that stays: everything
     int limit = p.vocab;
-    if (border.need != ~0ull) {
-        unsigned mine = 0, ties;
-        part.each([&](unsigned key, int) { mine += key == border.key; });
-        ties = __reduce_add_sync(0xffffffffu, mine);
-        if (lane == 0) s.u[warp] = ties;
-        __syncthreads();
-        if (tid == 0) {
-            unsigned n = 0;
-            for (int i = 0; i < kWarps; ++i) n += s.u[i];
-            s.shown.ties = n;
+    bool known = !by_k && !by_p;
+    if (!known && (p.vocab <= kList || (by_k && k <= kMostK))) {
+        // All tokens from a z on that k tokens reach (of a short row all) to the first block.
+        int last = kDigits - 1;
+        bool some = true;
+        if (p.vocab > kList) {
+            for (int g = tid; g < groups; g += kThreads)
+                if (s.most[g] > kNone) atomicAdd(&s.count[pieces.of(s.most[g])], 1u);
+            cluster_sync();
+            const Found f = locate<false, false>(s, kDigits, 0, 0, p.cluster, rank,
+                                                 [&](unsigned long long) { return static_cast<unsigned long long>(k); });
+            if (f.digit >= 0) last = f.digit;
+            some = f.above + f.here <= kList;            // (else there are too many tokens for certain)
         }
-        cluster_sync();
-        unsigned long long before = 0, here = 0;
-        for (int r = 0; r < p.cluster; ++r) {
-            const unsigned n = far(&s.shown.ties, r);
-            if (r < static_cast<int>(rank)) before += n;
-            else if (r == static_cast<int>(rank)) here = n;
-        }
-        if (border.need <= before) {
-            limit = -1;
-        } else if (border.need < before + here) {
-            // Its place in this block: in the order of the indices, kThreads vectors at a time.
-            unsigned left = static_cast<unsigned>(border.need - before);
-            __syncthreads();
-            if (tid == 0) s.limit = p.vocab;
-            for (int v = part.v0; v < part.v1; v += kThreads) {
+        for (int g = tid; g < groups; g += kThreads) {
+            if (!some || s.most[g] <= kNone || pieces.of(s.most[g]) > last) continue;
+            for (int x = 0; x < 1 << group; ++x) {
+                const int v = part.v0 + (g << group) + x;
+                if (v >= part.v1) break;
                 unsigned key[V];
-                unsigned n = 0;
-                const bool in = v + tid < part.v1;
-                if (in) {
-                    if constexpr (HELD) {
+                part.fetch(v, key);
 #pragma unroll
-                        for (int i = 0; i < V; ++i) key[i] = part.keys[(v + tid - part.v0) * V + i];
-                    } else {
-                        part.fetch(v + tid, key);
-                    }
-#pragma unroll
-                    for (int i = 0; i < V; ++i) n += key[i] == border.key;
-                }
-                unsigned all;
-                unsigned at = block_scan<kThreads>(n, reinterpret_cast<unsigned*>(s.scan), &all);
-                if (in && at < left && at + n >= left) {
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        if (key[i] == border.key && ++at == left) s.limit = (v + tid) * V + i - part.shift;
-                }
-                if (all >= left) break;
-                left -= all;
+                for (int i = 0; i < V; ++i)
+                    if (key[i] > kNone && pieces.of(key[i]) <= last) put_in_list(s, key[i], v * V + i - part.shift);
             }
-            __syncthreads();
-            limit = s.limit;
         }
         cluster_sync();
+        const unsigned n = gather_lists(s, p.cluster, rank);
+        if (some && n <= kList) {
+            if (rank == 0) finish_list(p, s, weigh, b, static_cast<int>(n), by_k ? k : 0, top_p, min_p, noise);
+            cluster_sync();               // (lists stay until they are read)
+            return;
+        }
+        cluster_sync();
+        if (tid == 0) s.shown.listed = 0u;
+    }
+    if (!known && !by_k) {
+        // The piece in which the weights reach top_p of their sum; its tokens to the first block.
+        clear(s.low, kDigits);
+        clear(s.high, kDigits);
+        __syncthreads();
+        part.each([&](unsigned key, int) {
+            if (key > kNone) add_weight(s, pieces.of(key), weigh.units(key));
+        });
+        cluster_sync();
+        unsigned long long target = 0;
+        const Found f = locate<true, false>(s, kDigits, 0, 0, p.cluster, rank, [&](unsigned long long all) {
+            return target = reach_of(top_p, all);
+        });
+        part.each([&](unsigned key, int at) {
+            if (key > kNone && pieces.of(key) == f.digit) put_in_list(s, key, at);
+        });
+        cluster_sync();
+        const unsigned n = gather_lists(s, p.cluster, rank);
+        if (n <= kList) {
+            known = true;
+            if (rank == 0) {
+                sort_list(s.list, n);
+                constexpr int PER = kList / kThreads;
+                const int per = (static_cast<int>(n) + kThreads - 1) / kThreads, i0 = tid * per;
+                unsigned long long mine = 0, all, units[PER];
+#pragma unroll
+                for (int j = 0; j < PER; ++j) {
+                    units[j] = j < per && i0 + j < static_cast<int>(n) ? weigh.units(static_cast<unsigned>(s.list[i0 + j] >> 32)) : 0;
+                    mine += units[j];
+                }
+                unsigned long long before = f.above_weight + block_scan<kThreads>(mine, s.scan, &all);
+#pragma unroll
+                for (int j = 0; j < PER; ++j) {
+                    if (units[j] > 0 && before < target && before + units[j] >= target) {
+                        s.shown.border = static_cast<unsigned>(s.list[i0 + j] >> 32);
+                        s.shown.limit = static_cast<int>(~static_cast<unsigned>(s.list[i0 + j]));
+                    }
+                    before += units[j];
+                }
+            }
+            cluster_sync();
+            border = far(&s.shown.border, 0);
+            limit = far(&s.shown.limit, 0);
+        }
+        cluster_sync();
+    }
+    if (!known) {
+        Border last = {border, ~0ull, 0ull, 0ull};
+        if (by_k) {
+            const Border found = find_border<false>(s, part, weigh, 0u, static_cast<unsigned long long>(k), p.cluster, rank);
+            if (found.need > 0) last = found;            // (else fewer than k tokens can be chosen)
+        }
+        if (by_p) {
+            // The sum over what top-k left.
+            unsigned long long mine = 0, all;
+            part.each([&](unsigned key, int) {
+                if (key > last.key || (key == last.key && last.need == ~0ull)) mine += weigh.units(key);
+            });
+            block_scan<kThreads>(mine, s.scan, &all);
+            if (tid == 0) s.shown.weight = all;
+            cluster_sync();
+            all = 0;
+            for (int r = 0; r < p.cluster; ++r) all += far(&s.shown.weight, r);
+            cluster_sync();
+            if (last.need != ~0ull) all += last.need * weigh.units(last.key);
+            const Border found = find_border<true>(s, part, weigh, last.key, reach_of(top_p, all), p.cluster, rank);
+            if (found.key > last.key || (found.key == last.key && found.need < last.need)) last = found;
+        }
+        border = last.key;
+        if (last.need != ~0ull) limit = limit_of(s, part, last, p.cluster, rank);
     }
     // The token, and the weights of what stays.
-    const float* const noise = p.noise != nullptr && part.hot > 0.0f ? p.noise + b * p.noise_stride : nullptr;
     float pick = kNegInf, sum = 0.0f, rest = 0.0f;       // (sum - rest: what rounding left out is kept)
     int best = 0x7fffffff;
     unsigned best_key = 0u;
     part.each([&](unsigned key, int at) {
-        if (key < border.key || key <= kNone || (key == border.key && at > limit)) return;
+        if (key < border || key <= kNone || (key == border && at > limit)) return;
         const float w = weigh.weight(key);
         if (w < min_p && key != top) return;
         const float y = w - rest, t = sum + y;
         rest = (t - sum) - y;
         sum = t;
-        const float x = noise != nullptr ? value_of(key) + noise[at] : value_of(key);
-        if (x > pick || (x == pick && at < best)) {
-            pick = x;
-            best = at;
-            best_key = key;
-        }
+        better(noise != nullptr ? value_of(key) + noise[at] : value_of(key), at, key, &pick, &best, &best_key);
     });
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        const float x = __shfl_xor_sync(0xffffffffu, pick, d);
-        const int i = __shfl_xor_sync(0xffffffffu, best, d);
-        const unsigned u = __shfl_xor_sync(0xffffffffu, best_key, d);
-        sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        if (x > pick || (x == pick && i < best)) {
-            pick = x;
-            best = i;
-            best_key = u;
-        }
-    }
-    if (lane == 0) {
-        s.f[warp] = pick;
-        s.g[warp] = sum;
-        s.i[warp] = best;
-        s.u[warp] = best_key;
-    }
-    __syncthreads();
+    join_block(s, &pick, &best, &best_key, &sum);
     if (tid == 0) {
-        for (int w = 1; w < kWarps; ++w) {
-            sum += s.g[w];
-            if (s.f[w] > pick || (s.f[w] == pick && s.i[w] < best)) {
-                pick = s.f[w];
-                best = s.i[w];
-                best_key = s.u[w];
-            }
-        }
         s.shown.pick = pick;
         s.shown.sum = sum;
         s.shown.best = best;
@@ -457,51 +758,27 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     cluster_sync();
     if (rank == 0 && tid == 0) {
         for (int r = 1; r < p.cluster; ++r) {
-            const float x = far(&s.shown.pick, r);
-            const int i = far(&s.shown.best, r);
             sum += far(&s.shown.sum, r);
-            if (x > pick || (x == pick && i < best)) {
-                pick = x;
-                best = i;
-                best_key = far(&s.shown.best_key, r);
-            }
+            better(far(&s.shown.pick, r), far(&s.shown.best, r), far(&s.shown.best_key, r), &pick, &best, &best_key);
         }
-        const bool none = best == 0x7fffffff;            // (noise of NaN everywhere)
-        if (none) flag(p.status, GS_DEV_EMPTY_ROW);
-        if (p.token != nullptr) p.token[b] = none ? -1 : best;
-        if (p.logprob != nullptr)
-            p.logprob[b] = none ? kNegInf : (best_key == top ? 0.0f : value_of(best_key) - weigh.ref) - logf(sum);
+        put_token(p, b, weigh, best, best_key, sum);
     }
     cluster_sync();                       // (what rank 0 read stays until it is read)
 }
 
-struct Plan {
-    int cluster, held;
-};
-
-// Blocks of a row: enough of them for every SM, but no part below 2048 tokens; more where a part would not
-// fit in shared memory, and where it does not fit with eight, parts are read again for each pass.
-Plan plan_of(const gs_sample_args* a) {
-    const long long most = (227 * 1024 - static_cast<long long>(sizeof(Shared))) / 4 - 64;
-    Plan plan = {1, 0};
-    while (plan.cluster < kMaxCluster &&
-           (a->vocab / plan.cluster > most ||
-            (a->vocab / plan.cluster >= 4096 && static_cast<long long>(a->batch) * plan.cluster < 2ll * sm_count())))
-        plan.cluster *= 2;
-    const long long part = (a->vocab + 16ll) / plan.cluster + 32;
-    plan.held = part <= most ? static_cast<int>(part / 8 * 8) : 0;
-    return plan;
+// Blocks of a row: enough of them for every SM, but no part below 4096 tokens.
+int cluster_of(const gs_sample_args* a) {
+    int n = 1;
+    while (n < kMaxCluster && a->vocab / n >= 8192 && static_cast<long long>(a->batch) * n < 4ll * sm_count()) n *= 2;
+    return n;
 }
 
 template <class T>
 gs_status launch_type(const SampleParams& p, gs_stream stream) {
     const dim3 grid(static_cast<unsigned>(p.batch) * p.cluster);
-    const int bytes = static_cast<int>(sizeof(Shared)) + 4 * p.held;
-    if (p.held > 0) {
-        if (!allow_smem<sample_kernel<T, true>>(bytes)) return GS_ERR_CUDA;
-        return launch(sample_kernel<T, true>, grid, kThreads, bytes, p.cluster, stream, p);
-    }
-    return launch(sample_kernel<T, false>, grid, kThreads, bytes, p.cluster, stream, p);
+    constexpr int bytes = static_cast<int>(sizeof(Shared));
+    if (!allow_smem<sample_kernel<T>>(bytes)) return GS_ERR_CUDA;
+    return launch(sample_kernel<T>, grid, kThreads, bytes, p.cluster, stream, p);
 }
 
 }  // namespace
@@ -519,12 +796,10 @@ extern "C" gs_status gs_sample(const gs_sample_args* a, gs_stream stream) {
         a->noise_stride < 0 || !aligned(a->temperature, 4) || !aligned(a->top_k, 4) || !aligned(a->top_p, 4) ||
         !aligned(a->min_p, 4) || !aligned(a->noise, 4) || !aligned(a->token, 4) || !aligned(a->logprob, 4))
         return GS_ERR_INVALID_ARG;
-    const Plan plan = plan_of(a);
     SampleParams p = {};
     p.batch = a->batch;
     p.vocab = a->vocab;
-    p.cluster = plan.cluster;
-    p.held = plan.held;
+    p.cluster = cluster_of(a);
     p.logits = a->logits;
     p.row_stride = a->batch > 1 ? a->row_stride : 0;
     p.temperature = a->temperature;
