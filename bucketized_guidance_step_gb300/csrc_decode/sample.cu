@@ -1,14 +1,16 @@
 // Sampling (sm_103a): temperature, top-k, top-p, min-p and the token from given random numbers.
 //
 // What the filters keep is a beginning of the row's tokens in the order of falling z (ties: rising
-// index), so it is known by its last token.  A row is a cluster's; each block streams its part once and
-// keeps the largest key of every 16-byte vector (keys are 32-bit numbers in the order of z).  Then
-//   with top-k: a histogram of these largest keys, over 2048 equal pieces of z's range, finds a z that at
-//     least k vectors reach, so at least k tokens do, and hardly more.  Only vectors that reach it are read
-//     again, and their tokens above it, a list of somewhat over k, go to the first block, which sorts them
-//     and has all it needs: the k-th token, the weights' sum, where top-p ends, min-p, the token.
+// index), so it is known by its last token.  A row is a cluster's; each block brings its part into shared
+// memory once (a part too large is read again for each pass).  Then
+//   with top-k: a histogram of the largest z of every 16-byte vector, over 2048 equal pieces of z's range,
+//     finds a z that at least k vectors reach, so at least k tokens do, and hardly more.  The tokens above
+//     it, a list of somewhat over k, go to the first block, which sorts them and has all it needs: the k-th
+//     token, the weights' sum, where top-p ends, min-p, the token.
 //   with top-p alone: a histogram of the weights finds the piece of z's range in which they reach p of
 //     their sum, and the tokens of that piece alone are listed and sorted; a last pass takes what is kept.
+//     (To list the first 1024 tokens as with top-k, and look whether they reach p, took longer: 28 us
+//     against 26 for a row of 16384 where they do, 74 against 53 for 128 rows of 32000 where not.)
 //   with neither, the last pass alone.
 // Where a list would be longer than its place (many tokens of one z; k over 1024), the last token is found
 // digit by digit in the keys instead: histograms of 2048, 2048 and 1024 digits count the tokens or sum
@@ -23,15 +25,15 @@
 namespace gs_decode {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32, kDigits = 2048;
+constexpr int kThreads = 512, kWarps = kThreads / 32, kDigits = 2048;
 constexpr int kMaxCluster = 8;
-constexpr int kGroups = 4096;             // groups of vectors of a block, of which the largest key is kept
+constexpr int kHeld = 66 * 1024;          // bytes of a row that a block holds: two blocks an SM
 constexpr int kList = 2048, kMostK = 1024;               // tokens of a list; largest top-k that goes by one
-constexpr unsigned kNone = 0x007fffffu;   // the key of -inf: such tokens, and NaN, are not kept
+constexpr unsigned kNone = 0x007fffffu;   // the key of -inf: such tokens are not kept
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct SampleParams {
-    int batch, vocab, cluster;
+    int batch, vocab, cluster, held;      // held: the blocks hold their parts
     const void* logits;
     long long row_stride;
     const float* temperature;
@@ -57,7 +59,7 @@ struct Shown {
     unsigned ties;                        // tokens at the border
     float pick, sum;                      // best token of the block, and the weights it keeps
     int best;
-    unsigned best_key;
+    float best_z;
     unsigned long long weight;
 };
 
@@ -68,10 +70,8 @@ struct alignas(16) Shared {
             unsigned low[kDigits], high[kDigits];
         };
     };
-    unsigned most[kGroups];
     unsigned count[kDigits];
     unsigned long long scan[kWarps + 1];
-    unsigned long long in[kMaxCluster];
     float f[kWarps], g[kWarps];
     int i[kWarps];
     unsigned u[kWarps], v[kWarps];
@@ -85,11 +85,11 @@ __device__ __forceinline__ float pow2(float x) {
     return y;
 }
 
-// Keys rise with z; NaN is below everything.
+// Keys rise with z (which is not NaN).
 __device__ __forceinline__ unsigned key_of(float z) {
     z += 0.0f;                            // -0 is 0
     const unsigned u = __float_as_uint(z);
-    return z != z ? 0u : u ^ (static_cast<unsigned>(static_cast<int>(u) >> 31) | 0x80000000u);
+    return u ^ (static_cast<unsigned>(static_cast<int>(u) >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float value_of(unsigned key) {
     return __uint_as_float(key ^ ((key >> 31) != 0u ? 0x80000000u : 0xffffffffu));
@@ -112,85 +112,152 @@ __device__ __forceinline__ V far(const V* local, unsigned r) {
     }
 }
 
+// A row's divisor.  Where it is usual, a product with the rounded reciprocal and one correction by its
+// remainder is the correctly rounded quotient of numbers that are neither huge nor tiny (P. Markstein,
+// Computation of elementary functions on the IBM RISC System/6000 processor, 1990); infinities and NaN stay.
+struct Divisor {
+    float by, inverse;
+    bool one, usual;
+    __device__ __forceinline__ explicit Divisor(float t) : by(t > 0.0f ? t : 1.0f), inverse(1.0f / by) {
+        one = by == 1.0f;
+        usual = by >= 0x1p-30f && by <= 0x1p30f;
+    }
+    template <int V>
+    __device__ __forceinline__ void divide(float (&z)[V], bool any_size) const {
+        if (one) return;
+        bool odd = !usual;
+        if (any_size) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const unsigned size = __float_as_uint(z[i]) & 0x7fffffffu;           // not 0, below 2^-60; from 2^96 on
+                odd = odd || size - 1u < 0x217fffffu || (size >= 0x6f800000u && size < 0x7f800000u);
+            }
+        }
+        if (!odd) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float q = z[i] * inverse, r = fmaf(fmaf(-q, by, z[i]), inverse, q);
+                z[i] = fabsf(q) < __builtin_huge_valf() ? r : q;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) z[i] = __fdiv_rn(z[i], by);
+        }
+    }
+    __device__ __forceinline__ float of(float z) const {
+        float x[1] = {z};
+        divide<1>(x, true);
+        return x[0];
+    }
+};
+
+// 16 bytes from global to shared memory.
+__device__ __forceinline__ void copy16(void* to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<unsigned>(__cvta_generic_to_shared(to))),
+                 "l"(from)
+                 : "memory");
+}
+
 // A block's part of its row: vectors v0 .. v1 - 1, counted from the 16-byte vector that holds the row's
-// first value.
+// first value.  A thread has every kThreads-th.
 template <class T>
 struct Part {
-    static constexpr int V = 16 / static_cast<int>(sizeof(T)), AHEAD = 4;    // values; vectors in flight
+    static constexpr int V = 16 / static_cast<int>(sizeof(T));       // values of a vector
     const T* row;
+    const uint4* from;                    // vector 0: in shared memory (held) or the row's
     int shift, vocab, v0, v1;             // values of the first vector that are not the row's
     int whole0, whole1;                   // vectors that are the row's entirely: whole0 .. whole1
-    float hot;
+    Divisor cool;
 
-    __device__ __forceinline__ uint4 raw(int v) const {              // (any vector, read only if whole)
-        const int at = min(max(v, whole0), whole1);
-        return whole0 <= whole1 ? *reinterpret_cast<const uint4*>(row + static_cast<long long>(at) * V - shift)
-                                : make_uint4(0u, 0u, 0u, 0u);
+    __device__ __forceinline__ void hold(uint4* place) {
+        const uint4* const far = reinterpret_cast<const uint4*>(row - shift);
+        for (int v = v0 + threadIdx.x; v < v1; v += kThreads)
+            if (v >= whole0 && v <= whole1) copy16(place + (v - v0), far + v);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        from = place - v0;                // (a thread reads what it has copied itself)
     }
-    // The keys of vector v, of which `r` is raw(v); 0 for what is not the row's.
-    __device__ __forceinline__ void keys(int v, const uint4& r, unsigned (&k)[V]) const {
-        float f[V];
+    // The largest logit of vector v as it is (a quotient's order is that of the logits); -inf for none.
+    __device__ __forceinline__ float most(int v) const {
+        if (v < whole0 || v > whole1) {
+            float m = kNegInf;
+#pragma unroll 1
+            for (int i = max(0, v * V - shift); i < min(vocab, (v + 1) * V - shift); ++i) m = fmaxf(m, static_cast<float>(row[i]));
+            return m;
+        }
+        const uint4 r = from[v];
+        if constexpr (sizeof(T) == 4) {
+            return fmaxf(fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)),
+                               fmaxf(__uint_as_float(r.z), __uint_as_float(r.w))), kNegInf);
+        } else {
+            using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+            const T2 m = __hmax2(__hmax2(*reinterpret_cast<const T2*>(&r.x), *reinterpret_cast<const T2*>(&r.y)),
+                                 __hmax2(*reinterpret_cast<const T2*>(&r.z), *reinterpret_cast<const T2*>(&r.w)));
+            return fmaxf(fmaxf(static_cast<float>(m.x), static_cast<float>(m.y)), kNegInf);
+        }
+    }
+    __device__ __forceinline__ float most_z(int v) const { return cool.of(most(v)); }
+    // z of vector v; -inf for NaN and what is not the row's.
+    __device__ __forceinline__ void values(int v, float (&z)[V]) const {
         if (v >= whole0 && v <= whole1) {
-            unpack16<T>(r, f);
+            unpack16<T>(from[v], z);
         } else {
             const int at = v * V - shift;
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                f[i] = at + i >= 0 && at + i < vocab ? static_cast<float>(row[at + i]) : __int_as_float(0x7fffffff);
+                z[i] = at + i >= 0 && at + i < vocab ? static_cast<float>(row[at + i]) : kNegInf;
         }
-        if (hot > 0.0f && hot != 1.0f) {
+        cool.divide<V>(z, !std::is_same<T, __half>::value);          // (fp16 has no numbers of odd size)
 #pragma unroll
-            for (int i = 0; i < V; ++i) f[i] = __fdiv_rn(f[i], hot);
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i) k[i] = key_of(f[i]);
+        for (int i = 0; i < V; ++i) z[i] = fmaxf(z[i], kNegInf);
     }
-    __device__ __forceinline__ void fetch(int v, unsigned (&k)[V]) const { keys(v, raw(v), k); }
-    // f(key, index in the row) for the thread's values.
+    // f(z, index in the row of the first) for the thread's vectors that are wanted.
+    template <class W, class F>
+    __device__ __forceinline__ void vectors(W wanted, F f) const {
+#pragma unroll 1
+        for (int v = v0 + threadIdx.x; v < v1; v += kThreads) {
+            if (!wanted(v)) continue;
+            float z[V];
+            values(v, z);
+            f(z, v * V - shift);
+        }
+    }
+    // f(z, index in the row) for the thread's values.
     template <class F>
     __device__ __forceinline__ void each(F f) const {
-        for (int v = v0 + threadIdx.x; v < v1; v += kThreads * AHEAD) {
-            uint4 r[AHEAD];
+        vectors([](int) { return true; }, [&](const float (&z)[V], int at) {
 #pragma unroll
-            for (int a = 0; a < AHEAD; ++a) r[a] = raw(v + a * kThreads);
-#pragma unroll
-            for (int a = 0; a < AHEAD; ++a) {
-                const int x = v + a * kThreads;
-                if (x >= v1) break;
-                unsigned k[V];
-                keys(x, r[a], k);
-#pragma unroll
-                for (int i = 0; i < V; ++i) f(k[i], x * V + i - shift);
-            }
-        }
+            for (int i = 0; i < V; ++i) f(z[i], at + i);
+        });
     }
 };
 
 // Weights relative to the largest.
 struct Weigh {
-    unsigned top;
     float ref;
-    __device__ __forceinline__ float weight(unsigned key) const {
-        return key == top ? 1.0f : pow2((value_of(key) - ref) * kLog2e);
+    __device__ __forceinline__ float weight(float z) const { return z == ref ? 1.0f : pow2((z - ref) * kLog2e); }
+    // In units of 2^-40, cut: 2^-8 in the upper word (two conversions to 32 bits, cheaper than one to 64).
+    static __device__ __forceinline__ void words_of(float w, unsigned* low, unsigned* high) {
+        const float a = w * 256.0f;
+        *high = static_cast<unsigned>(a);
+        *low = static_cast<unsigned>((a - static_cast<float>(*high)) * 4294967296.0f);
     }
-    // In units of 2^-40, rounded.
-    __device__ __forceinline__ unsigned long long units(unsigned key) const {
-        return __float2ull_rn(weight(key) * 1099511627776.0f);
+    __device__ __forceinline__ unsigned long long units(float z) const {
+        unsigned low, high;
+        words_of(weight(z), &low, &high);
+        return static_cast<unsigned long long>(high) << 32 | low;
     }
 };
 
-// The pieces of z's range, from the largest down: the first is the largest z, the last whatever is 32 and
-// more below it.
+// The pieces of z's range, from the largest down: the first is the largest z, the last whatever is `range`
+// and more below it.
 struct Pieces {
-    unsigned top;
     float ref, scale;
-    __device__ __forceinline__ Pieces(unsigned most, unsigned least) : top(most), ref(value_of(most)) {
-        const float range = fminf(ref - value_of(least), 32.0f);
-        scale = static_cast<float>(kDigits - 2) / range;
-    }
-    __device__ __forceinline__ int of(unsigned key) const {
-        if (key == top) return 0;
-        return 1 + static_cast<int>(fminf((ref - value_of(key)) * scale, static_cast<float>(kDigits - 2)));
+    __device__ __forceinline__ Pieces(float top, float range)
+        : ref(top), scale(static_cast<float>(kDigits - 2) / range) {}
+    __device__ __forceinline__ int of(float z) const {
+        // (The sum's last bits are the nearest whole number.)
+        const float x = fminf((ref - z) * scale, static_cast<float>(kDigits - 2)) + 8388608.0f;
+        return z == ref ? 0 : 1 + (__float_as_int(x) & (kDigits - 1));
     }
 };
 
@@ -209,19 +276,25 @@ __device__ __forceinline__ void add_weight(Shared& s, int d, unsigned long long 
     if (hi != 0u) atomicAdd(&s.high[d], hi);
 }
 
+__device__ __forceinline__ unsigned long long warp_sum(unsigned long long x) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    return x;
+}
+
 struct Found {
     int digit;                            // -1: the target is not reached
     unsigned long long above, above_weight, here, all;   // (all: counts, or weights, of all digits)
 };
 
 // The digit at which the counts (BY_WEIGHT false) or weights of the cluster's histograms reach `target`,
-// which reach(all) names.  Called once the histograms are whole (a cluster barrier); ends with one.  WITH:
-// the other sum is there too.
+// which reach(all) names.  Called once the histograms are whole (a cluster barrier); nobody reads them
+// afterwards, and what the blocks show stays until the next barrier.  WITH: the other sum is there too.
 template <bool BY_WEIGHT, bool WITH, class R>
 __device__ Found locate(Shared& s, int digits, unsigned long long before_all, unsigned long long before_weight,
                         int cluster, unsigned rank, R reach) {
     // This block's share of the digits, over all blocks.
-    const int share = digits / cluster, per = (share + kThreads - 1) / kThreads;
+    const int share = digits / cluster, per = (share + kThreads - 1) / kThreads, lane = threadIdx.x & 31;
     constexpr int MOST = kDigits / kThreads;
     unsigned count[MOST];
     unsigned long long weight[MOST], counts = 0, weights = 0;
@@ -232,10 +305,17 @@ __device__ Found locate(Shared& s, int digits, unsigned long long before_all, un
         const int x = threadIdx.x * per + j;
         if (j >= per || x >= share) continue;
         const int d = rank * share + x;
-        for (int r = 0; r < cluster; ++r) {
-            if (!BY_WEIGHT || WITH) count[j] += far(&s.count[d], r);
-            if (BY_WEIGHT || WITH)
-                weight[j] += (static_cast<unsigned long long>(far(&s.high[d], r)) << 32) + far(&s.low[d], r);
+        unsigned n[kMaxCluster], lo[kMaxCluster], hi[kMaxCluster];   // (asked for together)
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+            n[r] = (!BY_WEIGHT || WITH) && r < cluster ? far(&s.count[d], r) : 0u;
+            lo[r] = (BY_WEIGHT || WITH) && r < cluster ? far(&s.low[d], r) : 0u;
+            hi[r] = (BY_WEIGHT || WITH) && r < cluster ? far(&s.high[d], r) : 0u;
+        }
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+            count[j] += n[r];
+            weight[j] += (static_cast<unsigned long long>(hi[r]) << 32) + lo[r];
         }
         counts += count[j];
         weights += weight[j];
@@ -252,14 +332,13 @@ __device__ Found locate(Shared& s, int digits, unsigned long long before_all, un
     }
     cluster_sync();
     Found f = {-1, 0, 0, 0, 0};
-    unsigned long long earlier_w = before_weight, earlier_c = before_all;
-    for (int r = 0; r < cluster; ++r) {
-        f.all += far(&s.shown.all, r);
-        if (r < static_cast<int>(rank)) {
-            if (BY_WEIGHT || WITH) earlier_w += far(&s.shown.weight, r);
-            if (!BY_WEIGHT || WITH) earlier_c += far(&s.shown.ties, r);
-        }
-    }
+    const bool other = lane < cluster, earlier = lane < static_cast<int>(rank);
+    const unsigned long long theirs = other ? far(&s.shown.all, lane) : 0ull;
+    const unsigned long long their_w = other && WITH ? far(&s.shown.weight, lane) : BY_WEIGHT ? theirs : 0ull;
+    const unsigned long long their_c = other && WITH ? far(&s.shown.ties, lane) : BY_WEIGHT ? 0ull : theirs;
+    f.all = warp_sum(theirs);
+    const unsigned long long earlier_w = before_weight + (BY_WEIGHT || WITH ? warp_sum(earlier ? their_w : 0ull) : 0ull);
+    const unsigned long long earlier_c = before_all + (!BY_WEIGHT || WITH ? warp_sum(earlier ? their_c : 0ull) : 0ull);
     const unsigned long long target = reach(f.all);
     c += earlier_c;
     w += earlier_w;
@@ -278,15 +357,15 @@ __device__ Found locate(Shared& s, int digits, unsigned long long before_all, un
         w += weight[j];
     }
     cluster_sync();
-    for (int r = 0; r < cluster; ++r) {
-        const int d = far(&s.shown.digit, r);
-        if (d < 0) continue;
-        f.digit = d;
+    const int d = other ? far(&s.shown.digit, lane) : -1;
+    const unsigned has = __ballot_sync(0xffffffffu, d >= 0);
+    if (has != 0u) {
+        const unsigned r = __ffs(has) - 1;
+        f.digit = __shfl_sync(0xffffffffu, d, r);
         f.above = far(&s.shown.above, r);
         f.above_weight = far(&s.shown.above_weight, r);
         f.here = far(&s.shown.here, r);
     }
-    cluster_sync();
     return f;
 }
 
@@ -313,14 +392,15 @@ __device__ __noinline__ Border find_border(Shared& s, const P& part, const Weigh
         clear(s.low, digits);
         clear(s.high, digits);
         __syncthreads();
-        part.each([&](unsigned key, int) {
+        part.each([&](float z, int) {
+            const unsigned key = key_of(z);
             if (key < floor || key <= kNone) return;
             if (level > 0 && key >> (shift + bits) != prefix) return;
             const int d = digits - 1 - static_cast<int>(key >> shift & static_cast<unsigned>(digits - 1));
             atomicAdd(&s.count[d], 1u);
-            add_weight(s, d, weigh.units(key));
+            add_weight(s, d, weigh.units(z));
         });
-        cluster_sync();
+        cluster_sync();                   // (also: what the last level has shown is read)
         const Found f = locate<BY_WEIGHT, true>(s, digits, b.above, b.weight, cluster, rank,
                                                 [&](unsigned long long) { return target; });
         b.key = prefix << bits;
@@ -332,9 +412,10 @@ __device__ __noinline__ Border find_border(Shared& s, const P& part, const Weigh
             b.need = f.here;
         }
     }
+    cluster_sync();
     // b.need: all tokens at the border.
     if (BY_WEIGHT) {
-        const unsigned long long one = weigh.units(b.key), left = target - b.weight;
+        const unsigned long long one = weigh.units(value_of(b.key)), left = target - b.weight;
         if (one > 0) b.need = min(b.need, (left + one - 1) / one);
     } else {
         b.need = min(b.need, target - b.above);
@@ -348,7 +429,8 @@ __device__ __noinline__ int limit_of(Shared& s, const P& part, const Border& bor
     constexpr int V = P::V;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     unsigned mine = 0;
-    part.each([&](unsigned key, int) { mine += key == border.key; });
+    const float edge = value_of(border.key);
+    part.each([&](float z, int) { mine += z == edge; });
     mine = __reduce_add_sync(0xffffffffu, mine);
     if (lane == 0) s.u[warp] = mine;
     __syncthreads();
@@ -358,12 +440,9 @@ __device__ __noinline__ int limit_of(Shared& s, const P& part, const Border& bor
         s.shown.ties = n;
     }
     cluster_sync();
-    unsigned long long before = 0, here = 0;
-    for (int r = 0; r < cluster; ++r) {
-        const unsigned n = far(&s.shown.ties, r);
-        if (r < static_cast<int>(rank)) before += n;
-        else if (r == static_cast<int>(rank)) here = n;
-    }
+    const unsigned ties = lane < cluster ? far(&s.shown.ties, lane) : 0u;
+    const unsigned long long before = __reduce_add_sync(0xffffffffu, lane < static_cast<int>(rank) ? ties : 0u);
+    const unsigned long long here = __shfl_sync(0xffffffffu, ties, rank);
     int limit = part.vocab;
     if (border.need <= before) {
         limit = -1;
@@ -373,19 +452,19 @@ __device__ __noinline__ int limit_of(Shared& s, const P& part, const Border& bor
         __syncthreads();
         if (tid == 0) s.limit = part.vocab;
         for (int v = part.v0; v < part.v1; v += kThreads) {
-            unsigned key[V];
+            float z[V];
             unsigned n = 0, all;
             const bool in = v + tid < part.v1;
             if (in) {
-                part.fetch(v + tid, key);
+                part.values(v + tid, z);
 #pragma unroll
-                for (int i = 0; i < V; ++i) n += key[i] == border.key;
+                for (int i = 0; i < V; ++i) n += z[i] == edge;
             }
             unsigned at = block_scan<kThreads>(n, reinterpret_cast<unsigned*>(s.scan), &all);
             if (in && at < left && at + n >= left) {
 #pragma unroll
                 for (int i = 0; i < V; ++i)
-                    if (key[i] == border.key && ++at == left) s.limit = (v + tid) * V + i - part.shift;
+                    if (z[i] == edge && ++at == left) s.limit = (v + tid) * V + i - part.shift;
             }
             if (all >= left) break;
             left -= all;
@@ -404,91 +483,155 @@ __device__ __forceinline__ unsigned long long entry_of(unsigned key, int at) {
     return static_cast<unsigned long long>(key) << 32 | ~static_cast<unsigned>(at);
 }
 // Into the block's list.  What does not fit is counted only.
-__device__ __forceinline__ void put_in_list(Shared& s, unsigned key, int at) {
+__device__ __forceinline__ void put_in_list(Shared& s, float z, int at) {
     const unsigned n = atomicAdd(&s.shown.listed, 1u);
-    if (n < kList) s.list[n] = entry_of(key, at);
+    if (n < kList) s.list[n] = entry_of(key_of(z), at);
 }
 // The blocks' lists in the first one's, if they fit: their tokens in all.  Called behind a cluster barrier;
 // the others' lists are read until the next.
 __device__ __forceinline__ unsigned gather_lists(Shared& s, int cluster, unsigned rank) {
-    unsigned all = 0;
-    for (int r = 0; r < cluster; ++r) all += far(&s.shown.listed, r);
+    if (cluster == 1) return s.shown.listed;
+    const int lane = threadIdx.x & 31;
+    const unsigned mine = lane < cluster ? far(&s.shown.listed, lane) : 0u;
+    unsigned upto = mine;
+#pragma unroll
+    for (int d = 1; d < kMaxCluster; d <<= 1) {
+        const unsigned o = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += o;
+    }
+    const unsigned all = __shfl_sync(0xffffffffu, upto, kMaxCluster - 1);
     if (rank == 0 && all <= kList) {
-        unsigned at = s.shown.listed;
-        for (int r = 1; r < cluster; ++r) {
-            const unsigned n = far(&s.shown.listed, r);
-            for (unsigned i = threadIdx.x; i < n; i += kThreads) s.list[at + i] = far(&s.list[i], r);
-            at += n;
+        const unsigned own = __shfl_sync(0xffffffffu, mine, 0);
+        for (unsigned base = own; base < all; base += kThreads) {
+            const unsigned i = base + threadIdx.x;
+            unsigned r = 0, at = 0;       // entry i's block, and the entries before that block's
+#pragma unroll
+            for (int x = 0; x < kMaxCluster; ++x) {
+                const unsigned to = __shfl_sync(0xffffffffu, upto, x);
+                if (i >= to) {
+                    r = x + 1;
+                    at = to;
+                }
+            }
+            if (i < all) s.list[i] = far(&s.list[i - at], r);
         }
         __syncthreads();
     }
     return all;
 }
-// Falling order of the list's n entries (a block; ends with a barrier): compare and exchange in powers of two.
+// One exchange of a sort in falling order: entry number i keeps the larger of the pair where its run falls and
+// it is the pair's first, or neither.
+__device__ __forceinline__ unsigned long long exchange(unsigned long long mine, unsigned long long other, int i,
+                                                       int run, int step) {
+    const bool larger = ((i & run) == 0) == ((i & step) == 0);
+    return (mine < other) == larger ? other : mine;
+}
+// Falling order of the list's n entries (a block; ends with a barrier): compare and exchange in powers of two,
+// four neighbours a thread, by as many warps as that takes.  Steps within a thread are in registers, within a
+// warp by shuffles, further ones through the list's place.
 __device__ __noinline__ void sort_list(unsigned long long* list, int n) {
-    int size = 64;
+    constexpr int E = 4;
+    const int tid = threadIdx.x;
+    int size = 32 * E;
     while (size < n) size <<= 1;
-    for (int i = n + threadIdx.x; i < size; i += kThreads) list[i] = 0;
+    const bool active = tid * E < size;
     __syncthreads();
+    unsigned long long x[E];
+#pragma unroll
+    for (int j = 0; j < E; ++j) x[j] = tid * E + j < n ? list[tid * E + j] : 0ull;
+#pragma unroll 1
     for (int run = 2; run <= size; run <<= 1) {
-        for (int step = run >> 1; step > 0; step >>= 1) {
-            for (int t = threadIdx.x; t < size / 2; t += kThreads) {
-                const int i = 2 * t - (t & (step - 1));
-                const unsigned long long a = list[i], b = list[i + step];
-                if ((a < b) == ((i & run) == 0)) {
-                    list[i] = b;
-                    list[i + step] = a;
-                }
+#pragma unroll 1
+        for (int step = run >> 1; step >= 32 * E; step >>= 1) {
+            __syncthreads();
+            if (active) {
+#pragma unroll
+                for (int j = 0; j < E; ++j) list[tid * E + j] = x[j];
             }
-            // (Up to 32 apart, both of a pair are in 64 entries that one warp has.)
-            if (step > 32 || (step == 1 && run >= 64)) __syncthreads();
-            else __syncwarp();
+            __syncthreads();
+            if (active) {
+#pragma unroll
+                for (int j = 0; j < E; ++j) x[j] = exchange(x[j], list[(tid * E + j) ^ step], tid * E + j, run, step);
+            }
+        }
+        if (!active) continue;            // (whole warps)
+#pragma unroll 1
+        for (int step = min(run >> 1, 16 * E); step >= E; step >>= 1) {
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+                x[j] = exchange(x[j], __shfl_xor_sync(0xffffffffu, x[j], step / E), tid * E + j, run, step);
+        }
+#pragma unroll
+        for (int step = E / 2; step > 0; step >>= 1) {
+            if (step >= run) continue;
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+                if ((j & step) != 0) continue;
+                const unsigned long long a = x[j], b = x[j | step];
+                x[j] = exchange(a, b, tid * E + j, run, step);
+                x[j | step] = exchange(b, a, tid * E + (j | step), run, step);
+            }
         }
     }
     __syncthreads();
-}
-
-// The best of two tokens.
-__device__ __forceinline__ void better(float x, int i, unsigned key, float* pick, int* best, unsigned* best_key) {
-    if (x > *pick || (x == *pick && i < *best)) {
-        *pick = x;
-        *best = i;
-        *best_key = key;
-    }
-}
-// The block's best token and sum, in thread 0.
-__device__ __forceinline__ void join_block(Shared& s, float* pick, int* best, unsigned* best_key, float* sum) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (active) {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        const float x = __shfl_xor_sync(0xffffffffu, *pick, d);
-        const int i = __shfl_xor_sync(0xffffffffu, *best, d);
-        const unsigned u = __shfl_xor_sync(0xffffffffu, *best_key, d);
-        *sum += __shfl_xor_sync(0xffffffffu, *sum, d);
-        better(x, i, u, pick, best, best_key);
+        for (int j = 0; j < E; ++j) list[tid * E + j] = x[j];
     }
+    __syncthreads();
+}
+static_assert(kList == 4 * kThreads, "lists that are sorted");
+
+// The best token so far: what it is chosen by, its index, its z.
+struct Best {
+    float pick, z;
+    int at;
+    __device__ __forceinline__ void take(float x, int i, float value) {
+        if (x > pick || (x == pick && i < at)) {
+            pick = x;
+            at = i;
+            z = value;
+        }
+    }
+};
+constexpr int kNobody = 0x7fffffff;
+// The block's best token and sum, in thread 0.
+__device__ __forceinline__ void join_block(Shared& s, Best* best, float* sum) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    auto join_warp = [&](int from) {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+            if (d > from) continue;
+            const float x = __shfl_xor_sync(0xffffffffu, best->pick, d), z = __shfl_xor_sync(0xffffffffu, best->z, d);
+            const int i = __shfl_xor_sync(0xffffffffu, best->at, d);
+            *sum += __shfl_xor_sync(0xffffffffu, *sum, d);
+            best->take(x, i, z);
+        }
+    };
+    join_warp(16);
     __syncthreads();
     if (lane == 0) {
-        s.f[warp] = *pick;
+        s.f[warp] = best->pick;
         s.g[warp] = *sum;
-        s.i[warp] = *best;
-        s.u[warp] = *best_key;
+        s.i[warp] = best->at;
+        s.u[warp] = __float_as_uint(best->z);
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < kWarps; ++w) {
-            *sum += s.g[w];
-            better(s.f[w], s.i[w], s.u[w], pick, best, best_key);
-        }
+    if (warp == 0) {
+        const bool has = lane < kWarps;
+        best->pick = has ? s.f[lane] : kNegInf;
+        best->at = has ? s.i[lane] : kNobody;
+        best->z = has ? __uint_as_float(s.u[lane]) : 0.0f;
+        *sum = has ? s.g[lane] : 0.0f;
+        join_warp(kWarps / 2);
     }
 }
-__device__ __forceinline__ void put_token(const SampleParams& p, int b, const Weigh& weigh, int best, unsigned best_key,
-                                          float sum) {
-    const bool none = best == 0x7fffffff;                // (noise of NaN everywhere)
+__device__ __forceinline__ void put_token(const SampleParams& p, int b, const Weigh& weigh, const Best& best, float sum) {
+    const bool none = best.at == kNobody;                // (noise of NaN everywhere)
     if (none) flag(p.status, GS_DEV_EMPTY_ROW);
-    if (p.token != nullptr) p.token[b] = none ? -1 : best;
+    if (p.token != nullptr) p.token[b] = none ? -1 : best.at;
     if (p.logprob != nullptr)
-        p.logprob[b] = none ? kNegInf : (best_key == weigh.top ? 0.0f : value_of(best_key) - weigh.ref) - logf(sum);
+        p.logprob[b] = none ? kNegInf : (best.z == weigh.ref ? 0.0f : best.z - weigh.ref) - logf(sum);
 }
 
 // A token stays where the sum before it is below p of all.
@@ -507,36 +650,36 @@ __device__ __noinline__ void finish_list(const SampleParams& p, Shared& s, const
     unsigned long long mine = 0, all, units[PER];
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
-        units[j] = j < per && i0 + j < kept ? weigh.units(static_cast<unsigned>(s.list[i0 + j] >> 32)) : 0;
+        units[j] = j < per && i0 + j < kept ? weigh.units(value_of(static_cast<unsigned>(s.list[i0 + j] >> 32))) : 0;
         mine += units[j];
     }
     unsigned long long before = block_scan<kThreads>(mine, s.scan, &all);
     const unsigned long long target = top_p < 1.0f ? reach_of(top_p, all) : ~0ull;
-    float pick = kNegInf, sum = 0.0f, z[PER];
-    int best = 0x7fffffff, at[PER];
-    unsigned best_key = 0u, key[PER];
+    float sum = 0.0f, z[PER], add[PER];
+    int at[PER];
     bool stays[PER];
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
         stays[j] = j < per && i0 + j < kept;
         const unsigned long long e = stays[j] ? s.list[i0 + j] : 0;
-        key[j] = static_cast<unsigned>(e >> 32);
+        z[j] = value_of(static_cast<unsigned>(e >> 32));
         at[j] = static_cast<int>(~static_cast<unsigned>(e));
-        const float w = stays[j] ? weigh.weight(key[j]) : 0.0f;
-        stays[j] = stays[j] && before < target && (!(w < min_p) || key[j] == weigh.top);
+        const float w = stays[j] ? weigh.weight(z[j]) : 0.0f;
+        stays[j] = stays[j] && before < target && (!(w < min_p) || z[j] == weigh.ref);
         before += units[j];
         if (stays[j]) sum += w;
-        z[j] = stays[j] && noise != nullptr ? noise[at[j]] : 0.0f;
+        add[j] = stays[j] && noise != nullptr ? noise[at[j]] : 0.0f;
     }
+    Best best = {kNegInf, 0.0f, kNobody};
 #pragma unroll
     for (int j = 0; j < PER; ++j)
-        if (stays[j]) better(value_of(key[j]) + z[j], at[j], key[j], &pick, &best, &best_key);
-    join_block(s, &pick, &best, &best_key, &sum);
-    if (threadIdx.x == 0) put_token(p, b, weigh, best, best_key, sum);
+        if (stays[j]) best.take(z[j] + add[j], at[j], z[j]);
+    join_block(s, &best, &sum);
+    if (threadIdx.x == 0) put_token(p, b, weigh, best, sum);
 }
 
 template <class T>
-__global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_constant__ SampleParams p) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleParams p) {
     extern __shared__ __align__(16) unsigned char raw[];
     Shared& s = *reinterpret_cast<Shared*>(raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -546,13 +689,13 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
     clear(s.count, kDigits);
     grid_wait();
     grid_trigger();
-    Part<T> part;
+    const float hot = p.temperature != nullptr ? p.temperature[b] : 1.0f;
+    Part<T> part = {nullptr, nullptr, 0, 0, 0, 0, 0, 0, Divisor(hot)};
     constexpr int V = Part<T>::V;
     const T* const row = static_cast<const T*>(p.logits) + b * p.row_stride;
     part.shift = static_cast<int>((reinterpret_cast<unsigned long long>(row) & 15ull) / sizeof(T));
     part.row = row;
     part.vocab = p.vocab;
-    part.hot = p.temperature != nullptr ? p.temperature[b] : 1.0f;
     const int k = p.top_k != nullptr ? p.top_k[b] : 0;
     const float top_p = p.top_p != nullptr ? p.top_p[b] : 1.0f, min_p = p.min_p != nullptr ? p.min_p[b] : 0.0f;
     const int vectors = (p.vocab + part.shift + V - 1) / V;
@@ -560,37 +703,17 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
     part.v1 = static_cast<int>(static_cast<long long>(vectors) * (rank + 1) / p.cluster);
     part.whole0 = part.shift > 0 ? 1 : 0;
     part.whole1 = (p.vocab + part.shift) / V - 1;
-    int group = 0;                        // 2^group vectors make a group
-    while ((part.v1 - part.v0 - 1) >> group >= kGroups) ++group;
-    const int groups = part.v1 > part.v0 ? ((part.v1 - part.v0 - 1) >> group) + 1 : 0;
-    // The largest key of every group, and of the row; the smallest.
-    unsigned top = 0u, bottom = 0xffffffffu;
-    constexpr int AHEAD = Part<T>::AHEAD;
-    for (int g = tid; g < groups; g += kThreads * AHEAD) {
-        unsigned most[AHEAD] = {0u, 0u, 0u, 0u};
-        for (int x = 0; x < 1 << group; ++x) {
-            uint4 r[AHEAD];
-#pragma unroll
-            for (int a = 0; a < AHEAD; ++a) r[a] = part.raw(part.v0 + ((g + a * kThreads) << group) + x);
-#pragma unroll
-            for (int a = 0; a < AHEAD; ++a) {
-                const int v = part.v0 + ((g + a * kThreads) << group) + x;
-                if (v >= part.v1) break;
-                unsigned key[V];
-                part.keys(v, r[a], key);
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    most[a] = max(most[a], key[i]);
-                    bottom = min(bottom, key[i] > kNone ? key[i] : 0xffffffffu);
-                }
-            }
-        }
-#pragma unroll
-        for (int a = 0; a < AHEAD; ++a) {
-            if (g + a * kThreads < groups) s.most[g + a * kThreads] = most[a];
-            top = max(top, most[a]);
-        }
+    part.from = reinterpret_cast<const uint4*>(row - part.shift);
+    if (p.held != 0) part.hold(reinterpret_cast<uint4*>(raw + sizeof(Shared)));
+    // The largest key, and the smallest of the vectors' largest.
+    float largest = kNegInf, smallest = __builtin_huge_valf();
+#pragma unroll 4
+    for (int v = part.v0 + tid; v < part.v1; v += kThreads) {
+        const float m = part.most(v);
+        largest = fmaxf(largest, m);
+        smallest = fminf(smallest, m > kNegInf ? m : __builtin_huge_valf());
     }
+    unsigned top = key_of(part.cool.of(largest)), bottom = key_of(part.cool.of(smallest));
     top = __reduce_max_sync(0xffffffffu, top);
     bottom = __reduce_min_sync(0xffffffffu, bottom);
     if (lane == 0) {
@@ -607,12 +730,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
         }
     }
     cluster_sync();
-    top = 0u;
-    bottom = 0xffffffffu;
-    for (int r = 0; r < p.cluster; ++r) {
-        top = max(top, far(&s.shown.top, r));
-        bottom = min(bottom, far(&s.shown.bottom, r));
-    }
+    // (What other blocks show is read a block a lane: one after the other each costs a way to its SM and back.)
+    top = __reduce_max_sync(0xffffffffu, lane < p.cluster ? far(&s.shown.top, lane) : 0u);
+    bottom = __reduce_min_sync(0xffffffffu, lane < p.cluster ? far(&s.shown.bottom, lane) : 0xffffffffu);
     if (top <= kNone) {                   // nothing to choose from
         if (rank == 0 && tid == 0) {
             if (p.token != nullptr) p.token[b] = -1;
@@ -622,38 +742,57 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
         cluster_sync();
         return;
     }
-    const Weigh weigh = {top, value_of(top)};
-    const Pieces pieces(top, bottom);
-    const float* const noise = p.noise != nullptr && part.hot > 0.0f ? p.noise + b * p.noise_stride : nullptr;
+    const Weigh weigh = {value_of(top)};
+    Pieces pieces(weigh.ref, fminf(weigh.ref - value_of(bottom), 32.0f));
+    const float* const noise = p.noise != nullptr && hot > 0.0f ? p.noise + b * p.noise_stride : nullptr;
     const bool by_k = k > 0 && k < p.vocab, by_p = top_p < 1.0f;
-    unsigned border = kNone + 1u;         // the last token that stays: everything
-    int limit = p.vocab;
+    float edge = kNegInf;                 // what is above stays, and at it up to index limit: everything
+    int limit = -1;
     bool known = !by_k && !by_p;
+    // The block's sum of a value a thread, in thread 0.
+    auto block_sum = [&](float x) {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+        __syncthreads();
+        if (lane == 0) s.f[warp] = x;
+        __syncthreads();
+        x = lane < kWarps ? s.f[lane] : 0.0f;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+        return x;
+    };
+    // The sum of the values that the cluster's blocks show.
+    auto cluster_sum = [&] {
+        float x = lane < p.cluster ? far(&s.shown.sum, lane) : 0.0f;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+        return x;
+    };
     if (!known && (p.vocab <= kList || (by_k && k <= kMostK))) {
         // All tokens from a z on that k tokens reach (of a short row all) to the first block.
         int last = kDigits - 1;
         bool some = true;
         if (p.vocab > kList) {
-            for (int g = tid; g < groups; g += kThreads)
-                if (s.most[g] > kNone) atomicAdd(&s.count[pieces.of(s.most[g])], 1u);
+#pragma unroll 2
+            for (int v = part.v0 + tid; v < part.v1; v += kThreads) {
+                const float most = part.most_z(v);
+                if (most > kNegInf) atomicAdd(&s.count[pieces.of(most)], 1u);
+            }
             cluster_sync();
             const Found f = locate<false, false>(s, kDigits, 0, 0, p.cluster, rank,
                                                  [&](unsigned long long) { return static_cast<unsigned long long>(k); });
             if (f.digit >= 0) last = f.digit;
             some = f.above + f.here <= kList;            // (else there are too many tokens for certain)
         }
-        for (int g = tid; g < groups; g += kThreads) {
-            if (!some || s.most[g] <= kNone || pieces.of(s.most[g]) > last) continue;
-            for (int x = 0; x < 1 << group; ++x) {
-                const int v = part.v0 + (g << group) + x;
-                if (v >= part.v1) break;
-                unsigned key[V];
-                part.fetch(v, key);
+        if (some)
+            part.vectors([&](int v) {
+                const float most = part.most_z(v);
+                return most > kNegInf && pieces.of(most) <= last;
+            }, [&](const float (&z)[V], int at) {
 #pragma unroll
                 for (int i = 0; i < V; ++i)
-                    if (key[i] > kNone && pieces.of(key[i]) <= last) put_in_list(s, key[i], v * V + i - part.shift);
-            }
-        }
+                    if (z[i] > kNegInf && pieces.of(z[i]) <= last) put_in_list(s, z[i], at + i);
+            });
         cluster_sync();
         const unsigned n = gather_lists(s, p.cluster, rank);
         if (some && n <= kList) {
@@ -669,16 +808,60 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
         clear(s.low, kDigits);
         clear(s.high, kDigits);
         __syncthreads();
-        part.each([&](unsigned key, int) {
-            if (key > kNone) add_weight(s, pieces.of(key), weigh.units(key));
+        // A token of less than (1 - p) / vocab of the sum is not kept: all such together are less than 1 - p of
+        // it.  The sum is at least that of the vectors' largest weights.  Of the tokens below, the sum alone
+        // counts (in fp32: it is 1 - p of all at most), and the pieces need not reach them.
+        float least = 0.0f;
+#pragma unroll 2
+        for (int v = part.v0 + tid; v < part.v1; v += kThreads) {
+            least += weigh.weight(part.most_z(v));       // (0 for -inf)
+        }
+        least = block_sum(least);
+        if (tid == 0) s.shown.sum = least;
+        cluster_sync();
+        least = cluster_sum();
+        const float little = fminf(0.5f, (1.0f - fmaxf(top_p, 0.0f)) * least / static_cast<float>(p.vocab) * 0.99f);
+        pieces = Pieces(weigh.ref, fminf(logf(1.0f / little) + 0.01f, 32.0f));
+        float rest = 0.0f;
+        part.vectors([](int) { return true; }, [&](const float (&z)[V], int) {
+            unsigned lo[V], old[V], hi[V];
+            int d[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float w = weigh.weight(z[i]);
+                const bool counts = w > little;
+                rest += counts ? 0.0f : w;
+                lo[i] = hi[i] = 0u;
+                d[i] = 0;
+                if (counts) {
+                    Weigh::words_of(w, &lo[i], &hi[i]);
+                    d[i] = pieces.of(z[i]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) old[i] = lo[i] != 0u ? atomicAdd(&s.low[d[i]], lo[i]) : 0u;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                hi[i] += old[i] + lo[i] < old[i];
+                if (hi[i] != 0u) atomicAdd(&s.high[d[i]], hi[i]);
+            }
         });
+        // (The rest goes to the last piece: it lies behind all that may be kept.)
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, d);
+        if (lane == 0) add_weight(s, kDigits - 1, __float2ull_rz(rest * 1099511627776.0f));
         cluster_sync();
         unsigned long long target = 0;
         const Found f = locate<true, false>(s, kDigits, 0, 0, p.cluster, rank, [&](unsigned long long all) {
             return target = reach_of(top_p, all);
         });
-        part.each([&](unsigned key, int at) {
-            if (key > kNone && pieces.of(key) == f.digit) put_in_list(s, key, at);
+        part.vectors([&](int v) {
+            const float most = part.most_z(v);
+            return most > kNegInf && pieces.of(most) <= f.digit;
+        }, [&](const float (&z)[V], int at) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (z[i] > kNegInf && pieces.of(z[i]) == f.digit) put_in_list(s, z[i], at + i);
         });
         cluster_sync();
         const unsigned n = gather_lists(s, p.cluster, rank);
@@ -691,7 +874,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
                 unsigned long long mine = 0, all, units[PER];
 #pragma unroll
                 for (int j = 0; j < PER; ++j) {
-                    units[j] = j < per && i0 + j < static_cast<int>(n) ? weigh.units(static_cast<unsigned>(s.list[i0 + j] >> 32)) : 0;
+                    units[j] = j < per && i0 + j < static_cast<int>(n) ? weigh.units(value_of(static_cast<unsigned>(s.list[i0 + j] >> 32))) : 0;
                     mine += units[j];
                 }
                 unsigned long long before = f.above_weight + block_scan<kThreads>(mine, s.scan, &all);
@@ -705,13 +888,13 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
                 }
             }
             cluster_sync();
-            border = far(&s.shown.border, 0);
+            edge = value_of(far(&s.shown.border, 0));
             limit = far(&s.shown.limit, 0);
         }
         cluster_sync();
     }
     if (!known) {
-        Border last = {border, ~0ull, 0ull, 0ull};
+        Border last = {kNone + 1u, ~0ull, 0ull, 0ull};   // everything
         if (by_k) {
             const Border found = find_border<false>(s, part, weigh, 0u, static_cast<unsigned long long>(k), p.cluster, rank);
             if (found.need > 0) last = found;            // (else fewer than k tokens can be chosen)
@@ -719,64 +902,91 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const __grid_consta
         if (by_p) {
             // The sum over what top-k left.
             unsigned long long mine = 0, all;
-            part.each([&](unsigned key, int) {
-                if (key > last.key || (key == last.key && last.need == ~0ull)) mine += weigh.units(key);
+            const float over = last.need == ~0ull ? kNegInf : value_of(last.key);
+            part.each([&](float z, int) {
+                if (z > over) mine += weigh.units(z);
             });
             block_scan<kThreads>(mine, s.scan, &all);
             if (tid == 0) s.shown.weight = all;
             cluster_sync();
-            all = 0;
-            for (int r = 0; r < p.cluster; ++r) all += far(&s.shown.weight, r);
+            all = warp_sum(lane < p.cluster ? far(&s.shown.weight, lane) : 0ull);
             cluster_sync();
-            if (last.need != ~0ull) all += last.need * weigh.units(last.key);
+            if (last.need != ~0ull) all += last.need * weigh.units(value_of(last.key));
             const Border found = find_border<true>(s, part, weigh, last.key, reach_of(top_p, all), p.cluster, rank);
             if (found.key > last.key || (found.key == last.key && found.need < last.need)) last = found;
         }
-        border = last.key;
-        if (last.need != ~0ull) limit = limit_of(s, part, last, p.cluster, rank);
+        if (last.need != ~0ull) {
+            edge = value_of(last.key);
+            limit = limit_of(s, part, last, p.cluster, rank);
+        }
     }
     // The token, and the weights of what stays.
-    float pick = kNegInf, sum = 0.0f, rest = 0.0f;       // (sum - rest: what rounding left out is kept)
-    int best = 0x7fffffff;
-    unsigned best_key = 0u;
-    part.each([&](unsigned key, int at) {
-        if (key < border || key <= kNone || (key == border && at > limit)) return;
-        const float w = weigh.weight(key);
-        if (w < min_p && key != top) return;
-        const float y = w - rest, t = sum + y;
+    Best best = {kNegInf, 0.0f, kNobody};
+    float sum = 0.0f, rest = 0.0f;        // (sum - rest: what rounding left out is kept)
+    const float least = min_p * 0.99f;    // (weights of neighbouring z are not compared with min_p itself)
+    part.vectors([&](int v) {
+        if (edge == kNegInf && !(least > 0.0f)) return true;
+        const float most = part.most_z(v);
+        return most >= edge && (!(least > 0.0f) || weigh.weight(most) >= least || most == weigh.ref);
+    }, [&](const float (&z)[V], int at) {
+        float here = 0.0f, add[V];
+        bool stays[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float w = weigh.weight(z[i]);
+            stays[i] = (z[i] > edge || (z[i] == edge && at + i <= limit)) && (!(w < min_p) || z[i] == weigh.ref);
+            here += stays[i] ? w : 0.0f;
+            add[i] = stays[i] && noise != nullptr ? noise[at + i] : 0.0f;
+        }
+        const float y = here - rest, t = sum + y;
         rest = (t - sum) - y;
         sum = t;
-        better(noise != nullptr ? value_of(key) + noise[at] : value_of(key), at, key, &pick, &best, &best_key);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (stays[i]) best.take(z[i] + add[i], at + i, z[i]);
     });
-    join_block(s, &pick, &best, &best_key, &sum);
+    join_block(s, &best, &sum);
     if (tid == 0) {
-        s.shown.pick = pick;
+        s.shown.pick = best.pick;
+        s.shown.best = best.at;
+        s.shown.best_z = best.z;
         s.shown.sum = sum;
-        s.shown.best = best;
-        s.shown.best_key = best_key;
     }
     cluster_sync();
-    if (rank == 0 && tid == 0) {
-        for (int r = 1; r < p.cluster; ++r) {
-            sum += far(&s.shown.sum, r);
-            better(far(&s.shown.pick, r), far(&s.shown.best, r), far(&s.shown.best_key, r), &pick, &best, &best_key);
+    if (rank == 0 && warp == 0) {
+        const bool other = lane < p.cluster;
+        best.pick = other ? far(&s.shown.pick, lane) : kNegInf;
+        best.at = other ? far(&s.shown.best, lane) : kNobody;
+        best.z = other ? far(&s.shown.best_z, lane) : 0.0f;
+        sum = other ? far(&s.shown.sum, lane) : 0.0f;
+#pragma unroll
+        for (int d = kMaxCluster / 2; d > 0; d >>= 1) {
+            const float x = __shfl_xor_sync(0xffffffffu, best.pick, d), z = __shfl_xor_sync(0xffffffffu, best.z, d);
+            const int i = __shfl_xor_sync(0xffffffffu, best.at, d);
+            sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            best.take(x, i, z);
         }
-        put_token(p, b, weigh, best, best_key, sum);
+        if (lane == 0) put_token(p, b, weigh, best, sum);
     }
     cluster_sync();                       // (what rank 0 read stays until it is read)
 }
 
-// Blocks of a row: enough of them for every SM, but no part below 4096 tokens.
+// Blocks of a row: as many as it takes to hold the row, and more where they find SMs (two blocks each) and
+// have more than two vectors a thread: a barrier of a cluster costs more than one of a block.
 int cluster_of(const gs_sample_args* a) {
+    const long long bytes = a->vocab * elem_size(a->dtype);
     int n = 1;
-    while (n < kMaxCluster && a->vocab / n >= 8192 && static_cast<long long>(a->batch) * n < 4ll * sm_count()) n *= 2;
+    while (n < kMaxCluster &&
+           (bytes / n > kHeld - 64 ||
+            (bytes / n > 16 * 2 * kThreads && 2ll * a->batch * n <= 2ll * sm_count())))
+        n *= 2;
     return n;
 }
 
 template <class T>
 gs_status launch_type(const SampleParams& p, gs_stream stream) {
     const dim3 grid(static_cast<unsigned>(p.batch) * p.cluster);
-    constexpr int bytes = static_cast<int>(sizeof(Shared));
+    const int bytes = static_cast<int>(sizeof(Shared)) + p.held;
     if (!allow_smem<sample_kernel<T>>(bytes)) return GS_ERR_CUDA;
     return launch(sample_kernel<T>, grid, kThreads, bytes, p.cluster, stream, p);
 }
@@ -800,6 +1010,9 @@ extern "C" gs_status gs_sample(const gs_sample_args* a, gs_stream stream) {
     p.batch = a->batch;
     p.vocab = a->vocab;
     p.cluster = cluster_of(a);
+    // (A part has a vector or two more than its share.)
+    const long long part = (a->vocab * es + 16) / p.cluster + 32;
+    p.held = part <= kHeld ? static_cast<int>(part / 16 * 16) : 0;
     p.logits = a->logits;
     p.row_stride = a->batch > 1 ? a->row_stride : 0;
     p.temperature = a->temperature;
