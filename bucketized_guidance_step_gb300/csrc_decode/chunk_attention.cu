@@ -1,5 +1,11 @@
 // Attention of chunks of new tokens over a paged cache (sm_103a): the argument checks, and the kernel
 // that computes with fp32 multiply-adds, for fp32 caches.
+//
+// A block has a tile of 64 query rows and reads units of 64 positions (32 for heads of over 128 dims) by
+// 16-byte asynchronous copies, one unit ahead; where a unit's rows lie is looked up a unit before that.  Its
+// 16 x 16 threads have 4 rows and 4 positions (2) of the scores each, then 4 rows and every 16th group of 4
+// dims of the output.  Multiply-adds are two at a time (fma.rn.f32x2): over pairs of dims in the scores,
+// whose two sums are added at the end, and over pairs of outputs.
 #include <cmath>
 
 #include "chunk_attention.cuh"
@@ -9,28 +15,55 @@ namespace {
 
 constexpr int kThreads = 256, kRows = 64;
 
-// Rows of 64 queries against units of KT positions: 16 x 16 threads, of which one has 4 rows and
-// KT / 16 positions of the scores, then 4 rows and DP / 16 dims of the output.
-template <class T, int DP, int KT>
+template <int DP, int KT>
 struct Tile {
     static constexpr int kPitch = DP + 4, kScore = KT + 4;
     struct Smem {
-        float q[kRows][kPitch], k[KT][kPitch], v[KT][kPitch], s[kRows][kScore];
+        float q[kRows][kPitch], k[2][KT][kPitch], v[2][KT][kPitch], s[kRows][kScore];
         float top[kRows], sum[kRows], fade[kRows];
+        long long at[3][KT];              // bytes of a position's row in K and V; -1: read as zeros
     };
 };
 
-template <class T, int DP, int KT>
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Pair twice(float x) {
+    Pair r;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float2 halves(Pair p) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+    return r;
+}
+// 16 bytes from global to shared memory; size 0 fills with zeros and reads nothing.
+__device__ __forceinline__ void copy16(void* to, const void* from, int size) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(static_cast<unsigned>(__cvta_generic_to_shared(to))),
+                 "l"(from), "r"(size)
+                 : "memory");
+}
+
+template <int DP, int KT>
 __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ ChunkParams p) {
-    using S = typename Tile<T, DP, KT>::Smem;
+    using S = typename Tile<DP, KT>::Smem;
     using Cut = ChunkCut<kRows, kRows, KT, kThreads, kThreads>;
-    constexpr int V = 16 / static_cast<int>(sizeof(T)), CH = DP / V, CPT = KT / 16, NV = DP / 64;
+    constexpr int CPT = KT / 16, NV = DP / 64;
     extern __shared__ __align__(16) char smem[];
     S& s = *reinterpret_cast<S*>(smem);
     __shared__ typename Cut::Shared plan;
     __shared__ ChunkItem item;
     __shared__ int ok;
-    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, dim = p.c.dim;
+    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, dim = p.c.dim, pieces = dim / 4;
     grid_wait();
     grid_trigger();
     Cut cut;
@@ -46,97 +79,112 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         if (it.kind == 2) {
             if (tid == 0) ok = chunk_wait_parts(p.work + kChunkHead + it.share, it.need);
             __syncthreads();
-            if (ok) chunk_join<T>(p, it, tid >> 5, kThreads / 32, 0.0f);
+            if (ok) chunk_join<float>(p, it, tid >> 5, kThreads / 32, 0.0f);
             else if (tid == 0) flag(p.c.status, GS_DEV_TIMEOUT);
             __syncthreads();
             continue;
         }
-        // The queries, with the scale's sign; zeros past the tile's rows and past dim.
-        for (int x = tid; x < kRows * CH; x += kThreads) {
-            const int r = x / CH, c = x - r * CH, row = it.row + r;
-            float f[V];
-#pragma unroll
-            for (int i = 0; i < V; ++i) f[i] = 0.0f;
-            if (r < it.rows && c * V < dim) {
-                const int t = chunk_token(p, row), h = it.head * p.group + row - t * p.group;
-                const T* from = static_cast<const T*>(p.q) + (it.e.row + t) * p.q_token + h * p.q_head + c * V;
-                unpack16<T>(load16_any(from, p.q_aligned != 0), f);
+        const int count = it.hi - it.lo;
+        // Where unit u's rows lie (KT threads); its copies (all).
+        auto look_up = [&](int u) {
+            if (u >= count || tid >= KT) return;
+            int here, in_page;
+            const int at = units.first(it.span.unit(it.lo + u), &here, &in_page);
+            long long off = -1;
+            if (tid < min(here, it.e.len - at)) {
+                const int col = (at + tid) / p.c.page, row = at + tid - col * p.c.page;
+                const int page = p.c.table[static_cast<long long>(it.e.seq) * p.c.cols + col];
+                if (page >= 0 && page < p.c.pages)
+                    off = 4 * (page * p.c.page_stride + it.head * p.c.head_stride + row * p.c.token_stride);
+                else
+                    flag(p.c.status, GS_DEV_BAD_SEQ);
             }
-#pragma unroll
-            for (int i = 0; i < V; ++i) s.q[r][c * V + i] = f[i] * p.q_sign;
+            s.at[u % 3][tid] = off;
+        };
+        auto load = [&](int u) {
+            if (u < count) {
+                for (int x = tid; x < KT * pieces; x += kThreads) {
+                    const int r = x / pieces, c = x - r * pieces;
+                    const long long off = s.at[u % 3][r];
+                    const int size = off >= 0 ? 16 : 0;
+                    const long long from = off >= 0 ? off + 16 * c : 0;
+                    copy16(&s.k[u & 1][r][4 * c], p.c.k + from, size);
+                    copy16(&s.v[u & 1][r][4 * c], p.c.v + from, size);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        look_up(0);
+        look_up(1);
+        // The queries, with the scale's sign; zeros past the tile's rows.
+        for (int x = tid; x < kRows * pieces; x += kThreads) {
+            const int r = x / pieces, c = x - r * pieces, row = it.row + r;
+            float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (r < it.rows) {
+                const int t = chunk_token(p, row), h = it.head * p.group + row - t * p.group;
+                const float* from = static_cast<const float*>(p.q) + (it.e.row + static_cast<long long>(t)) * p.q_token +
+                                    h * p.q_head + c * 4;
+                unpack16<float>(load16_any(from, p.q_aligned != 0), &f.x);
+            }
+            *reinterpret_cast<float4*>(&s.q[r][c * 4]) =
+                make_float4(f.x * p.q_sign, f.y * p.q_sign, f.z * p.q_sign, f.w * p.q_sign);
         }
         for (int r = tid; r < kRows; r += kThreads) {
             s.top[r] = kNegInf;
             s.sum[r] = 0.0f;
         }
-        float o[4][NV * 4];
+        Pair o[4][NV][2];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int d = 0; d < NV * 4; ++d) o[i][d] = 0.0f;
+            for (int x = 0; x < NV; ++x) o[i][x][0] = o[i][x][1] = 0ull;
         const int from = it.e.len - it.e.m;              // position of the entry's first row
         const int first_row = from + chunk_token(p, it.row), last_row = from + chunk_token(p, it.row + it.rows - 1);
-        for (int n = it.lo; n < it.hi; ++n) {
-            int count, in_page;
-            const int at = units.first(it.span.unit(n), &count, &in_page);
-            const int valid = min(count, it.e.len - at);
-            __syncthreads();                             // (the last unit's rows are not read any more)
-            for (int x = tid; x < KT * CH; x += kThreads) {
-                const int r = x / CH, c = x - r * CH;
-                uint4 k = make_uint4(0u, 0u, 0u, 0u), v = k;
-                if (r < valid && c * V < dim) {
-                    const int col = (at + r) / p.c.page, row = at + r - col * p.c.page;
-                    const int page = p.c.table[static_cast<long long>(it.e.seq) * p.c.cols + col];
-                    if (page >= 0 && page < p.c.pages) {
-                        const long long off = (page * p.c.page_stride + it.head * p.c.head_stride +
-                                               row * p.c.token_stride + c * V) * static_cast<int>(sizeof(T));
-                        k = *reinterpret_cast<const uint4*>(p.c.k + off);
-                        v = *reinterpret_cast<const uint4*>(p.c.v + off);
-                    } else {
-                        flag(p.c.status, GS_DEV_BAD_SEQ);
-                    }
-                }
-                unpack16<T>(k, &s.k[r][c * V]);
-                unpack16<T>(v, &s.v[r][c * V]);
-            }
+        int pos[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pos[i] = from + chunk_token(p, it.row + ty * 4 + i);
+        __syncthreads();
+        load(0);
+        for (int u = 0; u < count; ++u) {
+            int here, in_page;
+            const int at = units.first(it.span.unit(it.lo + u), &here, &in_page);
+            const int valid = min(here, it.e.len - at), now = u & 1;
+            load(u + 1);
+            look_up(u + 2);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
             __syncthreads();
-            float a[4][CPT];
+            Pair a[4][CPT];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int c = 0; c < CPT; ++c) a[i][c] = 0.0f;
-#pragma unroll 4
-            for (int d = 0; d < DP; d += 4) {
-                float4 q[4], k[CPT];
+                for (int c = 0; c < CPT; ++c) a[i][c] = 0ull;
+#pragma unroll 2
+            for (int d = 0; d < dim; d += 4) {
+                ulonglong2 q[4], k[CPT];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const float4*>(&s.q[ty * 4 + i][d]);
+                for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const ulonglong2*>(&s.q[ty * 4 + i][d]);
 #pragma unroll
-                for (int c = 0; c < CPT; ++c) k[c] = *reinterpret_cast<const float4*>(&s.k[tx + 16 * c][d]);
+                for (int c = 0; c < CPT; ++c) k[c] = *reinterpret_cast<const ulonglong2*>(&s.k[now][tx + 16 * c][d]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int c = 0; c < CPT; ++c) {
-                        a[i][c] = fmaf(q[i].x, k[c].x, a[i][c]);
-                        a[i][c] = fmaf(q[i].y, k[c].y, a[i][c]);
-                        a[i][c] = fmaf(q[i].z, k[c].z, a[i][c]);
-                        a[i][c] = fmaf(q[i].w, k[c].w, a[i][c]);
-                    }
+                    for (int c = 0; c < CPT; ++c) a[i][c] = fma2(q[i].y, k[c].y, fma2(q[i].x, k[c].x, a[i][c]));
             }
             // Whether some row does not see the whole unit.
             const bool masked = valid < KT || at + KT - 1 > first_row ||
                                 (p.window > 0 && at <= last_row - p.window && at + KT > p.sinks);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int row = it.row + ty * 4 + i, pos = from + chunk_token(p, row);
-                float up = kNegInf;
+                float up = kNegInf, x[CPT];
                 bool seen[CPT];
 #pragma unroll
                 for (int c = 0; c < CPT; ++c) {
                     const int j = at + tx + 16 * c;
-                    seen[c] = !masked || (tx + 16 * c < valid && j <= pos &&
-                                          (p.window == 0 || j > pos - p.window || j < p.sinks));
-                    a[i][c] = seen[c] ? a[i][c] * p.scale_log2 : kNegInf;
-                    up = fmaxf(up, a[i][c]);
+                    const float2 h = halves(a[i][c]);
+                    seen[c] = !masked || (tx + 16 * c < valid && j <= pos[i] &&
+                                          (p.window == 0 || j > pos[i] - p.window || j < p.sinks));
+                    x[c] = seen[c] ? (h.x + h.y) * p.scale_log2 : kNegInf;
+                    up = fmaxf(up, x[c]);
                 }
 #pragma unroll
                 for (int d = 1; d < 16; d <<= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, d));
@@ -146,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 float sum = 0.0f;
 #pragma unroll
                 for (int c = 0; c < CPT; ++c) {
-                    const float w = chunk_pow2(a[i][c] - base);
+                    const float w = chunk_pow2(x[c] - base);
                     if (seen[c]) sum += w;
                     s.s[ty * 4 + i][tx + 16 * c] = seen[c] ? w : -1.0f;      // -1: not to be multiplied
                 }
@@ -162,29 +210,38 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             __syncwarp();                                // a warp's rows are its own
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float fade = s.fade[ty * 4 + i];
-#pragma unroll
-                for (int d = 0; d < NV * 4; ++d) o[i][d] *= fade;
-            }
-            for (int k = 0; k < valid; ++k) {
-                float w[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = s.s[ty * 4 + i][k];
+                const Pair fade = twice(s.fade[ty * 4 + i]);
 #pragma unroll
                 for (int x = 0; x < NV; ++x) {
-                    const float4 v = *reinterpret_cast<const float4*>(&s.v[k][x * 64 + tx * 4]);
+                    o[i][x][0] = mul2(o[i][x][0], fade);
+                    o[i][x][1] = mul2(o[i][x][1], fade);
+                }
+            }
+            // O += P V, V's infinities and NaN only to rows that see them.
+            auto add = [&](auto only_seen) {
+#pragma unroll 4
+                for (int k = 0; k < valid; ++k) {
+                    float w[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (!masked || w[i] >= 0.0f || w[i] != w[i]) {
-                            o[i][4 * x] = fmaf(w[i], v.x, o[i][4 * x]);
-                            o[i][4 * x + 1] = fmaf(w[i], v.y, o[i][4 * x + 1]);
-                            o[i][4 * x + 2] = fmaf(w[i], v.z, o[i][4 * x + 2]);
-                            o[i][4 * x + 3] = fmaf(w[i], v.w, o[i][4 * x + 3]);
+                    for (int i = 0; i < 4; ++i) w[i] = s.s[ty * 4 + i][k];
+#pragma unroll
+                    for (int x = 0; x < NV; ++x) {
+                        const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(&s.v[now][k][x * 64 + tx * 4]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (!decltype(only_seen)::value || !(w[i] < 0.0f)) {
+                                o[i][x][0] = fma2(twice(w[i]), v.x, o[i][x][0]);
+                                o[i][x][1] = fma2(twice(w[i]), v.y, o[i][x][1]);
+                            }
                         }
                     }
                 }
-            }
+            };
+            if (masked) add(std::true_type());
+            else add(std::false_type());
+            __syncthreads();                             // (the unit's place is filled again)
         }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();                                 // (the first values of top and sum, where no unit came)
         float* const slot = p.slots + it.slot * chunk_slot_words(p.slot_rows, dim);
 #pragma unroll
@@ -192,28 +249,23 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             const int r = ty * 4 + i;
             if (r >= it.rows) continue;
             const float sum = s.sum[r], top = s.top[r];
-            if (it.parts == 1) {
-                const float by = sum > 0.0f ? 1.0f / sum : sum;      // a NaN stays one
-                float* lse;
-                T* const to = chunk_out<T>(p, it, it.row + r, &lse);
+            const bool whole = it.parts == 1;
+            const float by = !whole ? 1.0f : sum > 0.0f ? 1.0f / sum : sum;          // a NaN stays one
+            float* lse = nullptr;
+            float* const to = whole ? chunk_out<float>(p, it, it.row + r, &lse)
+                                    : slot + 2 * p.slot_rows + static_cast<long long>(r) * dim;
 #pragma unroll
-                for (int x = 0; x < NV; ++x)
-                    if (x * 64 + tx * 4 < dim)
-                        chunk_put4<T>(p, to + x * 64 + tx * 4,
-                                      make_float4(o[i][4 * x] * by, o[i][4 * x + 1] * by, o[i][4 * x + 2] * by,
-                                                  o[i][4 * x + 3] * by));
-                if (tx == 0 && lse != nullptr) *lse = sum == 0.0f ? kNegInf : (top + log2f(sum)) * kChunkLn2;
-            } else {
-#pragma unroll
-                for (int x = 0; x < NV; ++x)
-                    if (x * 64 + tx * 4 < dim)
-                        *reinterpret_cast<float4*>(slot + 2 * p.slot_rows + static_cast<long long>(r) * dim +
-                                                   x * 64 + tx * 4) =
-                            make_float4(o[i][4 * x], o[i][4 * x + 1], o[i][4 * x + 2], o[i][4 * x + 3]);
-                if (tx == 0) {
-                    slot[r] = top;
-                    slot[p.slot_rows + r] = sum;
-                }
+            for (int x = 0; x < NV; ++x) {
+                if (x * 64 + tx * 4 >= dim) continue;
+                const float2 lo = halves(o[i][x][0]), hi = halves(o[i][x][1]);
+                const float4 f = make_float4(lo.x * by, lo.y * by, hi.x * by, hi.y * by);
+                if (whole) chunk_put4<float>(p, to + x * 64 + tx * 4, f);
+                else *reinterpret_cast<float4*>(to + x * 64 + tx * 4) = f;
+            }
+            if (tx == 0 && whole && lse != nullptr) *lse = sum == 0.0f ? kNegInf : (top + log2f(sum)) * kChunkLn2;
+            if (tx == 0 && !whole) {
+                slot[r] = top;
+                slot[p.slot_rows + r] = sum;
             }
         }
         if (it.parts > 1) {
@@ -225,11 +277,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     if (tid < 32) chunk_leave(p, cut.used());
 }
 
-template <class T, int DP, int KT>
+template <int DP, int KT>
 gs_status launch_as(const ChunkParams& p, int blocks, gs_stream stream) {
-    const int bytes = static_cast<int>(sizeof(typename Tile<T, DP, KT>::Smem));
-    if (!allow_smem<chunk_kernel<T, DP, KT>>(bytes)) return GS_ERR_CUDA;
-    return launch(chunk_kernel<T, DP, KT>, dim3(blocks), kThreads, bytes, 1, stream, p);
+    const int bytes = static_cast<int>(sizeof(typename Tile<DP, KT>::Smem));
+    if (!allow_smem<chunk_kernel<DP, KT>>(bytes)) return GS_ERR_CUDA;
+    return launch(chunk_kernel<DP, KT>, dim3(blocks), kThreads, bytes, 1, stream, p);
 }
 
 }  // namespace
@@ -237,9 +289,9 @@ gs_status launch_as(const ChunkParams& p, int blocks, gs_stream stream) {
 ChunkShape chunk_fp32_shape(int) { return {kRows, sm_count()}; }
 
 gs_status launch_chunk_fp32(const ChunkParams& p, int blocks, gs_stream stream) {
-    if (p.c.dim <= 64) return launch_as<float, 64, 64>(p, blocks, stream);
-    if (p.c.dim <= 128) return launch_as<float, 128, 64>(p, blocks, stream);
-    return launch_as<float, 256, 32>(p, blocks, stream);
+    if (p.c.dim <= 64) return launch_as<64, 64>(p, blocks, stream);
+    if (p.c.dim <= 128) return launch_as<128, 64>(p, blocks, stream);
+    return launch_as<256, 32>(p, blocks, stream);
 }
 
 namespace {
