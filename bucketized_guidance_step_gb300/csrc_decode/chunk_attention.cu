@@ -1,11 +1,17 @@
 // Attention of chunks of new tokens over a paged cache (sm_103a): the argument checks, and the kernel
-// that computes with fp32 multiply-adds, for fp32 caches.
+// for fp32 caches.
 //
-// A block has a tile of 64 query rows and reads units of 64 positions (32 for heads of over 128 dims) by
-// 16-byte asynchronous copies, one unit ahead; where a unit's rows lie is looked up a unit before that.  Its
-// 16 x 16 threads have 4 rows and 4 positions (2) of the scores each, then 4 rows and every 16th group of 4
-// dims of the output.  Multiply-adds are two at a time (fma.rn.f32x2): over pairs of dims in the scores,
-// whose two sums are added at the end, and over pairs of outputs.
+// Its products run on the tensor cores with numbers split in two: x = hi + lo, hi 11 bits of it, and
+// x y = hi hi' + hi lo' + lo hi' up to about 2^-21 of it, sums in fp32 (mma.sync m16n8k8).  8 chunks of up to
+// 129 tokens over up to 1001, 8 and 4 heads of 96, take 89 us; a 64 x 64 tile of fp32 multiply-adds from
+// shared memory, whose reads bound it, took 123 us.  Bound now by the issue of products and splits: a unit
+// is 144 products and about 700 other instructions for each of 16 warps.
+//
+// A block has a tile of 64 query rows and reads units of 32 positions by 16-byte asynchronous copies, one
+// unit ahead; where a unit's rows lie is looked up a unit before that.  Of its 8 warps, each has 16 rows and
+// half of every unit's positions, with a softmax and an output of its own; the two halves meet at the item's
+// end.  The scores' fragments are the second product's operands as they are: a step takes positions 2 t and
+// 2 t + 1 where the instruction numbers them t and t + 4, and reads V's rows likewise.
 #include <cmath>
 
 #include "chunk_attention.cuh"
@@ -14,64 +20,71 @@ namespace gs_decode {
 namespace {
 
 constexpr int kThreads = 256, kRows = 64;
+constexpr int KT = 32;                    // positions of a unit
 
-template <int DP, int KT>
+template <int DP>
 struct Tile {
-    static constexpr int kPitch = DP + 4, kScore = KT + 4;
+    static constexpr int kPitch = DP + 4; // (8 rows' neighbours in 32 banks)
     struct Smem {
-        float q[kRows][kPitch], k[2][KT][kPitch], v[2][KT][kPitch], s[kRows][kScore];
-        float top[kRows], sum[kRows], fade[kRows];
+        float q[kRows][kPitch], k[2][KT][kPitch], v[2][KT][kPitch];
         long long at[3][KT];              // bytes of a position's row in K and V; -1: read as zeros
+        float top[kRows], sum[kRows];
     };
 };
 
-using Pair = unsigned long long;
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-    Pair r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
-    Pair r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ Pair twice(float x) {
-    Pair r;
-    asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ float2 halves(Pair p) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
-    return r;
-}
 // 16 bytes from global to shared memory; size 0 fills with zeros and reads nothing.
 __device__ __forceinline__ void copy16(void* to, const void* from, int size) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(static_cast<unsigned>(__cvta_generic_to_shared(to))),
                  "l"(from), "r"(size)
                  : "memory");
 }
+// x = hi + lo: hi rounded to 11 bits (a), or cut to them (b: one operation less).
+__device__ __forceinline__ void split_a(float x, unsigned* hi, unsigned* lo) {
+    *hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+    *lo = __float_as_uint(x - __uint_as_float(*hi));
+}
+__device__ __forceinline__ void split_b(float x, unsigned* hi, unsigned* lo) {
+    *hi = __float_as_uint(x) & 0xffffe000u;
+    *lo = __float_as_uint(x - __uint_as_float(*hi));
+}
+__device__ __forceinline__ void mma(float (&d)[4], const unsigned (&a)[4], unsigned b0, unsigned b1) {
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// d += a b, a split already.
+__device__ __forceinline__ void mma_split(float (&d)[4], const unsigned (&hi)[4], const unsigned (&lo)[4], float b0, float b1) {
+    unsigned h0, l0, h1, l1;
+    split_b(b0, &h0, &l0);
+    split_b(b1, &h1, &l1);
+    mma(d, lo, h0, h1);
+    mma(d, hi, l0, l1);
+    mma(d, hi, h0, h1);
+}
 
-template <int DP, int KT>
-__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ ChunkParams p) {
-    using S = typename Tile<DP, KT>::Smem;
+template <int DP>
+__global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2) chunk_kernel(const __grid_constant__ ChunkParams p) {
+    using S = typename Tile<DP>::Smem;
     using Cut = ChunkCut<kRows, kRows, KT, kThreads, kThreads>;
-    constexpr int CPT = KT / 16, NV = DP / 64;
+    constexpr int NT = DP / 8;            // groups of 8 dims
     extern __shared__ __align__(16) char smem[];
     S& s = *reinterpret_cast<S*>(smem);
     __shared__ typename Cut::Shared plan;
     __shared__ ChunkItem item;
     __shared__ int ok;
-    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, dim = p.c.dim, pieces = dim / 4;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, dim = p.c.dim, pieces = dim / 4;
+    const int r0 = warp / 2 * 16, half = warp & 1, g = lane >> 2, t = lane & 3;      // rows r0 + g, r0 + g + 8
+    const int steps = (dim + 7) / 8;
+    // (Dims from dim on, up to the next multiple of 8.)
+    for (int x = tid; x < (kRows + 4 * KT) * 4; x += kThreads) s.q[x / 4][dim + x % 4] = 0.0f;
     grid_wait();
     grid_trigger();
     Cut cut;
     cut.s = &plan;
     cut.find(p);
-    const ChunkUnits<KT> units(p.c.page);
+    const ChunkUnits<KT> units(p.unit_page);
     for (;;) {
-        if (tid == 0) item = cut.item(p);
+        if (tid == 0) chunk_next_item(&cut, p, &item);
         __syncthreads();
         const ChunkItem it = item;
         __syncthreads();
@@ -79,7 +92,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         if (it.kind == 2) {
             if (tid == 0) ok = chunk_wait_parts(p.work + kChunkHead + it.share, it.need);
             __syncthreads();
-            if (ok) chunk_join<float>(p, it, tid >> 5, kThreads / 32, 0.0f);
+            if (ok) chunk_join<float>(p, it, warp, kThreads / 32, 0.0f);
             else if (tid == 0) flag(p.c.status, GS_DEV_TIMEOUT);
             __syncthreads();
             continue;
@@ -103,13 +116,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         };
         auto load = [&](int u) {
             if (u < count) {
-                for (int x = tid; x < KT * pieces; x += kThreads) {
-                    const int r = x / pieces, c = x - r * pieces;
+                // A warp has every 8th row, a lane every 32nd piece of it.
+                for (int r = warp; r < KT; r += kThreads / 32) {
                     const long long off = s.at[u % 3][r];
                     const int size = off >= 0 ? 16 : 0;
-                    const long long from = off >= 0 ? off + 16 * c : 0;
-                    copy16(&s.k[u & 1][r][4 * c], p.c.k + from, size);
-                    copy16(&s.v[u & 1][r][4 * c], p.c.v + from, size);
+                    for (int c = lane; c < pieces; c += 32) {
+                        const long long from = off >= 0 ? off + 16 * c : 0;
+                        copy16(&s.k[u & 1][r][4 * c], p.c.k + from, size);
+                        copy16(&s.v[u & 1][r][4 * c], p.c.v + from, size);
+                    }
                 }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
@@ -117,32 +132,25 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         look_up(0);
         look_up(1);
         // The queries, with the scale's sign; zeros past the tile's rows.
-        for (int x = tid; x < kRows * pieces; x += kThreads) {
-            const int r = x / pieces, c = x - r * pieces, row = it.row + r;
-            float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (r < it.rows) {
-                const int t = chunk_token(p, row), h = it.head * p.group + row - t * p.group;
-                const float* from = static_cast<const float*>(p.q) + (it.e.row + static_cast<long long>(t)) * p.q_token +
-                                    h * p.q_head + c * 4;
-                unpack16<float>(load16_any(from, p.q_aligned != 0), &f.x);
+        for (int r = warp; r < kRows; r += kThreads / 32) {
+            const int row = it.row + r, token = chunk_token(p, row), h = it.head * p.group + row - token * p.group;
+            const float* const from = static_cast<const float*>(p.q) + (it.e.row + static_cast<long long>(token)) * p.q_token +
+                                      h * p.q_head;
+            for (int c = lane; c < pieces; c += 32) {
+                float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (r < it.rows) unpack16<float>(load16_any(from + 4 * c, p.q_aligned != 0), &f.x);
+                *reinterpret_cast<float4*>(&s.q[r][c * 4]) =
+                    make_float4(f.x * p.q_sign, f.y * p.q_sign, f.z * p.q_sign, f.w * p.q_sign);
             }
-            *reinterpret_cast<float4*>(&s.q[r][c * 4]) =
-                make_float4(f.x * p.q_sign, f.y * p.q_sign, f.z * p.q_sign, f.w * p.q_sign);
         }
-        for (int r = tid; r < kRows; r += kThreads) {
-            s.top[r] = kNegInf;
-            s.sum[r] = 0.0f;
-        }
-        Pair o[4][NV][2];
+        float o[NT][4], top[2] = {kNegInf, kNegInf}, sum[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int x = 0; x < NV; ++x) o[i][x][0] = o[i][x][1] = 0ull;
+            for (int i = 0; i < 4; ++i) o[n][i] = 0.0f;
         const int from = it.e.len - it.e.m;              // position of the entry's first row
         const int first_row = from + chunk_token(p, it.row), last_row = from + chunk_token(p, it.row + it.rows - 1);
-        int pos[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) pos[i] = from + chunk_token(p, it.row + ty * 4 + i);
+        const int pos[2] = {from + chunk_token(p, it.row + r0 + g), from + chunk_token(p, it.row + r0 + g + 8)};
         __syncthreads();
         load(0);
         for (int u = 0; u < count; ++u) {
@@ -152,120 +160,189 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             load(u + 1);
             look_up(u + 2);
             asm volatile("cp.async.wait_group 1;" ::: "memory");
-            __syncthreads();
-            Pair a[4][CPT];
+            // Whether V has an infinity or NaN here: each thread looks at what it copied.
+            float zero = 0.0f;
+            for (int r = warp; r < KT; r += kThreads / 32)
+                for (int c = lane; c < pieces; c += 32) {
+                    const float4 f = *reinterpret_cast<const float4*>(&s.v[now][r][4 * c]);
+                    zero = fmaf(f.x, 0.0f, fmaf(f.y, 0.0f, fmaf(f.z, 0.0f, fmaf(f.w, 0.0f, zero))));
+                }
+            const bool odd = __syncthreads_or(zero != 0.0f) != 0;
+            // The scores of 16 rows and this half's 16 positions.
+            float x[2][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int c = 0; c < CPT; ++c) a[i][c] = 0ull;
+                for (int i = 0; i < 4; ++i) x[n][i] = 0.0f;
+            const float(*const kk)[Tile<DP>::kPitch] = s.k[now] + half * 16;
+            const float(*const vv)[Tile<DP>::kPitch] = s.v[now] + half * 16;
 #pragma unroll 2
-            for (int d = 0; d < dim; d += 4) {
-                ulonglong2 q[4], k[CPT];
+            for (int d = 0; d < steps; ++d) {
+                unsigned hi[4], lo[4];
+                split_a(s.q[r0 + g][8 * d + t], &hi[0], &lo[0]);
+                split_a(s.q[r0 + g + 8][8 * d + t], &hi[1], &lo[1]);
+                split_a(s.q[r0 + g][8 * d + t + 4], &hi[2], &lo[2]);
+                split_a(s.q[r0 + g + 8][8 * d + t + 4], &hi[3], &lo[3]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const ulonglong2*>(&s.q[ty * 4 + i][d]);
+                for (int n = 0; n < 2; ++n) mma_split(x[n], hi, lo, kk[8 * n + g][8 * d + t], kk[8 * n + g][8 * d + t + 4]);
+            }
+            // Infinities and NaNs (of queries or K) do not pass through split products.
+            float bad = 0.0f;
 #pragma unroll
-                for (int c = 0; c < CPT; ++c) k[c] = *reinterpret_cast<const ulonglong2*>(&s.k[now][tx + 16 * c][d]);
+            for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 4; ++i) bad = fmaf(x[n][i], 0.0f, bad);
+            if (__any_sync(0xffffffffu, bad != 0.0f)) {
 #pragma unroll
-                    for (int c = 0; c < CPT; ++c) a[i][c] = fma2(q[i].y, k[c].y, fma2(q[i].x, k[c].x, a[i][c]));
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (fabsf(x[n][i]) < __builtin_huge_valf()) continue;
+                        x[n][i] = 0.0f;
+                        for (int d = 0; d < dim; ++d)
+                            x[n][i] = fmaf(s.q[r0 + g + 4 * (i & 2)][d], kk[8 * n + 2 * t + (i & 1)][d], x[n][i]);
+                    }
             }
             // Whether some row does not see the whole unit.
             const bool masked = valid < KT || at + KT - 1 > first_row ||
                                 (p.window > 0 && at <= last_row - p.window && at + KT > p.sinks);
+            float w[2][4];
+            unsigned seen = 0xffu;                       // bit 4 n + i
+            float fade[2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float up = kNegInf, x[CPT];
-                bool seen[CPT];
+            for (int r = 0; r < 2; ++r) {                // rows r0 + g + 8 r
+                float up = kNegInf;
 #pragma unroll
-                for (int c = 0; c < CPT; ++c) {
-                    const int j = at + tx + 16 * c;
-                    const float2 h = halves(a[i][c]);
-                    seen[c] = !masked || (tx + 16 * c < valid && j <= pos[i] &&
-                                          (p.window == 0 || j > pos[i] - p.window || j < p.sinks));
-                    x[c] = seen[c] ? (h.x + h.y) * p.scale_log2 : kNegInf;
-                    up = fmaxf(up, x[c]);
-                }
+                for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int d = 1; d < 16; d <<= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, d));
-                const float old = s.top[ty * 4 + i];
-                up = fmaxf(up, old);
-                const float base = up == kNegInf ? 0.0f : up;
-                float sum = 0.0f;
-#pragma unroll
-                for (int c = 0; c < CPT; ++c) {
-                    const float w = chunk_pow2(x[c] - base);
-                    if (seen[c]) sum += w;
-                    s.s[ty * 4 + i][tx + 16 * c] = seen[c] ? w : -1.0f;      // -1: not to be multiplied
-                }
-#pragma unroll
-                for (int d = 1; d < 16; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                if (tx == 0) {
-                    const float fade = chunk_pow2(old - base);
-                    s.top[ty * 4 + i] = up;
-                    s.sum[ty * 4 + i] = fmaf(s.sum[ty * 4 + i], fade, sum);
-                    s.fade[ty * 4 + i] = fade;
-                }
-            }
-            __syncwarp();                                // a warp's rows are its own
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const Pair fade = twice(s.fade[ty * 4 + i]);
-#pragma unroll
-                for (int x = 0; x < NV; ++x) {
-                    o[i][x][0] = mul2(o[i][x][0], fade);
-                    o[i][x][1] = mul2(o[i][x][1], fade);
-                }
-            }
-            // O += P V, V's infinities and NaN only to rows that see them.
-            auto add = [&](auto only_seen) {
-#pragma unroll 4
-                for (int k = 0; k < valid; ++k) {
-                    float w[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) w[i] = s.s[ty * 4 + i][k];
-#pragma unroll
-                    for (int x = 0; x < NV; ++x) {
-                        const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(&s.v[now][k][x * 64 + tx * 4]);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if (!decltype(only_seen)::value || !(w[i] < 0.0f)) {
-                                o[i][x][0] = fma2(twice(w[i]), v.x, o[i][x][0]);
-                                o[i][x][1] = fma2(twice(w[i]), v.y, o[i][x][1]);
-                            }
-                        }
+                    for (int i = 2 * r; i < 2 * r + 2; ++i) {
+                        const int c = half * 16 + 8 * n + 2 * t + (i & 1), j = at + c;
+                        const bool yes = !masked || (c < valid && j <= pos[r] &&
+                                                     (p.window == 0 || j > pos[r] - p.window || j < p.sinks));
+                        if (!yes) seen &= ~(1u << (4 * n + i));
+                        x[n][i] = yes ? x[n][i] * p.scale_log2 : kNegInf;
+                        up = fmaxf(up, x[n][i]);
                     }
+                up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 1));
+                up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 2));
+                up = fmaxf(up, top[r]);
+                const float base = up == kNegInf ? 0.0f : up;
+                fade[r] = chunk_pow2(top[r] - base);
+                top[r] = up;
+                sum[r] *= fade[r];
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int i = 2 * r; i < 2 * r + 2; ++i) {
+                        w[n][i] = chunk_pow2(x[n][i] - base);
+                        if (seen >> (4 * n + i) & 1u) sum[r] += w[n][i];
+                        else w[n][i] = 0.0f;
+                    }
+            }
+            if (__any_sync(0xffffffffu, fade[0] != 1.0f || fade[1] != 1.0f)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    o[n][0] *= fade[0];
+                    o[n][1] *= fade[0];
+                    o[n][2] *= fade[1];
+                    o[n][3] *= fade[1];
                 }
-            };
-            if (masked) add(std::true_type());
-            else add(std::false_type());
+            }
+            // V's infinities and NaNs are added to the rows that see them (a weight of 0 would carry them on to
+            // the others), and zeros take their places.
+            if (odd) {
+                for (int k = 0; k < 16; ++k) {           // (lane 4 g + k / 2 % 4 has the weights of position k)
+                    const int lane_of = 4 * g + (k >> 1 & 3), i = k & 1;
+                    const unsigned bits = __shfl_sync(0xffffffffu, seen, lane_of) >> (4 * (k >> 3) + i);
+                    const float a = k < 8 ? (i ? w[0][1] : w[0][0]) : (i ? w[1][1] : w[1][0]);
+                    const float b = k < 8 ? (i ? w[0][3] : w[0][2]) : (i ? w[1][3] : w[1][2]);
+                    const float wk[2] = {__shfl_sync(0xffffffffu, a, lane_of), __shfl_sync(0xffffffffu, b, lane_of)};
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float y = vv[k][8 * n + 2 * t + (j & 1)];
+                            if (n < steps && (bits >> (j & 2) & 1u) != 0u && !(fabsf(y) < __builtin_huge_valf()))
+                                o[n][j] = fmaf(wk[j >> 1], y, o[n][j]);
+                        }
+                }
+                __syncthreads();
+                for (int r = warp; r < KT; r += kThreads / 32)
+                    for (int d = lane; d < dim; d += 32) {
+                        float* const y = &s.v[now][r][d];
+                        if (!(fabsf(*y) < __builtin_huge_valf())) *y = 0.0f;
+                    }
+                __syncthreads();
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {                // 8 positions: numbers t and t + 4 are 2 t and 2 t + 1
+                unsigned hi[4], lo[4];
+                split_a(w[k][0], &hi[0], &lo[0]);
+                split_a(w[k][2], &hi[1], &lo[1]);
+                split_a(w[k][1], &hi[2], &lo[2]);
+                split_a(w[k][3], &hi[3], &lo[3]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    if (n < steps) mma_split(o[n], hi, lo, vv[8 * k + 2 * t][8 * n + g], vv[8 * k + 2 * t + 1][8 * n + g]);
+            }
             __syncthreads();                             // (the unit's place is filled again)
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
-        __syncthreads();                                 // (the first values of top and sum, where no unit came)
-        float* const slot = p.slots + it.slot * chunk_slot_words(p.slot_rows, dim);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = ty * 4 + i;
-            if (r >= it.rows) continue;
-            const float sum = s.sum[r], top = s.top[r];
-            const bool whole = it.parts == 1;
-            const float by = !whole ? 1.0f : sum > 0.0f ? 1.0f / sum : sum;          // a NaN stays one
-            float* lse = nullptr;
-            float* const to = whole ? chunk_out<float>(p, it, it.row + r, &lse)
-                                    : slot + 2 * p.slot_rows + static_cast<long long>(r) * dim;
+        for (int r = 0; r < 2; ++r) {
+            sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
+            sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
+        }
+        // The second halves' outputs go through the place of K.
+        float(*const other)[Tile<DP>::kPitch] = reinterpret_cast<float(*)[Tile<DP>::kPitch]>(&s.k[0][0][0]);
+        __syncthreads();
+        if (half == 1) {
 #pragma unroll
-            for (int x = 0; x < NV; ++x) {
-                if (x * 64 + tx * 4 >= dim) continue;
-                const float2 lo = halves(o[i][x][0]), hi = halves(o[i][x][1]);
-                const float4 f = make_float4(lo.x * by, lo.y * by, hi.x * by, hi.y * by);
-                if (whole) chunk_put4<float>(p, to + x * 64 + tx * 4, f);
-                else *reinterpret_cast<float4*>(to + x * 64 + tx * 4) = f;
+            for (int r = 0; r < 2; ++r) {
+                const int row = r0 + g + 8 * r;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    *reinterpret_cast<float2*>(&other[row][8 * n + 2 * t]) = make_float2(o[n][2 * r], o[n][2 * r + 1]);
+                if (t == 0) {
+                    s.top[row] = top[r];
+                    s.sum[row] = sum[r];
+                }
             }
-            if (tx == 0 && whole && lse != nullptr) *lse = sum == 0.0f ? kNegInf : (top + log2f(sum)) * kChunkLn2;
-            if (tx == 0 && !whole) {
-                slot[r] = top;
-                slot[p.slot_rows + r] = sum;
+        }
+        __syncthreads();
+        if (half == 0) {
+            float* const slot = p.slots + it.slot * chunk_slot_words(p.slot_rows, dim);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int row = r0 + g + 8 * r;
+                if (row >= it.rows) continue;
+                const float up = fmaxf(top[r], s.top[row]), base = up == kNegInf ? 0.0f : up;
+                const float mine = chunk_pow2(top[r] - base), theirs = chunk_pow2(s.top[row] - base);
+                const float all = fmaf(s.sum[row], theirs, sum[r] * mine);
+                const bool whole = it.parts == 1;
+                const float by = !whole ? 1.0f : all > 0.0f ? 1.0f / all : all;        // a NaN stays one
+                float* lse = nullptr;
+                float* const to = whole ? chunk_out<float>(p, it, it.row + row, &lse)
+                                        : slot + 2 * p.slot_rows + static_cast<long long>(row) * dim;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const int d = 8 * n + 2 * t;
+                    if (d >= dim) break;
+                    const float2 y = *reinterpret_cast<const float2*>(&other[row][d]);
+                    const float2 f = make_float2(fmaf(y.x, theirs, o[n][2 * r] * mine) * by,
+                                                 fmaf(y.y, theirs, o[n][2 * r + 1] * mine) * by);
+                    if (!whole || p.out_aligned != 0) {
+                        *reinterpret_cast<float2*>(to + d) = f;
+                    } else {
+                        to[d] = f.x;
+                        to[d + 1] = f.y;
+                    }
+                }
+                if (t == 0 && whole && lse != nullptr) *lse = all == 0.0f ? kNegInf : (up + log2f(all)) * kChunkLn2;
+                if (t == 0 && !whole) {
+                    slot[row] = up;
+                    slot[p.slot_rows + row] = all;
+                }
             }
         }
         if (it.parts > 1) {
@@ -277,21 +354,23 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     if (tid < 32) chunk_leave(p, cut.used());
 }
 
-template <int DP, int KT>
+template <int DP>
 gs_status launch_as(const ChunkParams& p, int blocks, gs_stream stream) {
-    const int bytes = static_cast<int>(sizeof(typename Tile<DP, KT>::Smem));
-    if (!allow_smem<chunk_kernel<DP, KT>>(bytes)) return GS_ERR_CUDA;
-    return launch(chunk_kernel<DP, KT>, dim3(blocks), kThreads, bytes, 1, stream, p);
+    const int bytes = static_cast<int>(sizeof(typename Tile<DP>::Smem));
+    if (!allow_smem<chunk_kernel<DP>>(bytes)) return GS_ERR_CUDA;
+    return launch(chunk_kernel<DP>, dim3(blocks), kThreads, bytes, 1, stream, p);
 }
 
 }  // namespace
 
-ChunkShape chunk_fp32_shape(int) { return {kRows, sm_count()}; }
+int chunk_fp32_unit() { return KT; }
+
+ChunkShape chunk_fp32_shape(int dim) { return {kRows, dim > 128 ? sm_count() : 2 * sm_count()}; }
 
 gs_status launch_chunk_fp32(const ChunkParams& p, int blocks, gs_stream stream) {
-    if (p.c.dim <= 64) return launch_as<64, 64>(p, blocks, stream);
-    if (p.c.dim <= 128) return launch_as<128, 64>(p, blocks, stream);
-    return launch_as<256, 32>(p, blocks, stream);
+    if (p.c.dim <= 64) return launch_as<64>(p, blocks, stream);
+    if (p.c.dim <= 128) return launch_as<128>(p, blocks, stream);
+    return launch_as<256>(p, blocks, stream);
 }
 
 namespace {
@@ -396,6 +475,7 @@ extern "C" gs_status gs_chunk_attention(const gs_chunk_attention_args* args, gs_
     p.work = static_cast<int*>(args->workspace);
     p.slots = static_cast<float*>(args->workspace) + kChunkCounters;
     p.slot_rows = plan.rows;
+    p.unit_page = args->cache->dtype == GS_DTYPE_F32 ? chunk_fp32_unit() : p.c.page;
     if (args->cache->dtype == GS_DTYPE_F32) return launch_chunk_fp32(p, plan.shape.blocks, stream);
     return launch_chunk_mma(args->cache->dtype, p, plan.shape.blocks, stream);
 }

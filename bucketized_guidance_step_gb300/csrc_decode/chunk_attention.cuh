@@ -54,6 +54,7 @@ struct ChunkParams {
                                           // share: parts that are done of the tile it began and did not end
     float* slots;                         // two a share: for the tile it did not begin, the one it does not end
     int slot_rows;                        // rows of one
+    int unit_page;                        // tokens that units are cut by: a page's, or a unit's (fp32: rows are copied one by one)
 };
 
 // A slot: reference[rows], sum[rows], o[rows][dim].
@@ -336,7 +337,7 @@ struct ChunkCut {
 
     // This share's part of the tile it is at; false where it has none, or (join) nothing to join.
     __device__ __forceinline__ bool part(const ChunkParams& p, bool join, ChunkItem* it) const {
-        const ChunkUnits<KT> u(p.c.page);
+        const ChunkUnits<KT> u(p.unit_page);
         const ll at = tile_at(), all = cost.upto(tile + 1) - cost.upto(tile), end = at + all;
         it->kind = 1;
         it->e = e;
@@ -404,6 +405,14 @@ struct ChunkCut {
         }
     }
 };
+
+// The next item, apart from the kernel, whose registers are the products'.
+template <class C>
+__device__ __noinline__ void chunk_next_item(C* cut, const ChunkParams& p, ChunkItem* it) {
+    C mine = *cut;
+    *it = mine.item(p);
+    *cut = mine;
+}
 
 // The last block of the call puts the `used` words of the workspace back to 0.  A warp, after its
 // block's last use of them.
@@ -563,6 +572,7 @@ __device__ __noinline__ void chunk_join(const ChunkParams& p, const ChunkItem& i
 struct ChunkShape {
     int rows, blocks;                     // rows of a tile; blocks of the grid
 };
+int chunk_fp32_unit();                    // positions of a unit
 ChunkShape chunk_fp32_shape(int dim);
 ChunkShape chunk_mma_shape(int dim);
 gs_status launch_chunk_fp32(const ChunkParams& p, int blocks, gs_stream stream);

@@ -361,14 +361,6 @@ __device__ __noinline__ bool give_out(unsigned char* v, unsigned o_at, int dim, 
     return meet(bar, turn, dead);
 }
 
-// (Apart from the kernel, whose registers are the rows'.)
-template <class C>
-__device__ __noinline__ void next_item(C* cut, const ChunkParams& p, ChunkItem* it) {
-    C mine = *cut;
-    *it = mine.item(p);
-    *cut = mine;
-}
-
 template <class T, int DP>
 __global__ void __launch_bounds__(Shape<DP>::THREADS, 1)
 chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUtensorMap k_map,
@@ -458,7 +450,7 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
             } else {
                 if (lane == 0) {
                     ChunkItem it;
-                    next_item<typename S::Cut>(&cut, p, &it);
+                    chunk_next_item(&cut, p, &it);
                     if (bar_wait(smem_at(&s.item_empty[slot]), ((n >> 1) & 1) ^ 1, &s.dead)) {
                         s.items[slot] = it;
                         kind = it.kind;
