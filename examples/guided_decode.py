@@ -5,16 +5,18 @@ classifier-free guidance. Every sample has two branches over one shared prompt:
 
 * the prompt's keys and values are stored once (``write``), sequence by sequence;
 * the uncond branch forks from it (``fork``: full pages are shared, the last one is copied);
-* the cond branch then reads the sample's condition tokens;
+* the cond branch then reads the sample's condition tokens (prompts are read in chunks: ``write``,
+  then ``chunk_attention`` over everything stored so far);
 * a decode step makes room for one token of every branch (``extend``), attends layer by layer
   while storing the new keys and values (``attention`` with ``k_new`` / ``v_new``), and turns the
   two branches' logits into the next token (``guided_logits``: scale from the bucket plan,
-  penalties, temperature, a mask of allowed tokens, Gumbel noise as an input);
+  penalties, temperature, a mask of allowed tokens, Gumbel noise as an input); with ``--top-k``,
+  ``--top-p`` or ``--min-p`` the token comes from what these keep of its result (``sample``);
 * finished sequences are freed and the pool is made dense (``free``, ``compact``).
 
 The step has no host synchronisation: it is captured in a CUDA graph once and replayed.
 
-    python examples/guided_decode.py [--batch 4] [--steps 32] [--dtype bf16]
+    python examples/guided_decode.py [--batch 4] [--steps 32] [--dtype bf16] [--top-k 50] [--top-p 0.9]
 """
 
 import argparse
@@ -110,20 +112,29 @@ class Decoder:
         words = (c.vocab + 31) // 32
         self.mask = torch.full((1, words), -1, **i32)             # every token allowed
         self.mask[0, 0] = -2                                      # but token 0
+        self.kept = None                                          # sample's top_k, top_p and min_p
 
-    def read(self, seq, tokens):
-        """Prompt tokens ([n, t], the same number for every listed sequence) into the cache: each
-        position attends over what is stored before it, one position of all sequences at a time."""
-        n, t = tokens.shape
-        one = torch.arange(n + 1, dtype=torch.int32, device="cuda")
-        for i in range(t):
-            at = self.lens[seq.long()]
-            self.cache.extend(seq)
-            x = self.model.start(tokens[:, i], at)
+    def keep(self, top_k=0, top_p=1.0, min_p=0.0):
+        """Draw tokens from what top_k, then top_p, then min_p leave of guided_logits' result."""
+        full, dev = torch.full, "cuda"
+        self.kept = dict(top_k=full((self.batch,), top_k, dtype=torch.int32, device=dev),
+                         top_p=full((self.batch,), top_p, device=dev), min_p=full((self.batch,), min_p, device=dev))
+
+    def read(self, seq, tokens, chunk=64):
+        """Prompt tokens ([n, t], the same number for every listed sequence) into the cache, up to
+        `chunk` of each sequence at a time: their keys and values are stored, and each position
+        attends over everything up to itself."""
+        n = len(tokens)
+        for part in tokens.split(chunk, 1):
+            t = part.shape[1]
+            at = self.lens[seq.long()][:, None] + torch.arange(t, device="cuda")
+            self.cache.extend(seq, torch.full_like(seq, t))
+            start = t * torch.arange(n + 1, dtype=torch.int32, device="cuda")
+            x = self.model.start(part.flatten(), at.flatten())
             for layer in range(self.model.cfg.layers):
                 q, k, v = self.model.split(layer, x)
-                self.cache.write(layer, k, v, seq, one)
-                x = self.model.join(layer, x, self.cache.attention(q, layer, seq=seq))
+                self.cache.write(layer, k, v, seq, start)
+                x = self.model.join(layer, x, self.cache.chunk_attention(q, layer, seq, start))
 
     def step(self):
         """One token of every sample."""
@@ -138,17 +149,23 @@ class Decoder:
                              tokens=self.tokens, tokens_len=self.tokens_len, prompt_len=self.prompt_len,
                              mask=self.mask, noise=self.noise, out=self.z, token=self.token,
                              logprob=self.logprob, status=self.status, **self.settings)
+        if self.kept is not None:                                 # (z has the temperature in it)
+            decode.sample(self.z, noise=self.noise, token=self.token, logprob=self.logprob, status=self.status,
+                          **self.kept)
         self.tokens.scatter_(1, self.tokens_len.long()[:, None], self.token[:, None])
         self.tokens_len += 1
         self.step_idx += 1
 
 
-def run(batch=4, steps=32, dtype="bf16", cfg=Config(), prompt=21, condition=5, seed=0, graph=True, watch=None):
+def run(batch=4, steps=32, dtype="bf16", cfg=Config(), prompt=21, condition=5, seed=0, graph=True, watch=None,
+        keep=None):
     """Decodes `steps` tokens; returns (tokens [batch, steps], log-probabilities, decoder).
-    watch(decoder): called after every step."""
+    watch(decoder): called after every step. keep: Decoder.keep's arguments."""
     dt = DTYPES[dtype]
     model = Model(cfg, dt, seed)
     d = Decoder(model, batch, steps, dt)
+    if keep is not None:
+        d.keep(**keep)
     g = torch.Generator(device="cuda").manual_seed(seed + 1)
     shared = torch.randint(1, cfg.vocab, (1, prompt), generator=g, device="cuda", dtype=torch.int32)
     wanted = torch.randint(1, cfg.vocab, (batch, condition), generator=g, device="cuda", dtype=torch.int32)
@@ -189,8 +206,13 @@ def main():
     ap.add_argument("--batch", type=int, default=4)
     ap.add_argument("--steps", type=int, default=32)
     ap.add_argument("--dtype", choices=sorted(DTYPES), default="bf16")
+    ap.add_argument("--top-k", type=int, default=0, help="0: all")
+    ap.add_argument("--top-p", type=float, default=1.0)
+    ap.add_argument("--min-p", type=float, default=0.0)
     a = ap.parse_args()
-    tokens, logprobs, d = run(a.batch, a.steps, a.dtype)
+    keep = dict(top_k=a.top_k, top_p=a.top_p, min_p=a.min_p)
+    some = a.top_k > 0 or a.top_p < 1 or a.min_p > 0
+    tokens, logprobs, d = run(a.batch, a.steps, a.dtype, keep=keep if some else None)
     live = torch.zeros(1, dtype=torch.int32, device="cuda")
     for row, lp in zip(tokens.tolist(), logprobs.sum(1).tolist()):
         print(f"log-probability {lp:9.3f}: {row}")
