@@ -582,6 +582,82 @@ __device__ __noinline__ void sort_list(unsigned long long* list, int n) {
 }
 static_assert(kList == 4 * kThreads, "lists that are sorted");
 
+// The same, by 2048 pieces of the list's range of z, where hardly any share one: an entry's place is that of
+// its piece and the number of larger ones in it.  (From 128 entries on; below, one warp exchanges them.)
+constexpr int kCrowd = 24;                // entries of a piece that are compared with each other
+__device__ __noinline__ void order_list(Shared& s, int n) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int E = kList / kThreads;
+    if (n <= 128) {
+        sort_list(s.list, n);
+        return;
+    }
+    __syncthreads();
+    unsigned long long x[E];
+    unsigned top = 0u, bottom = 0xffffffffu;
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+        const int i = tid + j * kThreads;
+        x[j] = i < n ? s.list[i] : 0ull;
+        const unsigned key = static_cast<unsigned>(x[j] >> 32);
+        if (i < n) {
+            top = max(top, key);
+            bottom = min(bottom, key);
+        }
+        s.count[i] = 0u;
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    bottom = __reduce_min_sync(0xffffffffu, bottom);
+    if (lane == 0) {
+        s.u[warp] = top;
+        s.v[warp] = bottom;
+    }
+    __syncthreads();
+    top = __reduce_max_sync(0xffffffffu, s.u[lane & (kWarps - 1)]);
+    bottom = __reduce_min_sync(0xffffffffu, s.v[lane & (kWarps - 1)]);
+    const Pieces pieces(value_of(top), value_of(top) - value_of(bottom));
+    int piece[E];
+    unsigned nth[E];
+    bool crowded = false;
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+        piece[j] = pieces.of(value_of(static_cast<unsigned>(x[j] >> 32)));
+        nth[j] = tid + j * kThreads < n ? atomicAdd(&s.count[piece[j]], 1u) : 0u;
+        crowded = crowded || nth[j] >= kCrowd;
+    }
+    if (__syncthreads_or(crowded)) {
+        sort_list(s.list, n);
+        return;
+    }
+    unsigned c[E], mine = 0, all;
+#pragma unroll
+    for (int j = 0; j < E; ++j) mine += c[j] = s.count[tid * E + j];
+    unsigned before = block_scan<kThreads>(mine, reinterpret_cast<unsigned*>(s.scan), &all);
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+        s.count[tid * E + j] = before;
+        before += c[j];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+        if (tid + j * kThreads < n) s.list[s.count[piece[j]] + nth[j]] = x[j];
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+        if (tid + j * kThreads >= n) continue;
+        const unsigned first = s.count[piece[j]], end = piece[j] + 1 < kDigits ? s.count[piece[j] + 1] : n;
+        nth[j] = first;
+        for (unsigned i = first; i < end; ++i) nth[j] += s.list[i] > x[j];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+        if (tid + j * kThreads < n) s.list[nth[j]] = x[j];
+    __syncthreads();
+}
+static_assert(kList == kDigits, "a piece an entry");
+
 // The best token so far: what it is chosen by, its index, its z.
 struct Best {
     float pick, z;
@@ -643,7 +719,7 @@ __device__ __forceinline__ unsigned long long reach_of(float top_p, unsigned lon
 // The first block, with all tokens that may stay in its list: the filters and the token.
 __device__ __noinline__ void finish_list(const SampleParams& p, Shared& s, const Weigh& weigh, int b, int n, int k,
                                          float top_p, float min_p, const float* noise) {
-    sort_list(s.list, n);
+    order_list(s, n);
     const int kept = k > 0 ? min(k, n) : n;
     constexpr int PER = kList / kThreads;
     const int per = (n + kThreads - 1) / kThreads, i0 = threadIdx.x * per;
@@ -796,8 +872,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         cluster_sync();
         const unsigned n = gather_lists(s, p.cluster, rank);
         if (some && n <= kList) {
+            cluster_sync();               // (lists stay until they are read; the others' SMs take the next row)
             if (rank == 0) finish_list(p, s, weigh, b, static_cast<int>(n), by_k ? k : 0, top_p, min_p, noise);
-            cluster_sync();               // (lists stay until they are read)
             return;
         }
         cluster_sync();
@@ -868,7 +944,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         if (n <= kList) {
             known = true;
             if (rank == 0) {
-                sort_list(s.list, n);
+                order_list(s, static_cast<int>(n));
                 constexpr int PER = kList / kThreads;
                 const int per = (static_cast<int>(n) + kThreads - 1) / kThreads, i0 = tid * per;
                 unsigned long long mine = 0, all, units[PER];
