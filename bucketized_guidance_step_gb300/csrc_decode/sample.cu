@@ -1000,27 +1000,58 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     Best best = {kNegInf, 0.0f, kNobody};
     float sum = 0.0f, rest = 0.0f;        // (sum - rest: what rounding left out is kept)
     const float least = min_p * 0.99f;    // (weights of neighbouring z are not compared with min_p itself)
-    part.vectors([&](int v) {
-        if (edge == kNegInf && !(least > 0.0f)) return true;
-        const float most = part.most_z(v);
-        return most >= edge && (!(least > 0.0f) || weigh.weight(most) >= least || most == weigh.ref);
-    }, [&](const float (&z)[V], int at) {
-        float here = 0.0f, add[V];
-        bool stays[V];
+    const bool all = edge == kNegInf && !(least > 0.0f);
+    // What stays has z >= from, or in vectors up to the limit z >= edge, and no weight below `light`.
+    const float from = min_p > 1.0f && edge < weigh.ref ? weigh.ref : value_of(key_of(edge) + 1u);       // (NaN above +inf)
+    const float tied = edge == kNegInf ? from : min_p > 1.0f ? weigh.ref : edge, light = min_p > 1.0f ? 0.0f : min_p;
+    const bool by4 = noise != nullptr && part.shift == 0 && (reinterpret_cast<unsigned long long>(noise) & 15ull) == 0;
+    bool some = false;
+    auto pass = [&](auto take) {
+        part.vectors([&](int v) {
+            if (all) return true;
+            const float most = part.most_z(v);
+            return most >= edge && (!(least > 0.0f) || weigh.weight(most) >= least || most == weigh.ref);
+        }, [&](float (&z)[V], int at) {
+            float add[V], here = 0.0f;
+            const bool vector = by4 && at + V <= p.vocab;
+            if (vector) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float w = weigh.weight(z[i]);
-            stays[i] = (z[i] > edge || (z[i] == edge && at + i <= limit)) && (!(w < min_p) || z[i] == weigh.ref);
-            here += stays[i] ? w : 0.0f;
-            add[i] = stays[i] && noise != nullptr ? noise[at + i] : 0.0f;
-        }
-        const float y = here - rest, t = sum + y;
-        rest = (t - sum) - y;
-        sum = t;
+                for (int i = 0; i < V; i += 4) *reinterpret_cast<float4*>(add + i) = *reinterpret_cast<const float4*>(noise + at + i);
+            }
+            const float low = at > limit ? from : tied;
+            if (at <= limit && at + V - 1 > limit) {     // (one vector of the row)
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (stays[i]) best.take(z[i] + add[i], at + i, z[i]);
+                for (int i = 0; i < V; ++i)
+                    if (z[i] == edge && at + i > limit) z[i] = kNegInf;
+            }
+            bool stays[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float w = weigh.weight(z[i]);
+                stays[i] = z[i] >= low && !(w < light);
+                here += stays[i] ? w : 0.0f;
+                some = some || stays[i];
+            }
+            if (!vector) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) add[i] = stays[i] && noise != nullptr ? noise[at + i] : 0.0f;
+            }
+            const float y = here - rest, t = sum + y;
+            rest = (t - sum) - y;
+            sum = t;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (stays[i]) take(z[i] + add[i], at + i, z[i]);
+        });
+    };
+    // (A thread's indices rise: of equal ones the first stays.)
+    pass([&](float x, int at, float z) {
+        if (x > best.pick) best = {x, z, at};
     });
+    if (best.at == kNobody && some) {     // noise of -inf or NaN alone
+        sum = rest = 0.0f;
+        pass([&](float x, int at, float z) { best.take(x, at, z); });
+    }
     join_block(s, &best, &sum);
     if (tid == 0) {
         s.shown.pick = best.pick;
