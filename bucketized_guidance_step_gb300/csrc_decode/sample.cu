@@ -29,6 +29,7 @@ constexpr int kThreads = 512, kWarps = kThreads / 32, kDigits = 2048;
 constexpr int kMaxCluster = 8;
 constexpr int kHeld = 66 * 1024;          // bytes of a row that a block holds: two blocks an SM
 constexpr int kList = 2048, kMostK = 1024;               // tokens of a list; largest top-k that goes by one
+constexpr int kMostVocab = 1 << 23;       // (their weights' sum stays below 2^64 units)
 constexpr unsigned kNone = 0x007fffffu;   // the key of -inf: such tokens are not kept
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -54,8 +55,7 @@ struct Shown {
     unsigned long long above, above_weight, here;        // what lies above the found digit; its tokens
     int digit;
     unsigned listed;                      // tokens in the first block's list
-    unsigned border;                      // the last token that is kept
-    int limit;
+    unsigned long long border;            // the last token that is kept (an entry)
     unsigned ties;                        // tokens at the border
     float pick, sum;                      // best token of the block, and the weights it keeps
     int best;
@@ -71,6 +71,7 @@ struct alignas(16) Shared {
         };
     };
     unsigned count[kDigits];
+    unsigned long long weights[kDigits];  // of the whole row, a digit
     unsigned long long scan[kWarps + 1];
     float f[kWarps], g[kWarps];
     int i[kWarps];
@@ -110,6 +111,15 @@ __device__ __forceinline__ V far(const V* local, unsigned r) {
         asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(b) : "memory");
         return *reinterpret_cast<V*>(&v);
     }
+}
+
+template <class V>
+__device__ __forceinline__ void put_far(V* local, unsigned r, V v) {
+    const unsigned a = static_cast<unsigned>(__cvta_generic_to_shared(local));
+    unsigned b;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(a), "r"(r));
+    if constexpr (sizeof(V) == 8) asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(b), "l"(v) : "memory");
+    else asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(b), "r"(v) : "memory");
 }
 
 // A row's divisor.  Where it is usual, a product with the rounded reciprocal and one correction by its
@@ -289,8 +299,8 @@ struct Found {
 
 // The digit at which the counts (BY_WEIGHT false) or weights of the cluster's histograms reach `target`,
 // which reach(all) names.  Called once the histograms are whole (a cluster barrier); nobody reads them
-// afterwards, and what the blocks show stays until the next barrier.  WITH: the other sum is there too.
-template <bool BY_WEIGHT, bool WITH, class R>
+// afterwards, and what the blocks show stays until the next barrier.
+template <bool BY_WEIGHT, class R>
 __device__ Found locate(Shared& s, int digits, unsigned long long before_all, unsigned long long before_weight,
                         int cluster, unsigned rank, R reach) {
     // This block's share of the digits, over all blocks.
@@ -308,9 +318,9 @@ __device__ Found locate(Shared& s, int digits, unsigned long long before_all, un
         unsigned n[kMaxCluster], lo[kMaxCluster], hi[kMaxCluster];   // (asked for together)
 #pragma unroll
         for (int r = 0; r < kMaxCluster; ++r) {
-            n[r] = (!BY_WEIGHT || WITH) && r < cluster ? far(&s.count[d], r) : 0u;
-            lo[r] = (BY_WEIGHT || WITH) && r < cluster ? far(&s.low[d], r) : 0u;
-            hi[r] = (BY_WEIGHT || WITH) && r < cluster ? far(&s.high[d], r) : 0u;
+            n[r] = r < cluster ? far(&s.count[d], r) : 0u;
+            lo[r] = r < cluster ? far(&s.low[d], r) : 0u;
+            hi[r] = r < cluster ? far(&s.high[d], r) : 0u;
         }
 #pragma unroll
         for (int r = 0; r < kMaxCluster; ++r) {
@@ -322,8 +332,8 @@ __device__ Found locate(Shared& s, int digits, unsigned long long before_all, un
     }
     unsigned long long all, ignored;
     unsigned long long w = 0, c = 0;      // before this thread's digits
-    if (!BY_WEIGHT || WITH) c = block_scan<kThreads>(counts, s.scan, BY_WEIGHT ? &ignored : &all);
-    if (BY_WEIGHT || WITH) w = block_scan<kThreads>(weights, s.scan, BY_WEIGHT ? &all : &ignored);
+    c = block_scan<kThreads>(counts, s.scan, BY_WEIGHT ? &ignored : &all);
+    w = block_scan<kThreads>(weights, s.scan, BY_WEIGHT ? &all : &ignored);
     if (threadIdx.x == 0) {
         s.shown.all = all;
         s.shown.weight = BY_WEIGHT ? all : ignored;
@@ -334,11 +344,11 @@ __device__ Found locate(Shared& s, int digits, unsigned long long before_all, un
     Found f = {-1, 0, 0, 0, 0};
     const bool other = lane < cluster, earlier = lane < static_cast<int>(rank);
     const unsigned long long theirs = other ? far(&s.shown.all, lane) : 0ull;
-    const unsigned long long their_w = other && WITH ? far(&s.shown.weight, lane) : BY_WEIGHT ? theirs : 0ull;
-    const unsigned long long their_c = other && WITH ? far(&s.shown.ties, lane) : BY_WEIGHT ? 0ull : theirs;
+    const unsigned long long their_w = other ? far(&s.shown.weight, lane) : 0ull;
+    const unsigned long long their_c = other ? far(&s.shown.ties, lane) : 0ull;
     f.all = warp_sum(theirs);
-    const unsigned long long earlier_w = before_weight + (BY_WEIGHT || WITH ? warp_sum(earlier ? their_w : 0ull) : 0ull);
-    const unsigned long long earlier_c = before_all + (!BY_WEIGHT || WITH ? warp_sum(earlier ? their_c : 0ull) : 0ull);
+    const unsigned long long earlier_w = before_weight + warp_sum(earlier ? their_w : 0ull);
+    const unsigned long long earlier_c = before_all + warp_sum(earlier ? their_c : 0ull);
     const unsigned long long target = reach(f.all);
     c += earlier_c;
     w += earlier_w;
@@ -365,6 +375,65 @@ __device__ Found locate(Shared& s, int digits, unsigned long long before_all, un
         f.above = far(&s.shown.above, r);
         f.above_weight = far(&s.shown.above_weight, r);
         f.here = far(&s.shown.here, r);
+    }
+    return f;
+}
+
+// The same for kDigits digits and one of the sums: each block adds up its share of the digits and writes the
+// sums to all blocks, each of which then looks by itself (one way to other SMs and back fewer than above).
+// Sums of counts lie where s.low does.
+template <bool BY_WEIGHT, class R>
+__device__ __noinline__ Found locate_one(Shared& s, int cluster, unsigned rank, R reach) {
+    using Sum = typename std::conditional<BY_WEIGHT, unsigned long long, unsigned>::type;
+    constexpr int PER = kDigits / kThreads;
+    Sum* sums;
+    if constexpr (BY_WEIGHT) sums = s.weights;
+    else sums = cluster > 1 ? s.low : s.count;
+    if (cluster > 1 || BY_WEIGHT) {
+        const int share = kDigits / cluster;
+        for (int x = threadIdx.x; x < share; x += kThreads) {
+            const int d = rank * share + x;
+            Sum sum = 0;
+            if (cluster > 1) {
+                unsigned n[kMaxCluster], hi[kMaxCluster];            // (asked for together)
+#pragma unroll
+                for (int r = 0; r < kMaxCluster; ++r) {
+                    n[r] = r < cluster ? far(BY_WEIGHT ? &s.low[d] : &s.count[d], r) : 0u;
+                    hi[r] = BY_WEIGHT && r < cluster ? far(&s.high[d], r) : 0u;
+                }
+#pragma unroll
+                for (int r = 0; r < kMaxCluster; ++r) sum += static_cast<Sum>((static_cast<unsigned long long>(hi[r]) << 32) + n[r]);
+#pragma unroll
+                for (int r = 0; r < kMaxCluster; ++r)
+                    if (r < cluster) put_far(&sums[d], r, sum);
+            } else {
+                sums[d] = static_cast<Sum>((static_cast<unsigned long long>(s.high[d]) << 32) + s.low[d]);
+            }
+        }
+        if (cluster > 1) cluster_sync();
+        else __syncthreads();
+    }
+    Sum mine[PER], total = 0, all;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) total += mine[j] = sums[threadIdx.x * PER + j];
+    if (threadIdx.x == 0) s.shown.digit = -1;
+    Sum at = block_scan<kThreads>(total, reinterpret_cast<Sum*>(s.scan), &all);
+    const unsigned long long target = reach(all);
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        if (at < target && at + mine[j] >= target) {
+            s.shown.digit = static_cast<int>(threadIdx.x) * PER + j;
+            s.shown.above = at;
+            s.shown.here = mine[j];
+        }
+        at += mine[j];
+    }
+    __syncthreads();
+    Found f = {s.shown.digit, 0, 0, 0, all};
+    if (f.digit >= 0) {
+        f.above = BY_WEIGHT ? 0 : s.shown.above;
+        f.above_weight = BY_WEIGHT ? s.shown.above : 0;
+        f.here = BY_WEIGHT ? 0 : s.shown.here;
     }
     return f;
 }
@@ -401,7 +470,7 @@ __device__ __noinline__ Border find_border(Shared& s, const P& part, const Weigh
             add_weight(s, d, weigh.units(z));
         });
         cluster_sync();                   // (also: what the last level has shown is read)
-        const Found f = locate<BY_WEIGHT, true>(s, digits, b.above, b.weight, cluster, rank,
+        const Found f = locate<BY_WEIGHT>(s, digits, b.above, b.weight, cluster, rank,
                                                 [&](unsigned long long) { return target; });
         b.key = prefix << bits;
         b.need = 0;
@@ -584,7 +653,7 @@ static_assert(kList == 4 * kThreads, "lists that are sorted");
 
 // The same, by 2048 pieces of the list's range of z, where hardly any share one: an entry's place is that of
 // its piece and the number of larger ones in it.  (From 128 entries on; below, one warp exchanges them.)
-constexpr int kCrowd = 24;                // entries of a piece that are compared with each other
+constexpr int kCrowd = 64;                // entries of a piece that are compared with each other
 __device__ __noinline__ void order_list(Shared& s, int n) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int E = kList / kThreads;
@@ -855,8 +924,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
                 if (most > kNegInf) atomicAdd(&s.count[pieces.of(most)], 1u);
             }
             cluster_sync();
-            const Found f = locate<false, false>(s, kDigits, 0, 0, p.cluster, rank,
-                                                 [&](unsigned long long) { return static_cast<unsigned long long>(k); });
+            const Found f = locate_one<false>(s, p.cluster, rank,
+                                              [&](unsigned long long) { return static_cast<unsigned long long>(k); });
             if (f.digit >= 0) last = f.digit;
             some = f.above + f.here <= kList;            // (else there are too many tokens for certain)
         }
@@ -928,7 +997,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         if (lane == 0) add_weight(s, kDigits - 1, __float2ull_rz(rest * 1099511627776.0f));
         cluster_sync();
         unsigned long long target = 0;
-        const Found f = locate<true, false>(s, kDigits, 0, 0, p.cluster, rank, [&](unsigned long long all) {
+        const Found f = locate_one<true>(s, p.cluster, rank, [&](unsigned long long all) {
             return target = reach_of(top_p, all);
         });
         part.vectors([&](int v) {
@@ -957,17 +1026,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 #pragma unroll
                 for (int j = 0; j < PER; ++j) {
                     if (units[j] > 0 && before < target && before + units[j] >= target) {
-                        s.shown.border = static_cast<unsigned>(s.list[i0 + j] >> 32);
-                        s.shown.limit = static_cast<int>(~static_cast<unsigned>(s.list[i0 + j]));
+                        const unsigned long long e = s.list[i0 + j];
+                        if (p.cluster == 1) s.shown.border = e;
+                        for (int r = 0; p.cluster > 1 && r < p.cluster; ++r) put_far(&s.shown.border, r, e);
                     }
                     before += units[j];
                 }
             }
             cluster_sync();
-            edge = value_of(far(&s.shown.border, 0));
-            limit = far(&s.shown.limit, 0);
+            edge = value_of(static_cast<unsigned>(s.shown.border >> 32));
+            limit = static_cast<int>(~static_cast<unsigned>(s.shown.border));
+        } else {
+            cluster_sync();               // (what follows takes the lists' place)
         }
-        cluster_sync();
     }
     if (!known) {
         Border last = {kNone + 1u, ~0ull, 0ull, 0ull};   // everything
@@ -1105,7 +1176,7 @@ using namespace gs_decode;
 
 extern "C" gs_status gs_sample(const gs_sample_args* a, gs_stream stream) {
     if (a == nullptr || a->batch < 0 || a->vocab < 1 || !known_dtype(a->dtype)) return GS_ERR_INVALID_ARG;
-    if (a->batch > GS_MAX_SEQS || a->vocab > (1 << 28)) return GS_ERR_UNSUPPORTED;
+    if (a->batch > GS_MAX_SEQS || a->vocab > kMostVocab) return GS_ERR_UNSUPPORTED;
     if (a->token == nullptr && a->logprob == nullptr) return GS_ERR_INVALID_ARG;
     if (a->batch == 0) return GS_OK;
     const long long es = elem_size(a->dtype);

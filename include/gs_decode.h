@@ -375,7 +375,7 @@ typedef struct gs_sample_args {
  * the same weight and the others have none.  Sums of weights decide in units of 2^-40 of the largest
  * weight, the weights themselves are good to about 2^-21.
  * Errors: GS_ERR_INVALID_ARG (NULL logits, sizes, strides, unknown dtype, neither token nor logprob),
- * GS_ERR_UNSUPPORTED (batch over GS_MAX_SEQS, vocab over 2^28), GS_ERR_CUDA.  batch = 0 does nothing.
+ * GS_ERR_UNSUPPORTED (batch over GS_MAX_SEQS, vocab over 2^23), GS_ERR_CUDA.  batch = 0 does nothing.
  * No output may overlap an input or another output.
  */
 gs_status gs_sample(const gs_sample_args* args, gs_stream stream);

@@ -32,6 +32,7 @@ def _args():
 @pytest.mark.parametrize("field,value,status", [
     ("batch", -1, gs.GS_ERR_INVALID_ARG), ("batch", 8193, gs.GS_ERR_UNSUPPORTED),
     ("vocab", 0, gs.GS_ERR_INVALID_ARG), ("vocab", (1 << 28) + 1, gs.GS_ERR_UNSUPPORTED),
+    ("vocab", (1 << 23) + 1, gs.GS_ERR_UNSUPPORTED),
     ("dtype", 3, gs.GS_ERR_INVALID_ARG), ("logits", None, gs.GS_ERR_INVALID_ARG),
     ("logits", 0x10001, gs.GS_ERR_INVALID_ARG), ("row_stride", 99, gs.GS_ERR_INVALID_ARG),
     ("noise_stride", -1, gs.GS_ERR_INVALID_ARG), ("noise", 0x40002, gs.GS_ERR_INVALID_ARG),
