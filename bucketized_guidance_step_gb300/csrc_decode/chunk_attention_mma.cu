@@ -978,7 +978,7 @@ gs_status launch_chunk_mma(int dtype, ChunkParams& p, int blocks, gs_stream stre
     // TMA brings the queries as they are, in boxes that hold whole tokens of a group, from rows on 16 bytes.
     p.q_boxes = p.q_aligned != 0 && p.q_sign > 0.0f && 128 % p.group == 0 && (p.tokens == 1 || p.q_token > 0) &&
                 (p.q_heads == 1 || p.q_head > 0);
-    if (p.q_boxes != 0 && !encode_q(&m.q, dtype, p)) return GS_ERR_CUDA;
+    if (p.q_boxes != 0 && !encode_q(&m.q, dtype, p)) p.q_boxes = 0;  // (strides that no map holds)
     if (dtype == GS_DTYPE_BF16) return launch_type<__nv_bfloat16>(p, m, blocks, stream);
     return launch_type<__half>(p, m, blocks, stream);
 }

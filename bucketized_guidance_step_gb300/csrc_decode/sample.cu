@@ -127,9 +127,10 @@ __device__ __forceinline__ void put_far(V* local, unsigned r, V v) {
 // Computation of elementary functions on the IBM RISC System/6000 processor, 1990); infinities and NaN stay.
 struct Divisor {
     float by, inverse;
-    bool one, usual;
+    bool one, usual, endless;
     __device__ __forceinline__ explicit Divisor(float t) : by(t > 0.0f ? t : 1.0f), inverse(1.0f / by) {
         one = by == 1.0f;
+        endless = by == __builtin_huge_valf();
         usual = by >= 0x1p-30f && by <= 0x1p30f;
     }
     template <int V>
@@ -154,10 +155,10 @@ struct Divisor {
             for (int i = 0; i < V; ++i) z[i] = __fdiv_rn(z[i], by);
         }
     }
-    __device__ __forceinline__ float of(float z) const {
+    __device__ __forceinline__ float of(float z) const {             // (-inf for NaN)
         float x[1] = {z};
         divide<1>(x, true);
-        return x[0];
+        return fmaxf(x[0], kNegInf);
     }
 };
 
@@ -188,6 +189,13 @@ struct Part {
     }
     // The largest logit of vector v as it is (a quotient's order is that of the logits); -inf for none.
     __device__ __forceinline__ float most(int v) const {
+        if (cool.endless) {               // infinities become NaN: 0 where there is a finite logit
+            float z[V], m = kNegInf;
+            values(v, z);
+#pragma unroll
+            for (int i = 0; i < V; ++i) m = fmaxf(m, z[i]);
+            return m;
+        }
         if (v < whole0 || v > whole1) {
             float m = kNegInf;
 #pragma unroll 1

@@ -204,6 +204,24 @@ def test_infinities_and_nan(dtype):
     assert torch.all(token == -1) and torch.all(torch.isneginf(logprob)) and word == decode.GS_DEV_EMPTY_ROW
 
 
+@pytest.mark.parametrize("V", [1000, 40000, 600000])
+def test_endless_temperature(V):
+    """z is 0 for finite logits, and NaN, not kept, for infinite ones."""
+    inf = float("inf")
+    x = draw(4, V, F32, 12)
+    x[0, ::3] = inf
+    x[1, 1::2] = -inf
+    x[2] = inf
+    x[2, V - 7] = 2.0
+    x[3] = -inf
+    kw = dict(temperature=torch.full((4,), inf, device="cuda"))
+    for some in ({}, dict(top_k=torch.tensor([3, 50, 2, 1]).int().cuda()), dict(top_p=torch.full((4,), 0.4, device="cuda"))):
+        for noise in (None, gumbel((4, V), 3)):
+            token, logprob, word = run(x, noise=noise, **kw, **some)
+            check(x, token, logprob, noise=noise, **kw, **some)
+            assert word == decode.GS_DEV_EMPTY_ROW and int(token[2]) == V - 7 and int(token[3]) == -1
+
+
 def test_settings_outside_their_ranges():
     """Negative, zero, huge and tiny settings."""
     V = 3000
