@@ -13,7 +13,9 @@
 // there are blocks, each a run of neighbouring tiles and parts of tiles.  So ragged chunks and lengths
 // balance without the host knowing them, one long sequence spreads over every block, and there are two
 // parts a share at most.  A share whose edge would leave less than two units of a tile, or lies in a tile
-// of few, takes or leaves the tile whole.
+// of few, takes or leaves the tile whole.  Where tiles are more than the blocks and none is large, all stay whole:
+// shares of falling size balance them without joins (16 chunks of up to 512 tokens, window 1024, 16 and 4 heads of 128:
+// 105 us cut, 75 us whole; 8 prompts of up to 2048 tokens, 32 and 8 heads of 128: 164 us and 152 us).
 //
 // Blocks take shares from a queue, and once there are no more, the joins of the shares' parts: what waits
 // for a part waits for a block that is running.  The outputs of a share do not depend on who computes it
@@ -191,11 +193,16 @@ struct ChunkCut {
     static constexpr int kOver = 16 * 288;               // what a tile costs beside its positions
     static constexpr int kFew = 8;        // units of a tile that is not cut
     static constexpr int kLeast = 2;      // units of a part
+    static constexpr int kCut = KT == 64 ? 16 * 1920 : 16 * 128;     // what cutting costs a block (about 25 us and 10 us)
+    static constexpr int kLevels = 4;     // of sizes of shares, where tiles stay whole
     struct Shared {
         ll before[WIDTH];                 // cost before a thread's entries
         ll tmp[THREADS / 32 + 1];
         ll each;                          // shares: the first `more` have each + 1, the others each
         int more, shares;
+        int levels, per;                  // whole tiles: levels of shares, shares of a level, ...
+        ll begin[kLevels + 1], step[kLevels];            // ... and where they begin
+        unsigned most;                    // the largest tile's cost
     };
 
     // What the tiles of a head cost: a tile whose last row sees `a` positions kOver + a, a_t = from + (t + 1)
@@ -236,6 +243,34 @@ struct ChunkCut {
         return c;
     }
 
+    // Where tiles are many and none is large, whole tiles balance as well as cut ones, and need no joins.
+    __device__ __noinline__ void keep_whole(const ChunkParams& p, ll all, int tiles) {
+        const int per = (p.n + WIDTH - 1) / WIDTH, i0 = threadIdx.x * per, i1 = min(p.n, i0 + per);
+        unsigned mine = 0, ignore = 0;
+        for (int k = i0; k < i1; ++k) {
+            const Cost c = cost_of(p, chunk_entry(p, k, &ignore));
+            if (c.tiles > 0) mine = max(mine, static_cast<unsigned>(min(c.upto(c.tiles) - c.upto(c.tiles - 1), 0x7fffffffll)));
+        }
+        __syncthreads();
+        if (mine > 0) atomicMax(&s->most, mine);
+        __syncthreads();
+        if (threadIdx.x > 0) return;
+        const int blocks = gridDim.x;
+        const ll most = s->most;
+        if (tiles >= 2 * blocks ? 3 * most > 4 * kCut : 2 * most > s->each + kCut) return;
+        s->levels = tiles < 4 * blocks ? 2 : tiles < 8 * blocks ? 3 : kLevels;
+        s->per = blocks;
+        s->shares = s->levels * blocks;
+        ll at = 0;
+        for (int l = 0; l < s->levels; ++l) {
+            const ll size = l + 1 < s->levels ? (all - at) / 2 : all - at;
+            s->begin[l] = at;
+            s->step[l] = size / blocks;
+            at += size;
+        }
+        s->begin[s->levels] = all;
+    }
+
     // All threads; ends with a barrier.
     __device__ __forceinline__ void find(const ChunkParams& p) {
         const int per = (p.n + WIDTH - 1) / WIDTH, i0 = threadIdx.x * per, i1 = min(p.n, i0 + per);
@@ -266,15 +301,32 @@ struct ChunkCut {
             s->shares = static_cast<int>(n);
             s->each = n > 0 ? all / n : 0;
             s->more = n > 0 ? static_cast<int>(all - s->each * n) : 0;
+            s->levels = 0;
+            s->most = 0;
         }
+        if ((all_counts & 0x3ffffll) > gridDim.x) keep_whole(p, all, static_cast<int>(all_counts & 0x3ffffll));
         walking = false;
         __syncthreads();
     }
 
     // Words of the workspace that the call counts in.
-    __device__ __forceinline__ int used() const { return kChunkHead + s->shares; }
+    __device__ __forceinline__ int used() const { return kChunkHead + (s->levels == 0 ? s->shares : 0); }
 
+    // Where share n begins.
     __device__ __forceinline__ ll first_of(int n) const { return n * s->each + min(n, s->more); }
+    // The share's begin and end.  (Whole tiles: half of the work in shares of equal size, one a block, half of the
+    // rest, ..., so that the last ones taken are small.)
+    __device__ __forceinline__ void bound() {
+        if (s->levels == 0) {
+            x0 = first_of(share);
+            x1 = first_of(share + 1);
+            return;
+        }
+        int level = 0, i = share;
+        for (; i >= s->per; i -= s->per) ++level;
+        x0 = s->begin[level] + i * s->step[level];
+        x1 = i + 1 < s->per ? x0 + s->step[level] : s->begin[level + 1];
+    }
     __device__ __forceinline__ int share_of(ll x) const {
         const ll edge = s->more * (s->each + 1);
         return static_cast<int>(x < edge ? chunk_quotient(x, s->each + 1) : s->more + chunk_quotient(x - edge, s->each));
@@ -351,11 +403,16 @@ struct ChunkCut {
         const int from = e.len - e.m;
         it->span = chunk_span<KT>(p, u, from + chunk_token(p, it->row), from + chunk_token(p, it->row + rows - 1));
         const int units = it->span.count;
-        it->lo = at >= x0 ? 0 : cut(units, all, x0 - at);
-        it->hi = end <= x1 ? units : cut(units, all, x1 - at);
         it->parts = 1;
         it->share = share;
-        if (it->lo > 0 || it->hi < units) {
+        if (s->levels > 0) {              // who has the tile's middle has the tile
+            it->lo = at >= x0 || 2 * (x0 - at) < all ? 0 : units;
+            it->hi = end <= x1 || 2 * (x1 - at) >= all ? units : 0;
+        } else {
+            it->lo = at >= x0 ? 0 : cut(units, all, x0 - at);
+            it->hi = end <= x1 ? units : cut(units, all, x1 - at);
+        }
+        if (s->levels == 0 && (it->lo > 0 || it->hi < units)) {
             // The edges that cut the tile: those in it but a first and a last one that leave too little.
             int j0 = share_of(at) + 1, j1 = share_of(end - 1);
             if (j0 <= j1 && cut(units, all, first_of(j0) - at) == 0) ++j0;
@@ -395,14 +452,13 @@ struct ChunkCut {
                 if (some) return it;
             }
             const int n = atomicAdd(p.work, 1);
-            if (n >= 2 * s->shares) {
+            if (n >= (s->levels == 0 ? 2 : 1) * s->shares) {
                 it.kind = 0;
                 return it;
             }
             joining = n >= s->shares;
             share = joining ? n - s->shares : n;
-            x0 = first_of(share);
-            x1 = first_of(share + 1);
+            bound();
             seek(p, x0);
             first_at = tile_at();
         }

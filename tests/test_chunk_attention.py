@@ -253,6 +253,28 @@ def test_many_entries(dtype):
     check(cache, 1, q, *run(cache, q, seq, new), seq, new)
 
 
+@pytest.mark.parametrize("dtype,dim", [(BF16, 64), (F16, 192), (F32, 32)])
+@pytest.mark.parametrize("n,window", [(110, 0), (260, 70), (700, 0), (1500, 0)])
+def test_many_tiles(dtype, dim, n, window):
+    """More tiles than blocks, from one row to hundreds, over sequences of 1 to 900 tokens: every row is there."""
+    lens = [1 + (i * 211) % 900 for i in range(25)]
+    cache = build(lens, dtype=dtype, dim=dim, seed=n)
+    seq = [(i * 7) % 25 for i in range(n)]
+    new = [min(lens[s], (1, 3, 40, 0, 130)[i * i % 5] + i % 7) for i, s in enumerate(seq)]
+    q = queries(cache, sum(new) + 2, 3)
+    first = run(cache, q, seq, new, window=window)
+    assert not (first[1][:sum(new)] == LEFT).any()
+    rows = [sorted({0, m // 2, m - 1} & set(range(m))) if i % (n // 40) == 0 or i > n - 4 else [] for i, m in enumerate(new)]
+    check(cache, 1, q, *first, seq, new, window=window, rows=rows)
+    # An entry's rows alone give the same but for the order of sums.
+    i = max(range(n), key=lambda i: new[i])
+    at, m = sum(new[:i]), new[i]
+    one = run(cache, q[at:at + m], seq[i:i + 1], [m], window=window)
+    assert (one[1] - first[1][at:at + m]).abs().max() < 1e-3
+    again = run(cache, q, seq, new, window=window)
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_most_entries(dtype):
     cache = build([40], dtype=dtype, dim=64, heads=1, seed=6)
