@@ -53,14 +53,16 @@ __device__ __forceinline__ void mma(float (&d)[4], const unsigned (&a)[4], unsig
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// d += a b, a split already.
-__device__ __forceinline__ void mma_split(float (&d)[4], const unsigned (&hi)[4], const unsigned (&lo)[4], float b0, float b1) {
+// big + small += a b, a split already.  The tensor cores cut their sums instead of rounding them: sums stay short,
+// the small products have one of their own, and are added up by rounded additions.
+__device__ __forceinline__ void mma_split(float (&big)[4], float (&small)[4], const unsigned (&hi)[4], const unsigned (&lo)[4],
+                                          float b0, float b1) {
     unsigned h0, l0, h1, l1;
     split_b(b0, &h0, &l0);
     split_b(b1, &h1, &l1);
-    mma(d, lo, h0, h1);
-    mma(d, hi, l0, l1);
-    mma(d, hi, h0, h1);
+    mma(small, lo, h0, h1);
+    mma(small, hi, l0, l1);
+    mma(big, hi, h0, h1);
 }
 
 template <int DP>
@@ -170,23 +172,40 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2) chunk_kernel(const
                 }
             const bool odd = __syncthreads_or(zero != 0.0f) != 0;
             // The scores of 16 rows and this half's 16 positions.
-            float x[2][4];
+            float x[2][4], small[2][4];
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[n][i] = 0.0f;
+                for (int i = 0; i < 4; ++i) x[n][i] = small[n][i] = 0.0f;
             const float(*const kk)[Tile<DP>::kPitch] = s.k[now] + half * 16;
             const float(*const vv)[Tile<DP>::kPitch] = s.v[now] + half * 16;
-#pragma unroll 2
-            for (int d = 0; d < steps; ++d) {
-                unsigned hi[4], lo[4];
-                split_a(s.q[r0 + g][8 * d + t], &hi[0], &lo[0]);
-                split_a(s.q[r0 + g + 8][8 * d + t], &hi[1], &lo[1]);
-                split_a(s.q[r0 + g][8 * d + t + 4], &hi[2], &lo[2]);
-                split_a(s.q[r0 + g + 8][8 * d + t + 4], &hi[3], &lo[3]);
+            for (int d0 = 0; d0 < steps; d0 += 2) {
+                float big[2][4];
 #pragma unroll
-                for (int n = 0; n < 2; ++n) mma_split(x[n], hi, lo, kk[8 * n + g][8 * d + t], kk[8 * n + g][8 * d + t + 4]);
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) big[n][i] = 0.0f;
+#pragma unroll
+                for (int d = d0; d < d0 + 2; ++d) {
+                    if (d >= steps) break;
+                    unsigned hi[4], lo[4];
+                    split_a(s.q[r0 + g][8 * d + t], &hi[0], &lo[0]);
+                    split_a(s.q[r0 + g + 8][8 * d + t], &hi[1], &lo[1]);
+                    split_a(s.q[r0 + g][8 * d + t + 4], &hi[2], &lo[2]);
+                    split_a(s.q[r0 + g + 8][8 * d + t + 4], &hi[3], &lo[3]);
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+                        mma_split(big[n], small[n], hi, lo, kk[8 * n + g][8 * d + t], kk[8 * n + g][8 * d + t + 4]);
+                }
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[n][i] += big[n][i];
             }
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[n][i] += small[n][i];
             // Infinities and NaNs (of queries or K) do not pass through split products.
             float bad = 0.0f;
 #pragma unroll
@@ -221,12 +240,12 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2) chunk_kernel(const
                         const bool yes = !masked || (c < valid && j <= pos[r] &&
                                                      (p.window == 0 || j > pos[r] - p.window || j < p.sinks));
                         if (!yes) seen &= ~(1u << (4 * n + i));
-                        x[n][i] = yes ? x[n][i] * p.scale_log2 : kNegInf;
+                        x[n][i] = yes ? x[n][i] : kNegInf;
                         up = fmaxf(up, x[n][i]);
                     }
                 up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 1));
                 up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 2));
-                up = fmaxf(up, top[r]);
+                up = fmaxf(up * p.scale_log2, top[r]);
                 const float base = up == kNegInf ? 0.0f : up;
                 fade[r] = chunk_pow2(top[r] - base);
                 top[r] = up;
@@ -235,23 +254,19 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2) chunk_kernel(const
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
                     for (int i = 2 * r; i < 2 * r + 2; ++i) {
-                        w[n][i] = chunk_pow2(x[n][i] - base);
+                        w[n][i] = chunk_pow2(fmaf(x[n][i], p.scale_log2, -base));    // (one rounding)
                         if (seen >> (4 * n + i) & 1u) sum[r] += w[n][i];
                         else w[n][i] = 0.0f;
                     }
             }
-            if (__any_sync(0xffffffffu, fade[0] != 1.0f || fade[1] != 1.0f)) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    o[n][0] *= fade[0];
-                    o[n][1] *= fade[0];
-                    o[n][2] *= fade[1];
-                    o[n][3] *= fade[1];
-                }
-            }
             // V's infinities and NaNs are added to the rows that see them (a weight of 0 would carry them on to
             // the others), and zeros take their places.
             if (odd) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[n][i] *= fade[i >> 1];
+                fade[0] = fade[1] = 1.0f;
                 for (int k = 0; k < 16; ++k) {           // (lane 4 g + k / 2 % 4 has the weights of position k)
                     const int lane_of = 4 * g + (k >> 1 & 3), i = k & 1;
                     const unsigned bits = __shfl_sync(0xffffffffu, seen, lane_of) >> (4 * (k >> 3) + i);
@@ -275,16 +290,24 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2) chunk_kernel(const
                     }
                 __syncthreads();
             }
+            // 8 positions each: numbers t and t + 4 of a product are 2 t and 2 t + 1.
+            unsigned hi[2][4], lo[2][4];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {                // 8 positions: numbers t and t + 4 are 2 t and 2 t + 1
-                unsigned hi[4], lo[4];
-                split_a(w[k][0], &hi[0], &lo[0]);
-                split_a(w[k][2], &hi[1], &lo[1]);
-                split_a(w[k][1], &hi[2], &lo[2]);
-                split_a(w[k][3], &hi[3], &lo[3]);
+            for (int k = 0; k < 2; ++k) {
+                split_a(w[k][0], &hi[k][0], &lo[k][0]);
+                split_a(w[k][2], &hi[k][1], &lo[k][1]);
+                split_a(w[k][1], &hi[k][2], &lo[k][2]);
+                split_a(w[k][3], &hi[k][3], &lo[k][3]);
+            }
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    if (n < steps) mma_split(o[n], hi, lo, vv[8 * k + 2 * t][8 * n + g], vv[8 * k + 2 * t + 1][8 * n + g]);
+            for (int n = 0; n < NT; ++n) {
+                if (n >= steps) continue;
+                float big[4] = {0.0f, 0.0f, 0.0f, 0.0f}, rest[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    mma_split(big, rest, hi[k], lo[k], vv[8 * k + 2 * t][8 * n + g], vv[8 * k + 2 * t + 1][8 * n + g]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[n][i] = o[n][i] * fade[i >> 1] + (big[i] + rest[i]);
             }
             __syncthreads();                             // (the unit's place is filled again)
         }
