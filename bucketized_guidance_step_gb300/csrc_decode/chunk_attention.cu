@@ -3,7 +3,7 @@
 //
 // Its products run on the tensor cores with numbers split in two: x = hi + lo, hi 11 bits of it, and
 // x y = hi hi' + hi lo' + lo hi' up to about 2^-21 of it, sums in fp32 (mma.sync m16n8k8).  8 chunks of up to
-// 129 tokens over up to 1001, 8 and 4 heads of 96, take 89 us; a 64 x 64 tile of fp32 multiply-adds from
+// 129 tokens over up to 1001, 8 and 4 heads of 96, take 90 us; a 64 x 64 tile of fp32 multiply-adds from
 // shared memory, whose reads bound it, took 123 us.  Now the warps wait for each other: two barriers a unit,
 // and the next item, which one thread finds (issue slots 26 % busy, tensor pipe 19 %, HBM 2 %); a warp of its own for
 // that would take the registers that two blocks an SM leave.

@@ -21,7 +21,7 @@
 // Measured (bf16, 32 and 8 heads of 128): a chunk of 2048 tokens over 16384 takes 398 us, 1295 TFLOP/s or 68 % of
 // what a plain matrix product reaches; a unit of two tiles is 1940 cycles, of which the tensor cores need 1280
 // (S with N = 64 takes 48 cycles a product of 16 dims, not 32: with N = 128 two places would not fit beside O) and
-// the exponentials 1024.  32 sequences of up to 8200 tokens with 1 to 8 new ones: 125 us, HBM at 66 %.
+// the exponentials 1024.  32 sequences of up to 8200 tokens with 1 to 8 new ones: 127 us, HBM at 65 %.
 //
 // Positions that a row does not see get the weight 0.  So that 0 times an infinity or NaN reaches no
 // row, V is looked through in units that some row sees in part: what is not finite there is added to
