@@ -84,6 +84,7 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2) chunk_kernel(const
     grid_trigger();
     Cut cut;
     cut.s = &plan;
+    cut.ticket = tid == 0 ? atomicAdd(p.work, 1) : -1;
     cut.find(p);
     const ChunkUnits<KT> units(p.unit_page);
     for (;;) {

@@ -15,7 +15,7 @@
 // parts a share at most.  A share whose edge would leave less than two units of a tile, or lies in a tile
 // of few, takes or leaves the tile whole.  Where tiles are more than the blocks and none is large, all stay whole:
 // shares of falling size balance them without joins (16 chunks of up to 512 tokens, window 1024, 16 and 4 heads of 128:
-// 105 us cut, 75 us whole; 8 prompts of up to 2048 tokens, 32 and 8 heads of 128: 164 us and 152 us).
+// 105 us cut, 75 us whole; 8 prompts of up to 2048 tokens, 32 and 8 heads of 128: 164 us and 157 us).
 //
 // Blocks take shares from a queue, and once there are no more, the joins of the shares' parts: what waits
 // for a part waits for a block that is running.  The outputs of a share do not depend on who computes it
@@ -222,6 +222,7 @@ struct ChunkCut {
     ChunkEntry e;
     int i, share, head, tile;
     bool walking, joining;
+    int ticket;                           // taken from the queue ahead (its way to memory and back passes during find), or -1
     ll first_at;                          // joining: the share's first tile, until it is passed
 
     static __device__ __forceinline__ int tiles_of(const ChunkParams& p, const ChunkEntry& e) {
@@ -451,7 +452,8 @@ struct ChunkCut {
                 }
                 if (some) return it;
             }
-            const int n = atomicAdd(p.work, 1);
+            const int n = ticket >= 0 ? ticket : atomicAdd(p.work, 1);
+            ticket = -1;
             if (n >= (s->levels == 0 ? 2 : 1) * s->shares) {
                 it.kind = 0;
                 return it;

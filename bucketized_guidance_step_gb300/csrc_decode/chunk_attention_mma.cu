@@ -426,6 +426,7 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
     grid_trigger();
     typename S::Cut cut;
     cut.s = &s.plan;
+    cut.ticket = role == 0 && lane == 0 ? atomicAdd(p.work, 1) : -1;
     mma_fence_before();
     cut.find(p);                          // (ends with a barrier)
     mma_fence_after();
