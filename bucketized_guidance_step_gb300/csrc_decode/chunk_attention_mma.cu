@@ -602,11 +602,30 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
                 if (item == 0) break;
                 if (item == 2 || count == 0) continue;
                 const bool alone = TILES == 2 && rows <= 128;        // the tile of the two that has rows
+                // Every thread that waits for a unit of the rings has waited for all before it: a wait by parity
+                // takes an older phase for its own where the one before is not over.  So the second tile's
+                // thread goes through the units of an item that has no second tile, and frees them for its part.
+                // (Rows wait for a unit of V behind its scores, which this thread has issued behind the units of
+                // V before the last one.)
                 if (alone && w == 1) {
-                    k_turn ^= (k_stage + count) / S::K_STAGES & 1;
-                    k_stage = (k_stage + count) % S::K_STAGES;
-                    v_turn ^= (v_stage + count) / S::V_STAGES & 1;
-                    v_stage = (v_stage + count) % S::V_STAGES;
+                    for (unsigned u = 0; u < count + 2 && go; ++u) {
+                        if (u >= 2) {     // (in the order in which the first tile's thread takes them)
+                            if (!(go = bar_wait(smem_at(&s.v_full[v_stage]), v_turn, &s.dead))) break;
+                            bar_arrive(smem_at(&s.v_empty[v_stage]));
+                            if (++v_stage == S::V_STAGES) {
+                                v_stage = 0;
+                                v_turn ^= 1;
+                            }
+                        }
+                        if (u < count) {
+                            if (!(go = bar_wait(smem_at(&s.k_full[k_stage]), k_turn, &s.dead))) break;
+                            bar_arrive(smem_at(&s.k_empty[k_stage]));
+                            if (++k_stage == S::K_STAGES) {
+                                k_stage = 0;
+                                k_turn ^= 1;
+                            }
+                        }
+                    }
                     continue;
                 }
                 // Unit u's scores; the first ones wait for the queries.
@@ -634,7 +653,6 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
                     }
                     mma_commit(smem_at(&s.s_full[w][place]));
                     mma_commit(smem_at(&s.k_empty[k_stage]));
-                    if (alone) bar_arrive(smem_at(&s.k_empty[k_stage]));
                     if (u + 1 == count) mma_commit(smem_at(&s.q_empty[w]));
                     if (++k_stage == S::K_STAGES) {
                         k_stage = 0;
@@ -653,7 +671,6 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
                     mma_ts4(o_at, s_at + place * kUnit + S::P, v_low + v_stage * (S::STAGE / 16), high, what_o, add);
                     mma_commit(smem_at(&s.o_full[w][place]));
                     mma_commit(smem_at(&s.v_empty[v_stage]));
-                    if (alone) bar_arrive(smem_at(&s.v_empty[v_stage]));
                     if (++v_stage == S::V_STAGES) {
                         v_stage = 0;
                         v_turn ^= 1;
