@@ -195,6 +195,10 @@ struct ChunkCut {
     static constexpr int kLeast = 2;      // units of a part
     static constexpr int kCut = KT == 64 ? 16 * 1920 : 16 * 128;     // what cutting costs a block (about 25 us and 10 us)
     static constexpr int kLevels = 4;     // of sizes of shares, where tiles stay whole
+    // Tiles are counted in one number with the rows, in its lowest bits, which all threads' together may not pass.
+    static constexpr int kTileBits = 18;
+    static constexpr ll kMostTiles = 1023;               // that a thread counts: more than decide anything below
+    static_assert(WIDTH * kMostTiles < 1ll << kTileBits, "the tiles' count reaches into the rows'");
     struct Shared {
         ll before[WIDTH];                 // cost before a thread's entries
         ll tmp[THREADS / 32 + 1];
@@ -275,29 +279,30 @@ struct ChunkCut {
     // All threads; ends with a barrier.
     __device__ __forceinline__ void find(const ChunkParams& p) {
         const int per = (p.n + WIDTH - 1) / WIDTH, i0 = threadIdx.x * per, i1 = min(p.n, i0 + per);
-        ll mine = 0, counts = 0, all, all_counts;        // (counts: rows, and below bit 18 tiles, 1024 a thread at most)
+        ll mine = 0, counts = 0, all, all_counts;        // (counts: rows, and in the lowest bits tiles)
         int tiles = 0;
         unsigned bad = 0;
 #pragma unroll 4
         for (int k = i0; k < i1; ++k) {
             const ChunkEntry e = chunk_entry(p, k, &bad);
             const Cost c = cost_of(p, e);
-            tiles = static_cast<int>(min(1024ll, tiles + static_cast<ll>(c.tiles) * p.c.heads));
+            tiles = static_cast<int>(min(kMostTiles, tiles + static_cast<ll>(c.tiles) * p.c.heads));
             mine += c.upto(c.tiles) * p.c.heads;
-            counts += static_cast<ll>(e.m) << 18;
+            counts += static_cast<ll>(e.m) << kTileBits;
         }
         counts += tiles;
         const ll before = block_scan<THREADS>(mine, s->tmp, &all);
         block_scan<THREADS>(counts, s->tmp, &all_counts);
-        if (all_counts >> 18 > p.tokens) {               // entries share rows: there is no end to what they could ask for
+        if (all_counts >> kTileBits > p.tokens) {        // entries share rows: there is no end to what they could ask for
             bad |= GS_DEV_BAD_SEQ;
             all = all_counts = 0;
         }
+        const ll all_tiles = all_counts & ((1ll << kTileBits) - 1);
         if (blockIdx.x == 0) flag(p.c.status, bad);
         if (threadIdx.x < WIDTH) s->before[threadIdx.x] = before;
         if (threadIdx.x == 0) {
             // No more shares than blocks, than tiles, or than there are four units for.
-            ll n = max(all_counts & 0x3ffffll, all / (16 * 4 * KT));
+            ll n = max(all_tiles, all / (16 * 4 * KT));
             n = min(n, static_cast<ll>(gridDim.x));
             s->shares = static_cast<int>(n);
             s->each = n > 0 ? all / n : 0;
@@ -305,7 +310,7 @@ struct ChunkCut {
             s->levels = 0;
             s->most = 0;
         }
-        if ((all_counts & 0x3ffffll) > gridDim.x) keep_whole(p, all, static_cast<int>(all_counts & 0x3ffffll));
+        if (all_tiles > gridDim.x) keep_whole(p, all, static_cast<int>(all_tiles));
         walking = false;
         __syncthreads();
     }
