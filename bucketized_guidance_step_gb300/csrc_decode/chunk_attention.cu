@@ -491,8 +491,10 @@ extern "C" gs_status gs_chunk_attention(const gs_chunk_attention_args* args, gs_
     // and scale 0 makes them 0.
     p.scale_log2 = args->scale == 0.0f ? 1.0f : std::fabs(args->scale) * kChunkLog2e;
     p.q_sign = args->scale > 0.0f ? 1.0f : args->scale < 0.0f ? -1.0f : 0.0f;
-    p.window = args->window;
-    p.sinks = args->sinks;
+    // No position is past 2^30, so more leave none out; and a row 2^30 before its sequence less a window stays in 32 bits.
+    constexpr int kMostWindow = 1 << 30;
+    p.window = args->window < kMostWindow ? args->window : kMostWindow;
+    p.sinks = args->sinks < kMostWindow ? args->sinks : kMostWindow;
     p.out = args->out;
     p.out_token = args->out_token_stride;
     p.out_head = args->out_head_stride;
