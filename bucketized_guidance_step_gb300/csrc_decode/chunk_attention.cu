@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2) chunk_kernel(const
         __syncthreads();
         if (it.kind == 0) break;
         if (it.kind == 2) {
-            if (tid == 0) ok = chunk_wait_parts(p.work + kChunkHead + it.share, it.need);
+            if (tid == 0) ok = chunk_wait_parts(p.work + kChunkHead + it.share, it.need, plan.guard.limit);
             __syncthreads();
             if (ok) chunk_join<float>(p, it, warp, kThreads / 32, 0.0f);
             else if (tid == 0) flag(p.c.status, GS_DEV_TIMEOUT);

@@ -25,6 +25,7 @@
 // up to 257), a chain of lookups and scans; later ones are found while the last one is computed (16-bit caches).
 #pragma once
 
+#include "chunk_limit.h"
 #include "decode_common.cuh"
 
 namespace gs_decode {
@@ -34,7 +35,6 @@ constexpr float kChunkLn2 = 0.6931471805599453f;
 constexpr int kChunkCounters = GS_CHUNK_COUNTERS;        // words of the workspace that are 0 between calls
 constexpr int kChunkHead = 4;                            // of these, before the shares' counts
 constexpr int kChunkShares = kChunkCounters - kChunkHead;            // most shares
-constexpr unsigned long long kChunkLimitNs = 200ull * 1000ull * 1000ull;   // of a wait
 
 struct ChunkParams {
     CacheView c;                          // c.k and c.v are the layer's
@@ -60,6 +60,19 @@ struct ChunkParams {
     float* slots;                         // two a share: for the tile it did not begin, the one it does not end
     int slot_rows;                        // rows of one
     int unit_page;                        // tokens that units are cut by: a page's, or a unit's (fp32: rows are copied one by one)
+};
+
+__device__ __forceinline__ unsigned long long chunk_clock() {
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+
+// What ends a block's waits.
+struct ChunkGuard {
+    int dead;                             // one has run out
+    unsigned long long limit;             // nanoseconds
+    unsigned long long deadline;          // of all (16-bit caches): `limit` after the last item was found; 0: dead
 };
 
 // A slot: reference[rows], sum[rows], o[rows][dim].
@@ -207,6 +220,7 @@ struct ChunkCut {
         int levels, per;                  // whole tiles: levels of shares, shares of a level, ...
         ll begin[kLevels + 1], step[kLevels];            // ... and where they begin
         unsigned most;                    // the largest tile's cost
+        ChunkGuard guard;                 // (its limit)
     };
 
     // What the tiles of a head cost: a tile whose last row sees `a` positions kOver + a, a_t = from + (t + 1)
@@ -309,6 +323,9 @@ struct ChunkCut {
             s->more = n > 0 ? static_cast<int>(all - s->each * n) : 0;
             s->levels = 0;
             s->most = 0;
+            // (Tiles that stay whole cost `each` and kCut at most.)
+            s->guard.limit = chunk_limit_ns(s->each + kCut, KT == 64 ? kChunkNs : kChunkNsFp32);
+            s->guard.deadline = chunk_clock() + s->guard.limit;
         }
         if (all_tiles > gridDim.x) keep_whole(p, all, static_cast<int>(all_tiles));
         walking = false;
@@ -500,20 +517,14 @@ __device__ __forceinline__ float chunk_pow2(float x) {
     return y;
 }
 
-__device__ __forceinline__ unsigned long long chunk_clock() {
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-
-// Waits (200 ms at most) until all parts of a tile are in their slots.  One thread.
-__device__ __forceinline__ bool chunk_wait_parts(const int* count, int parts) {
+// Waits (`limit` at most) until all parts of a tile are in their slots.  One thread.
+__device__ __forceinline__ bool chunk_wait_parts(const int* count, int parts, unsigned long long limit) {
     const unsigned long long t0 = chunk_clock();
     for (;;) {
         int v;
         asm volatile("ld.acquire.gpu.s32 %0, [%1];" : "=r"(v) : "l"(count) : "memory");
         if (v >= parts) return true;
-        if (chunk_clock() - t0 > kChunkLimitNs) return false;
+        if (chunk_clock() - t0 > limit) return false;
         __nanosleep(100);
     }
 }

@@ -77,29 +77,36 @@ __device__ __forceinline__ bool bar_try(unsigned bar, unsigned parity) {
         : "memory");
     return ok != 0u;
 }
-// Waits (kChunkLimitNs at most) for the phase of this parity; once one wait of the block has run out,
-// all of them end.
-__device__ __forceinline__ bool bar_wait(unsigned bar, unsigned parity, volatile int* dead) {
+// Waits, to the block's deadline at most, for the phase of this parity; once one wait of the block has run out, all of
+// them end.  (A deadline, not a time for each: there are two dozen copies of this, and the smallest calls wait for
+// instructions; reading a limit beside the clock cost them 0.9 us of 16.  The clock is not read before the second look,
+// which waits for some time itself: the clock's own latency was 5 % of a long prompt.)
+__device__ __forceinline__ bool bar_wait(unsigned bar, unsigned parity, ChunkGuard* guard) {
     if (bar_try(bar, parity)) return true;
-    const unsigned long long t0 = chunk_clock();
     while (!bar_try(bar, parity)) {
-        if (*dead != 0) return false;
-        if (chunk_clock() - t0 > kChunkLimitNs) {
-            *dead = 1;
+        volatile unsigned long long* const deadline = &guard->deadline;
+        if (chunk_clock() > *deadline) {
+            *static_cast<volatile int*>(&guard->dead) = 1;
+            *deadline = 0;
             return false;
         }
     }
     return true;
 }
+// The time to the next item begins.  One thread.
+__device__ __forceinline__ void start_clock(ChunkGuard* guard) {
+    volatile unsigned long long* const deadline = &guard->deadline;
+    if (*static_cast<volatile int*>(&guard->dead) == 0) *deadline = chunk_clock() + guard->limit;
+}
 // The same for a warp: whether all its lanes saw the phase.
-__device__ __forceinline__ bool warp_wait(unsigned bar, unsigned parity, volatile int* dead) {
-    return __all_sync(0xffffffffu, bar_wait(bar, parity, dead));
+__device__ __forceinline__ bool warp_wait(unsigned bar, unsigned parity, ChunkGuard* guard) {
+    return __all_sync(0xffffffffu, bar_wait(bar, parity, guard));
 }
 // A barrier of the threads that a barrier in shared memory counts, whole warps (one that waits with a
 // limit, as every wait here).
-__device__ __forceinline__ bool meet(unsigned bar, unsigned* turn, volatile int* dead) {
+__device__ __forceinline__ bool meet(unsigned bar, unsigned* turn, ChunkGuard* guard) {
     bar_arrive(bar);
-    const bool ok = warp_wait(bar, *turn, dead);
+    const bool ok = warp_wait(bar, *turn, guard);
     *turn ^= 1;
     return ok;
 }
@@ -318,7 +325,7 @@ struct alignas(1024) Smem {
     unsigned long long q_full[2], q_empty[2], s_full[2][2], p_full[2][2], o_full[2][2];
     unsigned long long tile_meet[2], both_meet, tail, drain[2];
     ChunkItem items[kItems];
-    int dead, seeded[2], hot[2][2];
+    int seeded[2], hot[2][2];
     unsigned tmem;
     typename S::Cut::Shared plan;
 };
@@ -329,7 +336,7 @@ static_assert(sizeof(Smem<128>) <= 227 * 1024 && sizeof(Smem<256>) <= 227 * 1024
 template <class T, int DP>
 __device__ __noinline__ bool give_out(unsigned char* v, unsigned o_at, int dim, int lo, int hi, int sinks,
                                       int valid, bool first, int threads, unsigned bar, unsigned* turn,
-                                      volatile int* dead) {
+                                      ChunkGuard* guard) {
     using S = Shape<DP>;
     for (int d0 = 0; d0 < dim; d0 += 32) {
         float o[32];
@@ -355,7 +362,7 @@ __device__ __noinline__ bool give_out(unsigned char* v, unsigned o_at, int dim, 
         tmem_store32(o_at + d0, o);
         tmem_wait_store();
     }
-    if (!meet(bar, turn, dead)) return false;            // every row has what it sees
+    if (!meet(bar, turn, guard)) return false;           // every row has what it sees
     using W = Weights<T>;
     unsigned* const words = reinterpret_cast<unsigned*>(v);
     for (int x = threadIdx.x; x < S::STAGE / 4; x += threads) {
@@ -363,7 +370,7 @@ __device__ __noinline__ bool give_out(unsigned char* v, unsigned o_at, int dim, 
         if (hot != 0u) words[x] = w & ~((hot >> 15) * 0xffffu);
     }
     async_fence();
-    return meet(bar, turn, dead);
+    return meet(bar, turn, guard);
 }
 
 template <class T, int DP>
@@ -408,7 +415,7 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
         bar_init(smem_at(&s.both_meet), S::GROUP);
         bar_init(smem_at(&s.tail), 1);
         for (int i = 0; i < 2; ++i) bar_init(smem_at(&s.drain[i]), 1);
-        s.dead = 0;
+        s.plan.guard.dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (role == 2) {
@@ -451,15 +458,16 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
             const int slot = n & 1;
             int kind = 0;
             if (is_v) {
-                if (!warp_wait(smem_at(&s.item_full[slot]), (n >> 1) & 1, &s.dead)) break;
+                if (!warp_wait(smem_at(&s.item_full[slot]), (n >> 1) & 1, &s.plan.guard)) break;
                 kind = s.items[slot].kind;
             } else {
                 if (lane == 0) {
                     ChunkItem it;
                     chunk_next_item(&cut, p, &it);
-                    if (bar_wait(smem_at(&s.item_empty[slot]), ((n >> 1) & 1) ^ 1, &s.dead)) {
+                    if (bar_wait(smem_at(&s.item_empty[slot]), ((n >> 1) & 1) ^ 1, &s.plan.guard)) {
                         s.items[slot] = it;
                         kind = it.kind;
+                        start_clock(&s.plan.guard);
                         bar_arrive(smem_at(&s.item_full[slot]));
                     } else {
                         kind = -1;
@@ -519,7 +527,7 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
                     if (u + batch < hi) next = look_up(u + batch);
                 }
                 const int live = u + 1 < hi ? pages : live_last;
-                if (!(go = warp_wait(empty0 + 8 * stage, turn, &s.dead))) break;
+                if (!(go = warp_wait(empty0 + 8 * stage, turn, &s.plan.guard))) break;
                 unsigned char* const here = stage0 + stage * S::STAGE;
                 const unsigned full = full0 + 8 * stage;
                 if (++stage == stages) {
@@ -543,7 +551,7 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
                 }
                 if (!is_v && u == lo && p.q_boxes != 0) {            // the queries, once the last item's are done with
                     for (int w = 0; w < tiles && go; ++w) {
-                        go = warp_wait(smem_at(&s.q_empty[w]), q_turn >> w & 1, &s.dead);
+                        go = warp_wait(smem_at(&s.q_empty[w]), q_turn >> w & 1, &s.plan.guard);
                         q_turn ^= 1u << w;
                         if (!go) break;
                         const unsigned q_bar = smem_at(&s.q_full[w]);
@@ -558,7 +566,7 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
                     if (!go) break;
                 }
                 if (tail) {
-                    if (!(go = warp_wait(bar, tails & 1, &s.dead))) break;
+                    if (!(go = warp_wait(bar, tails & 1, &s.plan.guard))) break;
                     ++tails;
                     for (int x = lane; x < (kUnit - valid) * 8 * halves; x += 32) {
                         const int col = x / ((kUnit - valid) * 8), y = x - col * ((kUnit - valid) * 8);
@@ -574,7 +582,7 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
         flag(p.c.status, bad);
         // Where a wait has run out, the boxes under way land before the block ends.
         __syncwarp();
-        if (s.dead != 0) {
+        if (s.plan.guard.dead != 0) {
             const unsigned long long t0 = chunk_clock();
             while (chunk_clock() - t0 < 10ull * 1000ull * 1000ull) __nanosleep(10000);
         }
@@ -595,7 +603,7 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
             bool go = true;
             for (int n = 0; go; ++n) {
                 const int slot = n & 1;
-                if (!bar_wait(smem_at(&s.item_full[slot]), (n >> 1) & 1, &s.dead)) break;
+                if (!bar_wait(smem_at(&s.item_full[slot]), (n >> 1) & 1, &s.plan.guard)) break;
                 const int item = s.items[slot].kind, rows = s.items[slot].rows;
                 const unsigned count = s.items[slot].hi - s.items[slot].lo;
                 bar_arrive(smem_at(&s.item_empty[slot]));
@@ -610,7 +618,7 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
                 if (alone && w == 1) {
                     for (unsigned u = 0; u < count + 2 && go; ++u) {
                         if (u >= 2) {     // (in the order in which the first tile's thread takes them)
-                            if (!(go = bar_wait(smem_at(&s.v_full[v_stage]), v_turn, &s.dead))) break;
+                            if (!(go = bar_wait(smem_at(&s.v_full[v_stage]), v_turn, &s.plan.guard))) break;
                             bar_arrive(smem_at(&s.v_empty[v_stage]));
                             if (++v_stage == S::V_STAGES) {
                                 v_stage = 0;
@@ -618,7 +626,7 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
                             }
                         }
                         if (u < count) {
-                            if (!(go = bar_wait(smem_at(&s.k_full[k_stage]), k_turn, &s.dead))) break;
+                            if (!(go = bar_wait(smem_at(&s.k_full[k_stage]), k_turn, &s.plan.guard))) break;
                             bar_arrive(smem_at(&s.k_empty[k_stage]));
                             if (++k_stage == S::K_STAGES) {
                                 k_stage = 0;
@@ -630,9 +638,9 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
                 }
                 // Unit u's scores; the first ones wait for the queries.
                 auto scores = [&](unsigned u) {
-                    if (!(go = bar_wait(smem_at(&s.k_full[k_stage]), k_turn, &s.dead))) return;
+                    if (!(go = bar_wait(smem_at(&s.k_full[k_stage]), k_turn, &s.plan.guard))) return;
                     if (u == 0) {
-                        go = bar_wait(smem_at(&s.q_full[w]), q_turn, &s.dead);
+                        go = bar_wait(smem_at(&s.q_full[w]), q_turn, &s.plan.guard);
                         q_turn ^= 1;
                         if (!go) return;
                         mma_fence_after();
@@ -664,8 +672,8 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
                 for (unsigned u = 0; u < count && go; ++u) {
                     // (A place has a barrier of its own: a warp may be a unit ahead of another.)
                     const unsigned place = done + u & 1;
-                    if (!(go = bar_wait(smem_at(&s.v_full[v_stage]), v_turn, &s.dead))) break;
-                    if (!(go = bar_wait(smem_at(&s.p_full[w][place]), done + u >> 1 & 1, &s.dead))) break;
+                    if (!(go = bar_wait(smem_at(&s.v_full[v_stage]), v_turn, &s.plan.guard))) break;
+                    if (!(go = bar_wait(smem_at(&s.p_full[w][place]), done + u >> 1 & 1, &s.plan.guard))) break;
                     mma_fence_after();
                     const unsigned add = u > 0 || *static_cast<volatile int*>(&s.seeded[w]) != 0;
                     mma_ts4(o_at, s_at + place * kUnit + S::P, v_low + v_stage * (S::STAGE / 16), high, what_o, add);
@@ -679,7 +687,7 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
                 }
                 done += count;
             }
-            if (s.dead != 0) {            // products under way end before the block does
+            if (s.plan.guard.dead != 0) {  // products under way end before the block does
                 mma_commit(smem_at(&s.drain[w]));
                 const unsigned long long t0 = chunk_clock();
                 while (!bar_try(smem_at(&s.drain[w]), 0) && chunk_clock() - t0 < 10ull * 1000ull * 1000ull) {}
@@ -698,20 +706,20 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
         // Unit number `step`'s products with V are in O.  (The two barriers take turns with the places of
         // S: the one before last is known to be done, so that a phase is never taken for an older one.)
         auto added = [&](unsigned unit) {
-            const bool ok = warp_wait(smem_at(&s.o_full[w][unit & 1]), unit >> 1 & 1, &s.dead);
+            const bool ok = warp_wait(smem_at(&s.o_full[w][unit & 1]), unit >> 1 & 1, &s.plan.guard);
             mma_fence_after();
             return ok;
         };
         bool go = true;
         for (int n = 0; go; ++n) {
             const int slot = n & 1;
-            if (!warp_wait(smem_at(&s.item_full[slot]), (n >> 1) & 1, &s.dead)) break;
+            if (!warp_wait(smem_at(&s.item_full[slot]), (n >> 1) & 1, &s.plan.guard)) break;
             const ChunkItem& it = s.items[slot];
             if (it.kind == 0) break;
             if (it.kind == 2) {
-                if (mine == 0 && !chunk_wait_parts(p.work + kChunkHead + it.share, it.need))
-                    *static_cast<volatile int*>(&s.dead) = 1;
-                if (!meet(smem_at(&s.tile_meet[w]), &meet_turn, &s.dead)) break;
+                if (mine == 0 && !chunk_wait_parts(p.work + kChunkHead + it.share, it.need, s.plan.guard.limit))
+                    *static_cast<volatile int*>(&s.plan.guard.dead) = 1;
+                if (!meet(smem_at(&s.tile_meet[w]), &meet_turn, &s.plan.guard)) break;
                 chunk_join<T>(p, it, warp, S::GROUP / 32, W::kLift);
                 bar_arrive(smem_at(&s.item_empty[slot]));
                 continue;
@@ -746,7 +754,7 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
                     *reinterpret_cast<uint4*>(to + (c >> 3) * (128 * 128) + (((c & 7) ^ (mine & 7)) << 4)) = x;
                 }
                 async_fence();
-                if (!(go = meet(smem_at(&s.tile_meet[w]), &meet_turn, &s.dead))) break;
+                if (!(go = meet(smem_at(&s.tile_meet[w]), &meet_turn, &s.plan.guard))) break;
                 if (mine == 0) bar_arrive(smem_at(&s.q_full[w]));
             }
             float top = kNegInf, sum = 0.0f;
@@ -764,12 +772,12 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
                 const bool part = at + valid - 1 > first_pos ||
                                   (p.window > 0 && at <= last_pos - p.window && at + valid > p.sinks);
                 const unsigned place = done + u & 1;
-                if (!(go = warp_wait(smem_at(&s.s_full[w][place]), done + u >> 1 & 1, &s.dead))) break;
+                if (!(go = warp_wait(smem_at(&s.s_full[w][place]), done + u >> 1 & 1, &s.plan.guard))) break;
                 mma_fence_after();
                 bool odd = false;
                 if (part) {
                     const unsigned v_stage = (ring + u) % S::V_STAGES;
-                    if (!(go = warp_wait(smem_at(&s.v_full[v_stage]), (ring + u) / S::V_STAGES & 1, &s.dead))) break;
+                    if (!(go = warp_wait(smem_at(&s.v_full[v_stage]), (ring + u) / S::V_STAGES & 1, &s.plan.guard))) break;
                     unsigned hot = 0;
                     const uint4* const v = reinterpret_cast<const uint4*>(s.v[v_stage]);
 #pragma unroll 8
@@ -782,13 +790,13 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
                     ++looked;
                     if (__any_sync(0xffffffffu, (hot & 0x80008000u) != 0u) && lane == 0)
                         *static_cast<volatile int*>(&s.hot[w][looked & 1]) = looked;
-                    if (!(go = meet(smem_at(&s.tile_meet[w]), &meet_turn, &s.dead))) break;
+                    if (!(go = meet(smem_at(&s.tile_meet[w]), &meet_turn, &s.plan.guard))) break;
                     odd = *static_cast<volatile int*>(&s.hot[w][looked & 1]) == looked;
                     if (odd) {
                         if (u > 0 && !(go = added(done + u - 1))) break;
                         if (!(go = give_out<T, DP>(s.v[v_stage], o_at, dim, lo, hi, sink, valid, u == 0, 128 * tiles,
                                                    smem_at(tiles == 2 ? &s.both_meet : &s.tile_meet[w]),
-                                                   tiles == 2 ? &both_turn : &meet_turn, &s.dead)))
+                                                   tiles == 2 ? &both_turn : &meet_turn, &s.plan.guard)))
                             break;
                     }
                 }
@@ -920,7 +928,7 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
                     part[p.slot_rows + r] = sum;
                 }
                 __threadfence();
-                if (!(go = meet(smem_at(&s.tile_meet[w]), &meet_turn, &s.dead))) break;
+                if (!(go = meet(smem_at(&s.tile_meet[w]), &meet_turn, &s.plan.guard))) break;
                 if (mine == 0) atomicAdd(p.work + kChunkHead + it.share, 1);
             } else if (real && lse != nullptr) {
                 *lse = sum == 0.0f ? kNegInf : (top + log2f(sum) - W::kLift) * kChunkLn2;
@@ -932,7 +940,7 @@ chunk_mma_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ 
     __syncthreads();
     mma_fence_after();
     if (role == 2) {
-        if (s.dead != 0 && lane == 0) flag(p.c.status, GS_DEV_TIMEOUT);
+        if (s.plan.guard.dead != 0 && lane == 0) flag(p.c.status, GS_DEV_TIMEOUT);
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
     }
     if (warp == 0) chunk_leave(p, cut.used());

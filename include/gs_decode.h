@@ -254,8 +254,8 @@ gs_status gs_chunk_attention_workspace(const gs_chunk_attention_args* args, int6
  * Device-found: GS_DEV_BAD_SEQ (a sequence id outside the cache: as length 0; a page id outside the
  * pool: its rows read as zeros; a length past the table: cut; rows before the first token; an entry
  * whose rows do not rise or pass 0 .. tokens: skipped; entries that together have more rows than
- * there are tokens: nothing is computed), GS_DEV_TIMEOUT (a wait inside the kernel ran out: the
- * results are not whole).  Entries whose rows overlap leave either's results there.  out and lse may
+ * there are tokens: nothing is computed), GS_DEV_TIMEOUT (a wait inside the kernel ran out, after 0.2 s
+ * and many times what a block's share of the call takes: the results are not whole).  Entries whose rows overlap leave either's results there.  out and lse may
  * not overlap an input.
  * Errors: GS_ERR_INVALID_ARG (NULL pointers, sizes, q_heads not a multiple of kv_heads, layer outside
  * the cache, window or sinks < 0, sinks without window, a scale that is not finite, workspace too
