@@ -454,6 +454,7 @@ extern "C" gs_status gs_chunk_attention(const gs_chunk_attention_args* args, gs_
     if (st != GS_OK) return st;
     const long long es = elem_size(args->cache->dtype);
     if (args->layer < 0 || args->layer >= p.c.layers || !std::isfinite(args->scale)) return GS_ERR_INVALID_ARG;
+    if (args->split_weights != 0 && args->split_weights != 1) return GS_ERR_INVALID_ARG;
     if (args->tokens == 0 || args->n == 0) return GS_OK;
     if (args->q == nullptr || args->out == nullptr || args->seq == nullptr || args->start == nullptr ||
         !aligned(args->q, es) || !aligned(args->out, es) || !aligned(args->lse, 4) ||
@@ -504,5 +505,6 @@ extern "C" gs_status gs_chunk_attention(const gs_chunk_attention_args* args, gs_
     p.slot_rows = plan.rows;
     p.unit_page = args->cache->dtype == GS_DTYPE_F32 ? chunk_fp32_unit() : p.c.page;
     if (args->cache->dtype == GS_DTYPE_F32) return launch_chunk_fp32(p, plan.shape.blocks, stream);
+    if (args->split_weights != 0) return launch_chunk_mma_split(args->cache->dtype, p, plan.shape.blocks, stream);
     return launch_chunk_mma(args->cache->dtype, p, plan.shape.blocks, stream);
 }

@@ -1,6 +1,6 @@
 // Attention of chunks of new tokens over a paged cache: how the work is cut and handed out, and how
 // the parts of a cut row are joined.  The arithmetic is chunk_attention.cu's (split products, for fp32
-// caches) or chunk_attention_mma.cu's (tcgen05, for 16-bit caches).
+// caches) or chunk_attention_mma.cuh's (tcgen05, for 16-bit caches).
 //
 // An entry of the call is m new tokens of one sequence.  With one kv head it is m * group query rows
 // (group: query heads of a kv head; row r is token r / group, head r % group of the group), which
@@ -654,5 +654,6 @@ ChunkShape chunk_fp32_shape(int dim);
 ChunkShape chunk_mma_shape(int dim);
 gs_status launch_chunk_fp32(const ChunkParams& p, int blocks, gs_stream stream);
 gs_status launch_chunk_mma(int dtype, ChunkParams& p, int blocks, gs_stream stream);
+gs_status launch_chunk_mma_split(int dtype, ChunkParams& p, int blocks, gs_stream stream);
 
 }  // namespace gs_decode

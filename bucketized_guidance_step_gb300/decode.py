@@ -55,7 +55,8 @@ class ChunkAttentionArgs(ctypes.Structure):
     _fields_ = [("cache", ctypes.POINTER(KVCacheDesc)), ("layer", _I32), ("tokens", _I32),
                 ("n", _I32), ("seq", _P), ("start", _P), ("q_heads", _I32), ("q", _P),
                 ("q_token_stride", _I64), ("q_head_stride", _I64), ("scale", _F),
-                ("window", _I32), ("sinks", _I32), ("out", _P), ("out_token_stride", _I64),
+                ("window", _I32), ("sinks", _I32), ("split_weights", _I32), ("out", _P),
+                ("out_token_stride", _I64),
                 ("out_head_stride", _I64), ("lse", _P), ("workspace", _P),
                 ("workspace_bytes", _I64)]
 
@@ -351,7 +352,8 @@ class PagedCache:
         return out
 
     def prepare_chunk_attention(self, q, layer: int, seq, start, *, scale: Optional[float] = None,
-                                window: int = 0, sinks: int = 0, out=None, lse=None) -> Call:
+                                window: int = 0, sinks: int = 0, split_weights: bool = False,
+                                out=None, lse=None) -> Call:
         import torch
         d, dev, dt = self._desc, self.device, self.k.dtype
         if q.dim() != 3 or q.shape[2] != d.dim:
@@ -370,7 +372,7 @@ class PagedCache:
         a.q_token_stride, a.q_head_stride = _stride(q, 0), _stride(q, 1)
         a.out_token_stride, a.out_head_stride = _stride(out, 0), _stride(out, 1)
         a.scale = float(D) ** -0.5 if scale is None else float(scale)
-        a.window, a.sinks = int(window), int(sinks)
+        a.window, a.sinks, a.split_weights = int(window), int(sinks), int(split_weights)
         a.lse = _ptr(lse, "lse", dev, torch.float32, (T, Hq))
         work = _zeroed("gs_chunk_attention_workspace", a, dev, GS_CHUNK_COUNTERS)
         return Call("gs_chunk_attention", (ctypes.byref(a),), dev, (self, d, a, q, out, lse, seq, start, work))
@@ -381,7 +383,9 @@ class PagedCache:
         positions up to its own. Returns out.
 
         seq: int32 [n], start: int32 [n + 1]; scale (default dim ** -0.5); window and sinks: only the
-        last `window` positions up to the row's own and the first `sinks`; lse: fp32 [tokens, q_heads],
+        last `window` positions up to the row's own and the first `sinks`; split_weights: in 16-bit
+        caches the softmax's weights enter the product with V as sums of two 16-bit numbers, as in
+        attention (up to a quarter more time), else rounded to one; lse: fp32 [tokens, q_heads],
         receives the log-sum-exp of the scaled scores. Rows of no entry are left as they were (zeros,
         where out is made here)."""
         import torch

@@ -123,7 +123,7 @@ class Decoder:
     def read(self, seq, tokens, chunk=64):
         """Prompt tokens ([n, t], the same number for every listed sequence) into the cache, up to
         `chunk` of each sequence at a time: their keys and values are stored, and each position
-        attends over everything up to itself."""
+        attends over everything up to itself (in as many bits as the step's attention)."""
         n = len(tokens)
         for part in tokens.split(chunk, 1):
             t = part.shape[1]
@@ -134,7 +134,7 @@ class Decoder:
             for layer in range(self.model.cfg.layers):
                 q, k, v = self.model.split(layer, x)
                 self.cache.write(layer, k, v, seq, start)
-                x = self.model.join(layer, x, self.cache.chunk_attention(q, layer, seq, start))
+                x = self.model.join(layer, x, self.cache.chunk_attention(q, layer, seq, start, split_weights=True))
 
     def step(self):
         """One token of every sample."""

@@ -225,6 +225,10 @@ typedef struct gs_chunk_attention_args {
     float   scale;              /* of the scores (usually dim ** -0.5); finite            */
     int32_t window;             /* 0: every earlier position; else the last `window` ...  */
     int32_t sinks;              /* ... and the first `sinks` positions                    */
+    int32_t split_weights;      /* 16-bit caches: how the weights enter the product with V:
+                                   0 rounded to the cache's type, 1 as a sum of two such
+                                   numbers, as in gs_paged_attention (up to a quarter more
+                                   time)                                                  */
     void*   out;                /* device, cache dtype, [tokens][q_heads][dim]            */
     int64_t out_token_stride, out_head_stride;
     float*  lse;                /* device float[tokens][q_heads] or NULL                  */
@@ -247,10 +251,12 @@ gs_status gs_chunk_attention_workspace(const gs_chunk_attention_args* args, int6
  *   s_j = scale * q . k_j,  M = max_j s_j,  out = sum_j e^(s_j - M) v_j / sum_j e^(s_j - M),
  *   lse = M + ln sum_j e^(s_j - M).
  * Sums, maxima and the output's accumulator are fp32; for 16-bit caches the weights e^(s_j - M)
- * enter the product with V rounded to the cache's type.  A row before its sequence's first token
- * (m > lens) gives out = 0 and lse = -inf.  Rows that no entry has (behind start[n], say) are left as
- * they were.  Rows of a page past the sequence's length are never used, whatever they hold.  Several
- * entries may read one sequence.  Results do not depend on the grid's timing.
+ * enter the product with V rounded to the cache's type, or with split_weights as a sum of two such
+ * numbers (off by 2^-15 of them in bf16, 2^-21 in fp16; an infinity of V may then give NaN).  A row
+ * before its sequence's first token (m > lens) gives out = 0 and lse = -inf.  Rows that no entry has
+ * (behind start[n], say) are left as they were.  Rows of a page past the sequence's length are never
+ * used, whatever they hold.  Several entries may read one sequence.  Results do not depend on the
+ * grid's timing.
  * Device-found: GS_DEV_BAD_SEQ (a sequence id outside the cache: as length 0; a page id outside the
  * pool: its rows read as zeros; a length past the table: cut; rows before the first token; an entry
  * whose rows do not rise or pass 0 .. tokens: skipped; entries that together have more rows than
@@ -258,8 +264,8 @@ gs_status gs_chunk_attention_workspace(const gs_chunk_attention_args* args, int6
  * and many times what a block's share of the call takes: the results are not whole).  Entries whose rows overlap leave either's results there.  out and lse may
  * not overlap an input.
  * Errors: GS_ERR_INVALID_ARG (NULL pointers, sizes, q_heads not a multiple of kv_heads, layer outside
- * the cache, window or sinks < 0, sinks without window, a scale that is not finite, workspace too
- * small), GS_ERR_UNSUPPORTED (the cache's limits, n over GS_MAX_SEQS, tokens * q_heads over 2^30, n *
+ * the cache, window or sinks < 0, sinks without window, a scale that is not finite, split_weights not
+ * 0 or 1, workspace too small), GS_ERR_UNSUPPORTED (the cache's limits, n over GS_MAX_SEQS, tokens * q_heads over 2^30, n *
  * kv_heads over 2^28), GS_ERR_CUDA.  tokens = 0 or n = 0 does nothing.
  */
 gs_status gs_chunk_attention(const gs_chunk_attention_args* args, gs_stream stream);
