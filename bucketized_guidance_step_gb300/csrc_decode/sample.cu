@@ -254,7 +254,8 @@ struct Part {
     }
 };
 
-// Weights relative to the largest.
+// Weights relative to the largest: e^-d off by 2^-24 d each for d, log2 e (a quarter of that) and their product, and by
+// the exponential's 2^-22.
 struct Weigh {
     float ref;
     __device__ __forceinline__ float weight(float z) const { return z == ref ? 1.0f : pow2((z - ref) * kLog2e); }
