@@ -14,6 +14,7 @@
 // end.  The scores' fragments are the second product's operands as they are: a step takes positions 2 t and
 // 2 t + 1 where the instruction numbers them t and t + 4, and reads V's rows likewise.
 #include <cmath>
+#include <limits>
 
 #include "chunk_attention.cuh"
 
@@ -490,7 +491,8 @@ extern "C" gs_status gs_chunk_attention(const gs_chunk_attention_args* args, gs_
     p.slots_wide = aligned(args->workspace, 32);
     // Scores are kept in powers of two, the largest first: a negative scale turns the queries' signs,
     // and scale 0 makes them 0.
-    p.scale_log2 = args->scale == 0.0f ? 1.0f : std::fabs(args->scale) * kChunkLog2e;
+    // (The largest scales would become infinite, and scores of 0 with them NaN.)
+    p.scale_log2 = args->scale == 0.0f ? 1.0f : std::fmin(std::fabs(args->scale) * kChunkLog2e, std::numeric_limits<float>::max());
     p.q_sign = args->scale > 0.0f ? 1.0f : args->scale < 0.0f ? -1.0f : 0.0f;
     // No position is past 2^30, so more leave none out; and a row 2^30 before its sequence less a window stays in 32 bits.
     constexpr int kMostWindow = 1 << 30;
