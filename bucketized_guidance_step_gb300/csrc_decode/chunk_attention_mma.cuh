@@ -20,9 +20,9 @@
 // who asks for it gets them as sums of two 16-bit numbers, with which the output's own rounding is all that is
 // left, for a second product with V (below).
 //
-// Measured (bf16, 32 and 8 heads of 128): a chunk of 2048 tokens over 16384 takes 397 us, 1300 TFLOP/s or 69 % of
+// Measured (bf16, 32 and 8 heads of 128): a chunk of 2048 tokens over 16384 takes 400 us, 1290 TFLOP/s or 68 % of
 // what a plain matrix product reaches; a unit of two tiles is 1940 cycles, of which the tensor cores need 1280
-// (S with N = 64 takes 48 cycles a product of 16 dims, not 32: with N = 128 two places would not fit beside O) and
+// (S with N = 64 takes 48 cycles a product of 16 dims, not 32; of N = 128 one place a tile fits beside O, not two) and
 // the exponentials 1024.  32 sequences of up to 8200 tokens with 1 to 8 new ones: 127 us, HBM at 65 %.
 // With weights as two numbers a unit's products take 1792 cycles, and the two calls 481 and 137 us.
 //

@@ -19,8 +19,8 @@
 // Weights are summed as whole numbers (units of 2^-40 of the largest weight): sums do not depend on the
 // order of the additions, nor does the sorted list on the order in which blocks fill it.
 //
-// Measured: one row of 16384 bf16 logits 12 us with top-k 50, 20 us with top-p 0.9; 64 rows of 131072 fp32 logits 41 us
-// with top-k 500, 80 us with top-p 0.9.  HBM would take 5 us of the last two: what bounds the kernel are the cluster's
+// Measured: one row of 16384 bf16 logits 12 us with top-k 50, 22 us with top-p 0.9; 64 rows of 131072 fp32 logits 47 us
+// with top-k 500, 87 us with top-p 0.9 (inputs in turn, more than L2 holds).  HBM would take 5 us of the last two: what bounds the kernel are the cluster's
 // barriers and lookups in other blocks (a fifth of the issue slots are used), with top-p the shared atomics of the
 // histogram, and with more rows than the GPU holds at a time (32 of 8 blocks) the last of them.
 #include <cmath>

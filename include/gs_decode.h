@@ -261,12 +261,12 @@ gs_status gs_chunk_attention_workspace(const gs_chunk_attention_args* args, int6
  * pool: its rows read as zeros; a length past the table: cut; rows before the first token; an entry
  * whose rows do not rise or pass 0 .. tokens: skipped; entries that together have more rows than
  * there are tokens: nothing is computed), GS_DEV_TIMEOUT (a wait inside the kernel ran out, after 0.2 s
- * and many times what a block's share of the call takes: the results are not whole).  Entries whose rows overlap leave either's results there.  out and lse may
- * not overlap an input.
+ * and many times what a block's share of the call takes: the results are not whole).  Entries whose
+ * rows overlap leave either's results there.  out and lse may not overlap an input.
  * Errors: GS_ERR_INVALID_ARG (NULL pointers, sizes, q_heads not a multiple of kv_heads, layer outside
  * the cache, window or sinks < 0, sinks without window, a scale that is not finite, split_weights not
- * 0 or 1, workspace too small), GS_ERR_UNSUPPORTED (the cache's limits, n over GS_MAX_SEQS, tokens * q_heads over 2^30, n *
- * kv_heads over 2^28), GS_ERR_CUDA.  tokens = 0 or n = 0 does nothing.
+ * 0 or 1, workspace too small), GS_ERR_UNSUPPORTED (the cache's limits, n over GS_MAX_SEQS, tokens *
+ * q_heads over 2^30, n * kv_heads over 2^28), GS_ERR_CUDA.  tokens = 0 or n = 0 does nothing.
  */
 gs_status gs_chunk_attention(const gs_chunk_attention_args* args, gs_stream stream);
 
